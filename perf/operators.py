@@ -98,8 +98,8 @@ def work(c):
         T, E, k = c["T"], c["E"], c["k"]
         logits = T * E * (4 if c["type"] == "fp32" else 2)
         if op == "route":
-            return {"bytes": logits + T * (1 + 8 * k) + c["roots"] * (4 * E + 4), "flops": 5 * T * E}
-        return {"bytes": 2 * logits + T * (1 + 8 * k) + c["roots"] * (4 * E + 4), "flops": 10 * T * E}
+            return {"bytes": logits + T * (1 + 8 * k) + c["roots"] * (4 * E + 8), "flops": 5 * T * E}
+        return {"bytes": 2 * logits + T * (1 + 8 * k) + c["roots"] * (4 * E + 8), "flops": 10 * T * E}
     if op == "adamw":
         n = sum(_sizes(c)) * c["adapters"]
         p = 2 if c["param"] == "bf16" else 4
@@ -171,8 +171,8 @@ def _prepare_route(c, g):
         torch.arange(c["roots"], device=DEV),
         torch.tensor([b - a for a, b in zip(st["roots"], st["roots"][1:])], device=DEV))
     if c["op"] == "route_grad":
-        idx, w, counts, loss = _route_plain(c, st)
-        st.update(idx=idx, counts=counts, grad_w=_normal(g, T, k),
+        idx, w, counts, active, loss = _route_plain(c, st)
+        st.update(idx=idx, counts=counts, active=active, grad_w=_normal(g, T, k),
                   grad_loss=_normal(g, c["roots"], std=0.1 * math.sqrt(T)))
     return st
 
@@ -318,18 +318,18 @@ def _route_plain(c, st):
     n = _by_root(on.float()[:, None], st, roots)[:, 0]
     mass = _by_root(p.double(), st, roots)
     loss = (counts.double() * mass).sum(1) * E / (k * torch.clamp(n, min=1.0).double().square())
-    return torch.where(taken, idx, -1).to(torch.int32), w, counts.to(torch.int32), loss.float()
+    return torch.where(taken, idx, -1).to(torch.int32), w, counts.to(torch.int32), n.to(torch.int32), loss.float()
 
 
 def _route_grad_plain(c, st):
-    E, k, roots = c["E"], c["k"], c["roots"]
+    E, k = c["E"], c["k"]
     l = st["logits"].float()
     on = _active(st)
     p = _softmax(l, on)
     taken = st["idx"] >= 0
     idx = st["idx"].clamp(min=0).long()
     gw = torch.where(taken, st["grad_w"], 0.0)
-    n = torch.clamp(_by_root(on.float()[:, None], st, roots)[:, 0], min=1.0)
+    n = torch.clamp(st["active"].float(), min=1.0)
     coef = (st["grad_loss"] * E / (k * n.square()))[:, None] * st["counts"].float()  # [roots, E]
     up = coef[st["root_of"]]
     if c["renorm"]:
@@ -427,8 +427,8 @@ def _own(c, st):
     if op == "route":
         return st["handle"].forward(st["logits"], valid=st["valid"])
     if op == "route_grad":
-        return st["handle"].backward(st["logits"], st["idx"], st["counts"], st["grad_w"], st["grad_loss"],
-                                     valid=st["valid"])
+        return st["handle"].backward(st["logits"], st["idx"], st["counts"], st["active"], st["grad_w"],
+                                     st["grad_loss"], valid=st["valid"])
     if op == "adamw":
         h = st["hyper"]
         st["handle"].step(lr=h["lr"], step=h["step"], grad_scale=h["grad_scale"], seed=h["seed"])
@@ -474,14 +474,16 @@ def _route_exact(c, st):
     w = torch.where(idx >= 0, p.gather(1, idx.clamp(min=0)), 0.0)
     if c["renorm"]:
         w = w / torch.where(on, w.sum(1), 1.0)[:, None]
-    counts, loss = [], []
+    counts, active, loss = [], [], []
     for a, b in zip(st["roots"], st["roots"][1:]):
         got = idx[a:b].reshape(-1)
         cnt = torch.bincount(got[got >= 0], minlength=E)
         n = max(1, int(on[a:b].sum()))
         counts.append(cnt)
+        active.append(on[a:b].sum())
         loss.append((cnt.double() / (k * n) * (p[a:b].sum(0) / n)).sum() * E)
-    return idx.to(torch.int32), w, torch.stack(counts).to(torch.int32), torch.stack(loss)
+    return (idx.to(torch.int32), w, torch.stack(counts).to(torch.int32), torch.stack(active).to(torch.int32),
+            torch.stack(loss))
 
 
 def _route_grad_exact(c, st):
