@@ -354,6 +354,179 @@ moe_status moe_lora_backward_multi(const moe_lora_desc* desc, const moe_adapters
                                    const moe_lora_grads* grads, void* scratch, size_t scratch_bytes,
                                    void* stream);
 
+/* ------------------------------------------------------------------------
+ * The router: what a layer call takes as topk_idx and topk_w, the load of
+ * each expert and its balance loss, and the gradient of all of them.
+ *
+ * Token t of root a (roots as in moe_adapters; NULL adapters: one root) with
+ * logits l_te over E experts is ACTIVE when valid[t] != 0, no logit of it is
+ * NaN or +inf, and at least one is above -inf.  For an active token
+ *   idx_t   = the topk largest logits, descending, equals in ascending expert
+ *             order; an expert at -inf is never taken (missing routes: -1),
+ *   p_te    = exp(l_te) / sum_e' exp(l_te')          (max-shifted, fp32),
+ *   w_tj    = p at idx_tj, divided by their sum if `renorm`; 0 where idx is -1.
+ * An inactive token gets idx -1, w 0 and takes part in nothing below.
+ *   counts[a, e] = routes of root a's tokens to e,   n_a = active tokens of a,
+ *   loss[a]  = E / (topk n_a^2) sum_e counts[a, e] sum_t p_te    (n_a = 0: 0),
+ * the product of each expert's share of the routes and its mean probability
+ * (1 at perfect balance with topk routes per token).  With several roots the
+ * router runs once per root (OpenPipe/ART PR #1139, Behavior).
+ *
+ * Backward, for dL/dw = grad_w and dL/dloss = grad_loss (either may be NULL:
+ * zero), the counts taken as constants:
+ *   u_te = grad_loss[a] E / (topk n_a^2) counts[a, e]
+ *   dl_te = p_te (u_te - sum_e' p u) + the top-k term:
+ *     renorm:  at e = idx_tj: w_tj (grad_w_tj - sum_i w_ti grad_w_ti)
+ *     else:    p_te (G_te - sum_e' p G), G = grad_w at the chosen experts.
+ * grad_logits has the logits' type and is 0 for inactive tokens.
+ *
+ * Supported: T >= 1, 1 <= E <= 512, 1 <= topk <= min(16, E), T * E < 2^31,
+ * T * topk < 2^31 (others: MOE_ERR_UNSUPPORTED; topk > E or non-positive
+ * sizes: MOE_ERR_INVALID).  Sums over tokens run in a fixed order: results
+ * are bitwise repeatable.
+ * ------------------------------------------------------------------------ */
+#define MOE_TYPE_F32 0
+#define MOE_TYPE_BF16 1
+
+typedef struct moe_router_desc {
+  int32_t T, E, topk;
+  int32_t logits_type; /* MOE_TYPE_F32 or MOE_TYPE_BF16 */
+  int32_t renorm;      /* 0 or 1 */
+} moe_router_desc;
+
+/* Bytes of the workspace of moe_router_forward (nothing in it survives the
+ * call).  adapters may be NULL (one root). */
+moe_status moe_router_workspace_size(const moe_router_desc* desc, const moe_adapters* adapters, size_t* bytes);
+
+/* logits [T, E]; valid [T] uint8 or NULL (every token valid); outputs
+ * topk_idx [T, topk] int32, topk_w [T, topk] fp32, counts [roots, E] int32,
+ * active [roots] int32 (n_a), loss [roots] fp32; device_error (device int32,
+ * may be NULL) is overwritten with the number of valid tokens dropped for a
+ * NaN or +inf logit.  logits and workspace 16-byte aligned, the others by
+ * their element. */
+moe_status moe_router_forward(const moe_router_desc* desc, const moe_adapters* adapters, const void* logits,
+                              const uint8_t* valid, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                              int32_t* active, float* loss, int32_t* device_error, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* topk_idx, counts and active as moe_router_forward wrote them for the same
+ * logits and valid; grad_topk_w [T, topk] fp32 or NULL, grad_loss [roots]
+ * fp32 or NULL; grad_logits [T, E] of the logits' type (overwritten; may be
+ * the logits' own buffer). */
+moe_status moe_router_backward(const moe_router_desc* desc, const moe_adapters* adapters, const void* logits,
+                               const uint8_t* valid, const int32_t* topk_idx, const int32_t* counts,
+                               const int32_t* active, const float* grad_topk_w, const float* grad_loss,
+                               void* grad_logits, void* stream);
+
+/* ------------------------------------------------------------------------
+ * One AdamW step over many tensors (the six adapter factors of one or more
+ * layers and adapters).  Per element, with g = grad_scale * grad:
+ *   m <- beta1 m + (1 - beta1) g        v <- beta2 v + (1 - beta2) g^2
+ *   p <- p (1 - lr weight_decay) - lr (m / bias1) / (sqrt(v / bias2) + eps)
+ * with bias1 = 1 - beta1^step, bias2 = 1 - beta2^step, in fp32.  p is the
+ * fp32 master copy if there is one (then `param` receives its rounding), else
+ * `param` itself.
+ *
+ * state_bits 32: m, v fp32.  state_bits 8: per run of 128 elements of a
+ * tensor (the last one may be short) m is e4m3 codes times one fp32 scale
+ * (max|m| / 448) and v is e5m2 codes times one fp32 scale (max v / 57344);
+ * the step itself uses the unrounded m and v.  Codes are rounded at random:
+ * y = x * (448 or 57344) / max is clamped to the format's largest value, 16
+ * random bits are added below its last kept mantissa bit, the rest is cut
+ * (below the format's normal range the cut value is then rounded to nearest,
+ * ties to even).  Without it a decaying average would stop moving once a
+ * step changes it by less than half a code.  A positive v never falls to
+ * code 0, so that no m is divided by eps alone.  The random bits of element
+ * i of a tensor are a fixed mix of i and `seed`; pass another seed each step.
+ *   x0 = i * 0x9E3779B9 + seed, x1 = (x0 ^ x0 >> 16) * 0x6A09E667,
+ *   x2 = (x1 ^ x1 >> 15) * 0xBB67AE85, r = x2 ^ x2 >> 16 (mod 2^32):
+ *   bits 0-15 for m, 16-31 for v.
+ * A run whose new moments are not finite gets a non-finite scale; one whose
+ * largest moment is below 2^-100 counts as zero.
+ * All-zero codes and scales are the state before the first step.
+ * ------------------------------------------------------------------------ */
+typedef struct moe_adamw_tensor {
+  void* param;       /* [n] of param_type, updated */
+  float* master;     /* [n] fp32 or NULL (bf16 parameters only; all tensors of a call alike) */
+  const void* grad;  /* [n] of grad_type */
+  void* m;           /* [n] fp32, or e4m3 codes */
+  void* v;           /* [n] fp32, or e5m2 codes */
+  float* m_scale;    /* [ceil(n / 128)] with state_bits 8, else NULL */
+  float* v_scale;
+  int64_t n;         /* >= 0; 0: skipped, pointers not looked at */
+} moe_adamw_tensor;
+
+/* What changes from step to step, in device memory: for steps captured into
+ * a graph and replayed with other values. */
+typedef struct moe_adamw_control {
+  float lr, bias1, bias2, grad_scale;
+  uint32_t seed;
+} moe_adamw_control;
+
+typedef struct moe_adamw_desc {
+  int32_t param_type, grad_type; /* MOE_TYPE_* */
+  int32_t state_bits;            /* 32 or 8 */
+  uint32_t seed;                 /* read with state_bits 8 */
+  double lr, beta1, beta2, eps, weight_decay, grad_scale;
+  int64_t step;                  /* 1 for the first step */
+  const moe_adamw_control* control; /* DEVICE pointer or NULL: replaces lr, step's biases, grad_scale and seed */
+} moe_adamw_desc;
+
+/* Update `count` tensors (HOST array, read during the call).  Pointers of
+ * non-empty tensors 16-byte aligned (scales 4-byte); no buffer of the call
+ * may overlap another one that it writes (within a tensor this is checked).
+ * lr, weight_decay >= 0, eps > 0,
+ * betas in [0, 1), step >= 1, all finite, else MOE_ERR_INVALID. */
+moe_status moe_adamw_step(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors, int32_t count, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Expert products in 8-bit floating point with one fp32 scale for each block
+ * of 128: the base of a layer stored as e4m3 codes with a scale per 128 x 128
+ * block of a weight, activations as e4m3 codes with a scale per row and 128
+ * columns.  For pool row r of expert e (rows as build_pool laid them out)
+ *   out[r, n] = sum_c sa[a(r), c] sw[e, n / 128, c] sum_{k in block c} a[a(r), k] w[e, n, k]
+ * with fp32 accumulation and one rounding to bf16.  a(r) is the token
+ * row_to_route[r] / topk (gate / up: tokens are gathered) or r itself (down,
+ * and the gradients of pool rows).  The data gradient is the same product
+ * with the transposed weight and its transposed scales.
+ * E4M3 is OCP FP8 E4M3 (largest value 448, NaN 0x7F, no infinities).
+ * ------------------------------------------------------------------------ */
+#define MOE_FP8_PLAIN (-1)
+
+/* Rows to codes and scales: per row and 128 columns scale = max|x| / 448 and
+ * code = e4m3(x * (448 / max|x|)), to nearest, ties to even (fp32 arithmetic;
+ * an all-zero block, or one with a maximum below 2^-100: scale 0, codes 0).
+ * A block with a NaN or an infinity gets a non-finite scale.
+ *   act MOE_FP8_PLAIN: src [rows, K] bf16, x = src;
+ *   act MOE_ACT_SWIGLU / MOE_ACT_GEGLU: src [rows, 2K] bf16 = [gate | up],
+ *     x = act(gate) * up in fp32.
+ *   codes [rows, K] bytes, scales [rows, K / 128] fp32.  K % 128 == 0 (else
+ *   MOE_ERR_UNSUPPORTED), rows >= 0 (0: nothing is done). */
+moe_status moe_fp8_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes, float* scales,
+                                 void* stream);
+
+/* Weights W [E, N, K] bf16 to codes [E, N, K] and scales [E, N/128, K/128] by
+ * 128 x 128 blocks (the same rounding), and, if both are given, the same
+ * codes transposed per expert, codes_t [E, K, N] and scales_t [E, K/128,
+ * N/128].  N, K % 128 == 0 and at most 65536, 1 <= E <= 512, N * K < 2^31. */
+moe_status moe_fp8_quantize_weight(const void* W, int32_t E, int32_t N, int32_t K, void* codes, float* scales,
+                                   void* codes_t, float* scales_t, void* stream);
+
+typedef struct moe_fp8_desc {
+  int32_t E, N, K; /* N, K % 128 == 0, at most 65536; 1 <= E <= 512; N * K < 2^31 */
+  int32_t topk;    /* > 0: gather, row r reads activation row row_to_route[r] / topk; 0: row r */
+  int64_t a_rows;  /* rows of a: tokens (gather), at least the pool's rows in use otherwise; gather: a_rows * K < 2^31 */
+} moe_fp8_desc;
+
+/* out [pool->capacity, N] bf16: the rows of routes are written, padding and
+ * unused rows are left as they were.  pool: counts, offsets and row_to_route
+ * as build_pool wrote them (route_to_row is not read and may be NULL), E
+ * experts, capacity = its allocated rows.  a [a_rows, K], a_scales [a_rows,
+ * K/128], w [E, N, K], w_scales [E, N/128, K/128].  A route whose activation
+ * row is not below a_rows reads zeros. */
+moe_status moe_fp8_product(const moe_fp8_desc* desc, const moe_pool* pool, const void* a, const float* a_scales,
+                           const void* w, const float* w_scales, void* out, void* stream);
+
 /* Optional per-kernel timing (the pages' backward carries an optional kernel
  * trace: PR #9 review-bot Overview).  When enabled, every kernel the library
  * launches is bracketed by two HIP events recorded on its launch stream; the

@@ -27,6 +27,8 @@ MOE_BASE_BF16, MOE_BASE_MXFP4 = 0, 1
 MOE_SAVED_STATUS_OFFSET = 0
 MOE_SAVED_FP16_RANGE = 1
 MOE_MAX_ADAPTERS = 64
+MOE_TYPE_F32, MOE_TYPE_BF16 = 0, 1
+MOE_FP8_PLAIN = -1
 
 EXPORTS = (
     "moe_lora_status_string", "moe_lora_version", "moe_lora_block_m", "moe_lora_pool_capacity",
@@ -34,6 +36,8 @@ EXPORTS = (
     "moe_lora_transform_base", "moe_lora_split_e2m3x2", "moe_lora_trace_enable", "moe_lora_trace_collect", "moe_lora_trace_count",
     "moe_lora_trace_entry", "moe_lora_trace_reset", "moe_lora_multi_pool_capacity",
     "moe_lora_multi_workspace_size", "build_pool_multi", "moe_lora_forward_multi", "moe_lora_backward_multi",
+    "moe_router_workspace_size", "moe_router_forward", "moe_router_backward", "moe_adamw_step",
+    "moe_fp8_quantize_rows", "moe_fp8_quantize_weight", "moe_fp8_product",
 )
 
 
@@ -74,6 +78,28 @@ class MoeLoraGrads(ctypes.Structure):
 
 class MoeAdapters(ctypes.Structure):
     _fields_ = [("count", ctypes.c_int32), ("offsets", ctypes.POINTER(ctypes.c_int32))]
+
+
+class MoeRouterDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("logits_type", ctypes.c_int32), ("renorm", ctypes.c_int32)]
+
+
+class MoeAdamwTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "m", "v", "m_scale", "v_scale")] + [
+        ("n", ctypes.c_int64)]
+
+
+class MoeAdamwDesc(ctypes.Structure):
+    _fields_ = [("param_type", ctypes.c_int32), ("grad_type", ctypes.c_int32), ("state_bits", ctypes.c_int32),
+                ("seed", ctypes.c_uint32)] + [
+        (n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay", "grad_scale")] + [
+        ("step", ctypes.c_int64), ("control", ctypes.c_void_p)]
+
+
+class MoeFp8Desc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("a_rows", ctypes.c_int64)]
 
 
 def _adapters(roots: Optional[Sequence[int]]):
@@ -135,7 +161,18 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
                                            vp, ctypes.c_size_t, vp, ctypes.c_size_t, vp]
     lib.moe_lora_backward_multi.argtypes = [P(MoeLoraDesc), A, P(MoePool), vp, vp, P(MoeLoraParams), vp,
                                             ctypes.c_size_t, vp, vp, P(MoeLoraGrads), vp, ctypes.c_size_t, vp]
-    for fn in ("moe_lora_trace_collect", "moe_lora_trace_entry", "moe_lora_block_m", "moe_lora_pool_capacity", "moe_lora_workspace_size",
+    i32, i64, sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
+    RD = P(MoeRouterDesc)
+    lib.moe_router_workspace_size.argtypes = [RD, A, P(sz)]
+    lib.moe_router_forward.argtypes = [RD, A, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.moe_router_backward.argtypes = [RD, A, vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.moe_adamw_step.argtypes = [P(MoeAdamwDesc), P(MoeAdamwTensor), i32, vp]
+    lib.moe_fp8_quantize_rows.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+    lib.moe_fp8_quantize_weight.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.moe_fp8_product.argtypes = [P(MoeFp8Desc), P(MoePool), vp, vp, vp, vp, vp, vp]
+    for fn in ("moe_router_workspace_size", "moe_router_forward", "moe_router_backward", "moe_adamw_step",
+               "moe_fp8_quantize_rows", "moe_fp8_quantize_weight", "moe_fp8_product",
+               "moe_lora_trace_collect", "moe_lora_trace_entry", "moe_lora_block_m", "moe_lora_pool_capacity", "moe_lora_workspace_size",
                "build_pool", "moe_lora_forward", "moe_lora_forward_noalloc", "moe_lora_backward",
                "moe_lora_transform_base", "moe_lora_split_e2m3x2", "moe_lora_multi_pool_capacity",
                "moe_lora_multi_workspace_size", "build_pool_multi", "moe_lora_forward_multi",
@@ -471,6 +508,306 @@ def moe_lora_split_e2m3x2(src: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
                                          _ptr(scales, torch.int32, None, "scale_words"), _stream(stream))
     _check(st, "moe_lora_split_e2m3x2")
     return codes, scales
+
+
+class _On:
+    """The device and stream of one call: the device that every tensor of it
+    is on (made the current one for the call if it is not), and the caller's
+    stream there."""
+
+    __slots__ = ("stream", "_guard")
+
+    def __init__(self, stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
+        dev = first.device
+        if dev.type != "cuda":
+            raise ValueError("tensors must be device tensors")
+        for t in others:
+            if t is not None and t.device != dev:
+                raise ValueError(f"tensors on {dev} and {t.device}: one call runs on one device")
+        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        self.stream = _stream(torch.cuda.current_stream(dev) if stream is None else stream)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _made(stream, *tensors: torch.Tensor) -> None:
+    """Outputs allocated for a call on a stream that is not the current one:
+    their memory is not handed out again before that stream is done."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in tensors:
+            t.record_stream(stream)
+
+
+_FLOAT_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
+
+
+def _float_type(dtype, name: str) -> int:
+    if dtype not in _FLOAT_TYPES:
+        raise ValueError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return _FLOAT_TYPES[dtype]
+
+
+# --------------------------------------------------------------------------
+# router
+# --------------------------------------------------------------------------
+def make_router_desc(T: int, E: int, topk: int, dtype=torch.float32, renorm: bool = True) -> MoeRouterDesc:
+    return MoeRouterDesc(T, E, topk, _float_type(dtype, "logits"), int(renorm))
+
+
+def moe_router_workspace_size(desc: MoeRouterDesc, roots: Optional[Sequence[int]] = None) -> int:
+    v = ctypes.c_size_t()
+    ad = _adapters(roots)
+    _check(library().moe_router_workspace_size(ctypes.byref(desc), None if ad is None else ctypes.byref(ad),
+                                               ctypes.byref(v)), "moe_router_workspace_size")
+    return v.value
+
+
+class MoeRouter:
+    """Top-k routing of one shape: T tokens' logits [T, E] to expert ids and
+    weights, expert loads and the balance loss, and the gradient to the
+    logits.  Keeps the output buffers and the workspace; every call
+    overwrites them.
+
+    roots: several adapters in one pass, as in MoeLoraLayer; loads and loss
+    are per root.  renorm: a token's weights divided by their sum.  checked:
+    read the count of dropped tokens after the forward (a device-to-host
+    sync) and raise if a valid token had a NaN or +inf logit."""
+
+    def __init__(self, T: int, E: int, topk: int, dtype=torch.float32, renorm: bool = True,
+                 roots: Optional[Sequence[int]] = None, device="cuda", checked: bool = False):
+        self.desc = make_router_desc(T, E, topk, dtype, renorm)
+        self.dtype = dtype
+        self.checked = checked
+        self.roots = None if roots is None else [int(v) for v in roots]
+        na = 1 if roots is None else len(roots) - 1
+        nbytes = moe_router_workspace_size(self.desc, self.roots)
+        self._ad = _adapters(self.roots)
+        self._adp = None if self._ad is None else ctypes.byref(self._ad)
+        i32, f32 = torch.int32, torch.float32
+        self.topk_idx = torch.empty(T, topk, dtype=i32, device=device)
+        self.topk_w = torch.empty(T, topk, dtype=f32, device=device)
+        self.counts = torch.empty(na, E, dtype=i32, device=device)
+        self.active = torch.empty(na, dtype=i32, device=device)
+        self.loss = torch.empty(na, dtype=f32, device=device)
+        self.device_error = torch.empty(1, dtype=i32, device=device)
+        self.grad_logits = torch.empty(T, E, dtype=dtype, device=device)
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+    def forward(self, logits: torch.Tensor, valid: Optional[torch.Tensor] = None, stream=None):
+        """logits [T, E]; valid [T] uint8 (0: a padding token) or None.
+        Returns (topk_idx, topk_w, counts, active, loss)."""
+        d = self.desc
+        lp = _ptr(logits, self.dtype, (d.T, d.E), "logits")
+        vp = _ptr(valid, torch.uint8, (d.T,), "valid")
+        with _On(stream, self.topk_idx, logits, valid) as s:
+            st = library().moe_router_forward(
+                ctypes.byref(d), self._adp, lp, vp, self.topk_idx.data_ptr(), self.topk_w.data_ptr(),
+                self.counts.data_ptr(), self.active.data_ptr(), self.loss.data_ptr(), self.device_error.data_ptr(),
+                self.workspace.data_ptr(), self.workspace.numel(), s)
+        _check(st, "moe_router_forward")
+        if self.checked:
+            bad = self.dropped_tokens(stream)
+            if bad:
+                raise FloatingPointError(f"moe_router_forward: {bad} valid token(s) with a NaN or +inf logit were dropped")
+        return self.topk_idx, self.topk_w, self.counts, self.active, self.loss
+
+    def dropped_tokens(self, stream=None) -> int:
+        """Valid tokens the last forward dropped for a NaN or +inf logit (syncs)."""
+        _sync(stream)
+        return int(self.device_error.item())
+
+    def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, counts: torch.Tensor, active: torch.Tensor,
+                 grad_topk_w: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
+                 valid: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The gradient to the logits, [T, E] of their type, from the
+        forward's topk_idx, counts and active (the router's own buffers after
+        forward, or copies) and the gradients of topk_w [T, k] and of the
+        loss [roots] (None: zero)."""
+        d, f32, i32 = self.desc, torch.float32, torch.int32
+        na = self.counts.shape[0]
+        ptrs = (_ptr(logits, self.dtype, (d.T, d.E), "logits"), _ptr(valid, torch.uint8, (d.T,), "valid"),
+                _ptr(topk_idx, i32, (d.T, d.topk), "topk_idx"), _ptr(counts, i32, (na, d.E), "counts"),
+                _ptr(active, i32, (na,), "active"), _ptr(grad_topk_w, f32, (d.T, d.topk), "grad_topk_w"),
+                _ptr(grad_loss, f32, (na,), "grad_loss"))
+        with _On(stream, self.topk_idx, logits, valid, topk_idx, counts, active, grad_topk_w, grad_loss) as s:
+            st = library().moe_router_backward(ctypes.byref(d), self._adp, *ptrs, self.grad_logits.data_ptr(), s)
+        _check(st, "moe_router_backward")
+        return self.grad_logits
+
+
+# --------------------------------------------------------------------------
+# optimiser
+# --------------------------------------------------------------------------
+class MoeAdamW:
+    """AdamW over a list of tensors (the factors of one or more layers) in one
+    call per step.  params: bf16 or fp32, all of one type, updated in place;
+    grads: bf16 or fp32 buffers of the same sizes that are read at each step
+    (MoeLoraLayer.grads, say); masters: fp32 copies of bf16 params that are
+    updated instead, the params getting their rounding.  state_bits 32 or 8
+    (see include/moelora.h); states: {"m": [...], "v": [...], "m_scale":
+    [...], "v_scale": [...]} to go on from, else zeros."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+                 masters: Optional[Sequence[torch.Tensor]] = None, state_bits: int = 32, lr: float = 1e-3,
+                 betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, weight_decay: float = 0.0,
+                 states: Optional[Dict[str, Sequence[torch.Tensor]]] = None):
+        if not params or len(grads) != len(params) or (masters is not None and len(masters) != len(params)):
+            raise ValueError("params, grads and masters are lists of one length, not empty")
+        if state_bits not in (32, 8):
+            raise ValueError("state_bits must be 32 or 8")
+        self.params, self.grads = list(params), list(grads)
+        self.masters = None if masters is None else list(masters)
+        self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
+        self.state_bits = state_bits
+        self.steps = 0  # steps taken
+        eight = state_bits == 8
+        kinds = {"m": torch.float8_e4m3fn, "v": torch.float8_e5m2} if eight else dict.fromkeys("mv", torch.float32)
+        runs = [-(-p.numel() // 128) for p in self.params]
+        if states is None:
+            states = {n: [torch.zeros(p.shape, dtype=torch.uint8 if eight else t, device=p.device).view(t)
+                          for p in self.params] for n, t in kinds.items()}
+            if eight:
+                states.update({n: [torch.zeros(r, device=p.device) for p, r in zip(self.params, runs)]
+                               for n in ("m_scale", "v_scale")})
+        names = ("m", "v", "m_scale", "v_scale") if eight else ("m", "v")
+        if set(states) != set(names) or any(len(states[n]) != len(params) for n in names):
+            raise ValueError(f"states must hold {names}, one tensor each per param")
+        self.states = {n: list(states[n]) for n in names}
+        self._desc = MoeAdamwDesc(_float_type(params[0].dtype, "params"), _float_type(grads[0].dtype, "grads"), state_bits)
+        self._table = (MoeAdamwTensor * len(params))()
+        ptype, gtype, f32 = params[0].dtype, grads[0].dtype, torch.float32
+        if masters is not None and ptype != torch.bfloat16:
+            raise ValueError("masters stand beside bf16 params")
+        for i, p in enumerate(self.params):
+            n = p.numel()
+            every = [self.grads[i], *([] if masters is None else [masters[i]]), *(self.states[k][i] for k in names)]
+            if any(t.device != params[0].device for t in (p, *every)):
+                raise ValueError("one optimiser's tensors are on one device")
+            for t, k in [(self.grads[i], "grads")] + ([] if masters is None else [(masters[i], "masters")]) + [
+                    (self.states[k][i], k) for k in ("m", "v")]:
+                if t.numel() != n:
+                    raise ValueError(f"{k}[{i}] has {t.numel()} elements, params[{i}] {n}")
+            sc = [_ptr(self.states[k][i], f32, (runs[i],), k) for k in ("m_scale", "v_scale")] if eight else [None, None]
+            self._table[i] = MoeAdamwTensor(
+                _ptr(p, ptype, None, "params"), None if masters is None else _ptr(masters[i], f32, None, "masters"),
+                _ptr(self.grads[i], gtype, None, "grads"), _ptr(self.states["m"][i], kinds["m"], None, "m"),
+                _ptr(self.states["v"][i], kinds["v"], None, "v"), *sc, n)
+
+    def step(self, lr: Optional[float] = None, step: Optional[int] = None, grad_scale: float = 1.0,
+             seed: Optional[int] = None, control: Optional[torch.Tensor] = None, stream=None) -> None:
+        """One step.  lr: this step's rate (default: the optimiser's); step:
+        its number (default: one more than the last); grad_scale multiplies
+        the gradients (a clip coefficient, an accumulation's share); seed of
+        the 8-bit states' rounding (default: the step's number).  control:
+        those values in device memory (adamw_control), for a captured step."""
+        self.steps = self.steps + 1 if step is None else int(step)
+        d = self._desc
+        d.lr = self.lr if lr is None else lr
+        d.beta1, d.beta2 = self.betas
+        d.eps, d.weight_decay, d.grad_scale = self.eps, self.weight_decay, grad_scale
+        d.step = self.steps
+        d.seed = (self.steps if seed is None else seed) & 0xFFFFFFFF
+        d.control = _ptr(control, torch.int32, (5,), "control")
+        with _On(stream, self.params[0], control) as s:
+            st = library().moe_adamw_step(ctypes.byref(d), self._table, len(self._table), s)
+        _check(st, "moe_adamw_step")
+
+    def write_control(self, control: torch.Tensor, lr: float, step: int, grad_scale: float = 1.0,
+                      seed: Optional[int] = None) -> None:
+        """Fill a control buffer (int32 [5] on the device) with one step's
+        values: before each replay of a graph that captured a step with it."""
+        f = torch.tensor([lr, 1.0 - self.betas[0] ** step, 1.0 - self.betas[1] ** step, grad_scale],
+                         dtype=torch.float64).to(torch.float32).view(torch.int32)
+        s = (step if seed is None else seed) & 0xFFFFFFFF
+        control.copy_(torch.cat([f, torch.tensor([s - (1 << 32) if s >> 31 else s], dtype=torch.int32)]))
+
+
+# --------------------------------------------------------------------------
+# 8-bit expert products
+# --------------------------------------------------------------------------
+_ACTS = {None: MOE_FP8_PLAIN, "swiglu": MOE_ACT_SWIGLU, "geglu": MOE_ACT_GEGLU}
+_E4M3 = torch.float8_e4m3fn
+
+
+def fp8_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optional[torch.Tensor] = None,
+                      scales: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """src bf16 [rows, K] (act None) or [rows, 2K] = gate | up (act "swiglu",
+    "geglu") to e4m3 codes [rows, K] and fp32 scales [rows, K/128]."""
+    if src.dim() != 2 or act not in _ACTS or (act is not None and src.shape[1] % 2):
+        raise ValueError("src must be [rows, K], or [rows, 2K] with act 'swiglu' or 'geglu'")
+    rows, K = src.shape[0], src.shape[1] if act is None else src.shape[1] // 2
+    made = []
+    if codes is None:
+        codes = torch.empty(rows, K, dtype=_E4M3, device=src.device)
+        made.append(codes)
+    if scales is None:
+        scales = torch.empty(rows, K // 128, dtype=torch.float32, device=src.device)
+        made.append(scales)
+    with _On(stream, src, codes, scales) as s:
+        st = library().moe_fp8_quantize_rows(
+            _ptr(src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], _ptr(codes, _E4M3, (rows, K), "codes"),
+            _ptr(scales, torch.float32, (rows, K // 128), "scales"), s)
+    _check(st, "moe_fp8_quantize_rows")
+    _made(stream, *made)
+    return codes, scales
+
+
+def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) -> Tuple[torch.Tensor, ...]:
+    """W bf16 [E, N, K] to (codes [E, N, K], scales [E, N/128, K/128]) by
+    128 x 128 blocks; with transposed also the same codes as (codes_t
+    [E, K, N], scales_t [E, K/128, N/128]), the data gradient's operand."""
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    E, N, K = W.shape
+    out = [torch.empty(E, N, K, dtype=_E4M3, device=W.device),
+           torch.empty(E, N // 128, K // 128, dtype=torch.float32, device=W.device)]
+    if transposed:
+        out += [torch.empty(E, K, N, dtype=_E4M3, device=W.device),
+                torch.empty(E, K // 128, N // 128, dtype=torch.float32, device=W.device)]
+    with _On(stream, W) as s:
+        st = library().moe_fp8_quantize_weight(_ptr(W, torch.bfloat16, None, "W"), E, N, K,
+                                               *[t.data_ptr() for t in out], *([] if transposed else [None, None]), s)
+    _check(st, "moe_fp8_quantize_weight")
+    _made(stream, *out)
+    return tuple(out)
+
+
+def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
+                w_scales: torch.Tensor, topk: int = 0, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Every pool row times its expert's weight: out bf16 [capacity, N].
+    pool as in MoeLoraLayer.pool; a e4m3 [rows, K] with a_scales [rows,
+    K/128]: the tokens (topk > 0: pool row r reads token row_to_route[r] /
+    topk), or the pool rows themselves (topk = 0); w e4m3 [E, N, K] with
+    w_scales [E, N/128, K/128].  Rows of no route are left as they are (an
+    `out` made here holds zeros there)."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K] and w [E, N, K]")
+    rows, K = a.shape
+    E, N = w.shape[:2]
+    cap = pool["row_to_route"].numel()
+    made = out is None
+    if made:
+        out = torch.zeros(cap, N, dtype=torch.bfloat16, device=a.device)
+    i32, f32 = torch.int32, torch.float32
+    ps = MoePool(_ptr(pool["counts"], i32, (E,), "counts"), _ptr(pool["offsets"], i32, (E + 1,), "offsets"), None,
+                 _ptr(pool["row_to_route"], i32, None, "row_to_route"), cap, 0)
+    d = MoeFp8Desc(E, N, K, topk, rows)
+    with _On(stream, a, a_scales, w, w_scales, out, pool["counts"], pool["offsets"], pool["row_to_route"]) as s:
+        st = library().moe_fp8_product(
+            ctypes.byref(d), ctypes.byref(ps), _ptr(a, _E4M3, None, "a"), _ptr(a_scales, f32, (rows, K // 128), "a_scales"),
+            _ptr(w, _E4M3, (E, N, K), "w"), _ptr(w_scales, f32, (E, N // 128, K // 128), "w_scales"),
+            _ptr(out, torch.bfloat16, (cap, N), "out"), s)
+    _check(st, "moe_fp8_product")
+    if made:
+        _made(stream, out)
+    return out
 
 
 def moe_lora_trace_enable(on: bool) -> None:

@@ -19,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libmoelora.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
-SOURCES = ["pool.hip", "forward.hip", "backward.hip", "pack.hip", "api.hip", "trace.hip", "branch.hip"]
+SOURCES = ["pool.hip", "forward.hip", "backward.hip", "pack.hip", "api.hip", "trace.hip", "branch.hip",
+           "router.hip", "adamw.hip", "fp8.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

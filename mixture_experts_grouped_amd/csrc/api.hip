@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "../../include/moelora.h"
+#include "checks.hpp"
 #include "layer.hpp"
 
 using namespace moelora;
@@ -212,14 +213,6 @@ Plan make_plan(const moe_lora_desc* d, const Roots& R) {
   p.scratch = o;
   return p;
 }
-
-bool aligned16(const void* p) { return p != nullptr && ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;
-};
-Range rng(const void* p, size_t bytes) { return Range{(uintptr_t)p, (uintptr_t)p + bytes}; }
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi; }
 
 moe_status check_pool(const moe_lora_desc* d, const moe_pool* pool, const Plan& p) {
   if (pool == nullptr || pool->counts == nullptr || pool->offsets == nullptr ||

@@ -1,0 +1,493 @@
+// router.hip -- top-k routing with expert loads and balance loss, and its
+// gradient (include/moelora.h states the formulas).
+//
+// Sixteen lanes (one DPP row) hold one token's logits, lane j the experts
+// j, j + 16, ...: maxima, sums and index minima over a token are four DPP
+// instructions without LDS, a wave works on four tokens, and a lane's
+// experts are the same for every token, so the probability mass per expert
+// adds up in registers.  A pass reads each logit once.  The top-k takes the
+// largest key k times; a key is the logit's bits mapped to an unsigned
+// integer of the same order, so the choice is exact and equals go to the
+// lowest expert.
+#include <cmath>
+
+#include "../../include/moelora.h"
+#include "checks.hpp"
+#include "lanes.hpp"
+#include "layer.hpp"
+#include "trace.hpp"
+
+namespace moelora {
+namespace {
+
+constexpr int RT_THREADS = 256;
+constexpr int RT_ROWS = RT_THREADS / 16;  // tokens a workgroup works on at once
+constexpr int RT_TOKENS = 4 * RT_ROWS;    // tokens of one workgroup's chunk
+constexpr uint32_t KEY_NINF = 0x007FFFFFu;  // the key of -inf: nothing at or below it is chosen
+
+struct RouterArgs {
+  int T, E, k, renorm, na;
+  int roots[MAX_ADAPTERS + 1];
+  const void* logits;
+  const uint8_t* valid;
+  int32_t* idx;
+  float* w;
+  int32_t* counts;
+  int32_t* active;
+  float* loss;
+  int32_t* err;
+  // per chunk: mass [chunks][E] fp32, hits [chunks][E] int32, then active and bad tokens [chunks][2] int32
+  float* mass;
+  int32_t* hits;
+  int32_t* tally;
+  // backward
+  const float* gw;
+  const float* gloss;
+  void* glogits;
+};
+
+// chunk b of at most n tokens, never crossing roots: its tokens and root
+__device__ __forceinline__ bool chunk_of(const RouterArgs& a, int b, int n, int& t0, int& nt, int& root) {
+  for (int q = 0; q < a.na; ++q) {
+    const int r0 = a.roots[q], r1 = a.roots[q + 1];
+    const int c = (r1 - r0 + n - 1) / n;
+    if (b < c) {
+      t0 = r0 + b * n;
+      nt = min(n, r1 - t0);
+      root = q;
+      return true;
+    }
+    b -= c;
+  }
+  return false;
+}
+
+__device__ __forceinline__ uint32_t key_of(float l) {
+  const uint32_t b = __float_as_uint(l);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float logit_of(uint32_t key) {
+  return __uint_as_float(key ^ ((uint32_t)((int32_t)~key >> 31) | 0x80000000u));
+}
+
+// The logits of token t held by this lane (experts j + 16 i; -inf past E).
+template <bool BF, int V>
+__device__ __forceinline__ void load_logits(const RouterArgs& a, long t, int j, bool live, float (&l)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = j + 16 * i;
+    l[i] = -INFINITY;
+    if (live && e < a.E)
+      l[i] = BF ? bf2f(((const uint16_t*)a.logits)[t * a.E + e]) : ((const float*)a.logits)[t * a.E + e];
+    l[i] += 0.0f;  // -0 to +0: equal logits have equal keys
+  }
+}
+
+// whether any of the row's 16 lanes holds `c`
+__device__ __forceinline__ bool row_any(bool c) {
+  return ((__ballot(c) >> (threadIdx.x & 48)) & 0xFFFFull) != 0;
+}
+
+// Loads, counts and loss of one root from its chunks' sums, in chunk order.
+// `mass`, `hits`, `tally` point at the root's first chunk.  All threads call
+// it; red holds 2 * RT_THREADS words.
+__device__ void finish_root(const RouterArgs& a, int root, int nchunks, const float* mass, const int32_t* hits,
+                            const int32_t* tally, int& bad, char* red) {
+  const int tid = threadIdx.x;
+  double* rd = (double*)red;
+  int* ri = (int*)red;
+  int act = 0, b = 0;
+  for (int c = tid; c < nchunks; c += RT_THREADS) {
+    act += tally[2 * c];
+    b += tally[2 * c + 1];
+  }
+  ri[tid] = act;
+  ri[RT_THREADS + tid] = b;
+  __syncthreads();
+  for (int s = RT_THREADS / 2; s > 0; s >>= 1) {
+    if (tid < s) {
+      ri[tid] += ri[tid + s];
+      ri[RT_THREADS + tid] += ri[RT_THREADS + tid + s];
+    }
+    __syncthreads();
+  }
+  act = ri[0];
+  bad = ri[RT_THREADS];
+  __syncthreads();
+  double part = 0.0;
+  for (int e = tid; e < a.E; e += RT_THREADS) {
+    double m = 0.0;
+    int h = 0;
+    for (int c = 0; c < nchunks; ++c) {
+      m += (double)mass[(long)c * a.E + e];
+      h += hits[(long)c * a.E + e];
+    }
+    a.counts[(long)root * a.E + e] = h;
+    part += m * (double)h;
+  }
+  rd[tid] = part;
+  __syncthreads();
+  for (int s = RT_THREADS / 2; s > 0; s >>= 1) {
+    if (tid < s) rd[tid] += rd[tid + s];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.active[root] = act;
+    const double n = (double)(act > 0 ? act : 1);
+    a.loss[root] = (float)(rd[0] * (double)a.E / ((double)a.k * n * n));
+  }
+  __syncthreads();
+}
+
+template <bool BF, int V>
+__global__ __launch_bounds__(RT_THREADS) void k_route(RouterArgs a) {
+  __shared__ float smass[RT_ROWS / 4][16 * V];
+  __shared__ int shits[16 * V];
+  __shared__ int stally[2];
+  int t0, nt, root;
+  if (!chunk_of(a, blockIdx.x, RT_TOKENS, t0, nt, root)) return;
+  const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
+  for (int e = tid; e < 16 * V; e += RT_THREADS) shits[e] = 0;
+  if (tid < 2) stally[tid] = 0;
+  __syncthreads();
+  float mass[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) mass[i] = 0.0f;
+  for (int o = 0; o < nt; o += RT_ROWS) {
+    const long t = (long)t0 + o + row;
+    const bool in = o + row < nt;
+    const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
+    float l[V];
+    load_logits<BF, V>(a, t, j, on, l);
+    bool strange = false;
+#pragma unroll
+    for (int i = 0; i < V; ++i) strange |= !(l[i] < INFINITY);
+    const bool bad = row_any(strange);
+    uint32_t key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = bad ? 0u : key_of(l[i]);
+    int my_idx = -1;
+    uint32_t my_key = 0, top = 0;
+    for (int it = 0; it < a.k; ++it) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) best = max(best, key[i]);
+      best = row_max(best);
+      if (it == 0) top = best;
+      uint32_t at = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) at = key[i] == best ? (uint32_t)(j + 16 * i) : at;
+      at = row_min(at);
+      const bool take = best > KEY_NINF;
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = (uint32_t)(j + 16 * i) == at ? 0u : key[i];
+      if (j == it) {
+        my_idx = take ? (int)at : -1;
+        my_key = best;
+      }
+    }
+    const bool act = top > KEY_NINF;
+    const float mx = logit_of(top);
+    float p[V], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = act ? __expf(l[i] - mx) : 0.0f;
+      sum += p[i];
+    }
+    sum = row_sum(sum);
+    const float inv = act ? 1.0f / sum : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) mass[i] += p[i] * inv;
+    float wt = my_idx >= 0 ? __expf(logit_of(my_key) - mx) : 0.0f;
+    if (a.renorm) {
+      const float ws = row_sum(wt);
+      wt = act ? wt / ws : 0.0f;
+    } else {
+      wt *= inv;
+    }
+    if (in && j < a.k) {
+      a.idx[t * a.k + j] = my_idx;
+      a.w[t * a.k + j] = wt;
+      if (my_idx >= 0) atomicAdd(&shits[my_idx], 1);
+    }
+    if (in && j == 0) {
+      if (act) atomicAdd(&stally[0], 1);
+      if (bad) atomicAdd(&stally[1], 1);
+    }
+  }
+  // the four tokens of a wave, then the waves in order
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float m = mass[i];
+    m += __shfl_xor(m, 16, 64);
+    m += __shfl_xor(m, 32, 64);
+    if ((tid & 48) == 0) smass[tid >> 6][j + 16 * i] = m;
+  }
+  __syncthreads();
+  for (int e = tid; e < a.E; e += RT_THREADS) {
+    float m = 0.0f;
+#pragma unroll
+    for (int wv = 0; wv < RT_ROWS / 4; ++wv) m += smass[wv][e];
+    a.mass[(long)blockIdx.x * a.E + e] = m;
+    a.hits[(long)blockIdx.x * a.E + e] = shits[e];
+  }
+  if (tid < 2) a.tally[2 * (long)blockIdx.x + tid] = stally[tid];
+}
+
+__global__ __launch_bounds__(RT_THREADS) void k_route_sum(RouterArgs a) {
+  __shared__ __align__(16) char red[RT_THREADS * 8];
+  int first = 0;
+  int bad = 0;
+  for (int q = 0; q < a.na; ++q) {
+    const int nc = (a.roots[q + 1] - a.roots[q] + RT_TOKENS - 1) / RT_TOKENS;
+    int b;
+    finish_root(a, q, nc, a.mass + (long)first * a.E, a.hits + (long)first * a.E, a.tally + 2 * (long)first, b, red);
+    bad += b;
+    first += nc;
+  }
+  if (threadIdx.x == 0 && a.err != nullptr) *a.err = bad;
+}
+
+// The gradient: the token's softmax again from its logits, the chosen
+// experts' terms placed through a row of LDS per token.
+template <bool BF, int V>
+__global__ __launch_bounds__(RT_THREADS) void k_route_bwd(RouterArgs a) {
+  __shared__ float place[RT_ROWS][16 * V];
+  int t0, nt, root;
+  if (!chunk_of(a, blockIdx.x, RT_TOKENS, t0, nt, root)) return;
+  const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
+  float u[V];
+  {
+    const float n = (float)max(a.active[root], 1);
+    const float c = a.gloss != nullptr ? a.gloss[root] * (float)a.E / ((float)a.k * n * n) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int e = j + 16 * i;
+      u[i] = (a.gloss != nullptr && e < a.E) ? c * (float)a.counts[(long)root * a.E + e] : 0.0f;
+    }
+  }
+  float* mine = place[row];
+  for (int o = 0; o < nt; o += RT_ROWS) {
+    const long t = (long)t0 + o + row;
+    const bool in = o + row < nt;
+    const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
+    float l[V];
+    load_logits<BF, V>(a, t, j, on, l);
+    int idx = -1;
+    float g = 0.0f, lsel = 0.0f;
+    if (on && j < a.k && a.gw != nullptr) {
+      idx = a.idx[t * a.k + j];
+      if (idx < 0 || idx >= a.E) idx = -1;
+      if (idx >= 0) {
+        g = a.gw[t * a.k + j];
+        lsel = BF ? bf2f(((const uint16_t*)a.logits)[t * a.E + idx]) : ((const float*)a.logits)[t * a.E + idx];
+      }
+    }
+    bool strange = false;
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      strange |= !(l[i] < INFINITY);
+      top = max(top, key_of(l[i]));
+    }
+    top = row_max(top);
+    const bool act = !row_any(strange) && top > KEY_NINF;
+    const float mx = logit_of(top);
+    float p[V], sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = act ? __expf(l[i] - mx) : 0.0f;
+      sum += p[i];
+    }
+    const float inv = act ? 1.0f / row_sum(sum) : 0.0f;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] *= inv;
+      s += p[i] * u[i];
+    }
+    if (!act) idx = -1;
+    float psel = idx >= 0 ? __expf(lsel - mx) : 0.0f;
+    float term;
+    if (a.renorm) {
+      const float ws = row_sum(psel);
+      const float wt = psel > 0.0f ? psel / ws : 0.0f;
+      term = wt * (g - row_sum(wt * g));
+    } else {
+      term = psel * inv * g;
+      s += term;
+    }
+    s = row_sum(s);
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[j + 16 * i] = 0.0f;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (idx >= 0) mine[idx] = term;  // a row's ids are distinct
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (in) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = j + 16 * i;
+        if (e < a.E) {
+          const float d = act ? p[i] * (u[i] - s) + mine[e] : 0.0f;
+          if (BF)
+            ((uint16_t*)a.glogits)[t * a.E + e] = (uint16_t)f2bf(d);
+          else
+            ((float*)a.glogits)[t * a.E + e] = d;
+        }
+      }
+    }
+  }
+}
+
+int chunks_of(const RouterArgs& a) {
+  int n = 0;
+  for (int q = 0; q < a.na; ++q) n += (a.roots[q + 1] - a.roots[q] + RT_TOKENS - 1) / RT_TOKENS;
+  return n;
+}
+
+// experts a lane holds: the smallest of 4, 8, 16, 32 that covers E
+template <template <bool, int> class F, class... A>
+void by_shape(bool bf, int E, A&&... args) {
+  if (E <= 64)
+    bf ? F<true, 4>::go(args...) : F<false, 4>::go(args...);
+  else if (E <= 128)
+    bf ? F<true, 8>::go(args...) : F<false, 8>::go(args...);
+  else if (E <= 256)
+    bf ? F<true, 16>::go(args...) : F<false, 16>::go(args...);
+  else
+    bf ? F<true, 32>::go(args...) : F<false, 32>::go(args...);
+}
+template <bool BF, int V>
+struct GoRoute {
+  static void go(const RouterArgs& a, int n, hipStream_t st) {
+    MOE_LAUNCH_AS("k_route", (k_route<BF, V>), dim3(n), dim3(RT_THREADS), 0, st, a);
+  }
+};
+template <bool BF, int V>
+struct GoRouteBwd {
+  static void go(const RouterArgs& a, int n, hipStream_t st) {
+    MOE_LAUNCH_AS("k_route_bwd", (k_route_bwd<BF, V>), dim3(n), dim3(RT_THREADS), 0, st, a);
+  }
+};
+
+moe_status check_router(const moe_router_desc* d, const moe_adapters* ad, RouterArgs& a) {
+  if (d == nullptr || d->T < 1 || d->E < 1 || d->topk < 1 || d->topk > d->E) return MOE_ERR_INVALID;
+  if (d->renorm != 0 && d->renorm != 1) return MOE_ERR_INVALID;
+  if (d->E > 512 || d->topk > 16) return MOE_ERR_UNSUPPORTED;
+  if (d->logits_type != MOE_TYPE_F32 && d->logits_type != MOE_TYPE_BF16) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)d->T * d->E >= (int64_t)1 << 31 || (int64_t)d->T * d->topk >= (int64_t)1 << 31)
+    return MOE_ERR_UNSUPPORTED;
+  a = RouterArgs{};
+  a.T = d->T;
+  a.E = d->E;
+  a.k = d->topk;
+  a.renorm = d->renorm;
+  a.na = 1;
+  a.roots[1] = d->T;
+  if (ad == nullptr) return MOE_OK;
+  if (ad->offsets == nullptr || ad->count < 1) return MOE_ERR_INVALID;
+  if (ad->count > MAX_ADAPTERS) return MOE_ERR_UNSUPPORTED;
+  if (ad->offsets[0] != 0 || ad->offsets[ad->count] != d->T) return MOE_ERR_INVALID;
+  for (int q = 0; q < ad->count; ++q)
+    if (ad->offsets[q + 1] < ad->offsets[q]) return MOE_ERR_INVALID;
+  a.na = ad->count;
+  for (int q = 0; q <= ad->count; ++q) a.roots[q] = ad->offsets[q];
+  return MOE_OK;
+}
+
+size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
+size_t workspace_of(const RouterArgs& a) {
+  const size_t n = (size_t)chunks_of(a);
+  return 2 * up16(n * a.E * 4) + up16(n * 8);
+}
+
+}  // namespace
+}  // namespace moelora
+
+using namespace moelora;
+
+extern "C" {
+
+moe_status moe_router_workspace_size(const moe_router_desc* d, const moe_adapters* ad, size_t* bytes) {
+  RouterArgs a;
+  const moe_status st = check_router(d, ad, a);
+  if (st != MOE_OK) return st;
+  if (bytes == nullptr) return MOE_ERR_INVALID;
+  *bytes = workspace_of(a);
+  return MOE_OK;
+}
+
+moe_status moe_router_forward(const moe_router_desc* d, const moe_adapters* ad, const void* logits,
+                              const uint8_t* valid, int32_t* topk_idx, float* topk_w, int32_t* counts,
+                              int32_t* active, float* loss, int32_t* device_error, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  RouterArgs a;
+  const moe_status st = check_router(d, ad, a);
+  if (st != MOE_OK) return st;
+  if (!aligned16(logits) || !aligned(topk_idx, 4) || !aligned(topk_w, 4) || !aligned(counts, 4) ||
+      !aligned(active, 4) || !aligned(loss, 4) || (device_error != nullptr && !aligned(device_error, 4)) ||
+      !aligned16(workspace))
+    return MOE_ERR_INVALID;
+  const size_t need = workspace_of(a);
+  if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
+  const size_t le = d->logits_type == MOE_TYPE_BF16 ? 2 : 4, routes = (size_t)a.T * a.k;
+  const Range ins[] = {rng(logits, (size_t)a.T * a.E * le), rng(valid, (size_t)a.T)};
+  const Range outs[] = {rng(topk_idx, routes * 4), rng(topk_w, routes * 4), rng(counts, (size_t)a.na * a.E * 4),
+                        rng(active, (size_t)a.na * 4), rng(loss, (size_t)a.na * 4), rng(device_error, 4),
+                        rng(workspace, need)};
+  for (int i = 0; i < 7; ++i) {
+    for (const Range& r : ins)
+      if (overlap(outs[i], r)) return MOE_ERR_INVALID;
+    for (int j = 0; j < i; ++j)
+      if (overlap(outs[i], outs[j])) return MOE_ERR_INVALID;
+  }
+  const size_t n = (size_t)chunks_of(a);
+  a.logits = logits;
+  a.valid = valid;
+  a.idx = topk_idx;
+  a.w = topk_w;
+  a.counts = counts;
+  a.active = active;
+  a.loss = loss;
+  a.err = device_error;
+  a.mass = (float*)workspace;
+  a.hits = (int32_t*)((char*)workspace + up16(n * a.E * 4));
+  a.tally = (int32_t*)((char*)workspace + 2 * up16(n * a.E * 4));
+  const hipStream_t s = (hipStream_t)stream;
+  by_shape<GoRoute>(d->logits_type == MOE_TYPE_BF16, a.E, a, (int)n, s);
+  MOE_LAUNCH(k_route_sum, dim3(1), dim3(RT_THREADS), 0, s, a);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_router_backward(const moe_router_desc* d, const moe_adapters* ad, const void* logits,
+                               const uint8_t* valid, const int32_t* topk_idx, const int32_t* counts,
+                               const int32_t* active, const float* grad_topk_w, const float* grad_loss,
+                               void* grad_logits, void* stream) {
+  RouterArgs a;
+  const moe_status st = check_router(d, ad, a);
+  if (st != MOE_OK) return st;
+  if (!aligned16(logits) || !aligned16(grad_logits) || !aligned(topk_idx, 4) || !aligned(counts, 4) ||
+      !aligned(active, 4) || (grad_topk_w != nullptr && !aligned(grad_topk_w, 4)) ||
+      (grad_loss != nullptr && !aligned(grad_loss, 4)))
+    return MOE_ERR_INVALID;
+  const size_t le = d->logits_type == MOE_TYPE_BF16 ? 2 : 4, routes = (size_t)a.T * a.k;
+  const Range ro = rng(grad_logits, (size_t)a.T * a.E * le), rl = rng(logits, (size_t)a.T * a.E * le);
+  const Range ins[] = {rng(valid, (size_t)a.T), rng(topk_idx, routes * 4), rng(counts, (size_t)a.na * a.E * 4),
+                       rng(active, (size_t)a.na * 4), rng(grad_topk_w, routes * 4),
+                       rng(grad_loss, (size_t)a.na * 4)};
+  if (grad_logits != logits && overlap(ro, rl)) return MOE_ERR_INVALID;
+  for (const Range& r : ins)
+    if (overlap(ro, r)) return MOE_ERR_INVALID;
+  a.logits = logits;
+  a.valid = valid;
+  a.idx = const_cast<int32_t*>(topk_idx);
+  a.counts = const_cast<int32_t*>(counts);
+  a.active = const_cast<int32_t*>(active);
+  a.gw = grad_topk_w;
+  a.gloss = grad_loss;
+  a.glogits = grad_logits;
+  by_shape<GoRouteBwd>(d->logits_type == MOE_TYPE_BF16, a.E, a, chunks_of(a), (hipStream_t)stream);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"

@@ -16,5 +16,7 @@ Modules:
   moe_lora -- forward and backward of the layer, per route
   mxfp4    -- exact dequantisation of e2m1 values with e8m0 block scales
   multi_adapter -- several adapters in one pass, one root of tokens each
+  router   -- top-k routing, expert loads, balance loss and their gradient
+  float8   -- E4M3 / E5M2, block-scaled rows and products, the AdamW step
 """
-from . import pool, moe_lora, mxfp4, multi_adapter  # noqa: F401
+from . import pool, moe_lora, mxfp4, multi_adapter, router, float8  # noqa: F401

@@ -1,0 +1,210 @@
+"""The AdamW step against float64: parameter, gradient and state types, odd
+lengths and many tensors, the 8-bit states' codes and scales, non-finite
+gradients, device-side control values in a replayed graph."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_grouped_amd as M
+from oracle import float8 as O8
+from tests import harness as Hn
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+HYPER = dict(betas=(0.9, 0.99), eps=1e-6, weight_decay=0.1)
+# fp32 moments: two products and a sum of terms of the same order, three
+# roundings, the betas' own rounding to fp32: within 4 * 2^-24 of the terms'
+# magnitudes.  The update: sqrt, two quotients, a few products: 16 * 2^-24 of it.
+MOM, UPD = 4 * 2.0 ** -24, 16 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    Hn.ensure_built()
+
+
+def tensors(sizes, ptype, gtype, seed):
+    g = torch.Generator().manual_seed(seed)
+    ps = [torch.randn(n, generator=g).to(ptype).cuda() for n in sizes]
+    gs = [(torch.randn(n, generator=g) * torch.exp(torch.randn(n, generator=g))).to(gtype).cuda() for n in sizes]
+    return ps, gs
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def codes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def values8(opt, i, name):
+    fmt = "e4m3" if name == "m" else "e5m2"
+    s = f64(opt.states[name + "_scale"][i])
+    c = codes(opt.states[name][i]).reshape(-1)
+    return O8.decode(c, fmt) * np.repeat(s, 128)[:c.size]
+
+
+SIZES = [1, 7, 8, 127, 128, 129, 2048, 2049, 5000, 40960]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("ptype,gtype,master", [(BF, BF, True), (BF, BF, False), (BF, F32, True), (BF, F32, False),
+                                                (F32, F32, False), (F32, BF, False)])
+def test_steps(ptype, gtype, master, bits):
+    ps, gs = tensors(SIZES, ptype, gtype, 1)
+    masters = [p.float() for p in ps] if master else None
+    opt = M.MoeAdamW(ps, gs, masters=masters, state_bits=bits, lr=1e-2, **HYPER)
+    for step in range(1, 4):
+        before = [f64(t) for t in (masters or ps)]
+        if bits == 32:
+            m0, v0 = [f64(t) for t in opt.states["m"]], [f64(t) for t in opt.states["v"]]
+        else:
+            m0, v0 = ([values8(opt, i, n) for i in range(len(ps))] for n in "mv")
+        opt.step(grad_scale=0.5)
+        for i, n in enumerate(SIZES):
+            g = f64(gs[i])
+            p, m, v = O8.adamw(before[i], g, m0[i], v0[i], lr=1e-2, beta1=0.9, beta2=0.99, eps=1e-6, weight_decay=0.1,
+                               step=step, grad_scale=0.5)
+            # the update feels the moments' errors (m may cancel) and v's by its root
+            mterm = 0.9 * np.abs(m0[i]) + 0.1 * np.abs(0.5 * g)
+            upd = 1e-2 * mterm / (1 - 0.9 ** step) / (np.sqrt(v / (1 - 0.99 ** step)) + 1e-6)
+            tol = (UPD + 2 * MOM) * upd + 4 * 2.0 ** -24 * np.abs(before[i])
+            got = f64((masters or ps)[i])
+            if not master and ptype == BF:
+                tol = tol + 2.0 ** -8 * (np.abs(p) + tol)
+            assert np.all(np.abs(got - p) <= tol + 2.0 ** -126)
+            if master:
+                assert torch.equal(ps[i], masters[i].to(BF))
+            if bits == 32:
+                assert np.all(np.abs(f64(opt.states["m"][i]) - m) <= MOM * mterm + 2.0 ** -149)
+                assert np.all(np.abs(f64(opt.states["v"][i]) - v) <= MOM * v + 2.0 ** -149)
+                continue
+            rnd = O8.noise(n, step)
+            for name, x, xt, r, fmt, man in (("m", m, mterm, rnd & 0xFFFF, "e4m3", 3), ("v", v, v, rnd >> np.uint64(16), "e5m2", 2)):
+                want, scale = O8.moments8(x, r.astype(np.float64), fmt)
+                gs_ = f64(opt.states[name + "_scale"][i])
+                # the run's largest |moment|: its fp32 error, and the quotient's
+                big = np.array([xt[128 * q:128 * q + 128].max() for q in range(len(scale))]) / O8.FORMATS[fmt][1]
+                assert np.all(np.abs(gs_ - scale) <= 2 * MOM * big + 2.0 ** -23 * scale)
+                have = codes(opt.states[name][i]).reshape(-1)
+                same = have == want
+                # where fp32 crosses a cut the code is the neighbour: rare, and one step away
+                assert np.mean(~same) <= 1e-3 or (~same).sum() <= 1
+                per = np.repeat(scale, 128)[:n]
+                a, b = O8.decode(have, fmt) * per, O8.decode(want, fmt) * per
+                low = 2.0 ** (-9 if fmt == "e4m3" else -16) * per
+                assert np.all(np.abs(a - b) <= np.maximum(np.abs(a), np.abs(b)) * 2.0 ** -man * (1 + 1e-5) + low)
+                if name == "v":
+                    assert np.all((have == 0) == (v == 0))
+
+
+def test_rounding_follows_the_seed_and_repeats():
+    def run(seed):
+        ps, gs = tensors([4096], BF, BF, 2)
+        opt = M.MoeAdamW(ps, gs, state_bits=8)
+        opt.step(seed=seed)
+        return codes(opt.states["m"][0]), codes(opt.states["v"][0]), f64(ps[0])
+    a, b, c = run(5), run(5), run(6)
+    assert all(np.array_equal(x, y) for x, y in zip(a, b))
+    assert not np.array_equal(a[0], c[0]) and not np.array_equal(a[1], c[1]) and np.array_equal(a[2], c[2])
+
+
+def test_small_decay_is_not_lost_in_8_bits():
+    """v under a vanished gradient: 300 steps of 0.99 leave 0.049 of it.  Each
+    code is right on the mean; a run's largest value is held exactly.  The
+    mean of 4,064 codes, each rounded 300 times (a spread of a quarter of the
+    value at most, summed over an average of 100 remembered roundings each
+    hitting with the decay's share 0.01 / 0.25 of a code), is within 5 %."""
+    n = 4096
+    p, g = torch.zeros(n, device="cuda"), torch.full((n,), 1.0, device="cuda")
+    g[1::2] = 0.5
+    opt = M.MoeAdamW([p], [g], state_bits=8, betas=(0.9, 0.99))
+    opt.step()
+    v1 = values8(opt, 0, "v")
+    g.zero_()
+    for _ in range(300):
+        opt.step(lr=0.0)
+    v2 = values8(opt, 0, "v")
+    assert abs(v2[::2].mean() / (v1[::2].mean() * 0.99 ** 300) - 1) < 0.05
+    assert abs(v2[1::2].mean() / (0.0025 * 0.99 ** 300) - 1) < 0.05
+
+
+def test_many_tensors_and_views_leave_neighbours_alone():
+    flat = torch.full((130 * 256,), 7.0, device="cuda")
+    grads = torch.ones(130, 200, device="cuda")
+    ps = [flat[256 * i:256 * i + 197] for i in range(130)] + [flat[:0]]
+    gs = [grads[i, :].clone()[:197] for i in range(130)] + [grads[0, :0]]
+    opt = M.MoeAdamW(ps, gs, lr=0.5, eps=1e-8)
+    opt.step()
+    view = flat.view(130, 256)
+    assert (view[:, 197:] == 7.0).all()
+    assert torch.allclose(view[:, :197], torch.full_like(view[:, :197], 6.5), rtol=1e-6)
+
+
+def test_nonfinite_gradients_stay_in_their_run():
+    ps, gs = tensors([1024], F32, F32, 4)
+    gs[0][130], gs[0][700] = float("nan"), float("inf")
+    keep = ps[0].clone()
+    opt = M.MoeAdamW(ps, gs, state_bits=8)
+    opt.step()
+    m, v = values8(opt, 0, "m"), values8(opt, 0, "v")
+    bad = np.zeros(1024, bool)
+    bad[128:256] = bad[640:768] = True
+    assert not np.isfinite(m[bad]).any() and not np.isfinite(v[bad]).any()
+    assert np.isfinite(m[~bad]).all() and np.isfinite(v[~bad]).all()
+    assert torch.isfinite(ps[0]).sum() >= 1022 and not torch.equal(keep, ps[0])
+
+
+def test_tiny_and_zero_moments():
+    g = torch.zeros(256, device="cuda")
+    g[128:] = 1e-25
+    p = torch.ones(256, device="cuda")
+    opt = M.MoeAdamW([p], [g], state_bits=8)
+    for _ in range(3):
+        opt.step()
+    assert torch.equal(p, torch.ones_like(p)) and np.isfinite(values8(opt, 0, "m")).all()
+    assert not values8(opt, 0, "v").any()  # 1e-50: below the smallest scale
+
+
+def test_control_in_a_replayed_graph():
+    def fresh():
+        ps, gs = tensors([3000, 129], BF, BF, 6)
+        return ps, gs, M.MoeAdamW(ps, gs, masters=[p.float() for p in ps], state_bits=8, **HYPER)
+    ps, gs, opt = fresh()
+    qs, hs, other = fresh()
+    control = torch.zeros(5, dtype=torch.int32, device="cuda")
+    warm = M.MoeAdamW([torch.zeros(8, device="cuda")], [torch.zeros(8, device="cuda")])
+    warm.step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        other.step(control=control)
+    for step in range(1, 5):
+        lr = 1e-2 / step
+        opt.step(lr=lr, step=step, seed=step * 7, grad_scale=0.25)
+        other.write_control(control, lr, step, grad_scale=0.25, seed=step * 7)
+        warm.step()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(ps + opt.masters + opt.states["m"] + opt.states["v_scale"],
+                        qs + other.masters + other.states["m"] + other.states["v_scale"]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    del graph
+
+
+def test_goes_on_from_given_states_on_another_stream():
+    ps, gs = tensors([500, 300], F32, BF, 9)
+    qs = [p.clone() for p in ps]
+    a = M.MoeAdamW(ps, gs, state_bits=8)
+    a.step()
+    a.step()
+    b = M.MoeAdamW(qs, gs, state_bits=8)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b.step(stream=s)
+    c = M.MoeAdamW(qs, gs, state_bits=8, states=b.states)
+    c.step(step=2, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert all(torch.equal(x, y) for x, y in zip(ps, qs))

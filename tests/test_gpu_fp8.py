@@ -1,0 +1,260 @@
+"""8-bit rows, weights and expert products against float64: gathered and pool
+rows, experts with none, one and many rows, every N and K remainder, rows of
+no route left alone, non-finite inputs, other streams and replayed graphs."""
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_grouped_amd as M
+from mixture_experts_grouped_amd import binding as B
+from oracle import float8 as O8
+from tests import harness as Hn
+
+pytestmark = pytest.mark.gpu
+BF, F8 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    Hn.ensure_built()
+
+
+def codes(t):
+    return t.view(torch.uint8).cpu().numpy()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def same_codes(got, want, share):
+    """Equal codes but for a share of ties that fp32 turns the other way, each
+    then a neighbour."""
+    off = got != want
+    assert np.mean(off) <= share or off.sum() <= 1
+    step = np.abs((got[off] & 127).astype(int) - (want[off] & 127).astype(int))
+    assert (step <= 1).all()
+
+
+@pytest.mark.parametrize("rows,K", [(1, 128), (3, 256), (17, 640), (130, 2048)])
+def test_rows(rows, K):
+    g = torch.Generator().manual_seed(rows)
+    x = (torch.randn(rows, K, generator=g) * torch.exp(2 * torch.randn(1, K, generator=g))).to(BF)
+    c, s = M.fp8_quantize_rows(x.cuda())
+    wc, ws = O8.quantize_rows(f64(x))
+    # scale: one division, half a step; codes: bf16 quotients hit ties of the
+    # format, which the rounded reciprocal of the maximum can turn
+    assert np.all(np.abs(f64(s) - ws) <= 2.0 ** -24 * ws)
+    same_codes(codes(c), wc, 0.02)
+
+
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+@pytest.mark.parametrize("rows,K", [(1, 128), (33, 768)])
+def test_gated_rows(rows, K, act):
+    g = torch.Generator().manual_seed(K)
+    x = (torch.randn(rows, 2 * K, generator=g) * 2).to(BF)
+    c, s = M.fp8_quantize_rows(x.cuda(), act=act)
+    gate, up = x[:, :K].double(), x[:, K:].double()
+    f = torch.nn.functional.silu if act == "swiglu" else torch.nn.functional.gelu
+    h = (f(gate) * up).numpy()
+    back = O8.decode(codes(c), "e4m3") * np.repeat(f64(s), 128, 1)
+    # e4m3's half step, half its smallest step at the bottom, the activation's
+    # own error (sigmoid: 2^-20 relative; the normal distribution function: 1e-6
+    # of the gate)
+    tol = 2.0 ** -4 * np.abs(h) * (1 + 1e-5) + np.repeat(f64(s), 128, 1) * 2.0 ** -10 + 1e-6 * np.abs(x[:, :K].double() * up).numpy()
+    assert np.all(np.abs(back - h) <= tol)
+    amax = np.abs(h).reshape(rows, -1, 128).max(2) / 448
+    assert np.all(np.abs(f64(s) - amax) <= 2.0 ** -18 * amax + 1e-8)
+
+
+def test_rows_of_zero_tiny_and_nonfinite_blocks():
+    x = torch.randn(4, 512).to(BF)
+    x[0, :128] = 0
+    x[1, 128:256] = 1e-35
+    x[2, 300] = float("nan")
+    x[3, 400] = -float("inf")
+    c, s = M.fp8_quantize_rows(x.cuda())
+    v = O8.decode(codes(c), "e4m3") * np.repeat(f64(s), 128, 1)
+    assert not codes(c)[0, :128].any() and float(s[0, 0]) == 0
+    assert not (codes(c)[1, 128:256] & 127).any() and float(s[1, 1]) == 0
+    assert not np.isfinite(f64(s)[2, 2]) and not np.isfinite(f64(s)[3, 3])
+    keep = np.ones((4, 512), bool)
+    keep[2, 256:384] = keep[3, 384:] = False
+    assert np.isfinite(v[keep]).all()
+
+
+def test_no_rows():
+    c, s = M.fp8_quantize_rows(torch.zeros(0, 256, dtype=BF, device="cuda"))
+    assert c.shape == (0, 256) and s.shape == (0, 2)
+
+
+@pytest.mark.parametrize("E,N,K", [(1, 128, 128), (3, 256, 384)])
+def test_weights_and_their_transpose(E, N, K):
+    w = (torch.randn(E, N, K, generator=torch.Generator().manual_seed(N)) * 0.02).to(BF)
+    c, s, ct, st = M.fp8_quantize_weight(w.cuda(), transposed=True)
+    for e in range(E):
+        wc, ws = O8.quantize_weight(f64(w[e]))
+        assert np.all(np.abs(f64(s[e]) - ws) <= 2.0 ** -24 * ws)
+        same_codes(codes(c[e]), wc, 0.02)
+    assert np.array_equal(codes(ct), codes(c).transpose(0, 2, 1))
+    assert torch.equal(st, s.transpose(1, 2).contiguous())
+    c2, s2 = M.fp8_quantize_weight(w.cuda())
+    assert torch.equal(c2.view(torch.uint8), c.view(torch.uint8)) and torch.equal(s2, s)
+
+
+def build(idx, E):
+    T, k = idx.shape
+    layer = B.make_desc(T, 256, 256, E, k, 8)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    pool = {"counts": torch.empty(E, **i32), "offsets": torch.empty(E + 1, **i32),
+            "route_to_row": torch.empty(T * k, **i32), "row_to_route": torch.empty(B.moe_lora_pool_capacity(layer), **i32)}
+    M.build_pool(layer, idx.cuda(), pool["counts"], pool["offsets"], pool["route_to_row"], pool["row_to_route"])
+    return pool
+
+
+def operands(rows, E, N, K, seed):
+    g = torch.Generator().manual_seed(seed)
+    a, sa = M.fp8_quantize_rows(torch.randn(rows, K, generator=g).to(BF).cuda())
+    w, sw = M.fp8_quantize_weight((torch.randn(E, N, K, generator=g) * K ** -0.5).to(BF).cuda())
+    return a, sa, w, sw
+
+
+def check(idx, E, N, K, gather, seed=0):
+    T, k = idx.shape
+    pool = build(idx, E)
+    cap = pool["row_to_route"].numel()
+    a, sa, w, sw = operands(T if gather else cap, E, N, K, seed)
+    out = torch.full((cap, N), -77.0, dtype=BF, device="cuda")
+    got = M.fp8_product(pool, a, sa, w, sw, topk=k if gather else 0, out=out)
+    assert got.data_ptr() == out.data_ptr()
+    r2r = pool["row_to_route"].cpu().numpy()
+    off, cnt = pool["offsets"].cpu().numpy(), pool["counts"].cpu().numpy()
+    got = f64(got)
+    assert (got[r2r < 0] == -77.0).all()  # padding and unused rows
+    for e in range(E):
+        rows = np.arange(off[e], off[e] + cnt[e])
+        if rows.size == 0:
+            continue
+        src = r2r[rows] // k if gather else rows
+        ref, mag = O8.product(codes(a)[src], f64(sa)[src], codes(w[e]), f64(sw[e]))
+        # products of codes are exact in fp32, a block's 128 terms and the
+        # blocks' scaled sum are added in fp32: (128 + K / 128 + 3) roundings of
+        # at most the magnitudes' sum, then the output's half step
+        tol = (131 + K / 128) * 2.0 ** -24 * mag
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        assert np.all(np.abs(got[rows] - ref) <= tol), (e, np.max(np.abs(got[rows] - ref) / tol))
+    return pool
+
+
+def routing(T, E, k, seed, drop=0.0, only=None):
+    g = torch.Generator().manual_seed(seed)
+    idx = torch.stack([torch.randperm(max(E, k), generator=g)[:k] % E for _ in range(T)])
+    if only is not None:
+        idx = torch.tensor(only)[idx % len(only)]
+    if drop:
+        idx[torch.rand(T, k, generator=g) < drop] = -1
+    return idx.to(torch.int32)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+@pytest.mark.parametrize("T,E,k,N,K", [
+    (1, 1, 1, 128, 128),       # one row, one tile, one block
+    (1, 64, 6, 256, 512),      # a decoded token
+    (5, 8, 2, 384, 128),       # N not a multiple of a tile's columns
+    (40, 3, 2, 128, 1024),
+    (200, 4, 2, 512, 640),     # odd numbers of K blocks
+    (700, 2, 1, 256, 256),     # several full tiles of rows
+])
+def test_product(T, E, k, N, K, gather):
+    check(routing(T, E, k, T + N), E, N, K, gather, seed=T)
+
+
+@pytest.mark.parametrize("gather", [True, False])
+def test_product_of_uneven_experts(gather):
+    """Experts without rows, with one row and with hundreds, dropped routes."""
+    E = 100
+    idx = routing(300, E, 3, 2, drop=0.3, only=[0, 0, 0, 0, 7, 63, 64, 64, 98])
+    idx[0, 0] = 99
+    check(idx, E, 384, 256, gather)
+
+
+def test_product_of_no_routes():
+    pool = check(torch.full((7, 2), -1, dtype=torch.int32), 5, 128, 128, True)
+    assert int(pool["counts"].sum()) == 0
+
+
+def test_data_gradient_is_the_product_with_the_transpose():
+    E, N, K = 3, 256, 384
+    idx = routing(50, E, 2, 8)
+    pool = build(idx, E)
+    cap = pool["row_to_route"].numel()
+    w = (torch.randn(E, N, K, generator=torch.Generator().manual_seed(1)) * 0.05).to(BF).cuda()
+    c, s, ct, st = M.fp8_quantize_weight(w, transposed=True)
+    dy, sdy = M.fp8_quantize_rows(torch.randn(cap, N, generator=torch.Generator().manual_seed(2)).to(BF).cuda())
+    dx = f64(M.fp8_product(pool, dy, sdy, ct, st))
+    off, cnt = pool["offsets"].tolist(), pool["counts"].tolist()
+    for e in range(E):
+        rows = slice(off[e], off[e] + cnt[e])
+        wt = codes(c[e]).T.copy()
+        ref, mag = O8.product(codes(dy)[rows], f64(sdy)[rows], wt, f64(s[e]).T)
+        tol = (131 + N / 128) * 2.0 ** -24 * mag
+        assert np.all(np.abs(dx[rows] - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol))
+
+
+def test_nonfinite_rows_stay_in_their_rows():
+    E, N, K = 2, 256, 256
+    idx = routing(20, E, 1, 3)
+    pool = build(idx, E)
+    x = torch.randn(20, K).to(BF)
+    x[4, 200] = float("nan")
+    x[9, 3] = float("inf")
+    a, sa = M.fp8_quantize_rows(x.cuda())
+    _, _, w, sw = operands(4, E, N, K, 5)
+    out = M.fp8_product(pool, a, sa, w, sw, topk=1)
+    tok = (pool["row_to_route"].cpu()).numpy()
+    fine = np.isfinite(f64(out)).all(1)
+    assert not np.isfinite(f64(out))[np.isin(tok, [4, 9])].any()
+    assert fine[~np.isin(tok, [4, 9])].all()
+
+
+def test_one_row_alone_equals_the_row_in_a_batch():
+    """A row's sums do not depend on how many rows its expert has."""
+    E, N, K = 2, 256, 512
+    a, sa, w, sw = operands(600, E, N, K, 11)
+    idx = torch.zeros(600, 1, dtype=torch.int32)
+    big = M.fp8_product(build(idx, E), a, sa, w, sw, topk=1)
+    for t in (0, 255, 256, 599):
+        one = M.fp8_product(build(idx[:1], E), a[t:t + 1], sa[t:t + 1], w, sw, topk=1)
+        assert torch.equal(one[0], big[t])
+
+
+def test_streams_and_graphs():
+    E, N, K = 6, 256, 256
+    idx = routing(30, E, 2, 4)
+    pool = build(idx, E)
+    x = torch.randn(30, K).to(BF).cuda()
+    _, _, w, sw = operands(4, E, N, K, 6)
+    a, sa = M.fp8_quantize_rows(x)
+    want = M.fp8_product(pool, a, sa, w, sw, topk=2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    a2, sa2 = M.fp8_quantize_rows(x, stream=s)
+    with torch.cuda.stream(s):
+        out = torch.zeros_like(want)
+    M.fp8_product(pool, a2, sa2, w, sw, topk=2, out=out, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert torch.equal(out, want)
+    got = torch.zeros_like(want)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.fp8_quantize_rows(x, codes=a2, scales=sa2)
+        M.fp8_product(pool, a2, sa2, w, sw, topk=2, out=got)
+    for _ in range(3):
+        got.zero_()
+        a2.view(torch.uint8).zero_()
+        M.fp8_product(pool, a, sa, w, sw, topk=2)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    del g
