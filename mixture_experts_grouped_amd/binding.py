@@ -780,13 +780,15 @@ def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) 
 
 
 def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
-                w_scales: torch.Tensor, topk: int = 0, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+                w_scales: torch.Tensor, topk: int = 0, out: Optional[torch.Tensor] = None, block_m: int = 16,
+                stream=None) -> torch.Tensor:
     """Every pool row times its expert's weight: out bf16 [capacity, N].
     pool as in MoeLoraLayer.pool; a e4m3 [rows, K] with a_scales [rows,
     K/128]: the tokens (topk > 0: pool row r reads token row_to_route[r] /
     topk), or the pool rows themselves (topk = 0); w e4m3 [E, N, K] with
     w_scales [E, N/128, K/128].  Rows of no route are left as they are (an
-    `out` made here holds zeros there)."""
+    `out` made here holds zeros there).  block_m: the pool's (the library's
+    own choice is 16)."""
     if a.dim() != 2 or w.dim() != 3:
         raise ValueError("a must be [rows, K] and w [E, N, K]")
     rows, K = a.shape
@@ -797,7 +799,7 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
         out = torch.zeros(cap, N, dtype=torch.bfloat16, device=a.device)
     i32, f32 = torch.int32, torch.float32
     ps = MoePool(_ptr(pool["counts"], i32, (E,), "counts"), _ptr(pool["offsets"], i32, (E + 1,), "offsets"), None,
-                 _ptr(pool["row_to_route"], i32, None, "row_to_route"), cap, 0)
+                 _ptr(pool["row_to_route"], i32, None, "row_to_route"), cap, block_m)
     d = MoeFp8Desc(E, N, K, topk, rows)
     with _On(stream, a, a_scales, w, w_scales, out, pool["counts"], pool["offsets"], pool["row_to_route"]) as s:
         st = library().moe_fp8_product(

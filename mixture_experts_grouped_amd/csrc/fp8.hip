@@ -22,6 +22,7 @@ namespace {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr float E4M3_MAX = 448.0f;
+constexpr int MAX_DIM = 65536;     // N and K: a tile's row offsets stay in 32 bits
 constexpr float TINY = 0x1p-100f;  // a block below it counts as zero (its reciprocal would overflow)
 
 // ---------------------------------------------------------------------------
@@ -206,154 +207,457 @@ __device__ __forceinline__ i32x8 pair(u32x4 lo, u32x4 hi) {
 }
 
 // Tile of TM activation rows x TN weight rows, WM x WN waves, NBUF stages in
-// LDS (NBUF - 1 in flight).
+// LDS.  SPLIT: a stage's buffer is refilled in two parts (k_fp8_tile).
 template <int TM_, int TN_, int WM_, int WN_, int NBUF_>
 struct Geo8 {
   static constexpr int TM = TM_, TN = TN_, WM = WM_, WN = WN_, NBUF = NBUF_;
   static constexpr int NW = WM * WN, NT = 64 * NW;
   static constexpr int FM = TM / WM / 16, FN = TN / WN / 16;
+  static constexpr bool SPLIT = NBUF == 2;
   static constexpr int A_BYTES = TM * 128, W_BYTES = TN * 128, S_BYTES = NW * 256;
   static constexpr int STAGE = A_BYTES + W_BYTES + S_BYTES;
-  static constexpr int PITCH = TN * 2 + 16;  // bytes of an output image row
-  static constexpr int LDS = cmax(NBUF * STAGE, TM * PITCH);
-  static_assert(LDS <= 160 * 1024, "LDS of one workgroup");
-  static_assert(128 % (TN / WN) == 0, "a wave's weight rows lie in one block of 128");
-  static_assert(NW * 64 >= TM, "one scale a lane");
+  static constexpr int SW_AT = NBUF * STAGE;  // two tiles' weight scales, [2][TN / 128][stages]
+  static constexpr int stages(int K) { return cmax(K / 128, NBUF); }
+  static constexpr int table_at(int K) { return SW_AT + 2 * (TN / 128) * stages(K) * 4; }  // PoolTable
+  static constexpr int lds(int K, int E) { return table_at(K) + 12 * E; }
+  static_assert(128 % (TN / WN) == 0 && TN % 128 == 0, "a wave's weight rows lie in one block of 128");
+  static_assert(lds(MAX_DIM, 512) <= 160 * 1024 && NW * 64 >= TM && FN % 2 == 0, "one scale a lane; fragments are stored in pairs");
 };
 
+// The pool's tiles of TM rows, in LDS: for each expert the number of tiles up
+// to and with it, its rows and its first row.
+struct PoolTable {
+  int *end, *cnt, *off;
+  int total;
+};
+template <int TM>
+__device__ __forceinline__ void fill_table(const Fp8Args& p, PoolTable& t, char* at) {
+  t.end = (int*)at;
+  t.cnt = t.end + p.E;
+  t.off = t.cnt + p.E;
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {  // every wave walks all experts; wave 0 writes
+    const int e = e0 + lane, c = e < p.E ? p.counts[e] : 0;
+    int x = (c + TM - 1) / TM;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int y = __shfl_up(x, o, 64);
+      if (lane >= o) x += y;
+    }
+    if (threadIdx.x < 64 && e < p.E) {
+      t.end[e] = before + x;
+      t.cnt[e] = c;
+      t.off[e] = p.offsets[e];
+    }
+    before += __shfl(x, 63, 64);
+  }
+  t.total = __builtin_amdgcn_readfirstlane(before);
+  __syncthreads();
+}
+
+// One tile of the pool's nn N tiles per M tile (order as in pool_tile).
+struct Tile8 {
+  int e, nt, nrows;
+  long row0;
+};
+template <int TM>
+__device__ __forceinline__ bool find_tile(const PoolTable& t, int E, int b, int nn, Tile8& out) {
+  if (b >= t.total * nn) return false;
+  const int lane = threadIdx.x & 63;
+  const int L = xcd_remap(b, t.total * nn);
+  const int v = L / nn;
+  int e = 0;
+  for (int e0 = 0; e0 < E; e0 += 64) {
+    const unsigned long long past = __ballot(e0 + lane < E && t.end[min(e0 + lane, E - 1)] > v);
+    if (past != 0) {
+      e = e0 + __ffsll(past) - 1;
+      break;
+    }
+  }
+  const int rows = __builtin_amdgcn_readfirstlane(t.cnt[e]);
+  const int n = (rows + TM - 1) / TM, s = __builtin_amdgcn_readfirstlane(t.end[e]) - n;
+  const int cs = s + TILE_GM * ((v - s) / TILE_GM);
+  const int sz = s + n - cs < TILE_GM ? s + n - cs : TILE_GM;
+  const int r = L - cs * nn, m = cs + r % sz - s;
+  out.e = e;
+  out.nt = r / sz;
+  out.nrows = min(rows - m * TM, TM);
+  out.row0 = (long)__builtin_amdgcn_readfirstlane(t.off[e]) + (long)m * TM;
+  return true;
+}
+
+// Lane offsets of the 16-row fragments of a tile of 128-byte rows: lane l
+// takes row l % 16 and chunks 2 (l / 16) and 2 (l / 16) + 1, 32 bytes in a
+// row.  (The order of k inside the instruction does not matter as long as both
+// operands agree; with chunks l / 16 and l / 16 + 4 the 16 lanes that one
+// LDS pass serves, 0-3, 12-15 and 20-27 of 32, meet in the same banks under
+// this swizzle, which cost 47 % more LDS cycles.)  The chunk swizzle of tile
+// row 16 i + r is (r & 7) ^ (r >> 3) ^ 2 (i & 3): four offsets serve every
+// fragment, the second chunk in the slot beside.
+struct Frag8 {
+  uint32_t o[4];
+  __device__ __forceinline__ void init(int lane, int first) {  // first: tile index of the wave's fragment 0
+    const uint32_t r = lane & 15, c = 2 * (lane >> 4);
+    const uint32_t slot = c ^ (r & 7) ^ (r >> 3);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) o[v] = 128u * r + ((slot ^ (2u * ((v + first) & 3))) << 4);
+  }
+  __device__ __forceinline__ i32x8 get(const char* tile, int i) const {  // tile: at the wave's fragment 0
+    const u32x4 lo = *(const u32x4*)(tile + o[i & 3] + 2048 * i);
+    const u32x4 hi = *(const u32x4*)(tile + (o[i & 3] ^ 16u) + 2048 * i);
+    return pair(lo, hi);
+  }
+};
+
+// A workgroup walks tiles b, b + gridDim.x, ... with one unbroken stream of
+// stages: while the last stages of a tile are multiplied the first of the next
+// are already loading, and the finished tile is stored from registers.
+//
+// A stage s in steady state: the products of weight fragment i are issued
+// while those of i - 1 (the last ones, of the stage before) are scaled and
+// added and fragment i + 1 is read; the next stage's first fragments are read
+// under the last products.  With SPLIT a buffer is refilled for stage s + 2 in
+// two parts, each as soon as the workgroup has read it: at mid-stage the
+// activation rows (in registers by then) and the weight rows of the first
+// half of the fragments, at the end the others, so a load has one and a half
+// stages to arrive from two buffers (one with a refill at the end alone).
+// Without SPLIT whole stages are queued NBUF ahead.
+//
+// Loads past a tile's K (K / 128 < NBUF) or past the last tile go to offsets
+// outside every descriptor: zeros, no traffic, and the loop waits by constant
+// counts and has no branch.
 template <class G>
 __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   extern __shared__ __align__(16) char smem[];
   using LA = v2::KLoadA<G::TM, 64, G::NW>;
   using LW = v2::KLoadS<G::TN, 64, G::NW>;
-  constexpr int INSTS = LA::NJ + LW::NJ + 1;
-  int e, m, nt;
-  if (!pool_tile(p, G::TM, blockIdx.x, (p.N + G::TN - 1) / G::TN, TILE_GM, e, m, nt)) return;
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  constexpr int FM = G::FM, FN = G::FN;
+  constexpr int INSTS = LA::NJ + LW::NJ + 1;  // direct loads of a wave and stage
+  static_assert(!G::SPLIT || (G::TN == 256 && G::NW == 8 && G::WN == 2 && FN == 8),
+                "SPLIT: loads 0 and 2 of a stage are the rows of fragments 0-3, 1 and 3 those of 4-7");
+  const int KB = p.K / 128, ST = cmax(KB, G::NBUF), nn = (p.N + G::TN - 1) / G::TN;
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / G::WN, wn = w % G::WN;
-  const int n0 = nt * G::TN, KB = p.K / 128;
-  const long row0 = (long)p.offsets[e] + (long)m * G::TM;
-  const int nrows = min(p.counts[e] - m * G::TM, G::TM);
-  const int ncols = min(p.N - n0, G::TN);
-  // loads: rows of codes as rows of K / 2 16-bit words
+  const int fr = lane & 15, fc = lane >> 4;
+  PoolTable tab;
+  fill_table<G::TM>(p, tab, smem + G::table_at(p.K));
+  Tile8 cur;
+  int b = blockIdx.x;
+  if (!find_tile<G::TM>(tab, p.E, b, nn, cur)) return;
+
+  // tokens of the activation rows that this lane loads (LA::NJ rows of codes, one scale)
+  int tk[LA::NJ + 1];
+  auto tokens = [&](const Tile8& t) {
+    if (p.topk == 0) return;
+#pragma unroll
+    for (int j = 0; j <= LA::NJ; ++j) {
+      const int q = j < LA::NJ ? LA::row_of(j) : 64 * w + lane;
+      const int k = q < t.nrows ? p.row2r[t.row0 + q] / p.topk : -1;
+      tk[j] = k >= 0 && k < p.a_rows ? k : -1;
+    }
+  };
   LA la;
   LW lw;
   rsrc_t rs;
   uint32_t soff;
-  {
-    const int r = 64 * w + lane;  // this lane's activation row for the scales
+  // aim the loads at a tile, and queue its weight scales into half h
+  auto aim = [&](const Tile8& t, bool any, int h) {
+    const int n0 = t.nt * G::TN, ncols = min(p.N - n0, G::TN);
     if (p.topk > 0) {
-      la.rs = make_rsrc(p.a, (uint64_t)p.a_rows * p.K);
+      la.rs = make_rsrc(p.a, any ? (uint64_t)p.a_rows * p.K : 0);
+      rs = make_rsrc(p.sa, any ? (uint64_t)p.a_rows * KB * 4 : 0);
 #pragma unroll
-      for (int j = 0; j < LA::NJ; ++j) {
-        const int q = LA::row_of(j);
-        const int t = q < nrows ? p.row2r[row0 + q] / p.topk : -1;
-        la.set_row(j, t >= 0 && t < p.a_rows ? (uint32_t)t * (uint32_t)p.K : OFF_NONE);
+      for (int j = 0; j < LA::NJ; ++j) la.set_row(j, tk[j] >= 0 ? (uint32_t)tk[j] * (uint32_t)p.K : OFF_NONE);
+      soff = tk[LA::NJ] >= 0 ? (uint32_t)tk[LA::NJ] * (uint32_t)KB * 4u : OFF_NONE;
+    } else {
+      const long have = p.a_rows - t.row0;
+      const int live = any ? (int)(have < t.nrows ? (have > 0 ? have : 0) : t.nrows) : 0;
+      la.contig((const uint16_t*)p.a, t.row0, live, p.K / 2);
+      rs = make_rsrc(p.sa + t.row0 * KB, (uint64_t)live * KB * 4);
+      soff = 64 * w + lane < live ? (uint32_t)(64 * w + lane) * (uint32_t)KB * 4u : OFF_NONE;
+    }
+    lw.contig((const uint16_t*)(p.w + (long)t.e * p.N * p.K), n0, any ? ncols : 0, p.K / 2);
+    // scale blocks x stages, 64 values a load; block c of stages past K, and of columns past N, reads zero
+    const rsrc_t rw = make_rsrc(p.sw + ((long)t.e * (p.N / 128) + n0 / 128) * KB, any ? (uint64_t)(ncols / 128) * KB * 4 : 0);
+    char* to = smem + G::SW_AT + h * (G::TN / 128) * ST * 4;
+    for (int c = w; c * 64 < G::TN / 128 * ST; c += G::NW) {
+      const int i = 64 * c + lane, blk = i / ST, k = i - blk * ST;
+      if (i < G::TN / 128 * ST)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (v2::lds_void*)(to + 256 * c), 4,
+                                                 k < KB ? (uint32_t)(blk * KB + k) * 4u : OFF_NONE, 0, 0, 0);
+    }
+  };
+  // queue load q of a stage s of the tile aimed at into buffer g: the activation
+  // rows, the scales, the weight rows (with SPLIT 0 and 2 first, then 1 and 3)
+  auto issue1 = [&](int s, int g, int q) {
+    char* st = smem + g * G::STAGE;
+    const uint32_t k0 = s < KB ? 128u * (uint32_t)s : (uint32_t)RSRC_MAX;
+    if (q < LA::NJ) {
+      v2::lds_load16(la.rs, st + 1024 * (w + G::NW * q), la.voff[q], k0);
+    } else if (q == LA::NJ) {
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (v2::lds_void*)(st + G::A_BYTES + G::W_BYTES + 256 * w), 4, soff,
+                                               s < KB ? 4u * (uint32_t)s : (uint32_t)RSRC_MAX, 0, 0);
+    } else {
+      const int i = q - LA::NJ - 1, j = !G::SPLIT ? i : i < 2 ? 2 * i : 2 * i - 3;
+      v2::lds_load16(lw.rs, st + G::A_BYTES + 1024 * (w + G::NW * j), (j & 1) ? lw.v1 : lw.v0,
+                     k0 + (uint32_t)j * lw.jstep);
+    }
+  };
+
+  Frag8 fa, fw;
+  fa.init(lane, wm * FM);
+  fw.init(lane, wn * FN);
+  f32x4 acc[FN][FM], t[FM];
+  i32x8 x[FM], a;
+  float sc[FM], sl[FM];  // this stage's scales, and those of the products in t
+  auto clear = [&]() {
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < FN; ++i) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+  };
+  // the weight scale of stage s lies at smem + off
+  auto read_scales = [&](int g, int off, float (&to)[FM]) {
+    const float* sS = (const float*)(smem + g * G::STAGE + G::A_BYTES + G::W_BYTES) + wm * FM * 16 + fr;
+    const float ws = *(const float*)(smem + off);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) to[j] = sS[16 * j] * ws;
+  };
+  auto sw_at = [&](int h, int s) {
+    return G::SW_AT + ((h * (G::TN / 128) + wn * (G::TN / G::WN) / 128) * ST + s) * 4;
+  };
+  // multiply the stage in buffer g; queue stage q of the tile aimed at into
+  // it; read the next stage's first fragments (its weight scale at swn)
+  auto stage = [&](int g, int q, int swn) {
+    const int gn = g + 1 == G::NBUF ? 0 : g + 1;
+    const char* sW = smem + g * G::STAGE + G::A_BYTES + wn * FN * 2048;
+    const char* nA = smem + gn * G::STAGE + wm * FM * 2048;
+    float sn[FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+      i32x8 next;
+      if (G::SPLIT && i == FN / 2 - 1) {
+        v2::wait_lgkm0();  // this wave has read the activation rows and the first weight rows
+        v2::wait_vm<INSTS>();  // the other weight rows have landed
+        v2::bar();
       }
+      if (i + 1 < FN) {
+        next = fw.get(sW, i + 1);
+      } else {
+        v2::wait_lgkm0();  // this wave has read all of the stage
+        v2::wait_vm<G::SPLIT ? INSTS : (G::NBUF - 2) * INSTS>();  // the next one's first part has landed
+        v2::bar();
+        next = fw.get(smem + gn * G::STAGE + G::A_BYTES + wn * FN * 2048, 0);
+        read_scales(gn, swn, sn);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int j = 0; j < FM; ++j) {
+        const float f = i == 0 ? sl[j] : sc[j];
+        f32x4& to = acc[i == 0 ? FN - 1 : i - 1][j];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) to[c] = fmaf(t[j][c], f, to[c]);
+        t[j] = mma8(a, x[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        if (i == FN - 1) x[j] = fa.get(nA, j);
+        if constexpr (G::SPLIT) {  // two loads for each fragment from mid-stage on, the last two at the end
+          if (j % 2 == 1 && i >= FN / 2 - 1 && 2 * (i - FN / 2 + 1) + j / 2 < INSTS - 2 && i < FN - 1)
+            issue1(q, g, 2 * (i - FN / 2 + 1) + j / 2);
+          if (j % 2 == 1 && i == FN - 1) issue1(q, g, INSTS - 2 + j / 2);
+        } else if (i == FN - 1) {
+#pragma unroll
+          for (int l = j * INSTS / FM; l < (j + 1) * INSTS / FM; ++l) issue1(q, g, l);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      a = next;
+    }
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+      sl[j] = sc[j];
+      sc[j] = sn[j];
+    }
+  };
+
+  tokens(cur);
+  aim(cur, true, 0);
+  int h = 0, g = 0;  // half of the weight scales, buffer of the stage to multiply
+#pragma unroll
+  for (int s = 0; s < G::NBUF; ++s) {
+#pragma unroll
+    for (int l = 0; l < INSTS; ++l) issue1(s, s, l);
+  }
+  v2::wait_vm<(G::NBUF - 1) * INSTS>();
+  v2::bar();
+  a = fw.get(smem + G::A_BYTES + wn * FN * 2048, 0);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) x[j] = fa.get(smem + wm * FM * 2048, j);
+  read_scales(0, sw_at(0, 0), sc);
+#pragma unroll
+  for (int j = 0; j < FM; ++j) sl[j] = 0.0f;
+  clear();
+  while (true) {
+    Tile8 nxt = cur;
+    b += gridDim.x;
+    const bool more = find_tile<G::TM>(tab, p.E, b, nn, nxt);
+    if (more) tokens(nxt);
+    for (int s = 0; s + G::NBUF < ST; ++s) {
+      stage(g, s + G::NBUF, sw_at(h, s + 1));
+      g = g + 1 == G::NBUF ? 0 : g + 1;
+    }
+    aim(nxt, more, h ^ 1);
+    for (int s = 0; s < G::NBUF; ++s) {
+      stage(g, s, s + 1 < G::NBUF ? sw_at(h, ST - G::NBUF + s + 1) : sw_at(h ^ 1, 0));
+      g = g + 1 == G::NBUF ? 0 : g + 1;
+    }
+    // A lane holds four columns of a row for each fragment; of two neighbouring
+    // fragments, rows of 16 lanes trade so that it holds eight columns of one.
+    const rsrc_t ro = make_rsrc(p.out + cur.row0 * p.N + cur.nt * G::TN, (uint64_t)cur.nrows * p.N * 2);
+    const int ncols = min(p.N - cur.nt * G::TN, G::TN);
+#pragma unroll
+    for (int j = 0; j < FM; ++j) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[FN - 1][j][c] = fmaf(t[j][c], sl[j], acc[FN - 1][j][c]);
+      const int r = (wm * FM + j) * 16 + fr;
+#pragma unroll
+      for (int i = 0; i < FN; i += 2) {
+        const auto lo = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][0], acc[i][j][1]),
+                                                         pack2(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
+        const auto hi = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][2], acc[i][j][3]),
+                                                         pack2(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
+        const int c = (wn * FN + i + (fc & 1)) * 16 + 8 * (fc >> 1);
+        const uint32_t off = r < cur.nrows && c < ncols ? (uint32_t)(r * p.N + c) * 2u : OFF_NONE;
+        __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, (int)off, 0, 0);
+      }
+    }
+    if (!more) break;
+    clear();
+    cur = nxt;
+    h ^= 1;
+  }
+  v2::wait_vm<0>();  // the loads queued past the last tile have written their zeros
+}
+
+// Few rows per expert (decoding): the weights are read once and bound the
+// time, so they go from memory straight into the registers that the matrix
+// instruction takes.  A wave is 16 activation rows x 16 weight rows with the
+// next FEW_CH K blocks in flight while FEW_CH are multiplied.  It walks K in
+// order, so a row's sums are those of the tile kernels bit for bit.
+constexpr int FEW_ROWS = 16, FEW_CH = 4;
+__global__ __launch_bounds__(256) void k_fp8_few(Fp8Args p) {
+  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int fr = lane & 15, fc = lane >> 4;
+  const int KB = p.K / 128;
+  int e, m, nt;
+  for (int b = blockIdx.x; pool_tile(p, FEW_ROWS, b, p.N / 64, TILE_GM, e, m, nt); b += gridDim.x) {
+    const int n0 = nt * 64 + 16 * w;
+    const rsrc_t rw = make_rsrc(p.w + ((long)e * p.N + n0) * p.K, (uint64_t)16 * p.K);
+    const uint32_t wo = (uint32_t)fr * (uint32_t)p.K + 32u * (uint32_t)fc;
+    const long row0 = (long)p.offsets[e] + (long)m * FEW_ROWS;
+    const int nrows = min(p.counts[e] - m * FEW_ROWS, FEW_ROWS);
+    const float* sw = p.sw + ((long)e * (p.N / 128) + n0 / 128) * KB;
+    // this lane's activation row and scale row
+    rsrc_t ra, rs;
+    long ar = -1;
+    if (p.topk > 0) {
+      ra = make_rsrc(p.a, (uint64_t)p.a_rows * p.K);
       rs = make_rsrc(p.sa, (uint64_t)p.a_rows * KB * 4);
-      const int t = r < nrows ? p.row2r[row0 + r] / p.topk : -1;
-      soff = t >= 0 && t < p.a_rows ? (uint32_t)t * (uint32_t)KB * 4u : OFF_NONE;
+      if (fr < nrows) ar = p.row2r[row0 + fr] / p.topk;
+      if (ar >= p.a_rows) ar = -1;
     } else {
       const long have = p.a_rows - row0;
       const int live = (int)(have < nrows ? (have > 0 ? have : 0) : nrows);
-      la.contig((const uint16_t*)p.a, row0, live, p.K / 2);
+      ra = make_rsrc(p.a + row0 * p.K, (uint64_t)live * p.K);
       rs = make_rsrc(p.sa + row0 * KB, (uint64_t)live * KB * 4);
-      soff = r < live ? (uint32_t)r * (uint32_t)KB * 4u : OFF_NONE;
+      if (fr < live) ar = fr;
     }
-    lw.contig((const uint16_t*)(p.w + (long)e * p.N * p.K), n0, ncols, p.K / 2);
-  }
-  auto issue = [&](int s) {
-    char* st = smem + (s % G::NBUF) * G::STAGE;
-    la.issue(64 * s, st);
-    lw.issue(64 * s, st + G::A_BYTES);
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (v2::lds_void*)(st + G::A_BYTES + G::W_BYTES + 256 * w), 4, soff,
-                                             4u * (uint32_t)s, 0, 0);
-  };
-  // the wave's weight scale of K block s
-  const int nb = min((n0 + wn * (G::TN / G::WN)) / 128, p.N / 128 - 1);
-  const float* sw = p.sw + ((long)e * (p.N / 128) + nb) * KB;
-  f32x4 acc[G::FN][G::FM];
+    const uint32_t ao = ar >= 0 ? (uint32_t)ar * (uint32_t)p.K + 32u * (uint32_t)fc : OFF_NONE;
+    const uint32_t so = ar >= 0 ? (uint32_t)ar * (uint32_t)KB * 4u : OFF_NONE;
+    struct Set {
+      u32x4 wl[FEW_CH], wh[FEW_CH], al[FEW_CH], ah[FEW_CH];
+      float sc[FEW_CH], sb[FEW_CH];
+    };
+    auto load = [&](Set& q, int c0) {
 #pragma unroll
-  for (int i = 0; i < G::FN; ++i)
+      for (int i = 0; i < FEW_CH; ++i) {
+        const int c = c0 + i;
+        const bool in = c < KB, has = in && ar >= 0;
+        const uint32_t k = 128u * (uint32_t)c;
+        q.wl[i] = bload(rw, in ? wo + k : OFF_NONE);
+        q.wh[i] = bload(rw, in ? wo + k + 16u : OFF_NONE);
+        q.al[i] = bload(ra, has ? ao + k : OFF_NONE);
+        q.ah[i] = bload(ra, has ? ao + k + 16u : OFF_NONE);
+        q.sc[i] = __builtin_bit_cast(
+            float, __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(has ? so + 4u * (uint32_t)c : OFF_NONE), 0, 0));
+        q.sb[i] = in ? sw[c] : 0.0f;
+      }
+    };
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto mul = [&](const Set& q) {
 #pragma unroll
-    for (int j = 0; j < G::FM; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  // fragment row l % 16; chunks l / 16 and l / 16 + 4 of its 128 bytes (both
-  // operands alike, so the order of k inside the instruction does not matter)
-  const int fr = lane & 15, fc = lane >> 4;
+      for (int i = 0; i < FEW_CH; ++i) {
+        const f32x4 t = mma8(pair(q.wl[i], q.wh[i]), pair(q.al[i], q.ah[i]), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        const float sc = q.sc[i] * q.sb[i];
 #pragma unroll
-  for (int s = 0; s < G::NBUF - 1; ++s)
-    if (s < KB) issue(s);
-  for (int s = 0; s < KB; ++s) {
-    const int left = KB - 1 - s;
-    if (G::NBUF >= 4 && left >= 2)
-      v2::wait_vm<2 * INSTS>();
-    else if (G::NBUF >= 3 && left >= 1)
-      v2::wait_vm<INSTS>();
-    else
-      v2::wait_vm<0>();
-    v2::wait_lgkm0();  // this wave is done reading the buffer that is refilled after the barrier
-    v2::bar();
-    if (s + G::NBUF - 1 < KB) issue(s + G::NBUF - 1);
-    const char* st = smem + (s % G::NBUF) * G::STAGE;
-    const char* sA = st;
-    const char* sW = st + G::A_BYTES;
-    const float* sS = (const float*)(st + G::A_BYTES + G::W_BYTES);
-    const float ws = sw[s];
-    i32x8 x[G::FM];
-    float sc[G::FM];
-#pragma unroll
-    for (int j = 0; j < G::FM; ++j) {
-      const int r = (wm * G::FM + j) * 16 + fr;
-      x[j] = pair(*(const u32x4*)(sA + v2::koff<64>(r, fc)), *(const u32x4*)(sA + v2::koff<64>(r, fc + 4)));
-      sc[j] = sS[r] * ws;
+        for (int j = 0; j < 4; ++j) acc[j] = fmaf(t[j], sc, acc[j]);
+      }
+    };
+    Set s0, s1;
+    load(s0, 0);
+    for (int c = 0; c < KB; c += 2 * FEW_CH) {
+      load(s1, c + FEW_CH);
+      mul(s0);
+      load(s0, c + 2 * FEW_CH);
+      mul(s1);
     }
-#pragma unroll
-    for (int i = 0; i < G::FN; ++i) {
-      const int r = (wn * G::FN + i) * 16 + fr;
-      const i32x8 a = pair(*(const u32x4*)(sW + v2::koff<64>(r, fc)), *(const u32x4*)(sW + v2::koff<64>(r, fc + 4)));
-      f32x4 t[G::FM];
-#pragma unroll
-      for (int j = 0; j < G::FM; ++j) t[j] = mma8(a, x[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-      for (int j = 0; j < G::FM; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc[i][j][q] = fmaf(t[j][q], sc[j], acc[i][j][q]);
-    }
-  }
-  __syncthreads();  // LDS free for the image
-#pragma unroll
-  for (int i = 0; i < G::FN; ++i)
-#pragma unroll
-    for (int j = 0; j < G::FM; ++j) {
-      const int r = (wm * G::FM + j) * 16 + fr, c = (wn * G::FN + i) * 16 + 4 * fc;
-      *(u32x2*)(smem + r * G::PITCH + 2 * c) =
-          u32x2{pack2(acc[i][j][0], acc[i][j][1]), pack2(acc[i][j][2], acc[i][j][3])};
-    }
-  __syncthreads();
-  const int cpr = ncols / 8;  // 16-byte chunks per row
-  for (int i = tid; i < nrows * cpr; i += G::NT) {
-    const int r = i / cpr, c = i - r * cpr;
-    *(u32x4*)(p.out + (row0 + r) * p.N + n0 + 8 * c) = *(const u32x4*)(smem + r * G::PITCH + 16 * c);
+    if (fr < nrows)
+      *(u32x2*)(p.out + (row0 + fr) * p.N + n0 + 4 * fc) = u32x2{pack2(acc[0], acc[1]), pack2(acc[2], acc[3])};
   }
 }
 
 using GL = Geo8<256, 256, 4, 2, 2>;
+using GM = Geo8<64, 128, 1, 4, 3>;
+// routes per expert up to which k_fp8_few and the 64-row tile are taken
+constexpr int FEW_AVG = 8, MID_AVG = 96;
+
+
+// Workgroups for at most `tiles` tiles: every kernel here walks on by its grid
+// until the pool's tiles are done, so the grid is a matter of speed alone.
+// One per CU and resident workgroup, in whole rounds over the XCDs.
+hipError_t grid_of(int64_t tiles, int per_cu, unsigned& grid) {
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t most = (int64_t)cus * per_cu;
+  grid = (unsigned)(((tiles < most ? tiles : most) + 7) / 8 * 8);
+  return hipSuccess;
+}
 
 template <class G>
-hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, hipStream_t st) {
+hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, int per_cu, hipStream_t st) {
   static PerDeviceOnce once;
-  const hipError_t e = once.run([] {
+  hipError_t e = once.run([] {
     AttrInit ai;
-    ai.lds((const void*)k_fp8_tile<G>, G::LDS);
+    ai.lds((const void*)k_fp8_tile<G>, G::lds(MAX_DIM, 512));
     return ai.err;
   });
+  unsigned grid = 0;
+  if (e == hipSuccess) e = grid_of(mtiles * ((p.N + G::TN - 1) / G::TN), per_cu, grid);
   if (e != hipSuccess) return e;
-  const int64_t grid = mtiles * ((p.N + G::TN - 1) / G::TN);
-  MOE_LAUNCH_AS("k_fp8_tile", k_fp8_tile<G>, dim3((unsigned)grid), dim3(G::NT), G::LDS, st, p);
+  MOE_LAUNCH_AS("k_fp8_tile", k_fp8_tile<G>, dim3(grid), dim3(G::NT), G::lds(p.K, p.E), st, p);
   return hipGetLastError();
 }
 
-constexpr int MAX_DIM = 65536;  // a tile's row offsets stay in 32 bits
+hipError_t launch_few(const Fp8Args& p, int64_t mtiles, hipStream_t st) {
+  unsigned grid = 0;
+  const hipError_t e = grid_of(mtiles * (p.N / 64), 4, grid);
+  if (e != hipSuccess) return e;
+  MOE_LAUNCH(k_fp8_few, dim3(grid), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
 
 moe_status check_weight(int32_t E, int32_t N, int32_t K) {
   if (E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID;
@@ -415,8 +719,11 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
   if (d == nullptr || pool == nullptr) return MOE_ERR_INVALID;
   const moe_status st = check_weight(d->E, d->N, d->K);
   if (st != MOE_OK) return st;
-  if (d->topk < 0 || d->a_rows < 1 || pool->capacity < 1) return MOE_ERR_INVALID;
+  if (d->topk < 0 || d->a_rows < 1 || pool->capacity < 1 || pool->block_m < 1)
+    return MOE_ERR_INVALID;
   if (pool->capacity >= (int64_t)1 << 31 || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  // tile indices of the smallest tiles are 32 bits
+  if ((pool->capacity / FEW_ROWS + d->E) * (d->N / 64) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (d->topk > 0 && d->a_rows * d->K >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor
   if (!aligned(pool->counts, 4) || !aligned(pool->offsets, 4) || !aligned(pool->row_to_route, 4))
     return MOE_ERR_INVALID;
@@ -431,10 +738,20 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
     if (overlap(ro, r)) return MOE_ERR_INVALID;
   Fp8Args p{d->E, d->N, d->K, d->topk, (long)d->a_rows, pool->counts, pool->offsets, pool->row_to_route,
             (const uint8_t*)a, a_scales, (const uint8_t*)w, w_scales, (uint16_t*)out};
-  // M tiles of TM rows any counts of `capacity` rows can make
-  auto tiles = [&](int tm) { return pool->capacity / tm + (d->E < pool->capacity ? d->E : pool->capacity); };
-  if (tiles(GL::TM) * ((d->N + GL::TN - 1) / GL::TN) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
-  const hipError_t e = launch_tile<GL>(p, tiles(GL::TM), (hipStream_t)stream);
+  // the routes of a pool of this capacity: build_pool allots BLOCK_M - 1 rows
+  // of padding to each of min(E, routes) experts
+  const int64_t bm = pool->block_m, cap = pool->capacity, E = d->E;
+  const int64_t routes = cap >= E * bm ? cap - E * (bm - 1) : (cap + bm - 1) / bm;
+  const int64_t live = routes < E ? routes : E;  // experts with rows, at most
+  auto tiles = [&](int tm) { return routes / tm + live; };
+  const hipStream_t s = (hipStream_t)stream;
+  hipError_t e;
+  if (routes <= FEW_AVG * live)
+    e = launch_few(p, tiles(FEW_ROWS), s);
+  else if (routes <= MID_AVG * live)
+    e = launch_tile<GM>(p, tiles(GM::TM), 2, s);
+  else
+    e = launch_tile<GL>(p, tiles(GL::TM), 1, s);
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

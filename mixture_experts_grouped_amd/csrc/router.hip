@@ -22,11 +22,13 @@ namespace {
 
 constexpr int RT_THREADS = 256;
 constexpr int RT_ROWS = RT_THREADS / 16;  // tokens a workgroup works on at once
-constexpr int RT_TOKENS = 4 * RT_ROWS;    // tokens of one workgroup's chunk
+constexpr int RT_TOKENS = 4 * RT_ROWS;    // tokens of one workgroup's chunk, times the multiple that keeps
+constexpr int RT_CHUNKS = 512;            // the chunks (whose sums one workgroup adds) to about this many
 constexpr uint32_t KEY_NINF = 0x007FFFFFu;  // the key of -inf: nothing at or below it is chosen
 
 struct RouterArgs {
   int T, E, k, renorm, na;
+  int chunk;  // tokens of a workgroup, a multiple of RT_TOKENS
   int roots[MAX_ADAPTERS + 1];
   const void* logits;
   const uint8_t* valid;
@@ -88,64 +90,13 @@ __device__ __forceinline__ bool row_any(bool c) {
   return ((__ballot(c) >> (threadIdx.x & 48)) & 0xFFFFull) != 0;
 }
 
-// Loads, counts and loss of one root from its chunks' sums, in chunk order.
-// `mass`, `hits`, `tally` point at the root's first chunk.  All threads call
-// it; red holds 2 * RT_THREADS words.
-__device__ void finish_root(const RouterArgs& a, int root, int nchunks, const float* mass, const int32_t* hits,
-                            const int32_t* tally, int& bad, char* red) {
-  const int tid = threadIdx.x;
-  double* rd = (double*)red;
-  int* ri = (int*)red;
-  int act = 0, b = 0;
-  for (int c = tid; c < nchunks; c += RT_THREADS) {
-    act += tally[2 * c];
-    b += tally[2 * c + 1];
-  }
-  ri[tid] = act;
-  ri[RT_THREADS + tid] = b;
-  __syncthreads();
-  for (int s = RT_THREADS / 2; s > 0; s >>= 1) {
-    if (tid < s) {
-      ri[tid] += ri[tid + s];
-      ri[RT_THREADS + tid] += ri[RT_THREADS + tid + s];
-    }
-    __syncthreads();
-  }
-  act = ri[0];
-  bad = ri[RT_THREADS];
-  __syncthreads();
-  double part = 0.0;
-  for (int e = tid; e < a.E; e += RT_THREADS) {
-    double m = 0.0;
-    int h = 0;
-    for (int c = 0; c < nchunks; ++c) {
-      m += (double)mass[(long)c * a.E + e];
-      h += hits[(long)c * a.E + e];
-    }
-    a.counts[(long)root * a.E + e] = h;
-    part += m * (double)h;
-  }
-  rd[tid] = part;
-  __syncthreads();
-  for (int s = RT_THREADS / 2; s > 0; s >>= 1) {
-    if (tid < s) rd[tid] += rd[tid + s];
-    __syncthreads();
-  }
-  if (tid == 0) {
-    a.active[root] = act;
-    const double n = (double)(act > 0 ? act : 1);
-    a.loss[root] = (float)(rd[0] * (double)a.E / ((double)a.k * n * n));
-  }
-  __syncthreads();
-}
-
 template <bool BF, int V>
 __global__ __launch_bounds__(RT_THREADS) void k_route(RouterArgs a) {
   __shared__ float smass[RT_ROWS / 4][16 * V];
   __shared__ int shits[16 * V];
   __shared__ int stally[2];
   int t0, nt, root;
-  if (!chunk_of(a, blockIdx.x, RT_TOKENS, t0, nt, root)) return;
+  if (!chunk_of(a, blockIdx.x, a.chunk, t0, nt, root)) return;
   const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
   for (int e = tid; e < 16 * V; e += RT_THREADS) shits[e] = 0;
   if (tid < 2) stally[tid] = 0;
@@ -234,18 +185,72 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouterArgs a) {
   if (tid < 2) a.tally[2 * (long)blockIdx.x + tid] = stally[tid];
 }
 
-__global__ __launch_bounds__(RT_THREADS) void k_route_sum(RouterArgs a) {
-  __shared__ __align__(16) char red[RT_THREADS * 8];
-  int first = 0;
-  int bad = 0;
+// Loads and loss of root blockIdx.x from its chunks' sums: thread (slice,
+// expert) adds every SLICES-th chunk, the slices are added in order, so the
+// result does not depend on timing.  Workgroup 0 also counts the bad tokens.
+constexpr int RS_THREADS = 1024;
+__global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
+  __shared__ float sm[RS_THREADS];
+  __shared__ int sh[RS_THREADS];
+  __shared__ double part[RS_THREADS / 64];
+  __shared__ int stally[2];
+  const int tid = threadIdx.x, root = blockIdx.x;
+  int first = 0, nc = 0, all = 0;
   for (int q = 0; q < a.na; ++q) {
-    const int nc = (a.roots[q + 1] - a.roots[q] + RT_TOKENS - 1) / RT_TOKENS;
-    int b;
-    finish_root(a, q, nc, a.mass + (long)first * a.E, a.hits + (long)first * a.E, a.tally + 2 * (long)first, b, red);
-    bad += b;
-    first += nc;
+    const int c = (a.roots[q + 1] - a.roots[q] + a.chunk - 1) / a.chunk;
+    if (q == root) {
+      first = all;
+      nc = c;
+    }
+    all += c;
   }
-  if (threadIdx.x == 0 && a.err != nullptr) *a.err = bad;
+  if (tid < 2) stally[tid] = 0;
+  // EP experts side by side, the smallest power of two that covers E
+  const int lg = a.E <= 1 ? 0 : 32 - __clz(a.E - 1), EP = 1 << lg;
+  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg;
+  float m = 0.0f;
+  int h = 0;
+  if (e < a.E) {
+    const float* pm = a.mass + (long)first * a.E + e;
+    const int32_t* ph = a.hits + (long)first * a.E + e;
+#pragma unroll 8
+    for (int c = slice; c < nc; c += slices) {
+      m += pm[(long)c * a.E];
+      h += ph[(long)c * a.E];
+    }
+  }
+  sm[tid] = m;
+  sh[tid] = h;
+  __syncthreads();
+  int act = 0, bad = 0;
+  for (int c = tid; c < nc; c += RS_THREADS) act += a.tally[2 * (long)(first + c)];
+  if (root == 0)
+    for (int c = tid; c < all; c += RS_THREADS) bad += a.tally[2 * (long)c + 1];
+  if (act != 0) atomicAdd(&stally[0], act);
+  if (bad != 0) atomicAdd(&stally[1], bad);
+  double v = 0.0;
+  if (tid < a.E) {  // slice 0
+    double mass = 0.0;
+    int hits = 0;
+    for (int q = 0; q < slices; ++q) {
+      mass += (double)sm[(q << lg) + tid];
+      hits += sh[(q << lg) + tid];
+    }
+    a.counts[(long)root * a.E + tid] = hits;
+    v = mass * (double)hits;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  if ((tid & 63) == 0) part[tid >> 6] = v;
+  __syncthreads();
+  if (tid == 0) {
+    double s = 0.0;
+    for (int q = 0; q < RS_THREADS / 64; ++q) s += part[q];
+    a.active[root] = stally[0];
+    const double n = (double)(stally[0] > 0 ? stally[0] : 1);
+    a.loss[root] = (float)(s * (double)a.E / ((double)a.k * n * n));
+    if (root == 0 && a.err != nullptr) *a.err = stally[1];
+  }
 }
 
 // The gradient: the token's softmax again from its logits, the chosen
@@ -254,7 +259,7 @@ template <bool BF, int V>
 __global__ __launch_bounds__(RT_THREADS) void k_route_bwd(RouterArgs a) {
   __shared__ float place[RT_ROWS][16 * V];
   int t0, nt, root;
-  if (!chunk_of(a, blockIdx.x, RT_TOKENS, t0, nt, root)) return;
+  if (!chunk_of(a, blockIdx.x, a.chunk, t0, nt, root)) return;
   const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
   float u[V];
   {
@@ -341,7 +346,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_bwd(RouterArgs a) {
 
 int chunks_of(const RouterArgs& a) {
   int n = 0;
-  for (int q = 0; q < a.na; ++q) n += (a.roots[q + 1] - a.roots[q] + RT_TOKENS - 1) / RT_TOKENS;
+  for (int q = 0; q < a.na; ++q) n += (a.roots[q + 1] - a.roots[q] + a.chunk - 1) / a.chunk;
   return n;
 }
 
@@ -384,6 +389,7 @@ moe_status check_router(const moe_router_desc* d, const moe_adapters* ad, Router
   a.renorm = d->renorm;
   a.na = 1;
   a.roots[1] = d->T;
+  a.chunk = RT_TOKENS * ((d->T + RT_TOKENS * RT_CHUNKS - 1) / (RT_TOKENS * RT_CHUNKS));
   if (ad == nullptr) return MOE_OK;
   if (ad->offsets == nullptr || ad->count < 1) return MOE_ERR_INVALID;
   if (ad->count > MAX_ADAPTERS) return MOE_ERR_UNSUPPORTED;
@@ -455,7 +461,7 @@ moe_status moe_router_forward(const moe_router_desc* d, const moe_adapters* ad, 
   a.tally = (int32_t*)((char*)workspace + 2 * up16(n * a.E * 4));
   const hipStream_t s = (hipStream_t)stream;
   by_shape<GoRoute>(d->logits_type == MOE_TYPE_BF16, a.E, a, (int)n, s);
-  MOE_LAUNCH(k_route_sum, dim3(1), dim3(RT_THREADS), 0, s, a);
+  MOE_LAUNCH(k_route_sum, dim3(a.na), dim3(RS_THREADS), 0, s, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
