@@ -239,6 +239,8 @@ def moe_lora_multi_workspace_size(desc: MoeLoraDesc, roots: Sequence[int]) -> Tu
 def _ptr(t: Optional[torch.Tensor], dtype=None, shape=None, name="tensor") -> Optional[int]:
     if t is None:
         return None
+    if t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype) and (shape is None or t.shape == shape):
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if not t.is_contiguous():
@@ -510,31 +512,28 @@ def moe_lora_split_e2m3x2(src: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
     return codes, scales
 
 
-class _On:
-    """The device and stream of one call: the device that every tensor of it
-    is on (made the current one for the call if it is not), and the caller's
-    stream there."""
+# the current stream's handle by device index (a Stream object costs 2 us to make)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
-    __slots__ = ("stream", "_guard")
 
-    def __init__(self, stream, first: torch.Tensor, *others: Optional[torch.Tensor]):
-        dev = first.device
-        if dev.type != "cuda":
-            raise ValueError("tensors must be device tensors")
-        for t in others:
-            if t is not None and t.device != dev:
-                raise ValueError(f"tensors on {dev} and {t.device}: one call runs on one device")
-        self._guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-        self.stream = _stream(torch.cuda.current_stream(dev) if stream is None else stream)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _launch(what: str, fn, stream, tensors, *args) -> None:
+    """fn(*args, stream) on the device that every tensor of the call is on
+    (made the current one for the call if it is not); stream None: that
+    device's current one."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{what}: tensors on {tensors[0].device} and {t.device}: one call runs on one device")
+    if dev < 0:
+        raise ValueError(f"{what}: tensors must be device tensors")
+    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, handle)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, handle)
+    if st != MOE_OK:
+        raise MoeLoraError(st, what)
 
 
 def _made(stream, *tensors: torch.Tensor) -> None:
@@ -599,19 +598,17 @@ class MoeRouter:
         self.device_error = torch.empty(1, dtype=i32, device=device)
         self.grad_logits = torch.empty(T, E, dtype=dtype, device=device)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self._dp = ctypes.byref(self.desc)
+        self._lshape, self._kshape = (T, E), (T, topk)
+        self._outs = tuple(t.data_ptr() for t in (self.topk_idx, self.topk_w, self.counts, self.active, self.loss,
+                                                  self.device_error, self.workspace)) + (nbytes,)
 
     def forward(self, logits: torch.Tensor, valid: Optional[torch.Tensor] = None, stream=None):
         """logits [T, E]; valid [T] uint8 (0: a padding token) or None.
         Returns (topk_idx, topk_w, counts, active, loss)."""
-        d = self.desc
-        lp = _ptr(logits, self.dtype, (d.T, d.E), "logits")
-        vp = _ptr(valid, torch.uint8, (d.T,), "valid")
-        with _On(stream, self.topk_idx, logits, valid) as s:
-            st = library().moe_router_forward(
-                ctypes.byref(d), self._adp, lp, vp, self.topk_idx.data_ptr(), self.topk_w.data_ptr(),
-                self.counts.data_ptr(), self.active.data_ptr(), self.loss.data_ptr(), self.device_error.data_ptr(),
-                self.workspace.data_ptr(), self.workspace.numel(), s)
-        _check(st, "moe_router_forward")
+        _launch("moe_router_forward", library().moe_router_forward, stream, (self.topk_idx, logits, valid), self._dp,
+                self._adp, _ptr(logits, self.dtype, self._lshape, "logits"),
+                _ptr(valid, torch.uint8, self._lshape[:1], "valid"), *self._outs)
         if self.checked:
             bad = self.dropped_tokens(stream)
             if bad:
@@ -630,15 +627,13 @@ class MoeRouter:
         forward's topk_idx, counts and active (the router's own buffers after
         forward, or copies) and the gradients of topk_w [T, k] and of the
         loss [roots] (None: zero)."""
-        d, f32, i32 = self.desc, torch.float32, torch.int32
-        na = self.counts.shape[0]
-        ptrs = (_ptr(logits, self.dtype, (d.T, d.E), "logits"), _ptr(valid, torch.uint8, (d.T,), "valid"),
-                _ptr(topk_idx, i32, (d.T, d.topk), "topk_idx"), _ptr(counts, i32, (na, d.E), "counts"),
-                _ptr(active, i32, (na,), "active"), _ptr(grad_topk_w, f32, (d.T, d.topk), "grad_topk_w"),
-                _ptr(grad_loss, f32, (na,), "grad_loss"))
-        with _On(stream, self.topk_idx, logits, valid, topk_idx, counts, active, grad_topk_w, grad_loss) as s:
-            st = library().moe_router_backward(ctypes.byref(d), self._adp, *ptrs, self.grad_logits.data_ptr(), s)
-        _check(st, "moe_router_backward")
+        f32, i32, T = torch.float32, torch.int32, self._lshape[:1]
+        _launch("moe_router_backward", library().moe_router_backward, stream,
+                (self.topk_idx, logits, valid, topk_idx, counts, active, grad_topk_w, grad_loss), self._dp, self._adp,
+                _ptr(logits, self.dtype, self._lshape, "logits"), _ptr(valid, torch.uint8, T, "valid"),
+                _ptr(topk_idx, i32, self._kshape, "topk_idx"), _ptr(counts, i32, self.counts.shape, "counts"),
+                _ptr(active, i32, self.active.shape, "active"), _ptr(grad_topk_w, f32, self._kshape, "grad_topk_w"),
+                _ptr(grad_loss, f32, self.active.shape, "grad_loss"), self.grad_logits.data_ptr())
         return self.grad_logits
 
 
@@ -681,6 +676,7 @@ class MoeAdamW:
             raise ValueError(f"states must hold {names}, one tensor each per param")
         self.states = {n: list(states[n]) for n in names}
         self._desc = MoeAdamwDesc(_float_type(params[0].dtype, "params"), _float_type(grads[0].dtype, "grads"), state_bits)
+        self._dp = ctypes.byref(self._desc)
         self._table = (MoeAdamwTensor * len(params))()
         ptype, gtype, f32 = params[0].dtype, grads[0].dtype, torch.float32
         if masters is not None and ptype != torch.bfloat16:
@@ -715,9 +711,8 @@ class MoeAdamW:
         d.step = self.steps
         d.seed = (self.steps if seed is None else seed) & 0xFFFFFFFF
         d.control = _ptr(control, torch.int32, (5,), "control")
-        with _On(stream, self.params[0], control) as s:
-            st = library().moe_adamw_step(ctypes.byref(d), self._table, len(self._table), s)
-        _check(st, "moe_adamw_step")
+        _launch("moe_adamw_step", library().moe_adamw_step, stream, (self.params[0], control), self._dp, self._table,
+                len(self._table))
 
     def write_control(self, control: torch.Tensor, lr: float, step: int, grad_scale: float = 1.0,
                       seed: Optional[int] = None) -> None:
@@ -750,11 +745,9 @@ def fp8_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optio
     if scales is None:
         scales = torch.empty(rows, K // 128, dtype=torch.float32, device=src.device)
         made.append(scales)
-    with _On(stream, src, codes, scales) as s:
-        st = library().moe_fp8_quantize_rows(
+    _launch("moe_fp8_quantize_rows", library().moe_fp8_quantize_rows, stream, (src, codes, scales),
             _ptr(src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], _ptr(codes, _E4M3, (rows, K), "codes"),
-            _ptr(scales, torch.float32, (rows, K // 128), "scales"), s)
-    _check(st, "moe_fp8_quantize_rows")
+            _ptr(scales, torch.float32, (rows, K // 128), "scales"))
     _made(stream, *made)
     return codes, scales
 
@@ -771,10 +764,8 @@ def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) 
     if transposed:
         out += [torch.empty(E, K, N, dtype=_E4M3, device=W.device),
                 torch.empty(E, K // 128, N // 128, dtype=torch.float32, device=W.device)]
-    with _On(stream, W) as s:
-        st = library().moe_fp8_quantize_weight(_ptr(W, torch.bfloat16, None, "W"), E, N, K,
-                                               *[t.data_ptr() for t in out], *([] if transposed else [None, None]), s)
-    _check(st, "moe_fp8_quantize_weight")
+    _launch("moe_fp8_quantize_weight", library().moe_fp8_quantize_weight, stream, (W,),
+            _ptr(W, torch.bfloat16, None, "W"), E, N, K, *[t.data_ptr() for t in out], *([] if transposed else [None, None]))
     _made(stream, *out)
     return tuple(out)
 
@@ -801,12 +792,11 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
     ps = MoePool(_ptr(pool["counts"], i32, (E,), "counts"), _ptr(pool["offsets"], i32, (E + 1,), "offsets"), None,
                  _ptr(pool["row_to_route"], i32, None, "row_to_route"), cap, block_m)
     d = MoeFp8Desc(E, N, K, topk, rows)
-    with _On(stream, a, a_scales, w, w_scales, out, pool["counts"], pool["offsets"], pool["row_to_route"]) as s:
-        st = library().moe_fp8_product(
+    _launch("moe_fp8_product", library().moe_fp8_product, stream,
+            (a, a_scales, w, w_scales, out, pool["counts"], pool["offsets"], pool["row_to_route"]),
             ctypes.byref(d), ctypes.byref(ps), _ptr(a, _E4M3, None, "a"), _ptr(a_scales, f32, (rows, K // 128), "a_scales"),
             _ptr(w, _E4M3, (E, N, K), "w"), _ptr(w_scales, f32, (E, N // 128, K // 128), "w_scales"),
-            _ptr(out, torch.bfloat16, (cap, N), "out"), s)
-    _check(st, "moe_fp8_product")
+            _ptr(out, torch.bfloat16, (cap, N), "out"))
     if made:
         _made(stream, out)
     return out

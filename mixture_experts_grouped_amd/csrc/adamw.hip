@@ -4,9 +4,9 @@
 // One pass over memory: a thread takes eight consecutive elements, so bf16
 // operands move 16 bytes a lane and codes 8; the sixteen lanes of a DPP row
 // hold one run of 128 elements, whose largest moments are four DPP maxima.
-// The tensors' pointers travel in the kernel argument (up to ADAMW_MAX per
-// launch); a workgroup finds its tensor by one ballot over the tensors' first
-// chunks.
+// The tensors' pointers travel in the kernel argument (as many per launch as
+// 4 KB hold: 100 with fp32 moments, 63 with masters and 8-bit ones); a workgroup
+// finds its tensor by ballots over the tensors' first chunks.
 #include <cmath>
 
 #include "../../include/moelora.h"
@@ -19,20 +19,45 @@ namespace {
 
 constexpr int AW_THREADS = 256;
 constexpr int AW_CHUNK = AW_THREADS * 8;  // elements of a workgroup's chunk
-constexpr int ADAMW_MAX = 48;             // tensors per launch: 72 bytes each, under 4 KB of arguments
+constexpr size_t AW_ARGS = 4096;          // bytes of kernel arguments
 constexpr float E4M3_MAX = 448.0f, E5M2_MAX = 57344.0f;
 constexpr float TINY = 0x1p-100f;  // below it a run's moments count as zero (its reciprocal would overflow)
 
-struct AdamwArgs {
-  int count;
+struct AdamwHead {
+  int count, chunks;
   float b1, omb1, b2, omb2, eps, wd;
   float lr, bias1, bias2, gscale;
   uint32_t seed;
   const moe_adamw_control* control;
-  int first[ADAMW_MAX + 1];  // first chunk of each tensor; first[count] = chunks
-  moe_adamw_tensor t[ADAMW_MAX];
 };
-static_assert(sizeof(AdamwArgs) <= 4096, "kernel argument size");
+// One tensor's buffers; only those that the call's kinds have, so that as
+// many tensors as possible go into one launch.
+struct AwBase {
+  void* param;
+  const void* grad;
+  void *m, *v;
+  int first;      // the tensor's first chunk; its chunks end where the next one's begin
+  uint32_t tail;  // elements missing from its last chunk
+};
+template <bool MASTER>
+struct AwMaster {
+  float* master;
+};
+template <>
+struct AwMaster<false> {};
+template <bool S8>
+struct AwScales {
+  float *m_scale, *v_scale;
+};
+template <>
+struct AwScales<false> {};
+template <bool MASTER, bool S8>
+struct AwTensor : AwBase, AwMaster<MASTER>, AwScales<S8> {};
+template <bool MASTER, bool S8>
+struct AdamwArgs : AdamwHead {
+  static constexpr int FIT = (AW_ARGS - sizeof(AdamwHead)) / sizeof(AwTensor<MASTER, S8>), MAX = FIT < 128 ? FIT : 128;
+  AwTensor<MASTER, S8> t[MAX];
+};
 
 __device__ __forceinline__ uint32_t noise_of(uint32_t i, uint32_t seed) {
   uint32_t x = i * 0x9E3779B9u + seed;
@@ -164,14 +189,19 @@ __device__ __forceinline__ float encode(const float (&x)[8], const uint32_t (&no
 }
 
 template <class P, class G, bool MASTER, bool S8>
-__global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs a) {
+__global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs<MASTER, S8> a) {
   const int lane = threadIdx.x & 63;
   // the last tensor whose first chunk is not past this one (none is empty)
-  const bool before = lane < a.count && a.first[lane < a.count ? lane : 0] <= (int)blockIdx.x;
-  const int q = __popcll(__ballot(before)) - 1;
-  const moe_adamw_tensor& t = a.t[q];
-  const long n = t.n;
-  const long i = (long)((int)blockIdx.x - a.first[q]) * AW_CHUNK + 8 * threadIdx.x;
+  int q = -1;
+#pragma unroll
+  for (int h = 0; h < a.MAX; h += 64) {
+    const int i = h + lane;
+    q += __popcll(__ballot(i < a.count && a.t[i < a.count ? i : 0].first <= (int)blockIdx.x));
+  }
+  const AwTensor<MASTER, S8>& t = a.t[q];
+  const int end = q + 1 < a.count ? a.t[q + 1 < a.MAX ? q + 1 : q].first : a.chunks;
+  const long n = (long)(end - t.first) * AW_CHUNK - t.tail;
+  const long i = (long)((int)blockIdx.x - t.first) * AW_CHUNK + 8 * threadIdx.x;
   float lr = a.lr, c1 = a.bias1, c2 = a.bias2, gs = a.gscale;
   uint32_t seed = a.seed;
   if (a.control != nullptr) {
@@ -229,23 +259,51 @@ __global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs a) {
   }
 }
 
+template <class P, class G, bool MASTER, bool S8>
+void launch_all(const AdamwHead& head, const moe_adamw_tensor* tensors, int count, hipStream_t st) {
+  AdamwArgs<MASTER, S8> a;
+  (AdamwHead&)a = head;
+  a.count = a.chunks = 0;
+  auto flush = [&]() {
+    if (a.count != 0)
+      MOE_LAUNCH_AS("k_adamw", (k_adamw<P, G, MASTER, S8>), dim3(a.chunks), dim3(AW_THREADS), 0, st, a);
+    a.count = a.chunks = 0;
+  };
+  for (int q = 0; q < count; ++q) {
+    const moe_adamw_tensor& s = tensors[q];
+    if (s.n == 0) continue;
+    const int64_t chunks = (s.n + AW_CHUNK - 1) / AW_CHUNK;  // at most 2^29
+    if (a.count == a.MAX || a.chunks + chunks > (int64_t)1 << 30) flush();
+    AwTensor<MASTER, S8>& t = a.t[a.count++];
+    t.param = s.param;
+    t.grad = s.grad;
+    t.m = s.m;
+    t.v = s.v;
+    t.first = a.chunks;
+    t.tail = (uint32_t)(chunks * AW_CHUNK - s.n);
+    if constexpr (MASTER) t.master = s.master;
+    if constexpr (S8) {
+      t.m_scale = s.m_scale;
+      t.v_scale = s.v_scale;
+    }
+    a.chunks += (int)chunks;
+  }
+  flush();
+}
 template <class P, class G, bool MASTER>
-void launch_states(const AdamwArgs& a, bool s8, hipStream_t st) {
-  const dim3 g((unsigned)a.first[a.count]), b(AW_THREADS);
-  if (s8)
-    MOE_LAUNCH_AS("k_adamw", (k_adamw<P, G, MASTER, true>), g, b, 0, st, a);
-  else
-    MOE_LAUNCH_AS("k_adamw", (k_adamw<P, G, MASTER, false>), g, b, 0, st, a);
+void launch_states(const AdamwHead& h, bool s8, const moe_adamw_tensor* t, int count, hipStream_t st) {
+  s8 ? launch_all<P, G, MASTER, true>(h, t, count, st) : launch_all<P, G, MASTER, false>(h, t, count, st);
 }
 template <class G>
-void launch_params(const AdamwArgs& a, const moe_adamw_desc* d, bool master, hipStream_t st) {
+void launch_params(const AdamwHead& h, const moe_adamw_desc* d, bool master, const moe_adamw_tensor* t, int count,
+                   hipStream_t st) {
   const bool s8 = d->state_bits == 8;
   if (d->param_type == MOE_TYPE_F32)
-    launch_states<float, G, false>(a, s8, st);
+    launch_states<float, G, false>(h, s8, t, count, st);
   else if (master)
-    launch_states<uint16_t, G, true>(a, s8, st);
+    launch_states<uint16_t, G, true>(h, s8, t, count, st);
   else
-    launch_states<uint16_t, G, false>(a, s8, st);
+    launch_states<uint16_t, G, false>(h, s8, t, count, st);
 }
 
 bool unit(double b) { return b >= 0.0 && b < 1.0; }  // false for NaN
@@ -302,7 +360,7 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_desc* d, const moe_adamw_te
     if (tensors[q].n > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
   }
   if (!any) return MOE_OK;
-  AdamwArgs a{};
+  AdamwHead a{};
   a.b1 = (float)d->beta1;
   a.omb1 = (float)(1.0 - d->beta1);
   a.b2 = (float)d->beta2;
@@ -316,24 +374,9 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_desc* d, const moe_adamw_te
   a.seed = d->seed;
   a.control = d->control;
   const hipStream_t s = (hipStream_t)stream;
-  auto flush = [&]() {
-    if (a.count == 0) return;
-    if (d->grad_type == MOE_TYPE_BF16)
-      launch_params<uint16_t>(a, d, master, s);
-    else
-      launch_params<float>(a, d, master, s);
-    a.count = 0;
-  };
-  for (int q = 0; q < count; ++q) {
-    const int64_t n = tensors[q].n;
-    if (n == 0) continue;
-    const int64_t chunks = (n + AW_CHUNK - 1) / AW_CHUNK;  // below 2^29
-    if (a.count == ADAMW_MAX || (a.count > 0 && a.first[a.count] + chunks >= (int64_t)1 << 30)) flush();
-    if (a.count == 0) a.first[0] = 0;
-    a.t[a.count] = tensors[q];
-    a.first[a.count + 1] = a.first[a.count] + (int)chunks;
-    ++a.count;
-  }
-  flush();
+  if (d->grad_type == MOE_TYPE_BF16)
+    launch_params<uint16_t>(a, d, master, tensors, count, s);
+  else
+    launch_params<float>(a, d, master, tensors, count, s);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -159,44 +159,44 @@ struct Fp8Args {
 // by a kernel of its own, which costs more than the scan.  Order as in
 // group_tile: each XCD a contiguous range of (expert's M chunk, N tile, M
 // tile), so that workgroups of one XCD share a weight panel in its L2.
+constexpr int MAX_E = 512;
 __device__ __forceinline__ bool pool_tile(const Fp8Args& p, int TM, int b, int nn, int gm, int& e, int& m, int& nt) {
   const int lane = threadIdx.x & 63;
-  int total = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    int x = e0 + lane < p.E ? (p.counts[e0 + lane] + TM - 1) / TM : 0;
+  int cnt[MAX_E / 64], end[MAX_E / 64], total = 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) x += __shfl_xor(x, o, 64);
-    total += x;
+  for (int q = 0; q < MAX_E / 64; ++q) {
+    cnt[q] = 64 * q + lane < p.E ? (p.counts[64 * q + lane] + TM - 1) / TM : 0;
+    if (64 * q < p.E) {
+      int x = cnt[q];
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const int y = __shfl_up(x, o, 64);
+        if (lane >= o) x += y;
+      }
+      end[q] = total + x;  // tiles up to and with this lane's expert
+      total = __builtin_amdgcn_readlane(end[q], 63);
+    }
   }
-  total = __builtin_amdgcn_readfirstlane(total);
   if (b >= total * nn) return false;
   const int L = xcd_remap(b, total * nn);
   const int v = L / nn;
-  int before = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    const int c = e0 + lane < p.E ? (p.counts[e0 + lane] + TM - 1) / TM : 0;
-    int x = c;
+  bool found = false;
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(x, o, 64);
-      if (lane >= o) x += y;
-    }
-    const int end = before + x;  // tiles up to and with this lane's expert
-    const unsigned long long past = __ballot(end > v);
-    if (past != 0) {
-      const int l = __ffsll(past) - 1;
-      const int cnt = __shfl(c, l, 64), s = __shfl(end, l, 64) - cnt;
-      e = __builtin_amdgcn_readfirstlane(e0 + l);
-      const int cs = s + gm * ((v - s) / gm);
-      const int sz = s + cnt - cs < gm ? s + cnt - cs : gm;
-      const int r = L - cs * nn;
-      m = __builtin_amdgcn_readfirstlane(cs + r % sz - s);
-      nt = __builtin_amdgcn_readfirstlane(r / sz);
-      return true;
-    }
-    before += __shfl(x, 63, 64);
+  for (int q = 0; q < MAX_E / 64; ++q) {
+    if (64 * q >= p.E || found) continue;
+    const unsigned long long past = __ballot(end[q] > v);
+    if (past == 0) continue;
+    found = true;
+    const int l = __ffsll(past) - 1;
+    const int n = __builtin_amdgcn_readlane(cnt[q], l), s = __builtin_amdgcn_readlane(end[q], l) - n;
+    const int cs = s + gm * ((v - s) / gm);
+    const int sz = s + n - cs < gm ? s + n - cs : gm;
+    const int r = L - cs * nn;
+    e = 64 * q + l;
+    m = cs + r % sz - s;
+    nt = r / sz;
   }
-  return false;
+  return found;
 }
 
 __device__ __forceinline__ f32x4 mma8(i32x8 w, i32x8 x, f32x4 c) {
@@ -221,7 +221,7 @@ struct Geo8 {
   static constexpr int table_at(int K) { return SW_AT + 2 * (TN / 128) * stages(K) * 4; }  // PoolTable
   static constexpr int lds(int K, int E) { return table_at(K) + 12 * E; }
   static_assert(128 % (TN / WN) == 0 && TN % 128 == 0, "a wave's weight rows lie in one block of 128");
-  static_assert(lds(MAX_DIM, 512) <= 160 * 1024 && NW * 64 >= TM && FN % 2 == 0, "one scale a lane; fragments are stored in pairs");
+  static_assert(lds(MAX_DIM, MAX_E) <= 160 * 1024 && NW * 64 >= TM && FN % 2 == 0, "one scale a lane; fragments are stored in pairs");
 };
 
 // The pool's tiles of TM rows, in LDS: for each expert the number of tiles up
@@ -542,17 +542,18 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
 
 // Few rows per expert (decoding): the weights are read once and bound the
 // time, so they go from memory straight into the registers that the matrix
-// instruction takes.  A wave is 16 activation rows x 16 weight rows with the
-// next FEW_CH K blocks in flight while FEW_CH are multiplied.  It walks K in
+// instruction takes.  A workgroup is one wave (so that the few tiles spread
+// evenly over the CUs): 16 activation rows x 16 weight rows, the next FEW_CH K
+// blocks in flight while FEW_CH are multiplied.  It walks K in
 // order, so a row's sums are those of the tile kernels bit for bit.
 constexpr int FEW_ROWS = 16, FEW_CH = 4;
-__global__ __launch_bounds__(256) void k_fp8_few(Fp8Args p) {
-  const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+__global__ __launch_bounds__(64) void k_fp8_few(Fp8Args p) {
+  const int lane = threadIdx.x;
   const int fr = lane & 15, fc = lane >> 4;
   const int KB = p.K / 128;
   int e, m, nt;
-  for (int b = blockIdx.x; pool_tile(p, FEW_ROWS, b, p.N / 64, TILE_GM, e, m, nt); b += gridDim.x) {
-    const int n0 = nt * 64 + 16 * w;
+  for (int b = blockIdx.x; pool_tile(p, FEW_ROWS, b, p.N / 16, TILE_GM, e, m, nt); b += gridDim.x) {
+    const int n0 = nt * 16;
     const rsrc_t rw = make_rsrc(p.w + ((long)e * p.N + n0) * p.K, (uint64_t)16 * p.K);
     const uint32_t wo = (uint32_t)fr * (uint32_t)p.K + 32u * (uint32_t)fc;
     const long row0 = (long)p.offsets[e] + (long)m * FEW_ROWS;
@@ -641,7 +642,7 @@ hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, int per_cu, hipStream_t
   static PerDeviceOnce once;
   hipError_t e = once.run([] {
     AttrInit ai;
-    ai.lds((const void*)k_fp8_tile<G>, G::lds(MAX_DIM, 512));
+    ai.lds((const void*)k_fp8_tile<G>, G::lds(MAX_DIM, MAX_E));
     return ai.err;
   });
   unsigned grid = 0;
@@ -653,15 +654,15 @@ hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, int per_cu, hipStream_t
 
 hipError_t launch_few(const Fp8Args& p, int64_t mtiles, hipStream_t st) {
   unsigned grid = 0;
-  const hipError_t e = grid_of(mtiles * (p.N / 64), 4, grid);
+  const hipError_t e = grid_of(mtiles * (p.N / 16), 8, grid);
   if (e != hipSuccess) return e;
-  MOE_LAUNCH(k_fp8_few, dim3(grid), dim3(256), 0, st, p);
+  MOE_LAUNCH(k_fp8_few, dim3(grid), dim3(64), 0, st, p);
   return hipGetLastError();
 }
 
 moe_status check_weight(int32_t E, int32_t N, int32_t K) {
   if (E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID;
-  if (E > 512 || N % 128 != 0 || K % 128 != 0 || N > MAX_DIM || K > MAX_DIM || (int64_t)N * K >= (int64_t)1 << 31)
+  if (E > MAX_E || N % 128 != 0 || K % 128 != 0 || N > MAX_DIM || K > MAX_DIM || (int64_t)N * K >= (int64_t)1 << 31)
     return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
@@ -723,7 +724,7 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
     return MOE_ERR_INVALID;
   if (pool->capacity >= (int64_t)1 << 31 || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   // tile indices of the smallest tiles are 32 bits
-  if ((pool->capacity / FEW_ROWS + d->E) * (d->N / 64) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  if ((pool->capacity / FEW_ROWS + d->E) * (d->N / 16) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (d->topk > 0 && d->a_rows * d->K >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor
   if (!aligned(pool->counts, 4) || !aligned(pool->offsets, 4) || !aligned(pool->row_to_route, 4))
     return MOE_ERR_INVALID;

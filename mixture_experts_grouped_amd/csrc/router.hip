@@ -20,10 +20,13 @@
 namespace moelora {
 namespace {
 
-constexpr int RT_THREADS = 256;
-constexpr int RT_ROWS = RT_THREADS / 16;  // tokens a workgroup works on at once
-constexpr int RT_TOKENS = 4 * RT_ROWS;    // tokens of one workgroup's chunk, times the multiple that keeps
-constexpr int RT_CHUNKS = 512;            // the chunks (whose sums one workgroup adds) to about this many
+// A workgroup's threads by V, the experts a lane holds (more registers: fewer
+// waves); 16 of them work on one token.
+template <int V>
+constexpr int THREADS = V <= 8 ? 1024 : V == 16 ? 512 : 256;
+constexpr int BWD_THREADS = 256;  // 16 tokens: nothing is summed over tokens there
+constexpr int RT_TOKENS = 64;     // tokens of one workgroup's chunk, times the multiple that keeps
+constexpr int RT_CHUNKS = 512;    // the chunks (whose sums one workgroup adds) to about this many
 constexpr uint32_t KEY_NINF = 0x007FFFFFu;  // the key of -inf: nothing at or below it is chosen
 
 struct RouterArgs {
@@ -38,10 +41,9 @@ struct RouterArgs {
   int32_t* active;
   float* loss;
   int32_t* err;
-  // per chunk: mass [chunks][E] fp32, hits [chunks][E] int32, then active and bad tokens [chunks][2] int32
-  float* mass;
-  int32_t* hits;
-  int32_t* tally;
+  // per chunk E + 1 pairs: each expert's probability mass (fp32 bits) and
+  // routes, then the active and the bad tokens
+  uint2* sums;
   // backward
   const float* gw;
   const float* gloss;
@@ -90,21 +92,30 @@ __device__ __forceinline__ bool row_any(bool c) {
   return ((__ballot(c) >> (threadIdx.x & 48)) & 0xFFFFull) != 0;
 }
 
-template <bool BF, int V>
-__global__ __launch_bounds__(RT_THREADS) void k_route(RouterArgs a) {
-  __shared__ float smass[RT_ROWS / 4][16 * V];
+__device__ __forceinline__ float loss_of(const RouterArgs& a, double mass_hits, int active) {
+  const double n = (double)(active > 0 ? active : 1);
+  return (float)(mass_hits * (double)a.E / ((double)a.k * n * n));
+}
+
+// ONE: at most ONE_TOKENS tokens of a single root, whose sums are the results.
+constexpr int ONE_THREADS = 256, ONE_TOKENS = ONE_THREADS / 16;
+template <bool BF, int V, bool ONE>
+__global__ __launch_bounds__(ONE ? ONE_THREADS : THREADS<V>) void k_route(RouterArgs a) {
+  constexpr int NT = ONE ? ONE_THREADS : THREADS<V>, ROWS = NT / 16, WAVES = NT / 64;
+  __shared__ float smass[WAVES][16 * V];
   __shared__ int shits[16 * V];
   __shared__ int stally[2];
+  __shared__ double part[WAVES];
   int t0, nt, root;
   if (!chunk_of(a, blockIdx.x, a.chunk, t0, nt, root)) return;
   const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
-  for (int e = tid; e < 16 * V; e += RT_THREADS) shits[e] = 0;
+  for (int e = tid; e < 16 * V; e += NT) shits[e] = 0;
   if (tid < 2) stally[tid] = 0;
   __syncthreads();
   float mass[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) mass[i] = 0.0f;
-  for (int o = 0; o < nt; o += RT_ROWS) {
+  for (int o = 0; o < nt; o += ROWS) {
     const long t = (long)t0 + o + row;
     const bool in = o + row < nt;
     const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
@@ -175,18 +186,38 @@ __global__ __launch_bounds__(RT_THREADS) void k_route(RouterArgs a) {
     if ((tid & 48) == 0) smass[tid >> 6][j + 16 * i] = m;
   }
   __syncthreads();
-  for (int e = tid; e < a.E; e += RT_THREADS) {
+  uint2* sums = a.sums + (long)blockIdx.x * (a.E + 1);
+  double v = 0.0;
+  for (int e = tid; e < a.E; e += NT) {
     float m = 0.0f;
 #pragma unroll
-    for (int wv = 0; wv < RT_ROWS / 4; ++wv) m += smass[wv][e];
-    a.mass[(long)blockIdx.x * a.E + e] = m;
-    a.hits[(long)blockIdx.x * a.E + e] = shits[e];
+    for (int wv = 0; wv < WAVES; ++wv) m += smass[wv][e];
+    if constexpr (ONE) {
+      a.counts[e] = shits[e];
+      v += (double)m * (double)shits[e];
+    } else {
+      sums[e] = make_uint2(__float_as_uint(m), (uint32_t)shits[e]);
+    }
   }
-  if (tid < 2) a.tally[2 * (long)blockIdx.x + tid] = stally[tid];
+  if constexpr (ONE) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    if ((tid & 63) == 0) part[tid >> 6] = v;
+    __syncthreads();
+    if (tid == 0) {
+      double s = 0.0;
+      for (int q = 0; q < WAVES; ++q) s += part[q];
+      a.active[0] = stally[0];
+      a.loss[0] = loss_of(a, s, stally[0]);
+      if (a.err != nullptr) *a.err = stally[1];
+    }
+  } else if (tid == 0) {
+    sums[a.E] = make_uint2((uint32_t)stally[0], (uint32_t)stally[1]);
+  }
 }
 
 // Loads and loss of root blockIdx.x from its chunks' sums: thread (slice,
-// expert) adds every SLICES-th chunk, the slices are added in order, so the
+// expert) adds every slices-th chunk, the slices are added in order, so the
 // result does not depend on timing.  Workgroup 0 also counts the bad tokens.
 constexpr int RS_THREADS = 1024;
 __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
@@ -205,33 +236,38 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
     all += c;
   }
   if (tid < 2) stally[tid] = 0;
+  const uint2* from = a.sums + (long)first * (a.E + 1);
+  int act = 0, bad = 0;
+  for (int c = tid; c < nc; c += RS_THREADS) act += (int)from[(long)c * (a.E + 1) + a.E].x;
+  if (root == 0)
+    for (int c = tid; c < all; c += RS_THREADS) bad += (int)a.sums[(long)c * (a.E + 1) + a.E].y;
   // EP experts side by side, the smallest power of two that covers E
   const int lg = a.E <= 1 ? 0 : 32 - __clz(a.E - 1), EP = 1 << lg;
-  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg;
+  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg, W = a.E + 1;
   float m = 0.0f;
   int h = 0;
   if (e < a.E) {
-    const float* pm = a.mass + (long)first * a.E + e;
-    const int32_t* ph = a.hits + (long)first * a.E + e;
-#pragma unroll 8
-    for (int c = slice; c < nc; c += slices) {
-      m += pm[(long)c * a.E];
-      h += ph[(long)c * a.E];
+    for (int c = slice; c < nc; c += 16 * slices) {
+      uint2 r[16];  // in flight together
+#pragma unroll
+      for (int u = 0; u < 16; ++u) r[u] = c + u * slices < nc ? from[(long)(c + u * slices) * W + e] : make_uint2(0, 0);
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        m += __uint_as_float(r[u].x);
+        h += (int)r[u].y;
+      }
     }
   }
   sm[tid] = m;
   sh[tid] = h;
   __syncthreads();
-  int act = 0, bad = 0;
-  for (int c = tid; c < nc; c += RS_THREADS) act += a.tally[2 * (long)(first + c)];
-  if (root == 0)
-    for (int c = tid; c < all; c += RS_THREADS) bad += a.tally[2 * (long)c + 1];
   if (act != 0) atomicAdd(&stally[0], act);
   if (bad != 0) atomicAdd(&stally[1], bad);
   double v = 0.0;
   if (tid < a.E) {  // slice 0
     double mass = 0.0;
     int hits = 0;
+#pragma unroll 8
     for (int q = 0; q < slices; ++q) {
       mass += (double)sm[(q << lg) + tid];
       hits += sh[(q << lg) + tid];
@@ -245,10 +281,10 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
   __syncthreads();
   if (tid == 0) {
     double s = 0.0;
+#pragma unroll
     for (int q = 0; q < RS_THREADS / 64; ++q) s += part[q];
     a.active[root] = stally[0];
-    const double n = (double)(stally[0] > 0 ? stally[0] : 1);
-    a.loss[root] = (float)(s * (double)a.E / ((double)a.k * n * n));
+    a.loss[root] = loss_of(a, s, stally[0]);
     if (root == 0 && a.err != nullptr) *a.err = stally[1];
   }
 }
@@ -256,8 +292,9 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
 // The gradient: the token's softmax again from its logits, the chosen
 // experts' terms placed through a row of LDS per token.
 template <bool BF, int V>
-__global__ __launch_bounds__(RT_THREADS) void k_route_bwd(RouterArgs a) {
-  __shared__ float place[RT_ROWS][16 * V];
+__global__ __launch_bounds__(BWD_THREADS) void k_route_bwd(RouterArgs a) {
+  constexpr int ROWS = BWD_THREADS / 16;
+  __shared__ float place[ROWS][16 * V];
   int t0, nt, root;
   if (!chunk_of(a, blockIdx.x, a.chunk, t0, nt, root)) return;
   const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
@@ -272,7 +309,7 @@ __global__ __launch_bounds__(RT_THREADS) void k_route_bwd(RouterArgs a) {
     }
   }
   float* mine = place[row];
-  for (int o = 0; o < nt; o += RT_ROWS) {
+  for (int o = 0; o < nt; o += ROWS) {
     const long t = (long)t0 + o + row;
     const bool in = o + row < nt;
     const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
@@ -350,6 +387,10 @@ int chunks_of(const RouterArgs& a) {
   return n;
 }
 
+// Few tokens: one launch.  (Beyond one round of the workgroup the second
+// launch costs less than the further rounds.)
+bool one_launch(const RouterArgs& a) { return a.na == 1 && a.T <= ONE_TOKENS; }
+
 // experts a lane holds: the smallest of 4, 8, 16, 32 that covers E
 template <template <bool, int> class F, class... A>
 void by_shape(bool bf, int E, A&&... args) {
@@ -365,13 +406,16 @@ void by_shape(bool bf, int E, A&&... args) {
 template <bool BF, int V>
 struct GoRoute {
   static void go(const RouterArgs& a, int n, hipStream_t st) {
-    MOE_LAUNCH_AS("k_route", (k_route<BF, V>), dim3(n), dim3(RT_THREADS), 0, st, a);
+    if (one_launch(a))
+      MOE_LAUNCH_AS("k_route", (k_route<BF, V, true>), dim3(1), dim3(ONE_THREADS), 0, st, a);
+    else
+      MOE_LAUNCH_AS("k_route", (k_route<BF, V, false>), dim3(n), dim3(THREADS<V>), 0, st, a);
   }
 };
 template <bool BF, int V>
 struct GoRouteBwd {
   static void go(const RouterArgs& a, int n, hipStream_t st) {
-    MOE_LAUNCH_AS("k_route_bwd", (k_route_bwd<BF, V>), dim3(n), dim3(RT_THREADS), 0, st, a);
+    MOE_LAUNCH_AS("k_route_bwd", (k_route_bwd<BF, V>), dim3(n), dim3(BWD_THREADS), 0, st, a);
   }
 };
 
@@ -401,11 +445,7 @@ moe_status check_router(const moe_router_desc* d, const moe_adapters* ad, Router
   return MOE_OK;
 }
 
-size_t up16(size_t v) { return (v + 15) & ~(size_t)15; }
-size_t workspace_of(const RouterArgs& a) {
-  const size_t n = (size_t)chunks_of(a);
-  return 2 * up16(n * a.E * 4) + up16(n * 8);
-}
+size_t workspace_of(const RouterArgs& a) { return (size_t)chunks_of(a) * (a.E + 1) * sizeof(uint2); }
 
 }  // namespace
 }  // namespace moelora
@@ -447,7 +487,6 @@ moe_status moe_router_forward(const moe_router_desc* d, const moe_adapters* ad, 
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return MOE_ERR_INVALID;
   }
-  const size_t n = (size_t)chunks_of(a);
   a.logits = logits;
   a.valid = valid;
   a.idx = topk_idx;
@@ -456,12 +495,11 @@ moe_status moe_router_forward(const moe_router_desc* d, const moe_adapters* ad, 
   a.active = active;
   a.loss = loss;
   a.err = device_error;
-  a.mass = (float*)workspace;
-  a.hits = (int32_t*)((char*)workspace + up16(n * a.E * 4));
-  a.tally = (int32_t*)((char*)workspace + 2 * up16(n * a.E * 4));
+  a.sums = (uint2*)workspace;
+  const int n = chunks_of(a);
   const hipStream_t s = (hipStream_t)stream;
-  by_shape<GoRoute>(d->logits_type == MOE_TYPE_BF16, a.E, a, (int)n, s);
-  MOE_LAUNCH(k_route_sum, dim3(a.na), dim3(RS_THREADS), 0, s, a);
+  by_shape<GoRoute>(d->logits_type == MOE_TYPE_BF16, a.E, a, n, s);
+  if (!one_launch(a)) MOE_LAUNCH(k_route_sum, dim3(a.na), dim3(RS_THREADS), 0, s, a);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
@@ -492,6 +530,7 @@ moe_status moe_router_backward(const moe_router_desc* d, const moe_adapters* ad,
   a.gw = grad_topk_w;
   a.gloss = grad_loss;
   a.glogits = grad_logits;
+  a.chunk = BWD_THREADS / 16;
   by_shape<GoRouteBwd>(d->logits_type == MOE_TYPE_BF16, a.E, a, chunks_of(a), (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
