@@ -431,7 +431,8 @@ moe_status moe_router_backward(const moe_router_desc* desc, const moe_adapters* 
  * tensor (the last one may be short) m is e4m3 codes times one fp32 scale
  * (max|m| / 448) and v is e5m2 codes times one fp32 scale (max v / 57344);
  * the step itself uses the unrounded m and v.  Codes are rounded at random:
- * y = x * (448 or 57344) / max is clamped to the format's largest value, 16
+ * y = x * (top * (1 / max)), top = 448 or 57344 (each operation rounded to
+ * fp32, as in the moments above), is clamped to [-top, top], 16
  * random bits are added below its last kept mantissa bit, the rest is cut
  * (below the format's normal range the cut value is then rounded to nearest,
  * ties to even).  Without it a decaying average would stop moving once a

@@ -66,6 +66,16 @@ __device__ __forceinline__ uint32_t noise_of(uint32_t i, uint32_t seed) {
   return x ^ (x >> 16);
 }
 
+// one rounding each, never fused with another operation
+__device__ __forceinline__ float mul1(float a, float b) {
+#pragma clang fp contract(off)
+  return a * b;
+}
+__device__ __forceinline__ float add1(float a, float b) {
+#pragma clang fp contract(off)
+  return a + b;
+}
+
 // eight values of a T tensor at p + i; those past n read zero
 template <class T>
 __device__ __forceinline__ void load8(const T* p, long i, long n, float (&v)[8]) {
@@ -165,7 +175,7 @@ __device__ __forceinline__ float encode(const float (&x)[8], const uint32_t (&no
   for (int c = 0; c < 8; ++c) m = max(m, mag(x[c]));
   const float amax = __uint_as_float(row_max(m));
   const bool zero = amax < TINY;
-  const float inv = zero ? 0.0f : TOP / amax;
+  const float inv = zero ? 0.0f : mul1(1.0f / amax, TOP);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     float y[4];
@@ -229,9 +239,11 @@ __global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs<MASTER, S8> a) {
   }
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
-    const float gc = g[c] * gs;
-    m[c] = a.b1 * m[c] + a.omb1 * gc;
-    v[c] = a.b2 * v[c] + a.omb2 * (gc * gc);
+    const float gc = mul1(g[c], gs);
+    // one rounding an operation, none fused: which code a moment is rounded to
+    // then follows from the inputs alone, for anyone who computes it again
+    m[c] = add1(mul1(m[c], a.b1), mul1(gc, a.omb1));
+    v[c] = add1(mul1(v[c], a.b2), mul1(mul1(gc, gc), a.omb2));
     p[c] = p[c] * keep - step * m[c] / (sqrtf(v[c] * ic2) + a.eps);
   }
   store8((P*)t.param, i, n, p);

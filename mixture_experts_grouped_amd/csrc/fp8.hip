@@ -620,42 +620,50 @@ __global__ __launch_bounds__(64) void k_fp8_few(Fp8Args p) {
 
 using GL = Geo8<256, 256, 4, 2, 2>;
 using GM = Geo8<64, 128, 1, 4, 3>;
-// routes per expert up to which k_fp8_few and the 64-row tile are taken
-constexpr int FEW_AVG = 8, MID_AVG = 96;
 
-
-// Workgroups for at most `tiles` tiles: every kernel here walks on by its grid
-// until the pool's tiles are done, so the grid is a matter of speed alone.
-// One per CU and resident workgroup, in whole rounds over the XCDs.
-hipError_t grid_of(int64_t tiles, int per_cu, unsigned& grid) {
-  int dev = 0, cus = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-  if (e != hipSuccess) return e;
-  const int64_t most = (int64_t)cus * per_cu;
-  grid = (unsigned)(((tiles < most ? tiles : most) + 7) / 8 * 8);
-  return hipSuccess;
+// Which kernel: the routes are known, how they fall on the experts is not, so
+// an expert with rows is taken to have the mean, and an M tile more in half
+// the cases.  Costs in us per K block, measured at N, K of 1024 to 8192, 1 to
+// 64 experts, 1 to 4096 rows each: a 256-row tile a CU takes 1.35 while few
+// of them run and 2.1 when all CUs load; two 64-row tiles 0.5 and 0.84.
+// E.g. 8 experts, N = K = 4096: 128 rows each 40.6 us on 64-row tiles, 49.9 on
+// 256; 1024 rows 211 and 168.  k_fp8_few pays where the 64-row tiles are too
+// few for the CUs: its cost goes with the bytes its waves read, 16 weight rows
+// and the tile's activation rows, and 20,000 of these rows are where the two
+// meet (1 expert, N = K = 4096, 32 rows: 14.6 us and 17.5; 64 rows: 22.8 and
+// 18.0).
+enum class Pick { few, mid, large };
+Pick pick(const Fp8Args& p, int64_t routes, int cus) {
+  const double live = (double)(routes < p.E ? routes : p.E), avg = (double)routes / live, fill = cus / 256.0;
+  auto mtiles = [&](int tm) { return live * (avg / tm + 0.5 > 1.0 ? avg / tm + 0.5 : 1.0); };
+  const double few = mtiles(FEW_ROWS) * (p.N / 16) * (16.0 + (avg < 16.0 ? avg : 16.0));
+  if (few <= 20000.0 * fill) return Pick::few;
+  const double mid = 0.84 * mtiles(GM::TM) * ((p.N + GM::TN - 1) / GM::TN) / (2 * cus);
+  const double large = 2.1 * mtiles(GL::TM) * ((p.N + GL::TN - 1) / GL::TN) / cus;
+  return (mid > 0.5 ? mid : 0.5) <= (large > 1.35 ? large : 1.35) ? Pick::mid : Pick::large;
 }
 
+// Workgroups for at most `tiles` tiles: every kernel here walks on by its grid
+// until the pool's tiles are done, so the grid is a matter of speed alone: as
+// many as are resident, in whole rounds over the XCDs.
+unsigned grid_of(int64_t tiles, int64_t most) { return (unsigned)(((tiles < most ? tiles : most) + 7) / 8 * 8); }
+
 template <class G>
-hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, int per_cu, hipStream_t st) {
+hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, int resident, hipStream_t st) {
   static PerDeviceOnce once;
-  hipError_t e = once.run([] {
+  const hipError_t e = once.run([] {
     AttrInit ai;
     ai.lds((const void*)k_fp8_tile<G>, G::lds(MAX_DIM, MAX_E));
     return ai.err;
   });
-  unsigned grid = 0;
-  if (e == hipSuccess) e = grid_of(mtiles * ((p.N + G::TN - 1) / G::TN), per_cu, grid);
   if (e != hipSuccess) return e;
+  const unsigned grid = grid_of(mtiles * ((p.N + G::TN - 1) / G::TN), resident);
   MOE_LAUNCH_AS("k_fp8_tile", k_fp8_tile<G>, dim3(grid), dim3(G::NT), G::lds(p.K, p.E), st, p);
   return hipGetLastError();
 }
 
-hipError_t launch_few(const Fp8Args& p, int64_t mtiles, hipStream_t st) {
-  unsigned grid = 0;
-  const hipError_t e = grid_of(mtiles * (p.N / 16), 8, grid);
-  if (e != hipSuccess) return e;
+hipError_t launch_few(const Fp8Args& p, int64_t mtiles, int resident, hipStream_t st) {
+  const unsigned grid = grid_of(mtiles * (p.N / 16), resident);
   MOE_LAUNCH(k_fp8_few, dim3(grid), dim3(64), 0, st, p);
   return hipGetLastError();
 }
@@ -745,14 +753,16 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
   const int64_t routes = cap >= E * bm ? cap - E * (bm - 1) : (cap + bm - 1) / bm;
   const int64_t live = routes < E ? routes : E;  // experts with rows, at most
   auto tiles = [&](int tm) { return routes / tm + live; };
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return MOE_ERR_HIP;
   const hipStream_t s = (hipStream_t)stream;
-  hipError_t e;
-  if (routes <= FEW_AVG * live)
-    e = launch_few(p, tiles(FEW_ROWS), s);
-  else if (routes <= MID_AVG * live)
-    e = launch_tile<GM>(p, tiles(GM::TM), 2, s);
-  else
-    e = launch_tile<GL>(p, tiles(GL::TM), 1, s);
+  switch (pick(p, routes, cus)) {
+    case Pick::few: e = launch_few(p, tiles(FEW_ROWS), 8 * cus, s); break;
+    case Pick::mid: e = launch_tile<GM>(p, tiles(GM::TM), 2 * cus, s); break;
+    case Pick::large: e = launch_tile<GL>(p, tiles(GL::TM), cus, s); break;
+  }
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
