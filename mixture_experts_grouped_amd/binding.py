@@ -536,12 +536,17 @@ def _launch(what: str, fn, stream, tensors, *args) -> None:
         raise MoeLoraError(st, what)
 
 
-def _made(stream, *tensors: torch.Tensor) -> None:
-    """Outputs allocated for a call on a stream that is not the current one:
-    their memory is not handed out again before that stream is done."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in tensors:
-            t.record_stream(stream)
+def _made(stream, make, *shape, **kw) -> torch.Tensor:
+    """An output allocated for a call on `stream` (None: the current one): made
+    there, so that a fill is ordered before the call and the memory is not
+    handed out again too early, and used on the current stream afterwards."""
+    if stream is None:
+        return make(*shape, **kw)
+    s = stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream, kw["device"])
+    with torch.cuda.stream(s):
+        t = make(*shape, **kw)
+    t.record_stream(torch.cuda.current_stream(t.device))
+    return t
 
 
 _FLOAT_TYPES = {torch.float32: MOE_TYPE_F32, torch.bfloat16: MOE_TYPE_BF16}
@@ -738,17 +743,13 @@ def fp8_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optio
     if src.dim() != 2 or act not in _ACTS or (act is not None and src.shape[1] % 2):
         raise ValueError("src must be [rows, K], or [rows, 2K] with act 'swiglu' or 'geglu'")
     rows, K = src.shape[0], src.shape[1] if act is None else src.shape[1] // 2
-    made = []
     if codes is None:
-        codes = torch.empty(rows, K, dtype=_E4M3, device=src.device)
-        made.append(codes)
+        codes = _made(stream, torch.empty, rows, K, dtype=_E4M3, device=src.device)
     if scales is None:
-        scales = torch.empty(rows, K // 128, dtype=torch.float32, device=src.device)
-        made.append(scales)
+        scales = _made(stream, torch.empty, rows, K // 128, dtype=torch.float32, device=src.device)
     _launch("moe_fp8_quantize_rows", library().moe_fp8_quantize_rows, stream, (src, codes, scales),
             _ptr(src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], _ptr(codes, _E4M3, (rows, K), "codes"),
             _ptr(scales, torch.float32, (rows, K // 128), "scales"))
-    _made(stream, *made)
     return codes, scales
 
 
@@ -759,14 +760,12 @@ def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) 
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     E, N, K = W.shape
-    out = [torch.empty(E, N, K, dtype=_E4M3, device=W.device),
-           torch.empty(E, N // 128, K // 128, dtype=torch.float32, device=W.device)]
-    if transposed:
-        out += [torch.empty(E, K, N, dtype=_E4M3, device=W.device),
-                torch.empty(E, K // 128, N // 128, dtype=torch.float32, device=W.device)]
+    def pair(n, k):
+        return [_made(stream, torch.empty, E, n, k, dtype=_E4M3, device=W.device),
+                _made(stream, torch.empty, E, n // 128, k // 128, dtype=torch.float32, device=W.device)]
+    out = pair(N, K) + (pair(K, N) if transposed else [])
     _launch("moe_fp8_quantize_weight", library().moe_fp8_quantize_weight, stream, (W,),
             _ptr(W, torch.bfloat16, None, "W"), E, N, K, *[t.data_ptr() for t in out], *([] if transposed else [None, None]))
-    _made(stream, *out)
     return tuple(out)
 
 
@@ -785,9 +784,8 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
     rows, K = a.shape
     E, N = w.shape[:2]
     cap = pool["row_to_route"].numel()
-    made = out is None
-    if made:
-        out = torch.zeros(cap, N, dtype=torch.bfloat16, device=a.device)
+    if out is None:
+        out = _made(stream, torch.zeros, cap, N, dtype=torch.bfloat16, device=a.device)
     i32, f32 = torch.int32, torch.float32
     ps = MoePool(_ptr(pool["counts"], i32, (E,), "counts"), _ptr(pool["offsets"], i32, (E + 1,), "offsets"), None,
                  _ptr(pool["row_to_route"], i32, None, "row_to_route"), cap, block_m)
@@ -797,8 +795,6 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
             ctypes.byref(d), ctypes.byref(ps), _ptr(a, _E4M3, None, "a"), _ptr(a_scales, f32, (rows, K // 128), "a_scales"),
             _ptr(w, _E4M3, (E, N, K), "w"), _ptr(w_scales, f32, (E, N // 128, K // 128), "w_scales"),
             _ptr(out, torch.bfloat16, (cap, N), "out"))
-    if made:
-        _made(stream, out)
     return out
 
 

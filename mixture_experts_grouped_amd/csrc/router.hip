@@ -424,7 +424,7 @@ moe_status check_router(const moe_router_desc* d, const moe_adapters* ad, Router
   if (d->renorm != 0 && d->renorm != 1) return MOE_ERR_INVALID;
   if (d->E > 512 || d->topk > 16) return MOE_ERR_UNSUPPORTED;
   if (d->logits_type != MOE_TYPE_F32 && d->logits_type != MOE_TYPE_BF16) return MOE_ERR_UNSUPPORTED;
-  if ((int64_t)d->T * d->E >= (int64_t)1 << 31 || (int64_t)d->T * d->topk >= (int64_t)1 << 31)
+  if (d->T > 1 << 30 || (int64_t)d->T * d->E >= (int64_t)1 << 31 || (int64_t)d->T * d->topk >= (int64_t)1 << 31)
     return MOE_ERR_UNSUPPORTED;
   a = RouterArgs{};
   a.T = d->T;

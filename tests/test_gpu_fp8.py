@@ -61,7 +61,7 @@ def test_gated_rows(rows, K, act):
     # e4m3's half step, half its smallest step at the bottom, the activation's
     # own error (sigmoid: 2^-20 relative; the normal distribution function: 1e-6
     # of the gate)
-    tol = 2.0 ** -4 * np.abs(h) * (1 + 1e-5) + np.repeat(f64(s), 128, 1) * 2.0 ** -10 + 1e-6 * np.abs(x[:, :K].double() * up).numpy()
+    tol = 2.0 ** -4 * np.abs(h) * (1 + 1e-5) + np.repeat(f64(s), 128, 1) * 2.0 ** -10 + 1e-6 * (x[:, :K].double() * up).abs().numpy()
     assert np.all(np.abs(back - h) <= tol)
     amax = np.abs(h).reshape(rows, -1, 128).max(2) / 448
     assert np.all(np.abs(f64(s) - amax) <= 2.0 ** -18 * amax + 1e-8)
@@ -136,12 +136,8 @@ def check(idx, E, N, K, gather, seed=0):
         if rows.size == 0:
             continue
         src = r2r[rows] // k if gather else rows
-        ref, mag = O8.product(codes(a)[src], f64(sa)[src], codes(w[e]), f64(sw[e]))
-        # products of codes are exact in fp32, a block's 128 terms and the
-        # blocks' scaled sum are added in fp32: (128 + K / 128 + 3) roundings of
-        # at most the magnitudes' sum, then the output's half step
-        tol = (131 + K / 128) * 2.0 ** -24 * mag
-        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        ref, tol = O8.product(codes(a)[src], f64(sa)[src], codes(w[e]), f64(sw[e]))
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)  # the output's half step
         assert np.all(np.abs(got[rows] - ref) <= tol), (e, np.max(np.abs(got[rows] - ref) / tol))
     return pool
 
@@ -156,17 +152,40 @@ def routing(T, E, k, seed, drop=0.0, only=None):
     return idx.to(torch.int32)
 
 
+class Kernel:
+    """Which product kernel a call takes, from the library's own trace."""
+
+    def __enter__(self):
+        B.moe_lora_trace_reset()
+        B.moe_lora_trace_enable(True)
+        return self
+
+    def __exit__(self, *exc):
+        B.moe_lora_trace_enable(False)
+        names = {n for n in B.moe_lora_trace_collect() if n in ("k_fp8_few", "k_fp8_tile64", "k_fp8_tile256")}
+        self.names = names
+        B.moe_lora_trace_reset()
+
+
 @pytest.mark.parametrize("gather", [True, False])
-@pytest.mark.parametrize("T,E,k,N,K", [
-    (1, 1, 1, 128, 128),       # one row, one tile, one block
-    (1, 64, 6, 256, 512),      # a decoded token
-    (5, 8, 2, 384, 128),       # N not a multiple of a tile's columns
-    (40, 3, 2, 128, 1024),
-    (200, 4, 2, 512, 640),     # odd numbers of K blocks
-    (700, 2, 1, 256, 256),     # several full tiles of rows
+@pytest.mark.parametrize("T,E,k,N,K,kernel", [
+    (1, 1, 1, 128, 128, "k_fp8_few"),          # one row, one tile, one block
+    (1, 64, 6, 256, 512, "k_fp8_few"),         # a decoded token
+    (5, 8, 2, 384, 128, "k_fp8_few"),
+    (40, 3, 2, 128, 1024, "k_fp8_few"),
+    (33, 100, 2, 1024, 384, "k_fp8_tile64"),
+    (200, 4, 2, 1408, 128, "k_fp8_tile64"),    # fewer K blocks than stages
+    (300, 3, 2, 2176, 256, "k_fp8_tile64"),
+    (700, 2, 1, 1152, 640, "k_fp8_tile64"),    # odd numbers of K blocks
+    (4200, 1, 1, 4224, 128, "k_fp8_tile256"),  # N not a multiple of a tile's columns, one K block
+    (4000, 3, 1, 4224, 256, "k_fp8_tile256"),
+    (3000, 20, 2, 3968, 384, "k_fp8_tile256"),
+    (4096, 1, 1, 4096, 640, "k_fp8_tile256"),
 ])
-def test_product(T, E, k, N, K, gather):
-    check(routing(T, E, k, T + N), E, N, K, gather, seed=T)
+def test_product(T, E, k, N, K, kernel, gather):
+    with Kernel() as ran:
+        check(routing(T, E, k, T + N), E, N, K, gather, seed=T)
+    assert ran.names == {kernel}
 
 
 @pytest.mark.parametrize("gather", [True, False])
@@ -183,6 +202,20 @@ def test_product_of_no_routes():
     assert int(pool["counts"].sum()) == 0
 
 
+def test_small_products_beside_large_ones():
+    """256 * 256 and its negative cancel; what is left of a third product: all
+    of it down to 2^-13 of them in the same 8 columns, to 2^-23 elsewhere."""
+    idx = torch.zeros(4, 1, dtype=torch.int32)
+    pool = build(idx, 1)
+    one = torch.ones(4, 1, device="cuda"), torch.ones(1, 1, 1, device="cuda")
+    for k, small in ((2, 2.0 ** 3), (7, 1.5 * 2.0 ** 4), (8, 2.0 ** -7), (127, 2.0 ** -7), (64, 1.5 * 2.0 ** -6)):
+        a, w = torch.zeros(4, 128), torch.zeros(1, 128, 128)
+        a[:, 0], a[:, 1], w[0, :, 0], w[0, :, 1], w[0, :, k] = 256, -256, 256, 256, 1
+        a[0, k], a[1, k] = small, -small
+        out = M.fp8_product(pool, a.to(F8).cuda(), one[0], w.to(F8).cuda(), one[1], topk=1)
+        assert (out[0] == small).all() and (out[1] == -small).all() and not out[2:4].any(), (k, small)
+
+
 def test_data_gradient_is_the_product_with_the_transpose():
     E, N, K = 3, 256, 384
     idx = routing(50, E, 2, 8)
@@ -196,8 +229,7 @@ def test_data_gradient_is_the_product_with_the_transpose():
     for e in range(E):
         rows = slice(off[e], off[e] + cnt[e])
         wt = codes(c[e]).T.copy()
-        ref, mag = O8.product(codes(dy)[rows], f64(sdy)[rows], wt, f64(s[e]).T)
-        tol = (131 + N / 128) * 2.0 ** -24 * mag
+        ref, tol = O8.product(codes(dy)[rows], f64(sdy)[rows], wt, f64(s[e]).T)
         assert np.all(np.abs(dx[rows] - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol))
 
 
@@ -218,14 +250,44 @@ def test_nonfinite_rows_stay_in_their_rows():
 
 
 def test_one_row_alone_equals_the_row_in_a_batch():
-    """A row's sums do not depend on how many rows its expert has."""
-    E, N, K = 2, 256, 512
-    a, sa, w, sw = operands(600, E, N, K, 11)
-    idx = torch.zeros(600, 1, dtype=torch.int32)
-    big = M.fp8_product(build(idx, E), a, sa, w, sw, topk=1)
-    for t in (0, 255, 256, 599):
-        one = M.fp8_product(build(idx[:1], E), a[t:t + 1], sa[t:t + 1], w, sw, topk=1)
-        assert torch.equal(one[0], big[t])
+    """A row's sums depend neither on the other rows nor on the kernel."""
+    E, N, K = 1, 4096, 640
+    a, sa, w, sw = operands(4300, E, N, K, 11)
+    idx = torch.zeros(4300, 1, dtype=torch.int32)
+    outs, ran = {}, set()
+    for n in (1, 100, 700, 4300):
+        with Kernel() as kern:
+            outs[n] = M.fp8_product(build(idx[:n], E), a[:n].contiguous(), sa[:n].contiguous(), w, sw, topk=1)[:n]
+        ran |= kern.names
+    assert ran == {"k_fp8_few", "k_fp8_tile64", "k_fp8_tile256"}
+    for n in (1, 100, 700):
+        assert torch.equal(outs[n], outs[4300][:n])
+    for t in (255, 256, 4299):
+        one = M.fp8_product(build(idx[:1], E), a[t:t + 1].contiguous(), sa[t:t + 1].contiguous(), w, sw, topk=1)
+        assert torch.equal(one[0], outs[4300][t])
+
+
+@pytest.mark.parametrize("T,N", [(40, 256), (600, 2176), (4200, 4096)])
+def test_rows_past_the_activations_and_the_pool(T, N):
+    """Routes of tokens past a's rows read zeros; a pool whose arrays claim more
+    rows than its capacity writes none past it."""
+    E, K = 2, 256
+    idx = routing(T, E, 1, 5)
+    pool = build(idx, E)
+    a, sa, w, sw = operands(T, E, N, K, 3)
+    full = M.fp8_product(pool, a, sa, w, sw, topk=1)
+    few = T - 7
+    part = M.fp8_product(pool, a[:few].contiguous(), sa[:few].contiguous(), w, sw, topk=1)
+    tok = pool["row_to_route"].long()
+    assert torch.equal(part[(tok >= 0) & (tok < few)], full[(tok >= 0) & (tok < few)])
+    assert not part[tok >= few].any()
+    cap = pool["row_to_route"].numel()
+    broken = dict(pool, counts=pool["counts"] + torch.tensor([0, 1000], dtype=torch.int32, device="cuda"))
+    room = torch.full((cap + 2000, N), -7.0, dtype=BF, device="cuda")
+    M.fp8_product(broken, a, sa, w, sw, topk=1, out=room[:cap])
+    assert (room[cap:] == -7.0).all()
+    live = tok >= 0
+    assert torch.equal(room[:cap][live], full[live])
 
 
 def test_streams_and_graphs():
@@ -242,8 +304,10 @@ def test_streams_and_graphs():
     with torch.cuda.stream(s):
         out = torch.zeros_like(want)
     M.fp8_product(pool, a2, sa2, w, sw, topk=2, out=out, stream=s)
+    made = M.fp8_product(pool, a2, sa2, w, sw, topk=2, stream=s)  # zeroed on the call's stream
+    raw = M.fp8_product(pool, a2, sa2, w, sw, topk=2, stream=s.cuda_stream)
     torch.cuda.current_stream().wait_stream(s)
-    assert torch.equal(out, want)
+    assert torch.equal(out, want) and torch.equal(made, want) and torch.equal(raw, want)
     got = torch.zeros_like(want)
     torch.cuda.synchronize()
     g = torch.cuda.CUDAGraph()

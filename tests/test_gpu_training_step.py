@@ -134,11 +134,10 @@ def test_frozen_pass_in_8_bits():
     for t in range(T):
         for j in range(k):
             e, r = int(idx[t, j]), int(rows[t, j])
-            up, mag = O8.product(c(a)[t:t + 1], d(sa)[t:t + 1], c(q13[e]), d(s13[e]))
-            tol = (131 + H / 128) * 2.0 ** -24 * mag
+            up, tol = O8.product(c(a)[t:t + 1], d(sa)[t:t + 1], c(q13[e]), d(s13[e]))
             assert np.all(np.abs(d(gu)[r] - up[0]) <= tol + 2.0 ** -8 * (np.abs(up) + tol))
-            v, mag = O8.product(c(h)[r:r + 1], d(sh)[r:r + 1], c(q2[e]), d(s2[e]))
+            v, tol = O8.product(c(h)[r:r + 1], d(sh)[r:r + 1], c(q2[e]), d(s2[e]))
             wt = float(w[t, j])
             ref[t] += wt * v[0]
-            bound[t] += wt * ((131 + Id / 128) * 2.0 ** -24 * mag[0] * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(v[0]))
+            bound[t] += wt * (tol[0] * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(v[0]))
     assert np.all(np.abs(out - ref) <= bound * (1 + 1e-5))

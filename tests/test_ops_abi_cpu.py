@@ -34,6 +34,13 @@ def test_router_desc(field, value, status):
     assert e.value.status == status
 
 
+def test_router_longest_batch():
+    assert B.moe_router_workspace_size(B.make_router_desc(1 << 30, 1, 1)) > 0
+    with pytest.raises(B.MoeLoraError) as e:
+        B.moe_router_workspace_size(B.make_router_desc((1 << 30) + 1, 1, 1))
+    assert e.value.status == UNS
+
+
 def test_router_topk_beyond_sixteen():
     with pytest.raises(B.MoeLoraError) as e:
         B.moe_router_workspace_size(B.make_router_desc(4, 64, 17))
