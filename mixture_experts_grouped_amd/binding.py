@@ -521,7 +521,7 @@ def _launch(what: str, fn, stream, tensors, *args) -> None:
     (made the current one for the call if it is not); stream None: that
     device's current one."""
     dev = tensors[0].get_device()
-    for t in tensors:
+    for t in tensors[1:]:
         if t is not None and t.get_device() != dev:
             raise ValueError(f"{what}: tensors on {tensors[0].device} and {t.device}: one call runs on one device")
     if dev < 0:
@@ -649,7 +649,8 @@ class MoeAdamW:
     """AdamW over a list of tensors (the factors of one or more layers) in one
     call per step.  params: bf16 or fp32, all of one type, updated in place;
     grads: bf16 or fp32 buffers of the same sizes that are read at each step
-    (MoeLoraLayer.grads, say); masters: fp32 copies of bf16 params that are
+    (MoeLoraLayer.grads, say; all these tensors stay where they are, the
+    optimiser keeps their addresses); masters: fp32 copies of bf16 params that are
     updated instead, the params getting their rounding.  state_bits 32 or 8
     (see include/moelora.h); states: {"m": [...], "v": [...], "m_scale":
     [...], "v_scale": [...]} to go on from, else zeros."""
@@ -667,6 +668,7 @@ class MoeAdamW:
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits = state_bits
         self.steps = 0  # steps taken
+        self._same = None  # what the descriptor holds of betas, eps and weight_decay
         eight = state_bits == 8
         kinds = {"m": torch.float8_e4m3fn, "v": torch.float8_e5m2} if eight else dict.fromkeys("mv", torch.float32)
         runs = [-(-p.numel() // 128) for p in self.params]
@@ -710,11 +712,14 @@ class MoeAdamW:
         those values in device memory (adamw_control), for a captured step."""
         self.steps = self.steps + 1 if step is None else int(step)
         d = self._desc
+        same = (*self.betas, self.eps, self.weight_decay)
+        if same != self._same:  # fields that seldom change (setting one costs 60 ns)
+            d.beta1, d.beta2, d.eps, d.weight_decay = self._same = same
         d.lr = self.lr if lr is None else lr
-        d.beta1, d.beta2 = self.betas
-        d.eps, d.weight_decay, d.grad_scale = self.eps, self.weight_decay, grad_scale
+        d.grad_scale = grad_scale
         d.step = self.steps
-        d.seed = (self.steps if seed is None else seed) & 0xFFFFFFFF
+        if self.state_bits == 8:
+            d.seed = (self.steps if seed is None else seed) & 0xFFFFFFFF
         d.control = _ptr(control, torch.int32, (5,), "control")
         _launch("moe_adamw_step", library().moe_adamw_step, stream, (self.params[0], control), self._dp, self._table,
                 len(self._table))
