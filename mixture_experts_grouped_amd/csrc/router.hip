@@ -9,6 +9,14 @@
 // largest key k times; a key is the logit's bits mapped to an unsigned
 // integer of the same order, so the choice is exact and equals go to the
 // lowest expert.
+//
+// At 16,384 x 64 fp32 the logits are 4 MB, a microsecond of memory time, so
+// latency bounds all three kernels: k_route 6.6 us (each workgroup one round of
+// 64 tokens; four rounds of 16 took 9.7), k_route_sum 6.6 us (one workgroup
+// reads 131 KB of sums that other XCDs wrote; chunks of 128 tokens halve that
+// and cost k_route more: 14.0 us for the two against 12.8), k_route_bwd 5.6 us
+// (16 tokens a workgroup, so all loads of a wave are in flight at once; 8.6
+// with four rounds).  One token: k_route alone, 4.0 us.
 #include <cmath>
 
 #include "../../include/moelora.h"
@@ -74,17 +82,22 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
   return __uint_as_float(key ^ ((uint32_t)((int32_t)~key >> 31) | 0x80000000u));
 }
 
-// The logits of token t held by this lane (experts j + 16 i; -inf past E).
+// The logits of token t held by this lane (experts j + 16 i; -inf past E and
+// for a token that is not valid: its logits are loaded all the same, so that
+// they do not wait for the mask).  Returns whether the token is valid.
 template <bool BF, int V>
-__device__ __forceinline__ void load_logits(const RouterArgs& a, long t, int j, bool live, float (&l)[V]) {
+__device__ __forceinline__ bool load_logits(const RouterArgs& a, long t, int j, bool in, float (&l)[V]) {
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int e = j + 16 * i;
     l[i] = -INFINITY;
-    if (live && e < a.E)
+    if (in && e < a.E)
       l[i] = BF ? bf2f(((const uint16_t*)a.logits)[t * a.E + e]) : ((const float*)a.logits)[t * a.E + e];
-    l[i] += 0.0f;  // -0 to +0: equal logits have equal keys
   }
+  const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = on ? l[i] + 0.0f : -INFINITY;  // -0 to +0: equal logits have equal keys
+  return on;
 }
 
 // whether any of the row's 16 lanes holds `c`
@@ -118,9 +131,8 @@ __global__ __launch_bounds__(ONE ? ONE_THREADS : THREADS<V>) void k_route(Router
   for (int o = 0; o < nt; o += ROWS) {
     const long t = (long)t0 + o + row;
     const bool in = o + row < nt;
-    const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
     float l[V];
-    load_logits<BF, V>(a, t, j, on, l);
+    load_logits<BF, V>(a, t, j, in, l);
     bool strange = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) strange |= !(l[i] < INFINITY);
@@ -298,33 +310,35 @@ __global__ __launch_bounds__(BWD_THREADS) void k_route_bwd(RouterArgs a) {
   int t0, nt, root;
   if (!chunk_of(a, blockIdx.x, a.chunk, t0, nt, root)) return;
   const int tid = threadIdx.x, j = tid & 15, row = tid >> 4;
-  float u[V];
-  {
-    const float n = (float)max(a.active[root], 1);
-    const float c = a.gloss != nullptr ? a.gloss[root] * (float)a.E / ((float)a.k * n * n) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = j + 16 * i;
-      u[i] = (a.gloss != nullptr && e < a.E) ? c * (float)a.counts[(long)root * a.E + e] : 0.0f;
-    }
-  }
   float* mine = place[row];
+  float u[V], c = 0.0f;
+  if (a.gloss != nullptr) {
+    const float n = (float)max(a.active[root], 1);
+    c = a.gloss[root] * (float)a.E / ((float)a.k * n * n);
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = j + 16 * i;
+    u[i] = (a.gloss != nullptr && e < a.E) ? c * (float)a.counts[(long)root * a.E + e] : 0.0f;
+  }
   for (int o = 0; o < nt; o += ROWS) {
     const long t = (long)t0 + o + row;
     const bool in = o + row < nt;
-    const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
-    float l[V];
-    load_logits<BF, V>(a, t, j, on, l);
     int idx = -1;
     float g = 0.0f, lsel = 0.0f;
-    if (on && j < a.k && a.gw != nullptr) {
+    if (in && j < a.k && a.gw != nullptr) {
       idx = a.idx[t * a.k + j];
-      if (idx < 0 || idx >= a.E) idx = -1;
-      if (idx >= 0) {
-        g = a.gw[t * a.k + j];
-        lsel = BF ? bf2f(((const uint16_t*)a.logits)[t * a.E + idx]) : ((const float*)a.logits)[t * a.E + idx];
-      }
+      g = a.gw[t * a.k + j];
     }
+    float l[V];
+    const bool on = load_logits<BF, V>(a, t, j, in, l);
+    if (!on || idx < 0 || idx >= a.E) idx = -1;
+    // the chosen logits, through the token's row of LDS
+#pragma unroll
+    for (int i = 0; i < V; ++i) mine[j + 16 * i] = l[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    if (idx >= 0) lsel = mine[idx];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     bool strange = false;
     uint32_t top = 0;
 #pragma unroll
@@ -387,8 +401,9 @@ int chunks_of(const RouterArgs& a) {
   return n;
 }
 
-// Few tokens: one launch.  (Beyond one round of the workgroup the second
-// launch costs less than the further rounds.)
+// Few tokens: one launch, 4.0 us at one token (two: 3.7 and 2.9).  Beyond one
+// round of its workgroup a round costs about 1.5 us and the sums lose their
+// parallel chunks.
 bool one_launch(const RouterArgs& a) { return a.na == 1 && a.T <= ONE_TOKENS; }
 
 // experts a lane holds: the smallest of 4, 8, 16, 32 that covers E
