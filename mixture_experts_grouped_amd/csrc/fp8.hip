@@ -351,8 +351,12 @@ struct Frag8 {
 // barrier instead of spread over the fragments: 1.77 ms; a stage's fragments
 // read at its start, each product's result added at once: 2.41.  Touching
 // the lines of later stages for L2 cost 0.2 ms: the loads are bound by
-// throughput, not by misses.  The 64-row tile, 689 tokens x 6 with a fifth of
-// the routes dropped, 4096 x 2048: 116 us, 4.9 TB/s of weights.
+// throughput, not by misses.  Rows over an expert's last whole tile as
+// 64-row tiles in a launch of their own: no gain, on ragged experts a loss of
+// up to 17 %; waves without rows only loading: 2 % slower.  The 64-row tile, 689 tokens x 6 with a fifth of
+// the routes dropped, 4096 x 2048: 116 us, 4.9 TB/s of weights; with six
+// buffers instead of three, one workgroup a CU: no faster, 0.5 us a K block,
+// which is the chain of barrier, fragment reads and products.
 //
 // Loads past a tile's K (K / 128 < NBUF) or past the last tile go to offsets
 // outside every descriptor: zeros, no traffic, and the loop waits by constant

@@ -162,25 +162,25 @@ class Kernel:
 
     def __exit__(self, *exc):
         B.moe_lora_trace_enable(False)
-        names = {n for n in B.moe_lora_trace_collect() if n in ("k_fp8_few", "k_fp8_tile64", "k_fp8_tile256")}
-        self.names = names
+        self.names = {n[6:] for n in B.moe_lora_trace_collect() if n.startswith(("k_fp8_few", "k_fp8_tile"))}
         B.moe_lora_trace_reset()
 
 
 @pytest.mark.parametrize("gather", [True, False])
 @pytest.mark.parametrize("T,E,k,N,K,kernel", [
-    (1, 1, 1, 128, 128, "k_fp8_few"),          # one row, one tile, one block
-    (1, 64, 6, 256, 512, "k_fp8_few"),         # a decoded token
-    (5, 8, 2, 384, 128, "k_fp8_few"),
-    (40, 3, 2, 128, 1024, "k_fp8_few"),
-    (33, 100, 2, 1024, 384, "k_fp8_tile64"),
-    (200, 4, 2, 1408, 128, "k_fp8_tile64"),    # fewer K blocks than stages
-    (300, 3, 2, 2176, 256, "k_fp8_tile64"),
-    (700, 2, 1, 1152, 640, "k_fp8_tile64"),    # odd numbers of K blocks
-    (4200, 1, 1, 4224, 128, "k_fp8_tile256"),  # N not a multiple of a tile's columns, one K block
-    (4000, 3, 1, 4224, 256, "k_fp8_tile256"),
-    (3000, 20, 2, 3968, 384, "k_fp8_tile256"),
-    (4096, 1, 1, 4096, 640, "k_fp8_tile256"),
+    (1, 1, 1, 128, 128, "few"),          # one row, one tile, one block
+    (1, 64, 6, 256, 512, "few"),         # a decoded token
+    (5, 8, 2, 384, 128, "few"),
+    (40, 3, 2, 128, 1024, "few"),
+    (33, 100, 2, 1024, 384, "tile64"),
+    (200, 4, 2, 1408, 128, "tile64"),    # fewer K blocks than stages
+    (300, 3, 2, 2176, 256, "tile64"),
+    (700, 2, 1, 1152, 640, "tile64"),    # odd numbers of K blocks
+    (200, 4, 2, 1408, 896, "tile64"),
+    (4200, 1, 1, 4224, 128, "tile256"),  # N not a multiple of a tile's columns, one K block
+    (4000, 3, 1, 4224, 256, "tile256"),
+    (3000, 20, 2, 3968, 384, "tile256"),
+    (4096, 1, 1, 4096, 640, "tile256"),
 ])
 def test_product(T, E, k, N, K, kernel, gather):
     with Kernel() as ran:
@@ -195,6 +195,17 @@ def test_product_of_uneven_experts(gather):
     idx = routing(300, E, 3, 2, drop=0.3, only=[0, 0, 0, 0, 7, 63, 64, 64, 98])
     idx[0, 0] = 99
     check(idx, E, 384, 256, gather)
+
+
+def test_product_of_tails():
+    """256-row tiles, the last of an expert with 0, 1, 64, 65, 128, 129 and 255 rows,
+    experts below one tile, and one without rows."""
+    counts = [768, 513, 576, 1089, 640, 641, 511, 1, 130, 100, 0, 1500]
+    idx = torch.repeat_interleave(torch.arange(len(counts)), torch.tensor(counts)).to(torch.int32)
+    idx = idx[torch.randperm(idx.numel(), generator=torch.Generator().manual_seed(1))][:, None].contiguous()
+    with Kernel() as ran:
+        check(idx, len(counts), 4096, 256, True)
+    assert ran.names == {"tile256"}
 
 
 def test_product_of_no_routes():
@@ -251,16 +262,16 @@ def test_nonfinite_rows_stay_in_their_rows():
 
 def test_one_row_alone_equals_the_row_in_a_batch():
     """A row's sums depend neither on the other rows nor on the kernel."""
-    E, N, K = 1, 4096, 640
+    E, N, K = 1, 4096, 896
     a, sa, w, sw = operands(4300, E, N, K, 11)
     idx = torch.zeros(4300, 1, dtype=torch.int32)
     outs, ran = {}, set()
-    for n in (1, 100, 700, 4300):
+    for n in (1, 100, 700, 4200, 4300):
         with Kernel() as kern:
             outs[n] = M.fp8_product(build(idx[:n], E), a[:n].contiguous(), sa[:n].contiguous(), w, sw, topk=1)[:n]
         ran |= kern.names
-    assert ran == {"k_fp8_few", "k_fp8_tile64", "k_fp8_tile256"}
-    for n in (1, 100, 700):
+    assert ran == {"few", "tile64", "tile256"}
+    for n in (1, 100, 700, 4200):
         assert torch.equal(outs[n], outs[4300][:n])
     for t in (255, 256, 4299):
         one = M.fp8_product(build(idx[:1], E), a[t:t + 1].contiguous(), sa[t:t + 1].contiguous(), w, sw, topk=1)
