@@ -410,7 +410,7 @@ moe_status moe_router_forward(const moe_router_desc* desc, const moe_adapters* a
                               size_t workspace_bytes, void* stream);
 
 /* topk_idx, counts and active as moe_router_forward wrote them for the same
- * logits and valid; grad_topk_w [T, topk] fp32 or NULL, grad_loss [roots]
+ * logits and valid; grad_topk_w [T, topk] fp32 or NULL (not used where the id is -1), grad_loss [roots]
  * fp32 or NULL; grad_logits [T, E] of the logits' type (overwritten; may be
  * the logits' own buffer). */
 moe_status moe_router_backward(const moe_router_desc* desc, const moe_adapters* adapters, const void* logits,
@@ -454,7 +454,7 @@ typedef struct moe_adamw_tensor {
   void* v;           /* [n] fp32, or e5m2 codes */
   float* m_scale;    /* [ceil(n / 128)] with state_bits 8, else NULL */
   float* v_scale;
-  int64_t n;         /* >= 0; 0: skipped, pointers not looked at */
+  int64_t n;         /* 0 to 2^34 (more: MOE_ERR_UNSUPPORTED); 0: skipped, pointers not looked at */
 } moe_adamw_tensor;
 
 /* What changes from step to step, in device memory: for steps captured into
@@ -506,7 +506,7 @@ moe_status moe_adamw_step(const moe_adamw_desc* desc, const moe_adamw_tensor* te
  *   act MOE_ACT_SWIGLU / MOE_ACT_GEGLU: src [rows, 2K] bf16 = [gate | up],
  *     x = act(gate) * up in fp32.
  *   codes [rows, K] bytes, scales [rows, K / 128] fp32.  K % 128 == 0 (else
- *   MOE_ERR_UNSUPPORTED), rows >= 0 (0: nothing is done). */
+ *   MOE_ERR_UNSUPPORTED), K at most 65536, rows * K < 2^35, rows >= 0 (0: nothing is done). */
 moe_status moe_fp8_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes, float* scales,
                                  void* stream);
 

@@ -702,6 +702,15 @@ class MoeAdamW:
                 _ptr(p, ptype, None, "params"), None if masters is None else _ptr(masters[i], f32, None, "masters"),
                 _ptr(self.grads[i], gtype, None, "grads"), _ptr(self.states["m"][i], kinds["m"], None, "m"),
                 _ptr(self.states["v"][i], kinds["v"], None, "v"), *sc, n)
+        # memory that a step writes belongs to one tensor alone
+        spans = [(t.data_ptr(), t.numel() * t.element_size(), k) for k, ts in
+                 (("params", self.params), ("grads", self.grads), ("masters", self.masters or []), *self.states.items())
+                 for t in ts if t.numel()]
+        end, end_written = 0, 0
+        for at, size, k in sorted(spans):
+            if at < (end_written if k == "grads" else end):
+                raise ValueError(f"{k} overlap another tensor of the optimiser")
+            end, end_written = max(end, at + size), end_written if k == "grads" else max(end_written, at + size)
 
     def step(self, lr: Optional[float] = None, step: Optional[int] = None, grad_scale: float = 1.0,
              seed: Optional[int] = None, control: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -710,19 +719,20 @@ class MoeAdamW:
         the gradients (a clip coefficient, an accumulation's share); seed of
         the 8-bit states' rounding (default: the step's number).  control:
         those values in device memory (adamw_control), for a captured step."""
-        self.steps = self.steps + 1 if step is None else int(step)
+        number = self.steps + 1 if step is None else int(step)
         d = self._desc
         same = (*self.betas, self.eps, self.weight_decay)
         if same != self._same:  # fields that seldom change (setting one costs 60 ns)
             d.beta1, d.beta2, d.eps, d.weight_decay = self._same = same
         d.lr = self.lr if lr is None else lr
         d.grad_scale = grad_scale
-        d.step = self.steps
+        d.step = number
         if self.state_bits == 8:
-            d.seed = (self.steps if seed is None else seed) & 0xFFFFFFFF
+            d.seed = (number if seed is None else seed) & 0xFFFFFFFF
         d.control = _ptr(control, torch.int32, (5,), "control")
         _launch("moe_adamw_step", library().moe_adamw_step, stream, (self.params[0], control), self._dp, self._table,
                 len(self._table))
+        self.steps = number  # only a step that was taken
 
     def write_control(self, control: torch.Tensor, lr: float, step: int, grad_scale: float = 1.0,
                       seed: Optional[int] = None) -> None:

@@ -26,6 +26,7 @@ namespace {
 constexpr int AW_THREADS = 256;
 constexpr int AW_CHUNK = AW_THREADS * 8;  // elements of a workgroup's chunk
 constexpr size_t AW_ARGS = 4096;          // bytes of kernel arguments
+constexpr int64_t AW_GRID = 1 << 23;      // chunks of a launch (it holds fewer than 2^32 threads)
 constexpr float E4M3_MAX = 448.0f, E5M2_MAX = 57344.0f;
 constexpr float TINY = 0x1p-100f;  // below it a run's moments count as zero (its reciprocal would overflow)
 
@@ -290,8 +291,8 @@ void launch_all(const AdamwHead& head, const moe_adamw_tensor* tensors, int coun
   for (int q = 0; q < count; ++q) {
     const moe_adamw_tensor& s = tensors[q];
     if (s.n == 0) continue;
-    const int64_t chunks = (s.n + AW_CHUNK - 1) / AW_CHUNK;  // at most 2^29
-    if (a.count == a.MAX || a.chunks + chunks > (int64_t)1 << 30) flush();
+    const int64_t chunks = (s.n + AW_CHUNK - 1) / AW_CHUNK;  // at most AW_GRID
+    if (a.count == a.MAX || a.chunks + chunks > AW_GRID) flush();
     AwTensor<MASTER, S8>& t = a.t[a.count++];
     t.param = s.param;
     t.grad = s.grad;
@@ -370,12 +371,12 @@ extern "C" moe_status moe_adamw_step(const moe_adamw_desc* d, const moe_adamw_te
   for (int q = 0; q < count; ++q) {
     if (tensors[q].n < 0) return MOE_ERR_INVALID;
     if (tensors[q].n == 0) continue;
+    if (tensors[q].n > AW_GRID * AW_CHUNK) return MOE_ERR_UNSUPPORTED;
     if (!any) master = tensors[q].master != nullptr;
     any = true;
     if (master && d->param_type != MOE_TYPE_BF16) return MOE_ERR_INVALID;
     const moe_status s = check_tensor(d, tensors[q], master);
     if (s != MOE_OK) return s;
-    if (tensors[q].n > ((int64_t)1 << 40)) return MOE_ERR_UNSUPPORTED;
   }
   if (!any) return MOE_OK;
   AdamwHead a{};

@@ -179,8 +179,12 @@ __device__ __forceinline__ int token_of(const Fp8Args& p, long r) {
 // group_tile: each XCD a contiguous range of (expert's M chunk, N tile, M
 // tile), so that workgroups of one XCD share a weight panel in its L2.
 constexpr int MAX_E = 512;
+// More tiles than a pool can have: the sums stop there, so that no counts make
+// them wrap.
+__device__ __forceinline__ int most_tiles(const Fp8Args& p, int TM) { return p.cap / TM + p.E; }
 __device__ __forceinline__ bool pool_tile(const Fp8Args& p, int TM, int b, int nn, int gm, int& e, int& m, int& nt) {
   const int lane = threadIdx.x & 63;
+  const int most = most_tiles(p, TM);
   int cnt[MAX_E / 64], end[MAX_E / 64], total = 0;
 #pragma unroll
   for (int q = 0; q < MAX_E / 64; ++q) {
@@ -190,9 +194,9 @@ __device__ __forceinline__ bool pool_tile(const Fp8Args& p, int TM, int b, int n
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const int y = __shfl_up(x, o, 64);
-        if (lane >= o) x += y;
+        if (lane >= o) x = min(x + y, most);
       }
-      end[q] = total + x;  // tiles up to and with this lane's expert
+      end[q] = min(total + x, most);  // tiles up to and with this lane's expert
       total = __builtin_amdgcn_readlane(end[q], 63);
     }
   }
@@ -255,6 +259,7 @@ __device__ __forceinline__ void fill_table(const Fp8Args& p, PoolTable& t, char*
   t.cnt = t.end + p.E;
   t.off = t.cnt + p.E;
   const int lane = threadIdx.x & 63;
+  const int most = most_tiles(p, TM);
   int before = 0;
   for (int e0 = 0; e0 < p.E; e0 += 64) {  // every wave walks all experts; wave 0 writes
     const int e = e0 + lane, c = e < p.E ? rows_of(p, e) : 0;
@@ -262,14 +267,15 @@ __device__ __forceinline__ void fill_table(const Fp8Args& p, PoolTable& t, char*
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
       const int y = __shfl_up(x, o, 64);
-      if (lane >= o) x += y;
+      if (lane >= o) x = min(x + y, most);
     }
+    x = min(before + x, most);
     if (threadIdx.x < 64 && e < p.E) {
-      t.end[e] = before + x;
+      t.end[e] = x;
       t.cnt[e] = c;
       t.off[e] = p.offsets[e];
     }
-    before += __shfl(x, 63, 64);
+    before = __shfl(x, 63, 64);
   }
   t.total = __builtin_amdgcn_readfirstlane(before);
   __syncthreads();
@@ -720,8 +726,8 @@ extern "C" {
 moe_status moe_fp8_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes, float* scales,
                                  void* stream) {
   if (rows < 0 || K < 1) return MOE_ERR_INVALID;
-  if (K % 128 != 0 || K > MAX_DIM || rows >= (int64_t)1 << 31 || rows * (K / 8) >= ((int64_t)1 << 31) * 256)
-    return MOE_ERR_UNSUPPORTED;
+  // a launch holds fewer than 2^32 threads, eight columns each
+  if (K % 128 != 0 || K > MAX_DIM || rows >= (int64_t)1 << 31 || rows * K >= (int64_t)1 << 35) return MOE_ERR_UNSUPPORTED;
   if (act != MOE_FP8_PLAIN && act != MOE_ACT_SWIGLU && act != MOE_ACT_GEGLU) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!aligned16(src) || !aligned16(codes) || !aligned(scales, 4)) return MOE_ERR_INVALID;

@@ -35,6 +35,7 @@ constexpr int THREADS = V <= 8 ? 1024 : V == 16 ? 512 : 256;
 constexpr int BWD_THREADS = 256;  // 16 tokens: nothing is summed over tokens there
 constexpr int RT_TOKENS = 64;     // tokens of one workgroup's chunk, times the multiple that keeps
 constexpr int RT_CHUNKS = 512;    // the chunks (whose sums one workgroup adds) to about this many
+constexpr int BWD_CHUNKS = 1 << 20;  // workgroups of the gradient (a launch holds fewer than 2^32 threads)
 constexpr uint32_t KEY_NINF = 0x007FFFFFu;  // the key of -inf: nothing at or below it is chosen
 
 struct RouterArgs {
@@ -363,6 +364,7 @@ __global__ __launch_bounds__(BWD_THREADS) void k_route_bwd(RouterArgs a) {
       s += p[i] * u[i];
     }
     if (!act) idx = -1;
+    if (idx < 0) g = 0.0f;  // whatever the buffer holds where there is no route
     float psel = idx >= 0 ? __expf(lsel - mx) : 0.0f;
     float term;
     if (a.renorm) {
@@ -546,6 +548,7 @@ moe_status moe_router_backward(const moe_router_desc* d, const moe_adapters* ad,
   a.gloss = grad_loss;
   a.glogits = grad_logits;
   a.chunk = BWD_THREADS / 16;
+  a.chunk *= (a.T + a.chunk * BWD_CHUNKS - 1) / (a.chunk * BWD_CHUNKS);
   by_shape<GoRouteBwd>(d->logits_type == MOE_TYPE_BF16, a.E, a, chunks_of(a), (hipStream_t)stream);
   return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

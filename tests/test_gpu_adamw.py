@@ -208,3 +208,18 @@ def test_goes_on_from_given_states_on_another_stream():
     c.step(step=2, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert all(torch.equal(x, y) for x, y in zip(ps, qs))
+
+
+def test_refused_steps_and_shared_memory():
+    ps, gs = tensors([100, 300], F32, F32, 21)
+    opt = M.MoeAdamW(ps, gs)
+    opt.step()
+    with pytest.raises(M.MoeLoraError):
+        opt.step(lr=-1.0)
+    assert opt.steps == 1  # a refused step is not counted
+    M.MoeAdamW(ps, [gs[1][:100], gs[1]])  # gradients are only read
+    p = torch.zeros(512, device="cuda")
+    for params, grads in (([ps[0], ps[0]], [gs[0], gs[0]]), ([p[:300], p[256:]], [gs[1], gs[0].repeat(3)[:256]]),
+                          ([p[:256], ps[0]], [p[256:], p[200:300]])):
+        with pytest.raises(ValueError):
+            M.MoeAdamW(params, grads)

@@ -299,6 +299,10 @@ def test_rows_past_the_activations_and_the_pool(T, N):
     assert (room[cap:] == -7.0).all()
     live = tok >= 0
     assert torch.equal(room[:cap][live], full[live])
+    # every expert claims every row: more tiles than a pool can have
+    M.fp8_product(dict(pool, counts=torch.full_like(pool["counts"], 2 ** 31 - 1), offsets=torch.zeros_like(pool["offsets"])),
+                  a, sa, w, sw, topk=1, out=room[:cap])
+    assert (room[cap:] == -7.0).all()
 
 
 def test_streams_and_graphs():

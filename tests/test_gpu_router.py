@@ -118,6 +118,36 @@ def test_router_rows_that_leave_nothing():
     assert not r.counts.any() and not r.loss.any()
 
 
+@pytest.mark.parametrize("renorm", [False, True])
+def test_router_gradient_where_there_is_no_route(renorm):
+    """The weights' gradient at ids of -1 is whatever its buffer holds."""
+    l, valid, gw, gl = make(60, 12, torch.float32, 14, cut=0.7, mask=0.2)
+    r = check(l, valid, 6, renorm, None, gw, gl)
+    none = r.topk_idx.cpu() < 0
+    assert none.any() and not none.all()
+    clean = gw[:, :6].contiguous()
+    ld, vd, gld = l.cuda(), valid.cuda(), gl[:1].cuda()
+    args = ld, r.topk_idx, r.counts, r.active
+    want = r.backward(*args, clean.masked_fill(none, 0).cuda(), gld, vd).clone()
+    for x in (np.nan, np.inf, -np.inf):
+        assert torch.equal(r.backward(*args, clean.masked_fill(none, x).cuda(), gld, vd), want)
+
+
+def test_router_gradient_of_more_tokens_than_workgroups():
+    """Past 2^24 tokens a workgroup takes several rounds.  One expert: p = w = 1,
+    so the gradient is exactly 0; NaN tokens too."""
+    T = (1 << 24) + 5
+    r = M.MoeRouter(T, 1, 1)
+    l = torch.zeros(T, 1, device="cuda")
+    l[::1000003] = float("nan")
+    idx, w, counts, active, loss = r.forward(l)
+    bad = len(range(0, T, 1000003))
+    assert int(counts) == int(active) == T - bad and r.dropped_tokens() == bad
+    r.grad_logits.fill_(float("nan"))
+    r.backward(l, idx, counts, active, torch.ones(T, 1, device="cuda"), torch.ones(1, device="cuda"))
+    assert not r.grad_logits.any()
+
+
 def test_router_gradient_in_place_and_repeatable():
     l, valid, gw, gl = make(500, 64, torch.float32, 3, mask=0.1)
     r = check(l, valid, 6, True, None, gw, gl)

@@ -128,6 +128,8 @@ def test_adamw_lists():
     assert adam(adam_desc(), adam_tensor(n=0, param=None, grad=None)) == B.MOE_OK  # an empty tensor is not looked at
     assert adam(adam_desc(), adam_tensor(master=8 * MB), adam_tensor()) == INV       # masters for all or none
     assert adam(adam_desc(), adam_tensor(), adam_tensor(grad=None)) == INV           # the second is checked too
+    assert adam(adam_desc(), adam_tensor(n=(1 << 34) + 1)) == UNS
+    assert adam(adam_desc(), adam_tensor(n=(1 << 62) + 1)) == UNS
 
 
 def test_fp8_rows():
@@ -136,6 +138,8 @@ def test_fp8_rows():
     assert f(MB, 4, 0, -1, 2 * MB, 3 * MB, None) == INV
     assert f(MB, 4, 192, -1, 2 * MB, 3 * MB, None) == UNS
     assert f(MB, 4, 65664, -1, 2 * MB, 3 * MB, None) == UNS
+    assert f(MB, 1 << 28, 128, -1, 2 * MB, 3 * MB, None) == UNS  # more threads than a launch holds
+    assert f(MB, 1 << 31, 128, -1, 2 * MB, 3 * MB, None) == UNS
     assert f(MB, 4, 128, 2, 2 * MB, 3 * MB, None) == UNS
     assert f(MB + 2, 4, 128, -1, 2 * MB, 3 * MB, None) == INV
     assert f(MB, 4, 128, -1, None, 3 * MB, None) == INV
