@@ -11,12 +11,12 @@
 // lowest expert.
 //
 // At 16,384 x 64 fp32 the logits are 4 MB, a microsecond of memory time, so
-// latency bounds all three kernels: k_route 6.6 us (each workgroup one round of
-// 64 tokens; four rounds of 16 took 9.7), k_route_sum 6.6 us (one workgroup
-// reads 131 KB of sums that other XCDs wrote; chunks of 128 tokens halve that
-// and cost k_route more: 14.0 us for the two against 12.8), k_route_bwd 5.6 us
-// (16 tokens a workgroup, so all loads of a wave are in flight at once; 8.6
-// with four rounds).  One token: k_route alone, 4.0 us.
+// latency bounds all three kernels: k_route 6.3 us (each workgroup one round of
+// 64 tokens; four rounds of 16 took 9.7; the choice of six experts is about half
+// of it), k_route_sum 4.6 us (one workgroup reads 131 KB of sums that other XCDs
+// wrote, all loads in flight together; chunks of 128 tokens halve them and cost
+// k_route more: 1.2 us in sum), k_route_bwd 4.9 us (16 tokens a workgroup; 8.6
+// with four rounds).  One token: k_route alone, 3.7 us.
 #include <cmath>
 
 #include "../../include/moelora.h"
@@ -84,20 +84,22 @@ __device__ __forceinline__ float logit_of(uint32_t key) {
 }
 
 // The logits of token t held by this lane (experts j + 16 i; -inf past E and
-// for a token that is not valid: its logits are loaded all the same, so that
-// they do not wait for the mask).  Returns whether the token is valid.
+// for a token that is not `in` the chunk or not valid).  Returns whether it is
+// both.  Every lane loads, at t and an expert below E, and the mask is loaded
+// beside the logits: a load in a branch would be waited for at its end, one
+// after another.  t: a token of the batch.
 template <bool BF, int V>
 __device__ __forceinline__ bool load_logits(const RouterArgs& a, long t, int j, bool in, float (&l)[V]) {
+  uint32_t raw[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int e = j + 16 * i;
-    l[i] = -INFINITY;
-    if (in && e < a.E)
-      l[i] = BF ? bf2f(((const uint16_t*)a.logits)[t * a.E + e]) : ((const float*)a.logits)[t * a.E + e];
+    const long at = t * a.E + min(j + 16 * i, a.E - 1);
+    raw[i] = BF ? (uint32_t)((const uint16_t*)a.logits)[at] : ((const uint32_t*)a.logits)[at];
   }
   const bool on = in && (a.valid == nullptr || a.valid[t] != 0);
 #pragma unroll
-  for (int i = 0; i < V; ++i) l[i] = on ? l[i] + 0.0f : -INFINITY;  // -0 to +0: equal logits have equal keys
+  for (int i = 0; i < V; ++i)  // -0 to +0: equal logits have equal keys
+    l[i] = on && j + 16 * i < a.E ? (BF ? bf2f(raw[i]) : __uint_as_float(raw[i])) + 0.0f : -INFINITY;
   return on;
 }
 
@@ -130,8 +132,8 @@ __global__ __launch_bounds__(ONE ? ONE_THREADS : THREADS<V>) void k_route(Router
 #pragma unroll
   for (int i = 0; i < V; ++i) mass[i] = 0.0f;
   for (int o = 0; o < nt; o += ROWS) {
-    const long t = (long)t0 + o + row;
     const bool in = o + row < nt;
+    const long t = (long)t0 + min(o + row, nt - 1);
     float l[V];
     load_logits<BF, V>(a, t, j, in, l);
     bool strange = false;
@@ -213,8 +215,7 @@ __global__ __launch_bounds__(ONE ? ONE_THREADS : THREADS<V>) void k_route(Router
     }
   }
   if constexpr (ONE) {
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+    v = wave_sum(v);
     if ((tid & 63) == 0) part[tid >> 6] = v;
     __syncthreads();
     if (tid == 0) {
@@ -237,7 +238,7 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
   __shared__ float sm[RS_THREADS];
   __shared__ int sh[RS_THREADS];
   __shared__ double part[RS_THREADS / 64];
-  __shared__ int stally[2];
+  __shared__ int2 tally[RS_THREADS / 64];
   const int tid = threadIdx.x, root = blockIdx.x;
   int first = 0, nc = 0, all = 0;
   for (int q = 0; q < a.na; ++q) {
@@ -248,34 +249,36 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
     }
     all += c;
   }
-  if (tid < 2) stally[tid] = 0;
   const uint2* from = a.sums + (long)first * (a.E + 1);
+  // one chunk's tokens a thread, in flight with the sums below
+  static_assert(RT_CHUNKS + MAX_ADAPTERS <= RS_THREADS, "a chunk a thread");
   int act = 0, bad = 0;
-  for (int c = tid; c < nc; c += RS_THREADS) act += (int)from[(long)c * (a.E + 1) + a.E].x;
-  if (root == 0)
-    for (int c = tid; c < all; c += RS_THREADS) bad += (int)a.sums[(long)c * (a.E + 1) + a.E].y;
+  if (tid < nc) act = (int)from[(long)tid * (a.E + 1) + a.E].x;
+  if (root == 0 && tid < all) bad = (int)a.sums[(long)tid * (a.E + 1) + a.E].y;
   // EP experts side by side, the smallest power of two that covers E
   const int lg = a.E <= 1 ? 0 : 32 - __clz(a.E - 1), EP = 1 << lg;
-  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg, W = a.E + 1;
+  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg, W = a.E + 1;  // chunks * W: below 2^19
   float m = 0.0f;
   int h = 0;
   if (e < a.E) {
     for (int c = slice; c < nc; c += 16 * slices) {
       uint2 r[16];  // in flight together
 #pragma unroll
-      for (int u = 0; u < 16; ++u) r[u] = c + u * slices < nc ? from[(long)(c + u * slices) * W + e] : make_uint2(0, 0);
+      for (int u = 0; u < 16; ++u) r[u] = from[min(c + u * slices, nc - 1) * W + e];
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
-        m += __uint_as_float(r[u].x);
-        h += (int)r[u].y;
+        const bool in = c + u * slices < nc;
+        m += in ? __uint_as_float(r[u].x) : 0.0f;
+        h += in ? (int)r[u].y : 0;
       }
     }
   }
   sm[tid] = m;
   sh[tid] = h;
+  act = wave_sum(act);
+  bad = wave_sum(bad);
+  if ((tid & 63) == 0) tally[tid >> 6] = make_int2(act, bad);
   __syncthreads();
-  if (act != 0) atomicAdd(&stally[0], act);
-  if (bad != 0) atomicAdd(&stally[1], bad);
   double v = 0.0;
   if (tid < a.E) {  // slice 0
     double mass = 0.0;
@@ -288,17 +291,21 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
     a.counts[(long)root * a.E + tid] = hits;
     v = mass * (double)hits;
   }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, 64);
+  v = wave_sum(v);
   if ((tid & 63) == 0) part[tid >> 6] = v;
   __syncthreads();
   if (tid == 0) {
     double s = 0.0;
+    act = bad = 0;
 #pragma unroll
-    for (int q = 0; q < RS_THREADS / 64; ++q) s += part[q];
-    a.active[root] = stally[0];
-    a.loss[root] = loss_of(a, s, stally[0]);
-    if (root == 0 && a.err != nullptr) *a.err = stally[1];
+    for (int q = 0; q < RS_THREADS / 64; ++q) {
+      s += part[q];
+      act += tally[q].x;
+      bad += tally[q].y;
+    }
+    a.active[root] = act;
+    a.loss[root] = loss_of(a, s, act);
+    if (root == 0 && a.err != nullptr) *a.err = bad;
   }
 }
 
@@ -318,22 +325,26 @@ __global__ __launch_bounds__(BWD_THREADS) void k_route_bwd(RouterArgs a) {
     c = a.gloss[root] * (float)a.E / ((float)a.k * n * n);
   }
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = j + 16 * i;
-    u[i] = (a.gloss != nullptr && e < a.E) ? c * (float)a.counts[(long)root * a.E + e] : 0.0f;
+  for (int i = 0; i < V; ++i) u[i] = 0.0f;
+  if (a.gloss != nullptr) {
+    int n[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) n[i] = a.counts[(long)root * a.E + min(j + 16 * i, a.E - 1)];
+#pragma unroll
+    for (int i = 0; i < V; ++i) u[i] = j + 16 * i < a.E ? c * (float)n[i] : 0.0f;
   }
   for (int o = 0; o < nt; o += ROWS) {
-    const long t = (long)t0 + o + row;
     const bool in = o + row < nt;
+    const long t = (long)t0 + min(o + row, nt - 1);
     int idx = -1;
     float g = 0.0f, lsel = 0.0f;
-    if (in && j < a.k && a.gw != nullptr) {
-      idx = a.idx[t * a.k + j];
-      g = a.gw[t * a.k + j];
+    if (a.gw != nullptr) {
+      idx = a.idx[t * a.k + min(j, a.k - 1)];
+      g = a.gw[t * a.k + min(j, a.k - 1)];
     }
     float l[V];
     const bool on = load_logits<BF, V>(a, t, j, in, l);
-    if (!on || idx < 0 || idx >= a.E) idx = -1;
+    if (!on || j >= a.k || idx < 0 || idx >= a.E) idx = -1;
     // the chosen logits, through the token's row of LDS
 #pragma unroll
     for (int i = 0; i < V; ++i) mine[j + 16 * i] = l[i];
@@ -403,7 +414,7 @@ int chunks_of(const RouterArgs& a) {
   return n;
 }
 
-// Few tokens: one launch, 4.0 us at one token (two: 3.7 and 2.9).  Beyond one
+// Few tokens: one launch, 3.7 us at one token (two: 3.7 and 2.9).  Beyond one
 // round of its workgroup a round costs about 1.5 us and the sums lose their
 // parallel chunks.
 bool one_launch(const RouterArgs& a) { return a.na == 1 && a.T <= ONE_TOKENS; }
