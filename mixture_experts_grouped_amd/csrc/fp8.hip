@@ -149,6 +149,8 @@ __global__ __launch_bounds__(256) void k_fp8_weight(const uint16_t* __restrict__
 struct Fp8Args {
   int E, N, K, topk;
   int cap;  // rows of the pool
+  uint32_t tok_mul;  // route / topk = route * tok_mul >> tok_shift
+  int tok_shift;
   long a_rows;
   const int32_t* counts;
   const int32_t* offsets;
@@ -165,9 +167,9 @@ __device__ __forceinline__ int rows_of(const Fp8Args& p, int e) {
   const int off = p.offsets[e];
   return off >= 0 && off < p.cap ? max(min(p.counts[e], p.cap - off), 0) : 0;
 }
-// The activation row of pool row r (of a route), -1: none.
-__device__ __forceinline__ int token_of(const Fp8Args& p, long r) {
-  const int route = p.row2r[r], t = route / p.topk;
+// The activation row of a route, -1: none.
+__device__ __forceinline__ int token_of(const Fp8Args& p, int route) {
+  const int t = (int)((uint64_t)(uint32_t)route * p.tok_mul >> p.tok_shift);
   return route >= 0 && t < p.a_rows ? t : -1;
 }
 
@@ -242,8 +244,8 @@ struct Geo8 {
   static constexpr int SW_AT = NBUF * STAGE;  // two tiles' weight scales, [2][TN / 128][stages]
   static constexpr int stages(int K) { return cmax(K / 128, NBUF); }
   static constexpr int table_at(int K) { return SW_AT + 2 * (TN / 128) * stages(K) * 4; }  // PoolTable
-  static constexpr int lds(int K, int E) { return table_at(K) + 12 * E; }
-  static_assert(128 % (TN / WN) == 0 && TN % 128 == 0, "a wave's weight rows lie in one block of 128");
+  static constexpr int lds(int K, int E) { return table_at(K) + 12 * E + 4 * TM; }  // and the next tile's routes
+  static_assert(128 % (TN / WN) == 0 && TN % 128 == 0 && TN <= 256, "a wave's weight rows lie in one block of 128");
   static_assert(lds(MAX_DIM, MAX_E) <= 160 * 1024 && NW * 64 >= TM && FN % 2 == 0, "one scale a lane; fragments are stored in pairs");
 };
 
@@ -340,29 +342,38 @@ struct Frag8 {
 // are already loading, and the finished tile is stored from registers.
 //
 // A stage s in steady state: the products of weight fragment i are issued
-// while those of i - 1 (the last ones, of the stage before) are scaled and
-// added and fragment i + 1 is read; the next stage's first fragments are read
-// under the last products.  With SPLIT a buffer is refilled for stage s + 2 in
-// two parts, each as soon as the workgroup has read it: at mid-stage the
-// activation rows (in registers by then) and the weight rows of the first
-// half of the fragments, at the end the others, so a load has one and a half
-// stages to arrive from two buffers (one with a refill at the end alone).
-// Without SPLIT whole stages are queued NBUF ahead.
+// while those before them are scaled and added and fragment i + 1 is read.
+// With SPLIT the last two fragments are multiplied in turn, so that an
+// activation fragment is done with at every second product and the next
+// stage's is read in its place: read at every product, the next stage's five
+// fragments took more LDS time than the products above them (1 % slower).  With SPLIT
+// a buffer is refilled for stage s + 2 in two parts, each as soon as the
+// workgroup has read it: from mid-stage on the activation rows (in registers by
+// then) and the weight rows of the first half of the fragments, at the end the
+// others, so a load has one and a half stages to arrive from two buffers (one
+// with a refill at the end alone).  Without SPLIT whole stages are queued NBUF
+// ahead.  The next tile's routes come through LDS, queued a tile ahead: read
+// where they are needed, and with the lanes' offsets kept in scratch across the
+// K loop, each wait for one waited for all queued loads (2 % slower).
 //
-// What it measured, 98,304 rows of 4096 x 4096 on 64 experts: 1.66-1.70 ms,
-// 1,970 TFLOP/s (one expert, 8192^3: 2,290; a library's product with one
-// scale a tensor 2,660).  The matrix cores are busy 57 % of the cycles at 1.7
-// GHz; without loads the loop takes 1.26 ms, without products 1.31, the LDS
-// reads and multiply-adds alone 0.56.  Loads queued in one burst after the
-// barrier instead of spread over the fragments: 1.77 ms; a stage's fragments
-// read at its start, each product's result added at once: 2.41.  Touching
+// What it measured, 98,304 rows of 4096 x 4096 on 64 experts: 1.58-1.62 ms,
+// 2,060 TFLOP/s (experts of equal size: 1.49; one expert, 8192^3: 2,290; a
+// library's product with one scale a tensor 2,660).  The matrix cores are busy
+// 59 % of the cycles at 1.6 GHz, which is the power cap: activations of zeros
+// take 1.28 ms.  A tile costs 10 us beyond its 1.6 us a stage, most of it the
+// time that its 128 KB take to memory (three quarters of the stores left out:
+// 0.10 ms less): waits that leave them out for two stages gained nothing, nor did
+// workgroups that start up to 60 us apart.  Loads queued in one burst after the
+// barrier instead of spread over the products: 6 % slower; a stage's fragments
+// read at its start, each product's result added at once: 2.41 ms.  Touching
 // the lines of later stages for L2 cost 0.2 ms: the loads are bound by
 // throughput, not by misses.  Rows over an expert's last whole tile as
 // 64-row tiles in a launch of their own: no gain, on ragged experts a loss of
-// up to 17 %; waves without rows only loading: 2 % slower.  The 64-row tile, 689 tokens x 6 with a fifth of
-// the routes dropped, 4096 x 2048: 116 us, 4.9 TB/s of weights; with six
-// buffers instead of three, one workgroup a CU: no faster, 0.5 us a K block,
-// which is the chain of barrier, fragment reads and products.
+// up to 17 %; waves without rows only loading: 2 % slower.  The 64-row tile,
+// 689 tokens x 6 with a fifth of the routes dropped, 4096 x 2048: 116 us, 4.9
+// TB/s of weights; with six buffers instead of three, one workgroup a CU: no
+// faster, 0.5 us a K block, which is the chain of barrier, fragment reads and
+// products.
 //
 // Loads past a tile's K (K / 128 < NBUF) or past the last tile go to offsets
 // outside every descriptor: zeros, no traffic, and the loop waits by constant
@@ -379,49 +390,64 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   const int KB = p.K / 128, ST = cmax(KB, G::NBUF), nn = (p.N + G::TN - 1) / G::TN;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = w / G::WN, wn = w % G::WN;
-  const int fr = lane & 15, fc = lane >> 4;
+  const int fr = lane & 15;
   PoolTable tab;
   fill_table<G::TM>(p, tab, smem + G::table_at(p.K));
   Tile8 cur;
   int b = blockIdx.x;
   if (!find_tile<G::TM>(tab, p.E, b, nn, cur)) return;
 
-  // tokens of the activation rows that this lane loads (LA::NJ rows of codes, one scale)
-  int tk[LA::NJ + 1];
-  auto tokens = [&](const Tile8& t) {
-    if (p.topk == 0) return;
-#pragma unroll
-    for (int j = 0; j <= LA::NJ; ++j) {
-      const int q = j < LA::NJ ? LA::row_of(j) : 64 * w + lane;
-      tk[j] = q < t.nrows ? token_of(p, t.row0 + q) : -1;
-    }
+  // queue a tile's routes into LDS, where aim reads them
+  char* const routes = smem + G::table_at(p.K) + 12 * p.E;
+  auto queue_routes = [&](const Tile8& t) {
+    if (p.topk > 0 && 64 * w < G::TM)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(p.row2r + t.row0, (uint64_t)t.nrows * 4),
+                                               (v2::lds_void*)(routes + 256 * w), 4, 256u * w + 4u * lane, 0, 0, 0);
   };
   LA la;
   LW lw;
   rsrc_t rs;
   uint32_t soff;
-  // aim the loads at a tile, and queue its weight scales into half h
+  // aim the loads at a tile, and queue its weight scales into half h.  The
+  // lane's number passes through an empty asm so that what is computed from it
+  // is computed for each tile: kept across the K loop it went to scratch, and
+  // each reload waited for all queued loads.
   auto aim = [&](const Tile8& t, bool any, int h) {
+    int lane = threadIdx.x & 63;
+    asm volatile("" : "+v"(lane));
     const int n0 = t.nt * G::TN, ncols = min(p.N - n0, G::TN);
+    auto row_of = [&](int j) { return 8 * (w + G::NW * j) + (lane >> 3); };
+    auto chunk = [&](int j) { return 16u * (uint32_t)((lane & 7) ^ v2::kswz<64>(row_of(j))); };
     if (p.topk > 0) {
+      // tokens of the activation rows that this lane loads: LA::NJ rows of codes, one scale
+      int tk[LA::NJ + 1];
+#pragma unroll
+      for (int j = 0; j <= LA::NJ; ++j) {
+        const int q = j < LA::NJ ? row_of(j) : 64 * w + lane;
+        const int token = token_of(p, ((const int*)routes)[j < LA::NJ ? q : min(q, G::TM - 1)]);
+        tk[j] = q < t.nrows ? token : -1;
+      }
       la.rs = make_rsrc(p.a, any ? (uint64_t)p.a_rows * p.K : 0);
       rs = make_rsrc(p.sa, any ? (uint64_t)p.a_rows * KB * 4 : 0);
 #pragma unroll
-      for (int j = 0; j < LA::NJ; ++j) la.set_row(j, tk[j] >= 0 ? (uint32_t)tk[j] * (uint32_t)p.K : OFF_NONE);
+      for (int j = 0; j < LA::NJ; ++j) la.voff[j] = tk[j] >= 0 ? (uint32_t)tk[j] * (uint32_t)p.K + chunk(j) : OFF_NONE;
       soff = tk[LA::NJ] >= 0 ? (uint32_t)tk[LA::NJ] * (uint32_t)KB * 4u : OFF_NONE;
     } else {
       const long have = p.a_rows - t.row0;
       const int live = any ? (int)(have < t.nrows ? (have > 0 ? have : 0) : t.nrows) : 0;
-      la.contig((const uint16_t*)p.a, t.row0, live, p.K / 2);
+      la.rs = make_rsrc(p.a + t.row0 * p.K, (uint64_t)live * p.K);
+#pragma unroll
+      for (int j = 0; j < LA::NJ; ++j)
+        la.voff[j] = row_of(j) < live ? (uint32_t)row_of(j) * (uint32_t)p.K + chunk(j) : OFF_NONE;
       rs = make_rsrc(p.sa + t.row0 * KB, (uint64_t)live * KB * 4);
       soff = 64 * w + lane < live ? (uint32_t)(64 * w + lane) * (uint32_t)KB * 4u : OFF_NONE;
     }
-    lw.contig((const uint16_t*)(p.w + (long)t.e * p.N * p.K), n0, any ? ncols : 0, p.K / 2);
+    lw.rs = make_rsrc(p.w + ((long)t.e * p.N + n0) * p.K, any ? (uint64_t)ncols * p.K : 0);
     // scale blocks x stages, 64 values a load; block c of stages past K, and of columns past N, reads zero
     const rsrc_t rw = make_rsrc(p.sw + ((long)t.e * (p.N / 128) + n0 / 128) * KB, any ? (uint64_t)(ncols / 128) * KB * 4 : 0);
     char* to = smem + G::SW_AT + h * (G::TN / 128) * ST * 4;
     for (int c = w; c * 64 < G::TN / 128 * ST; c += G::NW) {
-      const int i = 64 * c + lane, blk = i / ST, k = i - blk * ST;
+      const int i = 64 * c + lane, blk = i >= ST ? 1 : 0, k = i - blk * ST;  // two blocks at most
       if (i < G::TN / 128 * ST)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (v2::lds_void*)(to + 256 * c), 4,
                                                  k < KB ? (uint32_t)(blk * KB + k) * 4u : OFF_NONE, 0, 0, 0);
@@ -468,50 +494,58 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   auto sw_at = [&](int h, int s) {
     return G::SW_AT + ((h * (G::TN / 128) + wn * (G::TN / G::WN) / 128) * ST + s) * 4;
   };
+  // Products of a stage in order: fragment I(m) of the weight, J(m) of the
+  // activations, its result in t[m % FM] until product m + FM has that place.
+  constexpr int N = FM * FN;
+  auto I = [](int m) constexpr { return G::SPLIT && m >= N - 2 * FM ? FN - 2 + (m & 1) : m / FM; };
+  auto J = [](int m) constexpr { return G::SPLIT && m >= N - 2 * FM ? (m - (N - 2 * FM)) / 2 : m % FM; };
   // multiply the stage in buffer g; queue stage q of the tile aimed at into
   // it; read the next stage's first fragments (its weight scale at swn)
   auto stage = [&](int g, int q, int swn) {
+    constexpr int LAST = G::SPLIT ? N - 2 * FM : N - FM;  // from here the next stage's fragments are read
     const int gn = g + 1 == G::NBUF ? 0 : g + 1;
     const char* sW = smem + g * G::STAGE + G::A_BYTES + wn * FN * 2048;
     const char* nA = smem + gn * G::STAGE + wm * FM * 2048;
     float sn[FM];
+    i32x8 b, c;  // the weight fragments after a
 #pragma unroll
-    for (int i = 0; i < FN; ++i) {
-      i32x8 next;
-      if (G::SPLIT && i == FN / 2 - 1) {
-        v2::wait_lgkm0();  // this wave has read the activation rows and the first weight rows
-        v2::wait_vm<INSTS>();  // the other weight rows have landed
-        v2::bar();
-      }
-      if (i + 1 < FN) {
-        next = fw.get(sW, i + 1);
-      } else {
-        v2::wait_lgkm0();  // this wave has read all of the stage
-        v2::wait_vm<G::SPLIT ? INSTS : (G::NBUF - 2) * INSTS>();  // the next one's first part has landed
-        v2::bar();
-        next = fw.get(smem + gn * G::STAGE + G::A_BYTES + wn * FN * 2048, 0);
-        read_scales(gn, swn, sn);
-      }
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < FM; ++j) {
-        const float f = i == 0 ? sl[j] : sc[j];
-        f32x4& to = acc[i == 0 ? FN - 1 : i - 1][j];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) to[c] = fmaf(t[j][c], f, to[c]);
-        t[j] = mma8(a, x[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-        if (i == FN - 1) x[j] = fa.get(nA, j);
-        if constexpr (G::SPLIT) {  // two loads for each fragment from mid-stage on, the last two at the end
-          if (j % 2 == 1 && i >= FN / 2 - 1 && 2 * (i - FN / 2 + 1) + j / 2 < INSTS - 2 && i < FN - 1)
-            issue1(q, g, 2 * (i - FN / 2 + 1) + j / 2);
-          if (j % 2 == 1 && i == FN - 1) issue1(q, g, INSTS - 2 + j / 2);
-        } else if (i == FN - 1) {
-#pragma unroll
-          for (int l = j * INSTS / FM; l < (j + 1) * INSTS / FM; ++l) issue1(q, g, l);
+    for (int m = 0; m < N; ++m) {
+      if (m % FM == 0 && m <= LAST) {
+        if (G::SPLIT && m == N / 2 - FM) {
+          v2::wait_lgkm0();  // this wave has read the activation rows and the first weight rows
+          v2::wait_vm<INSTS>();  // the other weight rows have landed
+          v2::bar();
+        }
+        if (m < LAST) {
+          b = fw.get(sW, m / FM + 1);
+          if (G::SPLIT && m + FM == LAST) c = fw.get(sW, m / FM + 2);
+        } else {
+          v2::wait_lgkm0();  // this wave has read all of the stage
+          // the next one's first part has landed (SPLIT: one load of the one after is not queued yet)
+          v2::wait_vm<G::SPLIT ? INSTS - 1 : (G::NBUF - 2) * INSTS>();
+          v2::bar();
+          a = fw.get(smem + gn * G::STAGE + G::A_BYTES + wn * FN * 2048, 0);
+          read_scales(gn, swn, sn);
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-      a = next;
+      const int done = m < FM ? m + N - FM : m - FM, j = J(m);
+      const float f = m < FM ? sl[J(done)] : sc[J(done)];
+      f32x4& to = acc[I(done)][J(done)];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) to[e] = fmaf(t[m % FM][e], f, to[e]);
+      t[m % FM] = mma8(m < LAST ? a : G::SPLIT && (m & 1) ? c : b, x[j], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+      if constexpr (G::SPLIT) {
+        if (m >= LAST && (m & 1)) x[j] = fa.get(nA, j);
+        // a load at every other product from mid-stage on
+        if ((m & 1) && m > N / 2 - FM && (m - (N / 2 - FM)) / 2 < INSTS) issue1(q, g, (m - (N / 2 - FM)) / 2);
+      } else if (m >= LAST) {
+        x[j] = fa.get(nA, j);
+#pragma unroll
+        for (int l = j * INSTS / FM; l < (j + 1) * INSTS / FM; ++l) issue1(q, g, l);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if (m % FM == FM - 1 && m + 1 < LAST) a = b;
     }
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
@@ -520,7 +554,10 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
     }
   };
 
-  tokens(cur);
+  lw.contig(nullptr, 0, 0, p.K / 2);  // the lane's offsets in any weight panel
+  queue_routes(cur);
+  v2::wait_vm<0>();
+  v2::bar();
   aim(cur, true, 0);
   int h = 0, g = 0;  // half of the weight scales, buffer of the stage to multiply
 #pragma unroll
@@ -541,10 +578,14 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
     Tile8 nxt = cur;
     b += gridDim.x;
     const bool more = find_tile<G::TM>(tab, p.E, b, nn, nxt);
-    if (more) tokens(nxt);
+    if (more) queue_routes(nxt);
     for (int s = 0; s + G::NBUF < ST; ++s) {
       stage(g, s + G::NBUF, sw_at(h, s + 1));
       g = g + 1 == G::NBUF ? 0 : g + 1;
+    }
+    if (ST < G::NBUF + 2) {  // the routes: the waits of two stages cover them, of fewer not
+      v2::wait_vm<0>();
+      v2::bar();
     }
     aim(nxt, more, h ^ 1);
     for (int s = 0; s < G::NBUF; ++s) {
@@ -553,12 +594,20 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
     }
     // A lane holds four columns of a row for each fragment; of two neighbouring
     // fragments, rows of 16 lanes trade so that it holds eight columns of one.
+    // Rows past the tile's lie outside the descriptor; a wave's columns are all
+    // below N or none.
+    int lane2 = lane;
+    asm volatile("" : "+v"(lane2));
+    const int fr = lane2 & 15, fc = lane2 >> 4;
+#pragma unroll
+    for (int m = N - FM; m < N; ++m) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) acc[I(m)][J(m)][c] = fmaf(t[m % FM][c], sl[J(m)], acc[I(m)][J(m)][c]);
+    }
+    const bool cols = cur.nt * G::TN + wn * FN * 16 < p.N;
     const rsrc_t ro = make_rsrc(p.out + cur.row0 * p.N + cur.nt * G::TN, (uint64_t)cur.nrows * p.N * 2);
-    const int ncols = min(p.N - cur.nt * G::TN, G::TN);
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) acc[FN - 1][j][c] = fmaf(t[j][c], sl[j], acc[FN - 1][j][c]);
       const int r = (wm * FM + j) * 16 + fr;
 #pragma unroll
       for (int i = 0; i < FN; i += 2) {
@@ -567,7 +616,7 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
         const auto hi = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][2], acc[i][j][3]),
                                                          pack2(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
         const int c = (wn * FN + i + (fc & 1)) * 16 + 8 * (fc >> 1);
-        const uint32_t off = r < cur.nrows && c < ncols ? (uint32_t)(r * p.N + c) * 2u : OFF_NONE;
+        const uint32_t off = cols ? (uint32_t)(r * p.N + c) * 2u : OFF_NONE;
         __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, (int)off, 0, 0);
       }
     }
@@ -607,7 +656,7 @@ __global__ __launch_bounds__(64) void k_fp8_few(Fp8Args p) {
     if (p.topk > 0) {
       ra = make_rsrc(p.a, (uint64_t)p.a_rows * p.K);
       rs = make_rsrc(p.sa, (uint64_t)p.a_rows * KB * 4);
-      if (fr < nrows) ar = token_of(p, row0 + fr);
+      if (fr < nrows) ar = token_of(p, p.row2r[row0 + fr]);
     } else {
       const long have = p.a_rows - row0;
       const int live = (int)(have < nrows ? (have > 0 ? have : 0) : nrows);
@@ -786,8 +835,14 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
                        rng(pool->row_to_route, (size_t)pool->capacity * 4)};
   for (const Range& r : ins)
     if (overlap(ro, r)) return MOE_ERR_INVALID;
-  Fp8Args p{d->E, d->N, d->K, d->topk, (int)pool->capacity, (long)d->a_rows, pool->counts, pool->offsets, pool->row_to_route,
-            (const uint8_t*)a, a_scales, (const uint8_t*)w, w_scales, (uint16_t*)out};
+  // floor(n / k) = floor(n m / 2^(31 + s)) for n < 2^31, with 2^s >= k the
+  // smallest and m = ceil(2^(31 + s) / k) < 2^32: n (m k - 2^(31 + s)) < 2^(31 + s)
+  const uint64_t k = d->topk > 0 ? (uint64_t)d->topk : 1;
+  int sh = 31;
+  while ((uint64_t)1 << (sh - 31) < k) ++sh;
+  const uint32_t mul = (uint32_t)((((uint64_t)1 << sh) + k - 1) / k);
+  Fp8Args p{d->E, d->N, d->K, d->topk, (int)pool->capacity, mul, sh, (long)d->a_rows, pool->counts, pool->offsets,
+            pool->row_to_route, (const uint8_t*)a, a_scales, (const uint8_t*)w, w_scales, (uint16_t*)out};
   // the routes of a pool of this capacity: build_pool allots BLOCK_M - 1 rows
   // of padding to each of min(E, routes) experts
   const int64_t bm = pool->block_m, cap = pool->capacity, E = d->E;
