@@ -757,14 +757,22 @@ def fp8_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optio
     "geglu") to e4m3 codes [rows, K] and fp32 scales [rows, K/128]."""
     if src.dim() != 2 or act not in _ACTS or (act is not None and src.shape[1] % 2):
         raise ValueError("src must be [rows, K], or [rows, 2K] with act 'swiglu' or 'geglu'")
-    rows, K = src.shape[0], src.shape[1] if act is None else src.shape[1] // 2
+    rows, K = src.shape
+    if act is not None:
+        K //= 2
+    given = (src, codes, scales)
     if codes is None:
         codes = _made(stream, torch.empty, rows, K, dtype=_E4M3, device=src.device)
+        to = codes.data_ptr()
+    else:
+        to = _ptr(codes, _E4M3, (rows, K), "codes")
     if scales is None:
         scales = _made(stream, torch.empty, rows, K // 128, dtype=torch.float32, device=src.device)
-    _launch("moe_fp8_quantize_rows", library().moe_fp8_quantize_rows, stream, (src, codes, scales),
-            _ptr(src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], _ptr(codes, _E4M3, (rows, K), "codes"),
-            _ptr(scales, torch.float32, (rows, K // 128), "scales"))
+        sto = scales.data_ptr()
+    else:
+        sto = _ptr(scales, torch.float32, (rows, K // 128), "scales")
+    _launch("moe_fp8_quantize_rows", library().moe_fp8_quantize_rows, stream, given,
+            _ptr(src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], to, sto)
     return codes, scales
 
 
