@@ -10,6 +10,7 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from typing import Dict, Optional, Sequence, Tuple
 
@@ -738,6 +739,8 @@ class MoeAdamW:
                       seed: Optional[int] = None) -> None:
         """Fill a control buffer (int32 [5] on the device) with one step's
         values: before each replay of a graph that captured a step with it."""
+        if not (step >= 1 and math.isfinite(lr) and lr >= 0 and math.isfinite(grad_scale)):
+            raise ValueError("write_control: step >= 1, lr >= 0 and grad_scale, all finite")
         f = torch.tensor([lr, 1.0 - self.betas[0] ** step, 1.0 - self.betas[1] ** step, grad_scale],
                          dtype=torch.float64).to(torch.float32).view(torch.int32)
         s = (step if seed is None else seed) & 0xFFFFFFFF

@@ -223,3 +223,25 @@ def test_refused_steps_and_shared_memory():
                           ([p[:256], ps[0]], [p[256:], p[200:300]])):
         with pytest.raises(ValueError):
             M.MoeAdamW(params, grads)
+
+
+def test_control_values_are_checked():
+    ps, gs = tensors([8], F32, F32, 22)
+    opt, c = M.MoeAdamW(ps, gs), torch.zeros(5, dtype=torch.int32, device="cuda")
+    for kw in (dict(lr=1e-3, step=0), dict(lr=-1.0, step=1), dict(lr=np.nan, step=1), dict(lr=1.0, step=1, grad_scale=np.inf)):
+        with pytest.raises(ValueError):
+            opt.write_control(c, **kw)
+    assert not c.any()
+
+
+def test_more_elements_than_32_bits_count():
+    n, tail = 2 ** 31 + 517, 5000
+    g = torch.Generator().manual_seed(5)
+    p, gr = torch.randn(tail, generator=g).to(BF).cuda(), torch.randn(tail, generator=g).to(BF).cuda()
+    big, grad = (torch.zeros(n, dtype=BF, device="cuda") for _ in range(2))
+    big[-tail:], grad[-tail:] = p, gr
+    opt, ref = M.MoeAdamW([big], [grad], lr=1e-2), M.MoeAdamW([p], [gr], lr=1e-2)
+    opt.step()
+    ref.step()
+    assert torch.equal(big[-tail:], p) and torch.equal(opt.states["v"][0][-tail:], ref.states["v"][0])
+    assert not big[:2 ** 20].any()

@@ -337,3 +337,51 @@ def test_streams_and_graphs():
         torch.cuda.synchronize()
         assert torch.equal(got, want)
     del g
+
+
+def test_rows_past_32_bits():
+    rows, K = 2 ** 31 // 4096 + 40, 4096
+    x = torch.zeros(rows, K, dtype=BF, device="cuda")
+    x[-40:] = torch.randn(40, K, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    c, s = M.fp8_quantize_rows(x)
+    wc, ws = M.fp8_quantize_rows(x[-40:].contiguous())
+    assert torch.equal(c[-40:].view(torch.uint8), wc.view(torch.uint8)) and torch.equal(s[-40:], ws)
+    assert not s[:1000].any()
+
+
+@pytest.mark.parametrize("T,kernel", [(1, "few"), (100, "tile64"), (9000, "tile256")])
+def test_weights_past_32_bits(T, kernel):
+    """All routes on the last of so many experts that its weights lie past 2^31."""
+    E, N, K = 33, 8192, 8192
+    g = torch.Generator().manual_seed(T)
+    last = (torch.randn(1, N, K, generator=g) * K ** -0.5).to(BF).cuda()
+    big = torch.zeros(E, N, K, dtype=BF, device="cuda")
+    big[-1] = last[0]
+    w, sw = M.fp8_quantize_weight(big)
+    del big
+    w1, sw1 = M.fp8_quantize_weight(last)
+    assert torch.equal(w[-1].view(torch.uint8), w1[0].view(torch.uint8)) and torch.equal(sw[-1], sw1[0])
+    a, sa = M.fp8_quantize_rows(torch.randn(T, K, generator=g).to(BF).cuda())
+    one = build(torch.zeros(T, 1, dtype=torch.int32), 1)
+    want = M.fp8_product(one, a, sa, w1, sw1, topk=1)
+    pool = build(torch.full((T, 1), E - 1, dtype=torch.int32), E)
+    with Kernel() as ran:
+        got = M.fp8_product(pool, a, sa, w, sw, topk=1)
+    assert ran.names == {kernel}
+    live, live1 = pool["row_to_route"] >= 0, one["row_to_route"] >= 0
+    assert int(live.sum()) == T and torch.equal(got[live], want[live1])
+
+
+def test_outputs_past_32_bits():
+    T, N, K = 2 ** 31 // 32768 + 300, 32768, 128
+    a, sa, w, sw = operands(T, 1, N, K, 2)
+    pool = build(torch.zeros(T, 1, dtype=torch.int32), 1)
+    for topk in (1, 0):
+        with Kernel() as ran:
+            out = M.fp8_product(pool, a, sa, w, sw, topk=topk)
+        tail = build(torch.zeros(300, 1, dtype=torch.int32), 1)
+        rows = pool["row_to_route"][T - 300:T].long()  # one expert: pool row r is a route of it
+        src = rows if topk else torch.arange(T - 300, T, device="cuda")
+        want = M.fp8_product(tail, a.view(torch.uint8)[src].view(F8), sa[src], w, sw, topk=0)
+        assert ran.names == {"tile256"} and torch.equal(out[T - 300:T], want[:300])
+        del out
