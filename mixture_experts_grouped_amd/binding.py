@@ -517,14 +517,28 @@ def moe_lora_split_e2m3x2(src: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
 
-def _launch(what: str, fn, stream, tensors, *args) -> None:
-    """fn(*args, stream) on the device that every tensor of the call is on
-    (made the current one for the call if it is not); stream None: that
-    device's current one."""
-    dev = tensors[0].get_device()
-    for t in tensors[1:]:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"{what}: tensors on {tensors[0].device} and {t.device}: one call runs on one device")
+def _on(dev: int, t: Optional[torch.Tensor], dtype, shape, name: str) -> Optional[int]:
+    """_ptr for a call that runs on device dev: t is there too."""
+    if t is None:
+        return None
+    if t.get_device() == dev and t.is_contiguous() and t.dtype is dtype and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    p = _ptr(t, dtype, shape, name)
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}: one call runs on one device")
+    return p
+
+
+def _device_of(t: torch.Tensor, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return dev
+
+
+def _launch(what: str, fn, dev: int, stream, *args) -> None:
+    """fn(*args, stream) on device dev (made the current one for the call if it
+    is not); stream None: that device's current one."""
     if dev < 0:
         raise ValueError(f"{what}: tensors must be device tensors")
     handle = _raw_stream(dev) if stream is None else _stream(stream)
@@ -605,16 +619,18 @@ class MoeRouter:
         self.grad_logits = torch.empty(T, E, dtype=dtype, device=device)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self._dp = ctypes.byref(self.desc)
-        self._lshape, self._kshape = (T, E), (T, topk)
+        self._dev = self.topk_idx.get_device()
+        self._lshape, self._kshape, self._tshape, self._cshape, self._rshape = (T, E), (T, topk), (T,), (na, E), (na,)
         self._outs = tuple(t.data_ptr() for t in (self.topk_idx, self.topk_w, self.counts, self.active, self.loss,
                                                   self.device_error, self.workspace)) + (nbytes,)
 
     def forward(self, logits: torch.Tensor, valid: Optional[torch.Tensor] = None, stream=None):
         """logits [T, E]; valid [T] uint8 (0: a padding token) or None.
         Returns (topk_idx, topk_w, counts, active, loss)."""
-        _launch("moe_router_forward", library().moe_router_forward, stream, (self.topk_idx, logits, valid), self._dp,
-                self._adp, _ptr(logits, self.dtype, self._lshape, "logits"),
-                _ptr(valid, torch.uint8, self._lshape[:1], "valid"), *self._outs)
+        dev = self._dev
+        _launch("moe_router_forward", library().moe_router_forward, dev, stream, self._dp, self._adp,
+                _on(dev, logits, self.dtype, self._lshape, "logits"),
+                _on(dev, valid, torch.uint8, self._tshape, "valid"), *self._outs)
         if self.checked:
             bad = self.dropped_tokens(stream)
             if bad:
@@ -633,13 +649,12 @@ class MoeRouter:
         forward's topk_idx, counts and active (the router's own buffers after
         forward, or copies) and the gradients of topk_w [T, k] and of the
         loss [roots] (None: zero)."""
-        f32, i32, T = torch.float32, torch.int32, self._lshape[:1]
-        _launch("moe_router_backward", library().moe_router_backward, stream,
-                (self.topk_idx, logits, valid, topk_idx, counts, active, grad_topk_w, grad_loss), self._dp, self._adp,
-                _ptr(logits, self.dtype, self._lshape, "logits"), _ptr(valid, torch.uint8, T, "valid"),
-                _ptr(topk_idx, i32, self._kshape, "topk_idx"), _ptr(counts, i32, self.counts.shape, "counts"),
-                _ptr(active, i32, self.active.shape, "active"), _ptr(grad_topk_w, f32, self._kshape, "grad_topk_w"),
-                _ptr(grad_loss, f32, self.active.shape, "grad_loss"), self.grad_logits.data_ptr())
+        f32, i32, dev = torch.float32, torch.int32, self._dev
+        _launch("moe_router_backward", library().moe_router_backward, dev, stream, self._dp, self._adp,
+                _on(dev, logits, self.dtype, self._lshape, "logits"), _on(dev, valid, torch.uint8, self._tshape, "valid"),
+                _on(dev, topk_idx, i32, self._kshape, "topk_idx"), _on(dev, counts, i32, self._cshape, "counts"),
+                _on(dev, active, i32, self._rshape, "active"), _on(dev, grad_topk_w, f32, self._kshape, "grad_topk_w"),
+                _on(dev, grad_loss, f32, self._rshape, "grad_loss"), self.grad_logits.data_ptr())
         return self.grad_logits
 
 
@@ -669,6 +684,7 @@ class MoeAdamW:
         self.lr, self.betas, self.eps, self.weight_decay = lr, betas, eps, weight_decay
         self.state_bits = state_bits
         self.steps = 0  # steps taken
+        self._dev = _device_of(params[0], "params")
         self._same = None  # what the descriptor holds of betas, eps and weight_decay
         eight = state_bits == 8
         kinds = {"m": torch.float8_e4m3fn, "v": torch.float8_e5m2} if eight else dict.fromkeys("mv", torch.float32)
@@ -730,9 +746,8 @@ class MoeAdamW:
         d.step = number
         if self.state_bits == 8:
             d.seed = (number if seed is None else seed) & 0xFFFFFFFF
-        d.control = _ptr(control, torch.int32, (5,), "control")
-        _launch("moe_adamw_step", library().moe_adamw_step, stream, (self.params[0], control), self._dp, self._table,
-                len(self._table))
+        d.control = _on(self._dev, control, torch.int32, (5,), "control")
+        _launch("moe_adamw_step", library().moe_adamw_step, self._dev, stream, self._dp, self._table, len(self._table))
         self.steps = number  # only a step that was taken
 
     def write_control(self, control: torch.Tensor, lr: float, step: int, grad_scale: float = 1.0,
@@ -763,19 +778,19 @@ def fp8_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optio
     rows, K = src.shape
     if act is not None:
         K //= 2
-    given = (src, codes, scales)
+    dev = _device_of(src, "src")
     if codes is None:
         codes = _made(stream, torch.empty, rows, K, dtype=_E4M3, device=src.device)
         to = codes.data_ptr()
     else:
-        to = _ptr(codes, _E4M3, (rows, K), "codes")
+        to = _on(dev, codes, _E4M3, (rows, K), "codes")
     if scales is None:
         scales = _made(stream, torch.empty, rows, K // 128, dtype=torch.float32, device=src.device)
         sto = scales.data_ptr()
     else:
-        sto = _ptr(scales, torch.float32, (rows, K // 128), "scales")
-    _launch("moe_fp8_quantize_rows", library().moe_fp8_quantize_rows, stream, given,
-            _ptr(src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], to, sto)
+        sto = _on(dev, scales, torch.float32, (rows, K // 128), "scales")
+    _launch("moe_fp8_quantize_rows", library().moe_fp8_quantize_rows, dev, stream,
+            _on(dev, src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], to, sto)
     return codes, scales
 
 
@@ -786,12 +801,14 @@ def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) 
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     E, N, K = W.shape
+    dev = _device_of(W, "W")
+
     def pair(n, k):
         return [_made(stream, torch.empty, E, n, k, dtype=_E4M3, device=W.device),
                 _made(stream, torch.empty, E, n // 128, k // 128, dtype=torch.float32, device=W.device)]
     out = pair(N, K) + (pair(K, N) if transposed else [])
-    _launch("moe_fp8_quantize_weight", library().moe_fp8_quantize_weight, stream, (W,),
-            _ptr(W, torch.bfloat16, None, "W"), E, N, K, *[t.data_ptr() for t in out], *([] if transposed else [None, None]))
+    _launch("moe_fp8_quantize_weight", library().moe_fp8_quantize_weight, dev, stream,
+            _on(dev, W, torch.bfloat16, None, "W"), E, N, K, *[t.data_ptr() for t in out], *([] if transposed else [None, None]))
     return tuple(out)
 
 
@@ -810,17 +827,17 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
     rows, K = a.shape
     E, N = w.shape[:2]
     cap = pool["row_to_route"].numel()
+    dev = _device_of(a, "a")
     if out is None:
         out = _made(stream, torch.zeros, cap, N, dtype=torch.bfloat16, device=a.device)
     i32, f32 = torch.int32, torch.float32
-    ps = MoePool(_ptr(pool["counts"], i32, (E,), "counts"), _ptr(pool["offsets"], i32, (E + 1,), "offsets"), None,
-                 _ptr(pool["row_to_route"], i32, None, "row_to_route"), cap, block_m)
+    ps = MoePool(_on(dev, pool["counts"], i32, (E,), "counts"), _on(dev, pool["offsets"], i32, (E + 1,), "offsets"), None,
+                 _on(dev, pool["row_to_route"], i32, None, "row_to_route"), cap, block_m)
     d = MoeFp8Desc(E, N, K, topk, rows)
-    _launch("moe_fp8_product", library().moe_fp8_product, stream,
-            (a, a_scales, w, w_scales, out, pool["counts"], pool["offsets"], pool["row_to_route"]),
-            ctypes.byref(d), ctypes.byref(ps), _ptr(a, _E4M3, None, "a"), _ptr(a_scales, f32, (rows, K // 128), "a_scales"),
-            _ptr(w, _E4M3, (E, N, K), "w"), _ptr(w_scales, f32, (E, N // 128, K // 128), "w_scales"),
-            _ptr(out, torch.bfloat16, (cap, N), "out"))
+    _launch("moe_fp8_product", library().moe_fp8_product, dev, stream, ctypes.byref(d), ctypes.byref(ps),
+            _on(dev, a, _E4M3, None, "a"), _on(dev, a_scales, f32, (rows, K // 128), "a_scales"),
+            _on(dev, w, _E4M3, (E, N, K), "w"), _on(dev, w_scales, f32, (E, N // 128, K // 128), "w_scales"),
+            _on(dev, out, torch.bfloat16, (cap, N), "out"))
     return out
 
 
