@@ -339,6 +339,31 @@ def test_streams_and_graphs():
     del g
 
 
+@pytest.mark.parametrize("T,E,k,N,K,kernel", [
+    (1, 1, 1, 128, 65536, "few"), (400, 1, 1, 512, 65536, "tile64"), (6000, 1, 1, 2048, 65536, "tile256"),
+    (1, 1, 1, 65536, 128, "tile64"), (900, 1, 1, 65536, 128, "tile256"), (3, 512, 16, 128, 128, "few"),
+    (900, 512, 16, 256, 256, "tile64")])
+def test_largest_sizes(T, E, k, N, K, kernel):
+    """The ends of the ranges; the last block of columns and some rows checked."""
+    idx = routing(T, E, k, T)
+    pool = build(idx, E)
+    a, sa, w, sw = operands(T, E, N, K, T)
+    with Kernel() as ran:
+        out = M.fp8_product(pool, a, sa, w, sw, topk=k)
+    assert ran.names == {kernel}
+    r2r = pool["row_to_route"].cpu().numpy()
+    off, cnt = pool["offsets"].cpu().numpy(), pool["counts"].cpu().numpy()
+    for e in sorted({0, 1, E // 2, E - 1} & set(range(E))):
+        rows = np.arange(off[e], off[e] + cnt[e])[:: max(1, cnt[e] // 8)]
+        if rows.size == 0:
+            continue
+        src = torch.from_numpy(r2r[rows] // k).long().cuda()
+        ref, tol = O8.product(codes(a.view(torch.uint8)[src]), f64(sa[src]), codes(w[e, N - 128:]), f64(sw[e, -1:]))
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+        got = f64(out[torch.from_numpy(rows).cuda()][:, N - 128:])
+        assert np.all(np.abs(got - ref) <= tol), (e, np.max(np.abs(got - ref) / tol))
+
+
 def test_rows_past_32_bits():
     rows, K = 2 ** 31 // 4096 + 40, 4096
     x = torch.zeros(rows, K, dtype=BF, device="cuda")
@@ -385,3 +410,32 @@ def test_outputs_past_32_bits():
         want = M.fp8_product(tail, a.view(torch.uint8)[src].view(F8), sa[src], w, sw, topk=0)
         assert ran.names == {"tile256"} and torch.equal(out[T - 300:T], want[:300])
         del out
+
+
+@pytest.mark.parametrize("T,N", [(12, 256), (300, 1024), (4200, 4096)])
+def test_replays_for_other_routes(T, N):
+    """Pool and product captured once, replayed for routes that fall otherwise:
+    spread, all on one expert, mostly dropped, none."""
+    E, k, K = 8, 2, 256
+    layer = B.make_desc(T, 256, 256, E, k, 8)
+    idx = routing(T, E, k, 1).cuda()
+    pool = build(idx, E)
+    a, sa, w, sw = operands(T, E, N, K, 4)
+    out = torch.zeros(pool["row_to_route"].numel(), N, dtype=BF, device="cuda")
+    names = ("counts", "offsets", "route_to_row", "row_to_route")
+    M.fp8_product(pool, a, sa, w, sw, topk=k, out=out)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.build_pool(layer, idx, *(pool[n] for n in names))
+        M.fp8_product(pool, a, sa, w, sw, topk=k, out=out)
+    one = torch.full((T, k), -1, dtype=torch.int32)
+    one[:, 1] = E - 1
+    for other in (routing(T, E, k, 2), one, routing(T, E, k, 3, drop=0.95), torch.full_like(one, -1), routing(T, E, k, 2)):
+        want = M.fp8_product(build(other, E), a, sa, w, sw, topk=k)
+        idx.copy_(other)
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    del g
