@@ -167,10 +167,11 @@ __device__ __forceinline__ int rows_of(const Fp8Args& p, int e) {
   const int off = p.offsets[e];
   return off >= 0 && off < p.cap ? max(min(p.counts[e], p.cap - off), 0) : 0;
 }
-// The activation row of a route, -1: none.
+// The activation row of a route, -1: none (a_rows < 2^31).  No branches: loads
+// of several routes stay together.
 __device__ __forceinline__ int token_of(const Fp8Args& p, int route) {
   const int t = (int)((uint64_t)(uint32_t)route * p.tok_mul >> p.tok_shift);
-  return route >= 0 && t < p.a_rows ? t : -1;
+  return (int)(route >= 0) & (int)(t < (int)p.a_rows) ? t : -1;
 }
 
 // Tile b of the pool cut into M tiles of TM rows that never cross experts,
@@ -302,15 +303,16 @@ __device__ __forceinline__ bool find_tile(const PoolTable& t, int E, int b, int 
       break;
     }
   }
-  const int rows = __builtin_amdgcn_readfirstlane(t.cnt[e]);
-  const int n = (rows + TM - 1) / TM, s = __builtin_amdgcn_readfirstlane(t.end[e]) - n;
+  const int cnt = t.cnt[e], end = t.end[e], off = t.off[e];  // read together
+  const int rows = __builtin_amdgcn_readfirstlane(cnt);
+  const int n = (rows + TM - 1) / TM, s = __builtin_amdgcn_readfirstlane(end) - n;
   const int cs = s + TILE_GM * ((v - s) / TILE_GM);
   const int sz = s + n - cs < TILE_GM ? s + n - cs : TILE_GM;
   const int r = L - cs * nn, m = cs + r % sz - s;
   out.e = e;
   out.nt = r / sz;
   out.nrows = min(rows - m * TM, TM);
-  out.row0 = (long)__builtin_amdgcn_readfirstlane(t.off[e]) + (long)m * TM;
+  out.row0 = (long)__builtin_amdgcn_readfirstlane(off) + (long)m * TM;
   return true;
 }
 
@@ -422,11 +424,11 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
       // tokens of the activation rows that this lane loads: LA::NJ rows of codes, one scale
       int tk[LA::NJ + 1];
 #pragma unroll
-      for (int j = 0; j <= LA::NJ; ++j) {
-        const int q = j < LA::NJ ? row_of(j) : 64 * w + lane;
-        const int token = token_of(p, ((const int*)routes)[j < LA::NJ ? q : min(q, G::TM - 1)]);
-        tk[j] = q < t.nrows ? token : -1;
-      }
+      for (int j = 0; j <= LA::NJ; ++j)
+        tk[j] = ((const int*)routes)[j < LA::NJ ? row_of(j) : min(64 * w + lane, G::TM - 1)];
+#pragma unroll
+      for (int j = 0; j <= LA::NJ; ++j)
+        tk[j] = token_of(p, (j < LA::NJ ? row_of(j) : 64 * w + lane) < t.nrows ? tk[j] : -1);
       la.rs = make_rsrc(p.a, any ? (uint64_t)p.a_rows * p.K : 0);
       rs = make_rsrc(p.sa, any ? (uint64_t)p.a_rows * KB * 4 : 0);
 #pragma unroll
