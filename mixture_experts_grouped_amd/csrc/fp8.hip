@@ -478,10 +478,13 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   f32x4 acc[FN][FM], t[FM];
   i32x8 x[FM], a;
   float sc[FM], sl[FM];  // this stage's scales, and those of the products in t
+  // A tile's first stage adds t * sl for products of none before it: both are
+  // zero then, for the scales of the last tile need not be finite.
   auto clear = [&]() {
 #pragma unroll
     for (int j = 0; j < FM; ++j) {
       t[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      sl[j] = 0.0f;
 #pragma unroll
       for (int i = 0; i < FN; ++i) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
@@ -573,8 +576,6 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
 #pragma unroll
   for (int j = 0; j < FM; ++j) x[j] = fa.get(smem + wm * FM * 2048, j);
   read_scales(0, sw_at(0, 0), sc);
-#pragma unroll
-  for (int j = 0; j < FM; ++j) sl[j] = 0.0f;
   clear();
   while (true) {
     Tile8 nxt = cur;

@@ -439,3 +439,38 @@ def test_replays_for_other_routes(T, N):
         torch.cuda.synchronize()
         assert torch.equal(out, want)
     del g
+
+
+@pytest.mark.parametrize("T,E,N,K,kernel", [(1536, 24, 8192, 512, "tile64"), (4096, 4, 8192, 384, "tile256")])
+def test_nonfinite_blocks_stay_in_their_tiles(T, E, N, K, kernel):
+    """A NaN or an infinity in the last 128 columns of a token or of an
+    expert's weight, with more tiles than workgroups that run at once (each
+    walks several): every other result is the clean run's, bit for bit."""
+    g = torch.Generator().manual_seed(T)
+    idx = torch.randint(0, E, (T, 1), generator=g).to(torch.int32)
+    pool = build(idx, E)
+    x, w = torch.randn(T, K, generator=g).to(BF), (torch.randn(E, N, K, generator=g) * K ** -0.5).to(BF)
+    q = M.fp8_quantize_weight(w.cuda())
+    rows = M.fp8_quantize_rows(x.cuda())
+    with Kernel() as ran:
+        clean = M.fp8_product(pool, *rows, *q, topk=1)
+    assert ran.names == {kernel}
+    tok = pool["row_to_route"].long()
+    live = tok >= 0
+    bad = [int(torch.nonzero(idx[:, 0] == e)[0]) for e in (0, E // 2, E - 1)]
+    for t, value in zip(bad, (float("nan"), float("inf"), -float("inf"))):
+        x[t, K - 1] = value
+    got = M.fp8_product(pool, *M.fp8_quantize_rows(x.cuda()), *q, topk=1)
+    hit = live & torch.isin(tok, torch.tensor(bad, device="cuda"))
+    assert int(hit.sum()) == len(bad) and not torch.isfinite(got[hit]).any()
+    assert torch.equal(got[live & ~hit], clean[live & ~hit])
+    for value in (float("nan"), float("inf")):
+        e, n = E // 2, N - 256 + 5  # the block of rows N - 256 .. N - 129
+        sick = w.clone()
+        sick[e, n, K - 1] = value
+        got = M.fp8_product(pool, *rows, *M.fp8_quantize_weight(sick.cuda()), topk=1)
+        its = live.clone()
+        its[live] = (idx[:, 0].cuda()[tok[live]] == e)
+        assert not torch.isfinite(got[its, N - 256:N - 128]).any()
+        got[its, N - 256:N - 128] = clean[its, N - 256:N - 128]
+        assert torch.equal(got[live], clean[live])
