@@ -432,16 +432,20 @@ moe_status moe_router_backward(const moe_router_desc* desc, const moe_adapters* 
  * (max|m| / 448) and v is e5m2 codes times one fp32 scale (max v / 57344);
  * the step itself uses the unrounded m and v.  Codes are rounded at random:
  * y = x * (top * (1 / max)), top = 448 or 57344 (each operation rounded to
- * fp32, as in the moments above), is clamped to [-top, top], 16
- * random bits are added below its last kept mantissa bit, the rest is cut
- * (below the format's normal range the cut value is then rounded to nearest,
- * ties to even).  Without it a decaying average would stop moving once a
- * step changes it by less than half a code.  A positive v never falls to
- * code 0, so that no m is divided by eps alone.  The random bits of element
- * i of a tensor are a fixed mix of i and `seed`; pass another seed each step.
+ * fp32, as in the moments above), is clamped to [-top, top] and becomes
+ * floor(|y| / s + u) * s with y's sign: s is the format's step at y (e4m3 2^-9
+ * below 2^-6, e5m2 2^-16 below 2^-14), u one of 2^16 equally likely multiples
+ * of 2^-16 in [0, 1).  On the mean a code is y, also below the normal range,
+ * to 2^-16 s.  Without it a decaying average would stop moving once a step
+ * changes it by less than half a code.  One exception: a positive v below
+ * 2^-16 / 57344 (2.7e-10) of its run's largest is held as that, the lowest
+ * code (its element moves less than with fp32 moments), so that in a run that
+ * does not count as zero (see below) no m is divided by eps alone.  The random
+ * bits of element i of a tensor are a fixed mix of i and `seed`; pass another
+ * seed each step.
  *   x0 = i * 0x9E3779B9 + seed, x1 = (x0 ^ x0 >> 16) * 0x6A09E667,
  *   x2 = (x1 ^ x1 >> 15) * 0xBB67AE85, r = x2 ^ x2 >> 16 (mod 2^32):
- *   bits 0-15 for m, 16-31 for v.
+ *   u = bits 0-15 / 2^16 for m, bits 16-31 / 2^16 for v.
  * A run whose new moments are not finite gets a non-finite scale; one whose
  * largest moment is below 2^-100 counts as zero.
  * All-zero codes and scales are the state before the first step.

@@ -170,35 +170,43 @@ __device__ __forceinline__ void decode(u32x2 w, float s, float (&v)[8]) {
   }
 }
 
-// Codes of a run's eight values in this lane; `noise`: 16 random bits each,
-// added right below the last kept bit (bit 20 of an e4m3 value, 21 of e5m2).
+// Codes of a run's eight values in this lane.  `noise`: random bits, of which
+// the conversion takes the upper ones as u, adds u times the format's step at y
+// below the last kept place and cuts: floor(|y| / step + u) * step, the step
+// 2^-9 (e4m3) or 2^-16 (e5m2) below the normal range.  Only 16 bits are set, so
+// y's own bits below 2^-16 of a step do not matter.  Adding the noise to y's fp32
+// mantissa and rounding to nearest instead puts it below the place that the
+// format keeps once y is subnormal: such moments were rounded to nearest, so
+// that small ones neither grew nor decayed.
 // Returns the run's scale.  A maximum that is not finite makes the scale so.
 template <bool E5M2>
 __device__ __forceinline__ float encode(const float (&x)[8], const uint32_t (&noise)[8], u32x2& w) {
   constexpr float TOP = E5M2 ? E5M2_MAX : E4M3_MAX;
-  constexpr int CUT = E5M2 ? 21 : 20;
   uint32_t m = 0;
 #pragma unroll
   for (int c = 0; c < 8; ++c) m = max(m, mag(x[c]));
   const float amax = __uint_as_float(row_max(m));
   const bool zero = amax < TINY;
   const float inv = zero ? 0.0f : mul1(1.0f / amax, TOP);
+  float y[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    y[c] = fminf(fmaxf(x[c] * inv, E5M2 ? 0.0f : -TOP), TOP);
+    if (E5M2 && x[c] > 0.0f) y[c] = fmaxf(y[c], 0x1p-16f);
+  }
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float y[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      float q = fminf(fmaxf(x[4 * h + c] * inv, E5M2 ? 0.0f : -TOP), TOP);
-      if (E5M2 && x[4 * h + c] > 0.0f) q = fmaxf(q, 0x1p-16f);
-      y[c] = __uint_as_float((__float_as_uint(q) + (noise[4 * h + c] << (CUT - 16))) & ~((1u << CUT) - 1u));
-    }
     int p = 0;
     if constexpr (E5M2) {
-      p = __builtin_amdgcn_cvt_pk_bf8_f32(y[0], y[1], p, false);
-      p = __builtin_amdgcn_cvt_pk_bf8_f32(y[2], y[3], p, true);
+      p = __builtin_amdgcn_cvt_sr_bf8_f32(y[4 * h], (int)noise[4 * h], p, 0);
+      p = __builtin_amdgcn_cvt_sr_bf8_f32(y[4 * h + 1], (int)noise[4 * h + 1], p, 1);
+      p = __builtin_amdgcn_cvt_sr_bf8_f32(y[4 * h + 2], (int)noise[4 * h + 2], p, 2);
+      p = __builtin_amdgcn_cvt_sr_bf8_f32(y[4 * h + 3], (int)noise[4 * h + 3], p, 3);
     } else {
-      p = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], p, false);
-      p = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], p, true);
+      p = __builtin_amdgcn_cvt_sr_fp8_f32(y[4 * h], (int)noise[4 * h], p, 0);
+      p = __builtin_amdgcn_cvt_sr_fp8_f32(y[4 * h + 1], (int)noise[4 * h + 1], p, 1);
+      p = __builtin_amdgcn_cvt_sr_fp8_f32(y[4 * h + 2], (int)noise[4 * h + 2], p, 2);
+      p = __builtin_amdgcn_cvt_sr_fp8_f32(y[4 * h + 3], (int)noise[4 * h + 3], p, 3);
     }
     w[h] = (uint32_t)p;
   }
@@ -260,8 +268,8 @@ __global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs<MASTER, S8> a) {
 #pragma unroll
     for (int c = 0; c < 8; ++c) {
       const uint32_t r = noise_of((uint32_t)(i + c), seed);
-      lo[c] = r & 0xFFFFu;
-      hi[c] = r >> 16;
+      lo[c] = r << 16;
+      hi[c] = r & 0xFFFF0000u;
     }
     u32x2 w;
     const float ms = encode<false>(m, lo, w);

@@ -26,6 +26,7 @@ def _table(exp_bits: int, man_bits: int, bias: int, ieee: bool) -> np.ndarray:
 E4M3 = _table(4, 3, 7, False)
 E5M2 = _table(5, 2, 15, True)
 FORMATS = {"e4m3": (E4M3, 448.0, 3), "e5m2": (E5M2, 57344.0, 2)}
+LOWEST = {"e4m3": -6, "e5m2": -14}  # exponent of the smallest normal value, and of all below it
 
 
 def decode(codes: np.ndarray, fmt: str) -> np.ndarray:
@@ -101,7 +102,7 @@ def noise(n: int, seed: int) -> np.ndarray:
 
 def moments8(x: np.ndarray, rnd16: np.ndarray, fmt: str) -> Tuple[np.ndarray, np.ndarray]:
     """(codes [n], scales [ceil(n/128)] float64) of flat moments x: |y| moved
-    up by rnd / 2^16 of its last kept place and cut there."""
+    up by rnd / 2^16 of the format's step there and cut to whole steps."""
     _, top, man = FORMATS[fmt]
     n = x.size
     pad = -n % BLOCK
@@ -113,7 +114,7 @@ def moments8(x: np.ndarray, rnd16: np.ndarray, fmt: str) -> Tuple[np.ndarray, np
     if fmt == "e5m2":
         y = np.where(x > 0, np.maximum(y, 2.0 ** -16), 0.0)
     m, e = np.frexp(np.abs(y))  # |y| = m 2^e, m in [0.5, 1)
-    last = np.ldexp(1.0, e - 1 - man)
+    last = np.ldexp(1.0, np.maximum(e - 1, LOWEST[fmt]) - man)
     cut = np.where(y == 0, 0.0, np.floor(np.abs(y) / last + rnd16 / 65536.0) * last)
     return nearest(np.copysign(cut, y), fmt), np.where(live, amax / top, 0.0)
 

@@ -245,3 +245,51 @@ def test_more_elements_than_32_bits_count():
     ref.step()
     assert torch.equal(big[-tail:], p) and torch.equal(opt.states["v"][0][-tail:], ref.states["v"][0])
     assert not big[:2 ** 20].any()
+
+
+def low_run(ratio):
+    """Gradients of 512 runs: the first element of each 1, the others `ratio`."""
+    g = torch.full((128 * 512,), ratio, device="cuda")
+    g[::128] = 1.0
+    return g, np.arange(128 * 512) % 128 != 0
+
+
+@pytest.mark.parametrize("name,ratio", [("m", 1e-5), ("m", 3e-6), ("m", 1e-6), ("v", 3e-5), ("v", 2e-5)])
+def test_moments_far_below_their_runs_largest_are_right_on_the_mean(name, ratio):
+    """Below the formats' normal range (m 3.5e-5, v 1.1e-9 of the largest) the
+    codes are whole steps of 2^-9 or 2^-16, taken up or down at random: one
+    rounding's variance is at most a quarter of a squared step, and the mean of
+    65,024 of them stays within five of its deviations (and fp32's own
+    roundings of the moment and of its quotient)."""
+    g, rest = low_run(ratio)
+    opt = M.MoeAdamW([torch.zeros_like(g)], [g], state_bits=8, betas=(0.9, 0.99))
+    opt.step()
+    want = 0.1 * ratio if name == "m" else 0.01 * ratio ** 2
+    step = (2.0 ** -9 if name == "m" else 2.0 ** -16) * float(opt.states[name + "_scale"][0][0])
+    got = values8(opt, 0, name)[rest]
+    assert 0.1 < want / step < 8 and got.min() <= want <= got.max() and got.max() - got.min() <= step * (1 + 1e-6)
+    assert abs(got.mean() - want) <= 5 * 0.5 * step / np.sqrt(rest.sum()) + 8 * 2.0 ** -24 * want
+
+
+def test_first_moments_far_below_their_runs_largest_decay():
+    """A gradient that ends: eleven steps of 0.9 later the mean is 0.9^11 of
+    what it was, within five deviations of the roundings' sum (each at most a
+    quarter of a squared step, the older ones decayed: in all at most 1/4 / (1
+    - 0.81) squared steps of the last scale, the scales only grow)."""
+    g, rest = low_run(2e-5)
+    opt = M.MoeAdamW([torch.zeros_like(g)], [g], state_bits=8, betas=(0.9, 0.99))
+    opt.step()
+    g[torch.from_numpy(rest).cuda()] = 0.0
+    for _ in range(11):
+        opt.step()
+    step = 2.0 ** -9 * float(opt.states["m_scale"][0][0])
+    got, want = values8(opt, 0, "m")[rest].mean(), 2e-6 * 0.9 ** 11
+    assert abs(got - want) <= 5 * np.sqrt(0.25 / 0.19) * step / np.sqrt(rest.sum())
+
+
+def test_the_smallest_second_moments_keep_the_lowest_code():
+    g, rest = low_run(1e-6)
+    opt = M.MoeAdamW([torch.zeros_like(g)], [g], state_bits=8)
+    for _ in range(5):
+        opt.step()
+        assert (codes(opt.states["v"][0])[rest] == 1).all()

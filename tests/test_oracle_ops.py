@@ -98,6 +98,22 @@ def test_moments_round_without_bias():
         assert np.allclose(O8.decode(c, fmt).reshape(-1, 128)[:, 0], O8.FORMATS[fmt][1])
 
 
+def test_moments_below_the_normal_range_round_without_bias():
+    """Over all 2^16 noise values the mean is the value to 2^-16 of a step."""
+    for fmt, low in (("e4m3", 2.0 ** -9), ("e5m2", 2.0 ** -16)):
+        top = O8.FORMATS[fmt][1]
+        for steps in (1.0, 1.3, 2.29, 3.6, 7.9):
+            x = np.full((1 << 16, 128), steps * low / top)
+            x[:, 0] = 1.0
+            c, s = O8.moments8(x.reshape(-1), np.repeat(np.arange(1 << 16), 128), fmt)
+            v = (O8.decode(c, fmt).reshape(-1, 128) / low)[:, 1]
+            assert abs(v.mean() - steps) <= 2.0 ** -16 and set(v) <= {np.floor(steps), np.ceil(steps)}
+    x = np.zeros(128)
+    x[:3] = 448.0, 0.229 * 2.0 ** -9, -0.229 * 2.0 ** -9
+    up = np.array([O8.decode(O8.moments8(x, np.full(128, r), "e4m3")[0], "e4m3")[1:3] for r in range(0, 1 << 16, 7)])
+    assert abs(up[:, 0].mean() / 2.0 ** -9 - 0.229) < 1e-3 and np.array_equal(up[:, 1], -up[:, 0])
+
+
 def test_positive_second_moment_keeps_a_code():
     x = np.concatenate([[1.0], np.full(127, 1e-12), [0.0]])
     c, s = O8.moments8(x, np.zeros(129), "e5m2")
