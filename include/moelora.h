@@ -423,7 +423,8 @@ moe_status moe_router_backward(const moe_router_desc* desc, const moe_adapters* 
  * layers and adapters).  Per element, with g = grad_scale * grad:
  *   m <- beta1 m + (1 - beta1) g        v <- beta2 v + (1 - beta2) g^2
  *   p <- p (1 - lr weight_decay) - lr (m / bias1) / (sqrt(v / bias2) + eps)
- * with bias1 = 1 - beta1^step, bias2 = 1 - beta2^step, in fp32.  p is the
+ * with bias1 = 1 - beta1^step, bias2 = 1 - beta2^step, in fp32; p's whole
+ * change, decay included, is formed first and subtracted once.  p is the
  * fp32 master copy if there is one (then `param` receives its rounding), else
  * `param` itself.
  *

@@ -236,7 +236,7 @@ __global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs<MASTER, S8> a) {
     gs = a.control->grad_scale;
     seed = a.control->seed;
   }
-  const float step = lr / c1, ic2 = 1.0f / c2, keep = 1.0f - lr * a.wd;
+  const float step = lr / c1, ic2 = 1.0f / c2, decay = lr * a.wd;
   float p[8], g[8], m[8], v[8];
   load8((const G*)t.grad, i, n, g);
   if constexpr (MASTER)
@@ -259,7 +259,9 @@ __global__ __launch_bounds__(AW_THREADS) void k_adamw(AdamwArgs<MASTER, S8> a) {
     // then follows from the inputs alone, for anyone who computes it again
     m[c] = add1(mul1(m[c], a.b1), mul1(gc, a.omb1));
     v[c] = add1(mul1(v[c], a.b2), mul1(mul1(gc, gc), a.omb2));
-    p[c] = p[c] * keep - step * m[c] / (sqrtf(v[c] * ic2) + a.eps);
+    // the whole change first, then one subtraction: 1 - decay in fp32 would be
+    // off by up to 2^-25 in every step alike (all of a decay below that)
+    p[c] -= fmaf(decay, p[c], step * m[c] / (sqrtf(v[c] * ic2) + a.eps));
   }
   store8((P*)t.param, i, n, p);
   if constexpr (MASTER) store8(t.master, i, n, p);

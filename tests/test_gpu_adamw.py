@@ -293,3 +293,37 @@ def test_the_smallest_second_moments_keep_the_lowest_code():
     for _ in range(5):
         opt.step()
         assert (codes(opt.states["v"][0])[rest] == 1).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_small_weight_decay_of_one_step(bits):
+    """lr weight_decay = 1e-7 of values in [1, 2): 0.84 to 1.7 of their last
+    place.  The change is exact to a few fp32 roundings of itself, so the
+    result is the rounding of the exact one (half a place, 2^-24)."""
+    p = (1 + torch.rand(1 << 16, generator=torch.Generator().manual_seed(3))).cuda()
+    before = f64(p)
+    M.MoeAdamW([p], [torch.zeros_like(p)], state_bits=bits, lr=1e-5, weight_decay=0.01).step()
+    want = before * (1 - 1e-7)
+    assert np.all(np.abs(f64(p) - want) <= 2.0 ** -24 + 4 * 2.0 ** -24 * 1e-7 * before)
+
+
+def test_small_weight_decay_over_many_steps():
+    """lr weight_decay = 2e-8, a sixth to a third of half a place, beside
+    updates of many places: each step's rounding is up or down at random, so
+    the mean of 65,536 elements over 200 steps is off by five deviations of
+    their sum, 5 * 2^-23 / sqrt(12) * sqrt(200 / 65536) = 0.08 * 2^-23, and by
+    the updates' own relative error, at most 24 * 2^-24 of 200 * lr in magnitude
+    (each is lr m / sqrt(v), at most a few lr).  A decay that is left out is 33 places off."""
+    n, lr, wd = 1 << 16, 2e-6, 0.01
+    g = torch.Generator(device="cuda").manual_seed(7)
+    p, grad = 1 + torch.rand(n, generator=g, device="cuda"), torch.zeros(n, device="cuda")
+    q, m, v = p.double(), torch.zeros(n, device="cuda").double(), torch.zeros(n, device="cuda").double()
+    opt = M.MoeAdamW([p], [grad], lr=lr, betas=(0.9, 0.99), weight_decay=wd)
+    for step in range(1, 201):
+        grad.normal_(generator=g)
+        opt.step()
+        m = 0.9 * m + 0.1 * grad.double()
+        v = 0.99 * v + 0.01 * grad.double().square()
+        q = q - lr * wd * q - lr * (m / (1 - 0.9 ** step)) / ((v / (1 - 0.99 ** step)).sqrt() + 1e-8)
+    off = float((p.double() - q).mean())
+    assert abs(off) <= 0.08 * 2.0 ** -23 + 24 * 2.0 ** -24 * 200 * 4 * lr
