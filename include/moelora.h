@@ -511,7 +511,7 @@ moe_status moe_adamw_step(const moe_adamw_desc* desc, const moe_adamw_tensor* te
  *   act MOE_ACT_SWIGLU / MOE_ACT_GEGLU: src [rows, 2K] bf16 = [gate | up],
  *     x = act(gate) * up in fp32.
  *   codes [rows, K] bytes, scales [rows, K / 128] fp32.  K % 128 == 0 (else
- *   MOE_ERR_UNSUPPORTED), K at most 65536, rows * K < 2^35, rows >= 0 (0: nothing is done). */
+ *   MOE_ERR_UNSUPPORTED), K at most 65536, rows * K at most 2^35 - 2048, rows >= 0 (0: nothing is done). */
 moe_status moe_fp8_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes, float* scales,
                                  void* stream);
 

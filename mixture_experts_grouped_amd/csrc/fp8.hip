@@ -778,8 +778,9 @@ extern "C" {
 moe_status moe_fp8_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes, float* scales,
                                  void* stream) {
   if (rows < 0 || K < 1) return MOE_ERR_INVALID;
-  // a launch holds fewer than 2^32 threads, eight columns each
-  if (K % 128 != 0 || K > MAX_DIM || rows >= (int64_t)1 << 31 || rows * K >= (int64_t)1 << 35) return MOE_ERR_UNSUPPORTED;
+  // a launch holds fewer than 2^32 threads, eight columns each, in whole workgroups of 256
+  if (K % 128 != 0 || K > MAX_DIM || rows >= (int64_t)1 << 31 || rows * K > ((int64_t)1 << 35) - 2048)
+    return MOE_ERR_UNSUPPORTED;
   if (act != MOE_FP8_PLAIN && act != MOE_ACT_SWIGLU && act != MOE_ACT_GEGLU) return MOE_ERR_UNSUPPORTED;
   if (rows == 0) return MOE_OK;
   if (!aligned16(src) || !aligned16(codes) || !aligned(scales, 4)) return MOE_ERR_INVALID;

@@ -199,3 +199,13 @@ def test_binding_refuses_host_tensors_and_wrong_shapes():
     r = M.MoeRouter(4, 8, 2, device="cpu")
     with pytest.raises(ValueError):
         r.forward(torch.zeros(4, 8))
+
+
+def test_fp8_rows_fill_a_launch():
+    """A launch holds fewer than 2^32 threads in whole workgroups of 256, eight
+    columns a thread: rows * K is at most 2^35 - 2048."""
+    f = B.library().moe_fp8_quantize_rows
+    src, codes, scales = 1 << 40, 1 << 42, 1 << 43  # far apart: nothing overlaps
+    for rows, K in (((1 << 28) - 1, 128), ((1 << 28) - 15, 128), ((1 << 26) - 1, 512), (1 << 26, 512)):
+        for act in (-1, B.MOE_ACT_SWIGLU, B.MOE_ACT_GEGLU):
+            assert f(src, rows, K, act, codes, scales, None) == UNS, (rows, K)
