@@ -54,6 +54,27 @@ __device__ __forceinline__ void widen8(u32x4 w, float (&v)[8]) {
   }
 }
 
+// The normal distribution function to fp32's relative precision: a block in its
+// lower tail is scaled by its own largest value, which norm_cdf's absolute error
+// of 1e-7 would shift (1 % at -8).  Phi(g) = 1/2 exp(-z^2) f(z) at z = -g / sqrt 2
+// >= 0, with f(z) = exp(z^2) erfc(z) = t P(t), t = 1 / (1 + 0.46 z): P of degree 7 is
+// fitted for the smallest largest relative error over all z, 6.8e-7 (8.7e-7
+// evaluated in fp32); here halved.  98,304 x 2048: 200 us, 195 with norm_cdf, 302
+// with the math library's erfcf.
+__device__ __forceinline__ float norm_cdf_rel(float g) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.46f * 0.70710678118654752f, fabsf(g), 1.0f));
+  float q = 0.0338571894f;
+  q = fmaf(q, t, -0.113314702f);
+  q = fmaf(q, t, 0.084595587f);
+  q = fmaf(q, t, 0.0263052463f);
+  q = fmaf(q, t, 0.093423918f);
+  q = fmaf(q, t, 0.115590938f);
+  q = fmaf(q, t, 0.129778633f);
+  q = fmaf(q, t, 0.12976353f);
+  const float tail = q * t * __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g);  // log2(e) / 2
+  return g < 0.0f ? tail : 1.0f - tail;
+}
+
 // Eight columns a thread, a block of 128 in one DPP row: one pass, bound by
 // memory (16,384 x 4096: 36 us, 5.7 TB/s; gated 2,064 x 2048 5.2 us, latency).
 // ACT < 0: src is [rows, K]; else [rows, 2K] = gate | up.
@@ -72,7 +93,7 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const uint16_t* __restrict__ s
     widen8(p[0], v);
     widen8(p[K8], u);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = (ACT == MOE_ACT_SWIGLU ? v[q] * sigmoidf_(v[q]) : v[q] * norm_cdf(v[q])) * u[q];
+    for (int q = 0; q < 8; ++q) v[q] = (ACT == MOE_ACT_SWIGLU ? v[q] * sigmoidf_(v[q]) : v[q] * norm_cdf_rel(v[q])) * u[q];
   }
   uint32_t m = 0;
 #pragma unroll

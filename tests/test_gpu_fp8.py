@@ -474,3 +474,26 @@ def test_nonfinite_blocks_stay_in_their_tiles(T, E, N, K, kernel):
         assert not torch.isfinite(got[its, N - 256:N - 128]).any()
         got[its, N - 256:N - 128] = clean[its, N - 256:N - 128]
         assert torch.equal(got[live], clean[live])
+
+
+@pytest.mark.parametrize("act", ["swiglu", "geglu"])
+def test_gated_rows_of_small_activations(act):
+    """Blocks whose gates lie all in the activation's lower tail: their scale is
+    that of small values alone.  x = gate Phi(gate) up or gate sigmoid(gate) up in
+    fp32: the tail's exponent, gate^2 / 2 or -gate, is off by two roundings of
+    itself (2^-23), the functions and products by 32 * 2^-24 in all."""
+    rows, K = 10, 256
+    g = torch.Generator().manual_seed(6)
+    x = torch.cat([-(torch.arange(2.0, 2.0 + rows)[:, None] + torch.rand(rows, K, generator=g)),
+                   1 + torch.rand(rows, K, generator=g)], 1).to(BF)
+    c, s = M.fp8_quantize_rows(x.cuda(), act=act)
+    gate, up = x[:, :K].double(), x[:, K:].double()
+    tail = 0.5 * torch.erfc(-gate * 0.5 ** 0.5) if act == "geglu" else torch.sigmoid(gate)
+    h = (gate * tail * up).numpy()
+    size = (gate.square() if act == "geglu" else gate.abs()).numpy()
+    rel = 2.0 ** -23 * size + 32 * 2.0 ** -24
+    amax = np.abs(h).reshape(rows, -1, 128).max(2) / 448
+    assert amax.min() > 2.0 ** -98
+    assert np.all(np.abs(f64(s) - amax) <= rel.reshape(rows, -1, 128).max(2) * amax)
+    back, spread = O8.decode(codes(c), "e4m3") * np.repeat(f64(s), 128, 1), np.repeat(f64(s), 128, 1)
+    assert np.all(np.abs(back - h) <= 2.0 ** -4 * np.abs(h) * (1 + rel) + rel * np.abs(h) + spread * 2.0 ** -10)
