@@ -665,8 +665,9 @@ class MoeAdamW:
     """AdamW over a list of tensors (the factors of one or more layers) in one
     call per step.  params: bf16 or fp32, all of one type, updated in place;
     grads: bf16 or fp32 buffers of the same sizes that are read at each step
-    (MoeLoraLayer.grads, say; all these tensors stay where they are, the
-    optimiser keeps their addresses); masters: fp32 copies of bf16 params that are
+    (MoeLoraLayer.grads, say; all these tensors stay where they are: the
+    optimiser keeps their memory, and goes on with it if a tensor is given
+    other memory, by `p.data = ...`, say); masters: fp32 copies of bf16 params that are
     updated instead, the params getting their rounding.  state_bits 32 or 8
     (see include/moelora.h); states: {"m": [...], "v": [...], "m_scale":
     [...], "v_scale": [...]} to go on from, else zeros."""
@@ -719,6 +720,8 @@ class MoeAdamW:
                 _ptr(p, ptype, None, "params"), None if masters is None else _ptr(masters[i], f32, None, "masters"),
                 _ptr(self.grads[i], gtype, None, "grads"), _ptr(self.states["m"][i], kinds["m"], None, "m"),
                 _ptr(self.states["v"][i], kinds["v"], None, "v"), *sc, n)
+        # aliases: the memory outlives a replacement of a tensor's own
+        self._held = [t.detach() for ts in (self.params, self.grads, self.masters or [], *self.states.values()) for t in ts]
         # memory that a step writes belongs to one tensor alone
         spans = [(t.data_ptr(), t.numel() * t.element_size(), k) for k, ts in
                  (("params", self.params), ("grads", self.grads), ("masters", self.masters or []), *self.states.items())

@@ -327,3 +327,18 @@ def test_small_weight_decay_over_many_steps():
         q = q - lr * wd * q - lr * (m / (1 - 0.9 ** step)) / ((v / (1 - 0.99 ** step)).sqrt() + 1e-8)
     off = float((p.double() - q).mean())
     assert abs(off) <= 0.08 * 2.0 ** -23 + 24 * 2.0 ** -24 * 200 * 4 * lr
+
+
+def test_memory_replaced_after_construction_stays_the_optimisers():
+    """`p.data = ...` leaves the optimiser with the memory it was made for: it
+    is not handed to another tensor while the optimiser writes it."""
+    n = 1 << 20
+    p, grad, master = torch.zeros(n, dtype=BF, device="cuda"), torch.ones(n, dtype=BF, device="cuda"), torch.zeros(n, device="cuda")
+    opt = M.MoeAdamW([p], [grad], masters=[master], state_bits=8, lr=0.5)
+    held = {t.data_ptr() for t in (p, grad, master)}
+    for t in (p, grad, master):
+        t.data = torch.zeros_like(t)
+    others = [torch.full((n,), 7.0, dtype=dt, device="cuda") for dt in (BF, BF, F32)]
+    assert not held & {t.data_ptr() for t in others}
+    opt.step()
+    assert all((t == 7.0).all() for t in others) and not any(t.any() for t in (p, grad, master))
