@@ -621,8 +621,11 @@ class MoeRouter:
         self._dp = ctypes.byref(self.desc)
         self._dev = self.topk_idx.get_device()
         self._lshape, self._kshape, self._tshape, self._cshape, self._rshape = (T, E), (T, topk), (T,), (na, E), (na,)
-        self._outs = tuple(t.data_ptr() for t in (self.topk_idx, self.topk_w, self.counts, self.active, self.loss,
-                                                  self.device_error, self.workspace)) + (nbytes,)
+        # aliases: the addresses that forward writes stay this router's, whatever the attributes are given
+        self._held = [t.detach() for t in (self.topk_idx, self.topk_w, self.counts, self.active, self.loss,
+                                           self.device_error, self.workspace)]
+        self._results, self._grad = tuple(self._held[:5]), self.grad_logits
+        self._outs = tuple(t.data_ptr() for t in self._held) + (nbytes,)
 
     def forward(self, logits: torch.Tensor, valid: Optional[torch.Tensor] = None, stream=None):
         """logits [T, E]; valid [T] uint8 (0: a padding token) or None.
@@ -635,12 +638,12 @@ class MoeRouter:
             bad = self.dropped_tokens(stream)
             if bad:
                 raise FloatingPointError(f"moe_router_forward: {bad} valid token(s) with a NaN or +inf logit were dropped")
-        return self.topk_idx, self.topk_w, self.counts, self.active, self.loss
+        return self._results
 
     def dropped_tokens(self, stream=None) -> int:
         """Valid tokens the last forward dropped for a NaN or +inf logit (syncs)."""
         _sync(stream)
-        return int(self.device_error.item())
+        return int(self._held[5].item())
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, counts: torch.Tensor, active: torch.Tensor,
                  grad_topk_w: Optional[torch.Tensor] = None, grad_loss: Optional[torch.Tensor] = None,
@@ -648,14 +651,18 @@ class MoeRouter:
         """The gradient to the logits, [T, E] of their type, from the
         forward's topk_idx, counts and active (the router's own buffers after
         forward, or copies) and the gradients of topk_w [T, k] and of the
-        loss [roots] (None: zero)."""
+        loss [roots] (None: zero).  It is written to self.grad_logits, which
+        may be given another tensor of that shape and type, logits itself too."""
         f32, i32, dev = torch.float32, torch.int32, self._dev
+        if self.grad_logits is not self._grad:  # another buffer, the logits' own, say
+            _on(dev, self.grad_logits, self.dtype, self._lshape, "grad_logits")
+            self._grad = self.grad_logits
         _launch("moe_router_backward", library().moe_router_backward, dev, stream, self._dp, self._adp,
                 _on(dev, logits, self.dtype, self._lshape, "logits"), _on(dev, valid, torch.uint8, self._tshape, "valid"),
                 _on(dev, topk_idx, i32, self._kshape, "topk_idx"), _on(dev, counts, i32, self._cshape, "counts"),
                 _on(dev, active, i32, self._rshape, "active"), _on(dev, grad_topk_w, f32, self._kshape, "grad_topk_w"),
-                _on(dev, grad_loss, f32, self._rshape, "grad_loss"), self.grad_logits.data_ptr())
-        return self.grad_logits
+                _on(dev, grad_loss, f32, self._rshape, "grad_loss"), self._grad.data_ptr())
+        return self._grad
 
 
 # --------------------------------------------------------------------------

@@ -212,3 +212,27 @@ def test_router_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip((*got, r.grad_logits), want))
     del g
+
+
+def test_router_writes_its_own_buffers_only():
+    """The results are the buffers made with the router, also where an attribute
+    has been given another tensor since; their memory is not another's."""
+    T, E, k = 4096, 64, 6
+    l, _, _, _ = make(T, E, torch.float32, 31)
+    r, ref = M.MoeRouter(T, E, k), M.MoeRouter(T, E, k)
+    want = [t.clone() for t in ref.forward(l.cuda())]
+    names = ("topk_idx", "topk_w", "counts", "active", "loss", "device_error", "workspace")
+    for n in names:
+        setattr(r, n, torch.zeros_like(getattr(r, n)))
+    shapes = [(getattr(r, n).shape, getattr(r, n).dtype) for n in names]
+    others = [torch.full(s, 7, dtype=dt, device="cuda") for s, dt in shapes]
+    got = r.forward(l.cuda())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert all((t == 7).all() for t in others)
+    for n in names[:5]:
+        assert not getattr(r, n).any()
+    idx, _, counts, active, _ = got
+    for other in (torch.zeros(T - 1, E), torch.zeros(T, E, dtype=torch.bfloat16), torch.zeros(E, T).t()):
+        r.grad_logits = other.cuda()
+        with pytest.raises(ValueError, match="grad_logits"):
+            r.backward(l.cuda(), idx, counts, active)
