@@ -482,7 +482,7 @@ typedef struct moe_adamw_desc {
  * non-empty tensors 16-byte aligned (scales 4-byte); no buffer of the call
  * may overlap another one that it writes (within a tensor this is checked).
  * lr, weight_decay >= 0, eps > 0,
- * betas in [0, 1), step >= 1, all finite, else MOE_ERR_INVALID. */
+ * betas in [0, 1), step >= 1, all finite in fp32, else MOE_ERR_INVALID. */
 moe_status moe_adamw_step(const moe_adamw_desc* desc, const moe_adamw_tensor* tensors, int32_t count, void* stream);
 
 /* ------------------------------------------------------------------------

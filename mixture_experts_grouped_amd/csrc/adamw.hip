@@ -336,18 +336,18 @@ void launch_params(const AdamwHead& h, const moe_adamw_desc* d, bool master, con
 }
 
 bool unit(double b) { return b >= 0.0 && b < 1.0; }  // false for NaN
-bool positive(double v) { return std::isfinite(v) && v >= 0.0; }
+bool finite(double v) { return std::isfinite((float)v); }  // as the kernel takes it
+bool positive(double v) { return finite(v) && v >= 0.0; }
 
 moe_status check_adamw(const moe_adamw_desc* d) {
   if (d == nullptr) return MOE_ERR_INVALID;
   for (const int32_t t : {d->param_type, d->grad_type})
     if (t != MOE_TYPE_F32 && t != MOE_TYPE_BF16) return MOE_ERR_UNSUPPORTED;
   if (d->state_bits != 32 && d->state_bits != 8) return MOE_ERR_UNSUPPORTED;
-  if (!unit(d->beta1) || !unit(d->beta2) || !positive(d->weight_decay) || !std::isfinite(d->eps) || d->eps <= 0.0 ||
-      (float)d->eps == 0.0f)
+  if (!unit(d->beta1) || !unit(d->beta2) || !positive(d->weight_decay) || !finite(d->eps) || !((float)d->eps > 0.0f))
     return MOE_ERR_INVALID;
   if (d->control != nullptr) return aligned(d->control, 4) ? MOE_OK : MOE_ERR_INVALID;
-  if (!positive(d->lr) || !std::isfinite(d->grad_scale) || d->step < 1) return MOE_ERR_INVALID;
+  if (!positive(d->lr) || !finite(d->grad_scale) || d->step < 1) return MOE_ERR_INVALID;
   return MOE_OK;
 }
 

@@ -209,3 +209,9 @@ def test_fp8_rows_fill_a_launch():
     for rows, K in (((1 << 28) - 1, 128), ((1 << 28) - 15, 128), ((1 << 26) - 1, 512), (1 << 26, 512)):
         for act in (-1, B.MOE_ACT_SWIGLU, B.MOE_ACT_GEGLU):
             assert f(src, rows, K, act, codes, scales, None) == UNS, (rows, K)
+
+
+@pytest.mark.parametrize("kw", [dict(lr=1e39), dict(weight_decay=1e39), dict(grad_scale=-1e39), dict(eps=1e39)])
+def test_adamw_values_beyond_fp32(kw):
+    """The step computes in fp32: a value that is infinite there is refused."""
+    assert adam(adam_desc(**kw), adam_tensor()) == INV
