@@ -10,7 +10,6 @@ is no fallback path.
 from __future__ import annotations
 
 import ctypes
-import math
 import os
 from typing import Dict, Optional, Sequence, Tuple
 
@@ -764,10 +763,14 @@ class MoeAdamW:
                       seed: Optional[int] = None) -> None:
         """Fill a control buffer (int32 [5] on the device) with one step's
         values: before each replay of a graph that captured a step with it."""
-        if not (step >= 1 and math.isfinite(lr) and lr >= 0 and math.isfinite(grad_scale)):
-            raise ValueError("write_control: step >= 1, lr >= 0 and grad_scale, all finite")
+        _on(self._dev, control, torch.int32, (5,), "control")
+        if step < 1:
+            raise ValueError("write_control: step >= 1")
         f = torch.tensor([lr, 1.0 - self.betas[0] ** step, 1.0 - self.betas[1] ** step, grad_scale],
-                         dtype=torch.float64).to(torch.float32).view(torch.int32)
+                         dtype=torch.float64).to(torch.float32)
+        if not (lr >= 0 and bool(torch.isfinite(f).all())):
+            raise ValueError("write_control: lr >= 0 and grad_scale, finite in fp32")
+        f = f.view(torch.int32)
         s = (step if seed is None else seed) & 0xFFFFFFFF
         control.copy_(torch.cat([f, torch.tensor([s - (1 << 32) if s >> 31 else s], dtype=torch.int32)]))
 

@@ -342,3 +342,18 @@ def test_memory_replaced_after_construction_stays_the_optimisers():
     assert not held & {t.data_ptr() for t in others}
     opt.step()
     assert all((t == 7.0).all() for t in others) and not any(t.any() for t in (p, grad, master))
+
+
+def test_control_values_beyond_fp32_and_wrong_buffers():
+    ps, gs = tensors([8], F32, F32, 22)
+    opt, c = M.MoeAdamW(ps, gs), torch.zeros(5, dtype=torch.int32, device="cuda")
+    for kw in (dict(lr=1e39, step=1), dict(lr=1.0, step=1, grad_scale=-1e39), dict(lr=1.0, step=-1)):
+        with pytest.raises(ValueError, match="write_control"):
+            opt.write_control(c, **kw)
+    for other in (c.float(), c.long(), torch.zeros(6, dtype=torch.int32, device="cuda"), c[None].clone()):
+        with pytest.raises(ValueError, match="control"):
+            opt.write_control(other, 1e-3, 1)
+        assert not other.any()
+    opt.write_control(c, 0.25, 3, grad_scale=0.5, seed=1 << 31)
+    f = c[:4].view(torch.float32).tolist()
+    assert f[0] == 0.25 and f[3] == 0.5 and abs(f[1] - 0.271) < 1e-6 and int(c[4]) == -(1 << 31)

@@ -215,3 +215,16 @@ def test_fp8_rows_fill_a_launch():
 def test_adamw_values_beyond_fp32(kw):
     """The step computes in fp32: a value that is infinite there is refused."""
     assert adam(adam_desc(**kw), adam_tensor()) == INV
+
+
+@pytest.mark.parametrize("control", [torch.zeros(5), torch.zeros(5, dtype=torch.int64), torch.zeros(6, dtype=torch.int32),
+                                     torch.zeros(1, 5, dtype=torch.int32), torch.zeros(10, dtype=torch.int32)[::2],
+                                     torch.zeros(5, dtype=torch.int32)])
+def test_control_buffers_are_checked(control):
+    """A control buffer is int32 [5], contiguous, on the optimiser's device."""
+    opt = object.__new__(M.MoeAdamW)
+    opt.betas, opt._dev = (0.9, 0.99), 0
+    before = control.clone()
+    with pytest.raises(ValueError, match="control"):
+        opt.write_control(control, 1e-3, 1)
+    assert torch.equal(control, before)
