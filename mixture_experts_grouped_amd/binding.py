@@ -490,11 +490,11 @@ def moe_lora_backward_multi(desc: MoeLoraDesc, roots: Sequence[int], pool: Dict[
     _check(st, "moe_lora_backward_multi")
 
 
-def _sync(stream) -> None:
+def _sync(stream, dev: Optional[int] = None) -> None:
     if hasattr(stream, "synchronize"):
         stream.synchronize()
     else:
-        torch.cuda.synchronize()
+        torch.cuda.synchronize(dev)
 
 
 def moe_lora_split_e2m3x2(src: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -641,7 +641,7 @@ class MoeRouter:
 
     def dropped_tokens(self, stream=None) -> int:
         """Valid tokens the last forward dropped for a NaN or +inf logit (syncs)."""
-        _sync(stream)
+        _sync(stream, self._dev)
         return int(self._held[5].item())
 
     def backward(self, logits: torch.Tensor, topk_idx: torch.Tensor, counts: torch.Tensor, active: torch.Tensor,

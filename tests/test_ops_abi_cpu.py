@@ -228,3 +228,14 @@ def test_control_buffers_are_checked(control):
     with pytest.raises(ValueError, match="control"):
         opt.write_control(control, 1e-3, 1)
     assert torch.equal(control, before)
+
+
+@pytest.mark.parametrize("stream", [None, 1234])
+def test_dropped_tokens_waits_for_the_routers_device(stream, monkeypatch):
+    """Without a stream object to wait for it is the router's device that is
+    waited for, not the current one."""
+    r, waited = M.MoeRouter(4, 8, 2, device="cpu"), []
+    r.device_error.fill_(2)
+    r._dev = 3
+    monkeypatch.setattr(torch.cuda, "synchronize", lambda device=None: waited.append(device))
+    assert r.dropped_tokens(stream) == 2 and waited == [3]
