@@ -34,7 +34,8 @@ template <int V>
 constexpr int THREADS = V <= 8 ? 1024 : V == 16 ? 512 : 256;
 constexpr int BWD_THREADS = 256;  // 16 tokens: nothing is summed over tokens there
 constexpr int RT_TOKENS = 64;     // tokens of one workgroup's chunk, times the multiple that keeps
-constexpr int RT_CHUNKS = 512;    // the chunks (whose sums one workgroup adds) to about this many
+constexpr int RT_CHUNKS = 512;    // the chunks (whose sums one workgroup adds) to about this many,
+constexpr int RT_MOST = 64;       // but this at most: a lane adds its tokens' probabilities in fp32
 constexpr int BWD_CHUNKS = 1 << 20;  // workgroups of the gradient (a launch holds fewer than 2^32 threads)
 constexpr uint32_t KEY_NINF = 0x007FFFFFu;  // the key of -inf: nothing at or below it is chosen
 
@@ -235,7 +236,7 @@ __global__ __launch_bounds__(ONE ? ONE_THREADS : THREADS<V>) void k_route(Router
 // result does not depend on timing.  Workgroup 0 also counts the bad tokens.
 constexpr int RS_THREADS = 1024;
 __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
-  __shared__ float sm[RS_THREADS];
+  __shared__ double sm[RS_THREADS];
   __shared__ int sh[RS_THREADS];
   __shared__ double part[RS_THREADS / 64];
   __shared__ int2 tally[RS_THREADS / 64];
@@ -250,15 +251,15 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
     all += c;
   }
   const uint2* from = a.sums + (long)first * (a.E + 1);
-  // one chunk's tokens a thread, in flight with the sums below
-  static_assert(RT_CHUNKS + MAX_ADAPTERS <= RS_THREADS, "a chunk a thread");
+  // one chunk's tokens a thread (below two million tokens), in flight with the sums below
   int act = 0, bad = 0;
-  if (tid < nc) act = (int)from[(long)tid * (a.E + 1) + a.E].x;
-  if (root == 0 && tid < all) bad = (int)a.sums[(long)tid * (a.E + 1) + a.E].y;
+  for (int c = tid; c < nc; c += RS_THREADS) act += (int)from[(long)c * (a.E + 1) + a.E].x;
+  if (root == 0)
+    for (int c = tid; c < all; c += RS_THREADS) bad += (int)a.sums[(long)c * (a.E + 1) + a.E].y;
   // EP experts side by side, the smallest power of two that covers E
   const int lg = a.E <= 1 ? 0 : 32 - __clz(a.E - 1), EP = 1 << lg;
-  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg, W = a.E + 1;  // chunks * W: below 2^19
-  float m = 0.0f;
+  const int e = tid & (EP - 1), slice = tid >> lg, slices = RS_THREADS >> lg, W = a.E + 1;  // chunks * W: below 2^21
+  double m = 0.0;
   int h = 0;
   if (e < a.E) {
     for (int c = slice; c < nc; c += 16 * slices) {
@@ -268,7 +269,7 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
 #pragma unroll
       for (int u = 0; u < 16; ++u) {
         const bool in = c + u * slices < nc;
-        m += in ? __uint_as_float(r[u].x) : 0.0f;
+        m += (double)(in ? __uint_as_float(r[u].x) : 0.0f);
         h += in ? (int)r[u].y : 0;
       }
     }
@@ -285,7 +286,7 @@ __global__ __launch_bounds__(RS_THREADS) void k_route_sum(RouterArgs a) {
     int hits = 0;
 #pragma unroll 8
     for (int q = 0; q < slices; ++q) {
-      mass += (double)sm[(q << lg) + tid];
+      mass += sm[(q << lg) + tid];
       hits += sh[(q << lg) + tid];
     }
     a.counts[(long)root * a.E + tid] = hits;
@@ -461,7 +462,8 @@ moe_status check_router(const moe_router_desc* d, const moe_adapters* ad, Router
   a.renorm = d->renorm;
   a.na = 1;
   a.roots[1] = d->T;
-  a.chunk = RT_TOKENS * ((d->T + RT_TOKENS * RT_CHUNKS - 1) / (RT_TOKENS * RT_CHUNKS));
+  const int mult = (d->T + RT_TOKENS * RT_CHUNKS - 1) / (RT_TOKENS * RT_CHUNKS);
+  a.chunk = RT_TOKENS * (mult < RT_MOST ? mult : RT_MOST);
   if (ad == nullptr) return MOE_OK;
   if (ad->offsets == nullptr || ad->count < 1) return MOE_ERR_INVALID;
   if (ad->count > MAX_ADAPTERS) return MOE_ERR_UNSUPPORTED;

@@ -236,3 +236,18 @@ def test_router_writes_its_own_buffers_only():
         r.grad_logits = other.cuda()
         with pytest.raises(ValueError, match="grad_logits"):
             r.backward(l.cuda(), idx, counts, active)
+
+
+@pytest.mark.parametrize("T,roots", [(1 << 27, None), ((1 << 22) + 3, None), (1 << 26, [0, 5, 5, (1 << 25) + 77, 1 << 26])])
+def test_router_loss_of_very_many_tokens(T, roots):
+    """Tokens that are all alike: p = (1/7, 4/7, 2/7), every route on expert 1,
+    so the loss is 3 * 4/7 whatever their number.  No sum may grow so long in
+    fp32 that its roundings, which are alike too, add up past REL."""
+    l = torch.tensor([0.0, 2.0, 1.0]) * float(np.log(2.0))
+    r = M.MoeRouter(T, 3, 1, roots=roots)
+    idx, w, counts, active, loss = r.forward(l.cuda().expand(T, 3).contiguous())
+    sizes = np.diff(roots or [0, T])
+    assert active.tolist() == sizes.tolist() and counts[:, 1].tolist() == sizes.tolist()
+    assert not counts[:, 0].any() and not counts[:, 2].any() and (idx == 1).all() and r.dropped_tokens() == 0
+    want = np.where(sizes > 0, 12 / 7, 0.0)
+    assert np.all(np.abs(loss.cpu().double().numpy() - want) <= REL * want), loss
