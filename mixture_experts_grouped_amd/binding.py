@@ -726,8 +726,8 @@ class MoeAdamW:
                 _ptr(p, ptype, None, "params"), None if masters is None else _ptr(masters[i], f32, None, "masters"),
                 _ptr(self.grads[i], gtype, None, "grads"), _ptr(self.states["m"][i], kinds["m"], None, "m"),
                 _ptr(self.states["v"][i], kinds["v"], None, "v"), *sc, n)
-        # aliases: the memory outlives a replacement of a tensor's own
-        self._held = [t.detach() for ts in (self.params, self.grads, self.masters or [], *self.states.values()) for t in ts]
+        # the memory outlives a replacement of a tensor's own
+        self._held = [t.untyped_storage() for ts in (self.params, self.grads, self.masters or [], *self.states.values()) for t in ts]
         # memory that a step writes belongs to one tensor alone
         spans = [(t.data_ptr(), t.numel() * t.element_size(), k) for k, ts in
                  (("params", self.params), ("grads", self.grads), ("masters", self.masters or []), *self.states.items())
