@@ -525,13 +525,13 @@ moe_status moe_fp8_quantize_weight(const void* W, int32_t E, int32_t N, int32_t 
 typedef struct moe_fp8_desc {
   int32_t E, N, K; /* N, K % 128 == 0, at most 65536; 1 <= E <= 512; N * K < 2^31 */
   int32_t topk;    /* > 0: gather, row r reads activation row row_to_route[r] / topk; 0: row r */
-  int64_t a_rows;  /* rows of a: tokens (gather), at least the pool's rows in use otherwise; gather: a_rows * K < 2^31 */
+  int64_t a_rows;  /* rows of a, at least 1: tokens (gather; a_rows * K < 2^31), at least the pool's rows in use otherwise */
 } moe_fp8_desc;
 
 /* out [pool->capacity, N] bf16: the rows of routes are written, padding and
  * unused rows are left as they were.  pool: counts, offsets and row_to_route
  * as build_pool wrote them (route_to_row is not read and may be NULL), E
- * experts, capacity = its allocated rows.  a [a_rows, K], a_scales [a_rows,
+ * experts, capacity = its allocated rows, at least 1.  a [a_rows, K], a_scales [a_rows,
  * K/128], w [E, N, K], w_scales [E, N/128, K/128].  A route whose activation
  * row is not below a_rows reads zeros; rows past the capacity are not
  * touched whatever the pool says.  Which kernel runs follows from the shapes;

@@ -8,11 +8,13 @@
 // 4 KB hold: 100 with fp32 moments, 63 with masters and 8-bit ones); a workgroup
 // finds its tensor by ballots over the tensors' first chunks.
 //
-// Memory bounds it: the production factors (52 M elements, bf16 parameters
-// and gradients, fp32 masters, 8-bit moments: 16 bytes an element) take 157 us,
-// 5.3 TB/s, about 80 vector instructions an element and 76 % of their issue
-// slots; 96 tensors of 14,080 fp32 elements on average, one launch, 8.6 us
-// (two launches of 48: 12.5); 110 K elements in six tensors 4.0 us, latency.
+// Memory bounds it, and vector instructions not far behind: the production
+// factors (52 M elements, bf16 parameters and gradients, fp32 masters, 8-bit
+// moments: 16 bytes an element) take 157 us, 5.4 TB/s of the 6.5 that a plain
+// copy kernel reaches, with 79 vector instructions an element in 73 % of their
+// issue slots; 96 tensors of 14,080 fp32 elements on average, one launch, 9.7 us
+// (8.6 with inputs left in the caches; two launches of 48 took 12.5 where one
+// took 9.2); 110 K elements in six tensors 4.2 us, latency.
 #include <cmath>
 
 #include "../../include/moelora.h"

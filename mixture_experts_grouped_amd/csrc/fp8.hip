@@ -59,8 +59,8 @@ __device__ __forceinline__ void widen8(u32x4 w, float (&v)[8]) {
 // of 1e-7 would shift (1 % at -8).  Phi(g) = 1/2 exp(-z^2) f(z) at z = -g / sqrt 2
 // >= 0, with f(z) = exp(z^2) erfc(z) = t P(t), t = 1 / (1 + 0.46 z): P of degree 7 is
 // fitted for the smallest largest relative error over all z, 6.8e-7 (8.7e-7
-// evaluated in fp32); here halved.  98,304 x 2048: 200 us, 195 with norm_cdf, 302
-// with the math library's erfcf.
+// evaluated in fp32); here halved.  98,304 x 2048, same inputs: 200 us, 195 with
+// norm_cdf, 302 with the math library's erfcf.
 __device__ __forceinline__ float norm_cdf_rel(float g) {
   const float t = __builtin_amdgcn_rcpf(fmaf(0.46f * 0.70710678118654752f, fabsf(g), 1.0f));
   float q = 0.0338571894f;
@@ -76,7 +76,10 @@ __device__ __forceinline__ float norm_cdf_rel(float g) {
 }
 
 // Eight columns a thread, a block of 128 in one DPP row: one pass, bound by
-// memory (16,384 x 4096: 36 us, 5.7 TB/s; gated 2,064 x 2048 5.2 us, latency).
+// memory (16,384 x 4096: 34 us, 6.0 TB/s of the 6.5 that plain loads and stores
+// reach, 30 us with inputs left in the caches; gated 98,304 x 2048 172 us, 5.9
+// TB/s; gated 2,064 x 2048 5.8 us, latency).  GEGLU fills the vector issue slots:
+// 98,304 x 2048 200 to 219 us, 2,064 x 2048 6.0 to 7.2.
 // ACT < 0: src is [rows, K]; else [rows, 2K] = gate | up.
 template <int ACT>
 __global__ __launch_bounds__(256) void k_fp8_rows(const uint16_t* __restrict__ src, long n8, int K8,
@@ -105,7 +108,10 @@ __global__ __launch_bounds__(256) void k_fp8_rows(const uint16_t* __restrict__ s
 }
 
 // One 128 x 128 block of one expert's weight a workgroup: thread t holds 64
-// values (row t / 2, half t % 2).  The transposed codes go through LDS.
+// values (row t / 2, half t % 2).  The transposed codes go through LDS, four
+// bytes from four rows a word (1.7 bank conflicts an instruction).  64 experts of
+// 4096 x 4096: 705 us, 4.6 TB/s; with the transposed copy 995 us, 4.3 TB/s.  A
+// program does this once for its frozen weights.
 __global__ __launch_bounds__(256) void k_fp8_weight(const uint16_t* __restrict__ W, int N, int K,
                                                     uint8_t* __restrict__ codes, float* __restrict__ scales,
                                                     uint8_t* __restrict__ codes_t, float* __restrict__ scales_t) {
@@ -379,10 +385,10 @@ struct Frag8 {
 // where they are needed, and with the lanes' offsets kept in scratch across the
 // K loop, each wait for one waited for all queued loads (2 % slower).
 //
-// What it measured, 98,304 rows of 4096 x 4096 on 64 experts: 1.58-1.62 ms,
-// 2,060 TFLOP/s (experts of equal size: 1.49; one expert, 8192^3: 2,290; a
-// library's product with one scale a tensor 2,660).  The matrix cores are busy
-// 59 % of the cycles at 1.6 GHz, which is the power cap: activations of zeros
+// What it measured, 98,304 rows of 4096 x 4096 on 64 experts: 1.55-1.62 ms,
+// 2,040-2,130 TFLOP/s (experts of equal size: 1.49; one expert, 8192^3: 2,290; a
+// library's product with one scale a tensor 2,660-2,760).  The matrix cores are
+// busy 61 % of the cycles at 1.6 GHz, which is the power cap: activations of zeros
 // take 1.28 ms.  A tile costs 10 us beyond its 1.6 us a stage, most of it the
 // time that its 128 KB take to memory (three quarters of the stores left out:
 // 0.10 ms less): waits that leave them out for two stages gained nothing, nor did
@@ -394,7 +400,7 @@ struct Frag8 {
 // 64-row tiles in a launch of their own: no gain, on ragged experts a loss of
 // up to 17 %; waves without rows only loading: 2 % slower.  The 64-row tile,
 // 689 tokens x 6 with a fifth of the routes dropped, 4096 x 2048: 116 us, 4.9
-// TB/s of weights; with six buffers instead of three, one workgroup a CU: no
+// TB/s of weights (a kernel that only reads: 7.1); with six buffers instead of three, one workgroup a CU: no
 // faster, 0.5 us a K block, which is the chain of barrier, fragment reads and
 // products.
 //
@@ -658,7 +664,9 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
 // evenly over the CUs): 16 activation rows x 16 weight rows, the next FEW_CH K
 // blocks in flight while FEW_CH are multiplied.  It walks K in
 // order, so a row's sums are those of the tile kernels bit for bit.
-// One expert of 4096 x 4096, 1 to 16 rows: 11 us; split over four waves of a
+// One expert of 4096 x 4096, 1 to 16 rows: 12 us (reading its weights alone: 2.4),
+// two of eight 12.6, eight of 128 experts of 1024 x 2048 10.3: each wave's chain
+// of K / 128 blocks sets the time, not the bytes.  Split over four waves of a
 // workgroup along K instead, with its join, six experts took 44 us, whole
 // workgroups of 64 weight rows 27 (384 of them on 256 CUs), single waves 21.
 constexpr int FEW_ROWS = 16, FEW_CH = 4;

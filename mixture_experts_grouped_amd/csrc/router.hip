@@ -10,13 +10,15 @@
 // integer of the same order, so the choice is exact and equals go to the
 // lowest expert.
 //
-// At 16,384 x 64 fp32 the logits are 4 MB, a microsecond of memory time, so
-// latency bounds all three kernels: k_route 6.3 us (each workgroup one round of
-// 64 tokens; four rounds of 16 took 9.7; the choice of six experts is about half
-// of it), k_route_sum 4.6 us (one workgroup reads 131 KB of sums that other XCDs
-// wrote, all loads in flight together; chunks of 128 tokens halve them and cost
-// k_route more: 1.2 us in sum), k_route_bwd 4.9 us (16 tokens a workgroup; 8.6
-// with four rounds).  One token: k_route alone, 3.7 us.
+// At 16,384 x 64 fp32 the logits are 4 MB, 0.7 us of memory time, so latency
+// bounds all three kernels: k_route 6.4 us (bf16 logits the same; each workgroup
+// one round of 64 tokens; four rounds of 16 took 9.7; the choice of six experts is
+// about half of it), k_route_sum 4.8 us (one workgroup reads 131 KB of sums that
+// other XCDs wrote, all loads in flight together; chunks of 128 tokens halve them
+// and cost k_route more: 1.2 us in sum), k_route_bwd 5.1 us (16 tokens a workgroup;
+// 8.6 with four rounds; its tokens' LDS rows padded apart: no bank conflicts
+// instead of 2.8 an instruction, and the same time).  One token: k_route alone,
+// 3.8 us.
 #include <cmath>
 
 #include "../../include/moelora.h"
@@ -415,7 +417,7 @@ int chunks_of(const RouterArgs& a) {
   return n;
 }
 
-// Few tokens: one launch, 3.7 us at one token (two: 3.7 and 2.9).  Beyond one
+// Few tokens: one launch, 3.8 us at one token (two: 3.7 and 2.9).  Beyond one
 // round of its workgroup a round costs about 1.5 us and the sums lose their
 // parallel chunks.
 bool one_launch(const RouterArgs& a) { return a.na == 1 && a.T <= ONE_TOKENS; }
