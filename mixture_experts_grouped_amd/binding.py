@@ -591,7 +591,8 @@ class MoeRouter:
     """Top-k routing of one shape: T tokens' logits [T, E] to expert ids and
     weights, expert loads and the balance loss, and the gradient to the
     logits.  Keeps the output buffers and the workspace; every call
-    overwrites them.
+    overwrites them, so calls that run at the same time (on two streams, in
+    two captured graphs) need a router each.
 
     roots: several adapters in one pass, as in MoeLoraLayer; loads and loss
     are per root.  renorm: a token's weights divided by their sum.  checked:
