@@ -20,7 +20,7 @@
 #include "checks.hpp"
 #include "engine2.hpp"
 #include "lanes.hpp"
-#include "layer.hpp"
+#include "pool_tiles.hpp"
 #include "trace.hpp"
 
 namespace moelora {
@@ -46,35 +46,6 @@ __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
   int p = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
   return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(c, d, p, true);
 }
-__device__ __forceinline__ void widen8(u32x4 w, float (&v)[8]) {
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    v[2 * c] = bf2f(w[c] & 0xffffu);
-    v[2 * c + 1] = bf2f(w[c] >> 16);
-  }
-}
-
-// The normal distribution function to fp32's relative precision: a block in its
-// lower tail is scaled by its own largest value, which norm_cdf's absolute error
-// of 1e-7 would shift (1 % at -8).  Phi(g) = 1/2 exp(-z^2) f(z) at z = -g / sqrt 2
-// >= 0, with f(z) = exp(z^2) erfc(z) = t P(t), t = 1 / (1 + 0.46 z): P of degree 7 is
-// fitted for the smallest largest relative error over all z, 6.8e-7 (8.7e-7
-// evaluated in fp32); here halved.  98,304 x 2048, same inputs: 200 us, 195 with
-// norm_cdf, 302 with the math library's erfcf.
-__device__ __forceinline__ float norm_cdf_rel(float g) {
-  const float t = __builtin_amdgcn_rcpf(fmaf(0.46f * 0.70710678118654752f, fabsf(g), 1.0f));
-  float q = 0.0338571894f;
-  q = fmaf(q, t, -0.113314702f);
-  q = fmaf(q, t, 0.084595587f);
-  q = fmaf(q, t, 0.0263052463f);
-  q = fmaf(q, t, 0.093423918f);
-  q = fmaf(q, t, 0.115590938f);
-  q = fmaf(q, t, 0.129778633f);
-  q = fmaf(q, t, 0.12976353f);
-  const float tail = q * t * __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g);  // log2(e) / 2
-  return g < 0.0f ? tail : 1.0f - tail;
-}
-
 // Eight columns a thread, a block of 128 in one DPP row: one pass, bound by
 // memory (16,384 x 4096: 34 us, 6.0 TB/s of the 6.5 that plain loads and stores
 // reach, 30 us with inputs left in the caches; gated 98,304 x 2048 172 us, 5.9
@@ -173,84 +144,14 @@ __global__ __launch_bounds__(256) void k_fp8_weight(const uint16_t* __restrict__
 // ---------------------------------------------------------------------------
 // products
 // ---------------------------------------------------------------------------
-struct Fp8Args {
-  int E, N, K, topk;
-  int cap;  // rows of the pool
-  uint32_t tok_mul;  // route / topk = route * tok_mul >> tok_shift
-  int tok_shift;
-  long a_rows;
-  const int32_t* counts;
-  const int32_t* offsets;
-  const int32_t* row2r;
+struct Fp8Args : PoolArgs {
+  int N, K;
   const uint8_t* a;
   const float* sa;
   const uint8_t* w;
   const float* sw;
   uint16_t* out;
 };
-
-// Rows of expert e, none past the pool whatever its arrays hold.
-__device__ __forceinline__ int rows_of(const Fp8Args& p, int e) {
-  const int off = p.offsets[e];
-  return off >= 0 && off < p.cap ? max(min(p.counts[e], p.cap - off), 0) : 0;
-}
-// The activation row of a route, -1: none (a_rows < 2^31).  No branches: loads
-// of several routes stay together.
-__device__ __forceinline__ int token_of(const Fp8Args& p, int route) {
-  const int t = (int)((uint64_t)(uint32_t)route * p.tok_mul >> p.tok_shift);
-  return (int)(route >= 0) & (int)(t < (int)p.a_rows) ? t : -1;
-}
-
-// Tile b of the pool cut into M tiles of TM rows that never cross experts,
-// times nn N tiles: its expert, its index among the expert's M tiles and its
-// N tile; false past the last.  Every lane of the wave calls it; the counts
-// are summed here (E <= 512: at most eight rounds of a wave scan) rather than
-// by a kernel of its own, which costs more than the scan.  Order as in
-// group_tile: each XCD a contiguous range of (expert's M chunk, N tile, M
-// tile), so that workgroups of one XCD share a weight panel in its L2.
-constexpr int MAX_E = 512;
-// More tiles than a pool can have: the sums stop there, so that no counts make
-// them wrap.
-__device__ __forceinline__ int most_tiles(const Fp8Args& p, int TM) { return p.cap / TM + p.E; }
-__device__ __forceinline__ bool pool_tile(const Fp8Args& p, int TM, int b, int nn, int gm, int& e, int& m, int& nt) {
-  const int lane = threadIdx.x & 63;
-  const int most = most_tiles(p, TM);
-  int cnt[MAX_E / 64], end[MAX_E / 64], total = 0;
-#pragma unroll
-  for (int q = 0; q < MAX_E / 64; ++q) {
-    cnt[q] = 64 * q + lane < p.E ? (rows_of(p, 64 * q + lane) + TM - 1) / TM : 0;
-    if (64 * q < p.E) {
-      int x = cnt[q];
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int y = __shfl_up(x, o, 64);
-        if (lane >= o) x = min(x + y, most);
-      }
-      end[q] = min(total + x, most);  // tiles up to and with this lane's expert
-      total = __builtin_amdgcn_readlane(end[q], 63);
-    }
-  }
-  if (b >= total * nn) return false;
-  const int L = xcd_remap(b, total * nn);
-  const int v = L / nn;
-  bool found = false;
-#pragma unroll
-  for (int q = 0; q < MAX_E / 64; ++q) {
-    if (64 * q >= p.E || found) continue;
-    const unsigned long long past = __ballot(end[q] > v);
-    if (past == 0) continue;
-    found = true;
-    const int l = __ffsll(past) - 1;
-    const int n = __builtin_amdgcn_readlane(cnt[q], l), s = __builtin_amdgcn_readlane(end[q], l) - n;
-    const int cs = s + gm * ((v - s) / gm);
-    const int sz = s + n - cs < gm ? s + n - cs : gm;
-    const int r = L - cs * nn;
-    e = 64 * q + l;
-    m = cs + r % sz - s;
-    nt = r / sz;
-  }
-  return found;
-}
 
 __device__ __forceinline__ f32x4 mma8(i32x8 w, i32x8 x, f32x4 c) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w, x, c, 0, 0, 0, 0, 0, 0);
@@ -276,72 +177,6 @@ struct Geo8 {
   static_assert(128 % (TN / WN) == 0 && TN % 128 == 0 && TN <= 256, "a wave's weight rows lie in one block of 128");
   static_assert(lds(MAX_DIM, MAX_E) <= 160 * 1024 && NW * 64 >= TM && FN % 2 == 0, "one scale a lane; fragments are stored in pairs");
 };
-
-// The pool's tiles of TM rows, in LDS: for each expert the number of tiles up
-// to and with it, its rows and its first row.
-struct PoolTable {
-  int *end, *cnt, *off;
-  int total;
-};
-template <int TM>
-__device__ __forceinline__ void fill_table(const Fp8Args& p, PoolTable& t, char* at) {
-  t.end = (int*)at;
-  t.cnt = t.end + p.E;
-  t.off = t.cnt + p.E;
-  const int lane = threadIdx.x & 63;
-  const int most = most_tiles(p, TM);
-  int before = 0;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {  // every wave walks all experts; wave 0 writes
-    const int e = e0 + lane, c = e < p.E ? rows_of(p, e) : 0;
-    int x = (c + TM - 1) / TM;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int y = __shfl_up(x, o, 64);
-      if (lane >= o) x = min(x + y, most);
-    }
-    x = min(before + x, most);
-    if (threadIdx.x < 64 && e < p.E) {
-      t.end[e] = x;
-      t.cnt[e] = c;
-      t.off[e] = p.offsets[e];
-    }
-    before = __shfl(x, 63, 64);
-  }
-  t.total = __builtin_amdgcn_readfirstlane(before);
-  __syncthreads();
-}
-
-// One tile of the pool's nn N tiles per M tile (order as in pool_tile).
-struct Tile8 {
-  int e, nt, nrows;
-  long row0;
-};
-template <int TM>
-__device__ __forceinline__ bool find_tile(const PoolTable& t, int E, int b, int nn, Tile8& out) {
-  if (b >= t.total * nn) return false;
-  const int lane = threadIdx.x & 63;
-  const int L = xcd_remap(b, t.total * nn);
-  const int v = L / nn;
-  int e = 0;
-  for (int e0 = 0; e0 < E; e0 += 64) {
-    const unsigned long long past = __ballot(e0 + lane < E && t.end[min(e0 + lane, E - 1)] > v);
-    if (past != 0) {
-      e = e0 + __ffsll(past) - 1;
-      break;
-    }
-  }
-  const int cnt = t.cnt[e], end = t.end[e], off = t.off[e];  // read together
-  const int rows = __builtin_amdgcn_readfirstlane(cnt);
-  const int n = (rows + TM - 1) / TM, s = __builtin_amdgcn_readfirstlane(end) - n;
-  const int cs = s + TILE_GM * ((v - s) / TILE_GM);
-  const int sz = s + n - cs < TILE_GM ? s + n - cs : TILE_GM;
-  const int r = L - cs * nn, m = cs + r % sz - s;
-  out.e = e;
-  out.nt = r / sz;
-  out.nrows = min(rows - m * TM, TM);
-  out.row0 = (long)__builtin_amdgcn_readfirstlane(off) + (long)m * TM;
-  return true;
-}
 
 // Lane offsets of the 16-row fragments of a tile of 128-byte rows: lane l
 // takes row l % 16 and chunks 2 (l / 16) and 2 (l / 16) + 1, 32 bytes in a
@@ -422,13 +257,13 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   const int fr = lane & 15;
   PoolTable tab;
   fill_table<G::TM>(p, tab, smem + G::table_at(p.K));
-  Tile8 cur;
+  PoolTile cur;
   int b = blockIdx.x;
   if (!find_tile<G::TM>(tab, p.E, b, nn, cur)) return;
 
   // queue a tile's routes into LDS, where aim reads them
   char* const routes = smem + G::table_at(p.K) + 12 * p.E;
-  auto queue_routes = [&](const Tile8& t) {
+  auto queue_routes = [&](const PoolTile& t) {
     if (p.topk > 0 && 64 * w < G::TM)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(make_rsrc(p.row2r + t.row0, (uint64_t)t.nrows * 4),
                                                (v2::lds_void*)(routes + 256 * w), 4, 256u * w + 4u * lane, 0, 0, 0);
@@ -441,7 +276,7 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   // lane's number passes through an empty asm so that what is computed from it
   // is computed for each tile: kept across the K loop it went to scratch, and
   // each reload waited for all queued loads.
-  auto aim = [&](const Tile8& t, bool any, int h) {
+  auto aim = [&](const PoolTile& t, bool any, int h) {
     int lane = threadIdx.x & 63;
     asm volatile("" : "+v"(lane));
     const int n0 = t.nt * G::TN, ncols = min(p.N - n0, G::TN);
@@ -605,7 +440,7 @@ __global__ __launch_bounds__(G::NT) void k_fp8_tile(Fp8Args p) {
   read_scales(0, sw_at(0, 0), sc);
   clear();
   while (true) {
-    Tile8 nxt = cur;
+    PoolTile nxt = cur;
     b += gridDim.x;
     const bool more = find_tile<G::TM>(tab, p.E, b, nn, nxt);
     if (more) queue_routes(nxt);
@@ -765,11 +600,6 @@ Pick pick(const Fp8Args& p, int64_t routes, int cus) {
   return (mid > 0.5 ? mid : 0.5) <= (large > 1.35 ? large : 1.35) ? Pick::mid : Pick::large;
 }
 
-// Workgroups for at most `tiles` tiles: every kernel here walks on by its grid
-// until the pool's tiles are done, so the grid is a matter of speed alone: as
-// many as are resident, in whole rounds over the XCDs.
-unsigned grid_of(int64_t tiles, int64_t most) { return (unsigned)(((tiles < most ? tiles : most) + 7) / 8 * 8); }
-
 template <class G>
 hipError_t launch_tile(const Fp8Args& p, int64_t mtiles, int resident, hipStream_t st) {
   static PerDeviceOnce once;
@@ -868,23 +698,12 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
                        rng(pool->row_to_route, (size_t)pool->capacity * 4)};
   for (const Range& r : ins)
     if (overlap(ro, r)) return MOE_ERR_INVALID;
-  // floor(n / k) = floor(n m / 2^(31 + s)) for n < 2^31, with 2^s >= k the
-  // smallest and m = ceil(2^(31 + s) / k) < 2^32: n (m k - 2^(31 + s)) < 2^(31 + s)
-  const uint64_t k = d->topk > 0 ? (uint64_t)d->topk : 1;
-  int sh = 31;
-  while ((uint64_t)1 << (sh - 31) < k) ++sh;
-  const uint32_t mul = (uint32_t)((((uint64_t)1 << sh) + k - 1) / k);
-  Fp8Args p{d->E, d->N, d->K, d->topk, (int)pool->capacity, mul, sh, (long)d->a_rows, pool->counts, pool->offsets,
-            pool->row_to_route, (const uint8_t*)a, a_scales, (const uint8_t*)w, w_scales, (uint16_t*)out};
-  // the routes of a pool of this capacity: build_pool allots BLOCK_M - 1 rows
-  // of padding to each of min(E, routes) experts
-  const int64_t bm = pool->block_m, cap = pool->capacity, E = d->E;
-  const int64_t routes = cap >= E * bm ? cap - E * (bm - 1) : (cap + bm - 1) / bm;
+  Fp8Args p{pool_args(d->E, d->topk, d->a_rows, pool), d->N, d->K, (const uint8_t*)a, a_scales, (const uint8_t*)w, w_scales, (uint16_t*)out};
+  const int64_t E = d->E, routes = pool_routes(pool, E);
   const int64_t live = routes < E ? routes : E;  // experts with rows, at most
   auto tiles = [&](int tm) { return routes / tm + live; };
-  int dev = 0, cus = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  int cus = 0;
+  hipError_t e = device_cus(cus);
   if (e != hipSuccess) return MOE_ERR_HIP;
   const hipStream_t s = (hipStream_t)stream;
   switch (pick(p, routes, cus)) {

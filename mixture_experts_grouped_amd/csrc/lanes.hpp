@@ -1,5 +1,5 @@
 // lanes.hpp -- reductions over the 16 lanes of a DPP row and small numeric
-// helpers shared by the router, the optimiser and the fp8 kernels.
+// helpers shared by the router, the optimisers and the 8- and 4-bit kernels.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -71,5 +71,35 @@ __device__ __forceinline__ double wave_sum(double v) {
 // magnitudes, infinity above every finite value and NaN above infinity, so
 // an integer maximum keeps a NaN that a floating one would drop.
 __device__ __forceinline__ uint32_t mag(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
+
+// Eight bf16 values of a 16-byte chunk.
+__device__ __forceinline__ void widen8(u32x4 w, float (&v)[8]) {
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    v[2 * c] = bf2f(w[c] & 0xffffu);
+    v[2 * c + 1] = bf2f(w[c] >> 16);
+  }
+}
+
+// The normal distribution function to fp32's relative precision: a block in its
+// lower tail is scaled by its own largest value, which norm_cdf's absolute error
+// of 1e-7 would shift (1 % at -8).  Phi(g) = 1/2 exp(-z^2) f(z) at z = -g / sqrt 2
+// >= 0, with f(z) = exp(z^2) erfc(z) = t P(t), t = 1 / (1 + 0.46 z): P of degree 7 is
+// fitted for the smallest largest relative error over all z, 6.8e-7 (8.7e-7
+// evaluated in fp32); here halved.  98,304 x 2048, same inputs: 200 us, 195 with
+// norm_cdf, 302 with the math library's erfcf.
+__device__ __forceinline__ float norm_cdf_rel(float g) {
+  const float t = __builtin_amdgcn_rcpf(fmaf(0.46f * 0.70710678118654752f, fabsf(g), 1.0f));
+  float q = 0.0338571894f;
+  q = fmaf(q, t, -0.113314702f);
+  q = fmaf(q, t, 0.084595587f);
+  q = fmaf(q, t, 0.0263052463f);
+  q = fmaf(q, t, 0.093423918f);
+  q = fmaf(q, t, 0.115590938f);
+  q = fmaf(q, t, 0.129778633f);
+  q = fmaf(q, t, 0.12976353f);
+  const float tail = q * t * __builtin_amdgcn_exp2f(-0.72134752044448170f * g * g);  // log2(e) / 2
+  return g < 0.0f ? tail : 1.0f - tail;
+}
 
 }  // namespace moelora
