@@ -539,6 +539,145 @@ typedef struct moe_fp8_desc {
 moe_status moe_fp8_product(const moe_fp8_desc* desc, const moe_pool* pool, const void* a, const float* a_scales,
                            const void* w, const float* w_scales, void* out, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Expert products in bf16 on the pool's rows, for weights outside a fused layer
+ * call (a base trained with its own gradients, an unfused layer).  For pool row
+ * r of expert e (rows as build_pool laid them out), with a(r) the token
+ * row_to_route[r] / topk (topk > 0: tokens are gathered) or r itself (topk 0),
+ *   out[r, n]  = sum_k a[a(r), k] w[e, n, k]      w [E, N, K]
+ *                         (transposed: w[e, k, n], w [E, K, N])
+ *   dw[e, n, k] = sum_{r of e} grad[r, n] a[a(r), k]   (+ dw, if `accumulate`)
+ * in fp32, rounded once.  The data gradient of a product with weight [E, N, K]
+ * is the transposed product of the same weight (with the two widths' names
+ * exchanged): no second copy of the weight is needed.  The order of all sums
+ * is fixed: results are bitwise repeatable, and a row of `out` does not depend
+ * on the other rows' values.
+ * ------------------------------------------------------------------------ */
+typedef struct moe_expert_desc {
+  int32_t E, N, K;    /* N, K % 8 == 0, at most 65536; 1 <= E <= 512; N * K < 2^30 */
+  int32_t topk;       /* > 0: gather, row r reads activation row row_to_route[r] / topk; 0: row r */
+  int64_t a_rows;     /* rows of a, at least 1; gather: a_rows * K < 2^30 */
+  int32_t transposed; /* moe_expert_product: 1: w is [E, K, N] */
+  int32_t out_type;   /* moe_expert_weight_grad: MOE_TYPE_* of dw */
+  int32_t accumulate; /* moe_expert_weight_grad: 1: added to dw; 0: dw is overwritten, zeros for an expert without rows */
+} moe_expert_desc;
+
+/* out [pool->capacity, N] bf16: the rows of routes are written, padding and
+ * unused rows are left as they were.  a [a_rows, K] bf16, w bf16.  pool:
+ * counts, offsets and row_to_route as build_pool wrote them (route_to_row is
+ * not read and may be NULL).  A route whose activation row is not below a_rows
+ * reads zeros; rows past the capacity are not touched whatever the pool says. */
+moe_status moe_expert_product(const moe_expert_desc* desc, const moe_pool* pool, const void* a, const void* w,
+                              void* out, void* stream);
+
+/* grad [pool->capacity, N] bf16 (rows of no route are not used), a [a_rows, K]
+ * bf16, dw [E, N, K] of out_type. */
+moe_status moe_expert_weight_grad(const moe_expert_desc* desc, const moe_pool* pool, const void* grad, const void* a,
+                                  void* dw, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The same in microscaled 4-bit floating point (OCP MX v1.0, MXFP4; the layout
+ * of MOE_BASE_MXFP4): e2m1 codes, element 2i in the low nibble of byte i, and
+ * one e8m0 exponent per 32 elements along the contraction axis.
+ *
+ * A block of 32 with largest magnitude m gets the exponent floor(log2 m) - 2
+ * (held plus 127; a block of zeros, and one below 2^-125, holds 0) and each
+ * element the nearest of 0, 0.5, 1, 1.5, 2, 3, 4, 6 times 2^exponent, ties to
+ * the even code, what is beyond 6 to 6; a negative value that rounds to zero
+ * is +0.  A block with a NaN or an infinity holds the exponent 255 (NaN).
+ * ------------------------------------------------------------------------ */
+/* act as in moe_fp8_quantize_rows: src [rows, K] bf16 (MOE_FP8_PLAIN) or
+ * [rows, 2K] = [gate | up].  codes [rows, K / 2] bytes, exponents [rows, K / 32]
+ * bytes.  K % 128 == 0 and at most 65536, rows >= 0, rows * K at most 2^35. */
+moe_status moe_mxfp4_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes,
+                                   void* exponents, void* stream);
+
+/* W bf16 [E, N, K] to codes [E, N, K / 2] and exponents [E, N, K / 32] (blocks
+ * along K) and, if both are given, of the transposed weight: codes_t [E, K,
+ * N / 2] and exponents_t [E, K, N / 32] (blocks along N: other roundings of the
+ * same weight), the data gradient's operand.  N, K % 128 == 0 and at most
+ * 65536, 1 <= E <= 512, N * K < 2^31. */
+moe_status moe_mxfp4_quantize_weight(const void* W, int32_t E, int32_t N, int32_t K, void* codes, void* exponents,
+                                     void* codes_t, void* exponents_t, void* stream);
+
+/* What codes and exponents stand for, exactly, as bf16 [rows, K] (values below
+ * bf16's smallest normal 2^-126 included; 255: NaN).  K % 128 == 0. */
+moe_status moe_mxfp4_dequantize(const void* codes, const void* exponents, int64_t rows, int32_t K, void* out,
+                                void* stream);
+
+typedef struct moe_mxfp4_desc {
+  int32_t E, N, K; /* N % 32 == 0, K % 128 == 0, at most 65536; 1 <= E <= 512; N * K < 2^31 */
+  int32_t topk;    /* as in moe_expert_desc */
+  int64_t a_rows;  /* rows of a, at least 1; gather: a_rows * K < 2^32 */
+} moe_mxfp4_desc;
+
+/* out [pool->capacity, N] bf16 as moe_expert_product writes it, of a [a_rows,
+ * K / 2], a_exponents [a_rows, K / 32], w [E, N, K / 2], w_exponents [E, N,
+ * K / 32] (an MXFP4 base's W13 or W2 as the layer takes it): the products of
+ * what the codes stand for, added by the scaled matrix instructions in fp32,
+ * 128 at a time.  A NaN exponent makes its row's results NaN (a weight's: its
+ * column's). */
+moe_status moe_mxfp4_product(const moe_mxfp4_desc* desc, const moe_pool* pool, const void* a, const void* a_exponents,
+                             const void* w, const void* w_exponents, void* out, void* stream);
+
+/* ------------------------------------------------------------------------
+ * One optimiser step with an orthogonalised update (momentum, then rounds of a
+ * quintic polynomial that drive the update's singular values towards one) over
+ * many matrices: adapter factors, each tensor [batch, m, n] a stack of matrices
+ * (an expert-local factor: one matrix per expert).  Per matrix, with
+ * g = grad_scale * grad:
+ *   M <- momentum M + g,   U = g + momentum M (nesterov) or M,
+ *   X <- U / (|U| + eps)            (|U| the root of the sum of its squares),
+ *   `rounds` times  X <- a X + (b S + c S^2) X,  S = X X^T  (X^T X if m > n),
+ *   p <- p - lr (rms sqrt(max(m, n)) X + weight_decay p).
+ * M and p in fp32; p is the fp32 master copy if there is one (then `param`
+ * receives its rounding), else `param` itself; p's whole change is formed first
+ * and subtracted once.  X after the rounds is a polynomial of S times U: S and
+ * the polynomial are formed in fp64, and multiply U in fp32 once.  A matrix of
+ * zeros moves by its weight decay alone; one with a NaN or an infinity in U
+ * becomes NaN and leaves the others alone.  All sums run in a fixed order:
+ * results are bitwise repeatable.
+ *
+ * min(m, n) <= 256, m * n < 2^31, batch <= 2^20, batch * m * n < 2^40 (more:
+ * MOE_ERR_UNSUPPORTED).
+ * ------------------------------------------------------------------------ */
+typedef struct moe_muon_tensor {
+  void* param;       /* [batch, m, n] of param_type, updated */
+  float* master;     /* fp32 or NULL (bf16 parameters only; all tensors of a call alike) */
+  const void* grad;  /* of grad_type */
+  float* momentum;   /* fp32, updated; zeros before the first step */
+  int64_t batch;     /* 0: skipped, pointers not looked at */
+  int32_t m, n;
+} moe_muon_tensor;
+
+/* What changes from step to step, in device memory: for steps captured into a
+ * graph and replayed with other values. */
+typedef struct moe_muon_control {
+  float lr, grad_scale;
+} moe_muon_control;
+
+typedef struct moe_muon_desc {
+  int32_t param_type, grad_type; /* MOE_TYPE_* */
+  int32_t nesterov;              /* 0 or 1 */
+  int32_t rounds;                /* 1 to 16 */
+  double lr, momentum, weight_decay, rms, eps, grad_scale;
+  double a, b, c;                /* the quintic's coefficients */
+  const moe_muon_control* control; /* DEVICE pointer or NULL: replaces lr and grad_scale */
+} moe_muon_desc;
+
+/* Bytes of the workspace of moe_muon_step on the current device for these
+ * tensors (nothing in it survives the call; pointers are not looked at). */
+moe_status moe_muon_workspace_size(const moe_muon_desc* desc, const moe_muon_tensor* tensors, int32_t count,
+                                   size_t* bytes);
+
+/* Update `count` tensors (HOST array, read during the call).  Pointers of
+ * non-empty tensors and the workspace 16-byte aligned; no buffer of the call
+ * may overlap another one that it writes (within a tensor this is checked).
+ * lr, weight_decay, rms >= 0, momentum in [0, 1), eps > 0, all finite in fp32,
+ * else MOE_ERR_INVALID. */
+moe_status moe_muon_step(const moe_muon_desc* desc, const moe_muon_tensor* tensors, int32_t count, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /* Optional per-kernel timing (the pages' backward carries an optional kernel
  * trace: PR #9 review-bot Overview).  When enabled, every kernel the library
  * launches is bracketed by two HIP events recorded on its launch stream; the

@@ -38,6 +38,8 @@ EXPORTS = (
     "moe_lora_multi_workspace_size", "build_pool_multi", "moe_lora_forward_multi", "moe_lora_backward_multi",
     "moe_router_workspace_size", "moe_router_forward", "moe_router_backward", "moe_adamw_step",
     "moe_fp8_quantize_rows", "moe_fp8_quantize_weight", "moe_fp8_product",
+    "moe_expert_product", "moe_expert_weight_grad", "moe_mxfp4_quantize_rows", "moe_mxfp4_quantize_weight",
+    "moe_mxfp4_dequantize", "moe_mxfp4_product", "moe_muon_workspace_size", "moe_muon_step",
 )
 
 
@@ -100,6 +102,27 @@ class MoeAdamwDesc(ctypes.Structure):
 class MoeFp8Desc(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("topk", ctypes.c_int32),
                 ("a_rows", ctypes.c_int64)]
+
+
+class MoeExpertDesc(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32), ("topk", ctypes.c_int32),
+                ("a_rows", ctypes.c_int64), ("transposed", ctypes.c_int32), ("out_type", ctypes.c_int32),
+                ("accumulate", ctypes.c_int32)]
+
+
+class MoeMxfp4Desc(ctypes.Structure):
+    _fields_ = MoeFp8Desc._fields_
+
+
+class MoeMuonTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("param", "master", "grad", "momentum")] + [
+        ("batch", ctypes.c_int64), ("m", ctypes.c_int32), ("n", ctypes.c_int32)]
+
+
+class MoeMuonDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("param_type", "grad_type", "nesterov", "rounds")] + [
+        (n, ctypes.c_double) for n in ("lr", "momentum", "weight_decay", "rms", "eps", "grad_scale", "a", "b", "c")] + [
+        ("control", ctypes.c_void_p)]
 
 
 def _adapters(roots: Optional[Sequence[int]]):
@@ -170,7 +193,18 @@ def library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.moe_fp8_quantize_rows.argtypes = [vp, i64, i32, i32, vp, vp, vp]
     lib.moe_fp8_quantize_weight.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
     lib.moe_fp8_product.argtypes = [P(MoeFp8Desc), P(MoePool), vp, vp, vp, vp, vp, vp]
-    for fn in ("moe_router_workspace_size", "moe_router_forward", "moe_router_backward", "moe_adamw_step",
+    lib.moe_expert_product.argtypes = [P(MoeExpertDesc), P(MoePool), vp, vp, vp, vp]
+    lib.moe_expert_weight_grad.argtypes = [P(MoeExpertDesc), P(MoePool), vp, vp, vp, vp]
+    lib.moe_mxfp4_quantize_rows.argtypes = [vp, i64, i32, i32, vp, vp, vp]
+    lib.moe_mxfp4_quantize_weight.argtypes = [vp, i32, i32, i32, vp, vp, vp, vp, vp]
+    lib.moe_mxfp4_dequantize.argtypes = [vp, vp, i64, i32, vp, vp]
+    lib.moe_mxfp4_product.argtypes = [P(MoeMxfp4Desc), P(MoePool), vp, vp, vp, vp, vp, vp]
+    MD, MT = P(MoeMuonDesc), P(MoeMuonTensor)
+    lib.moe_muon_workspace_size.argtypes = [MD, MT, i32, P(sz)]
+    lib.moe_muon_step.argtypes = [MD, MT, i32, vp, sz, vp]
+    for fn in ("moe_expert_product", "moe_expert_weight_grad", "moe_mxfp4_quantize_rows", "moe_mxfp4_quantize_weight",
+               "moe_mxfp4_dequantize", "moe_mxfp4_product", "moe_muon_workspace_size", "moe_muon_step",
+               "moe_router_workspace_size", "moe_router_forward", "moe_router_backward", "moe_adamw_step",
                "moe_fp8_quantize_rows", "moe_fp8_quantize_weight", "moe_fp8_product",
                "moe_lora_trace_collect", "moe_lora_trace_entry", "moe_lora_block_m", "moe_lora_pool_capacity", "moe_lora_workspace_size",
                "build_pool", "moe_lora_forward", "moe_lora_forward_noalloc", "moe_lora_backward",
@@ -666,8 +700,18 @@ class MoeRouter:
 
 
 # --------------------------------------------------------------------------
-# optimiser
+# optimisers
 # --------------------------------------------------------------------------
+def _own_memory(tensors: Sequence[Tuple[str, Sequence[torch.Tensor]]], read: str = "grads") -> None:
+    """Memory that a step writes belongs to one tensor alone; tensors named `read` may share theirs."""
+    spans = [(t.data_ptr(), t.numel() * t.element_size(), k) for k, ts in tensors for t in ts if t.numel()]
+    end, end_written = 0, 0
+    for at, size, k in sorted(spans):
+        if at < (end_written if k == read else end):
+            raise ValueError(f"{k} overlap another tensor of the optimiser")
+        end, end_written = max(end, at + size), end_written if k == read else max(end_written, at + size)
+
+
 class MoeAdamW:
     """AdamW over a list of tensors (the factors of one or more layers) in one
     call per step.  params: bf16 or fp32, all of one type, updated in place;
@@ -729,15 +773,7 @@ class MoeAdamW:
                 _ptr(self.states["v"][i], kinds["v"], None, "v"), *sc, n)
         # the memory outlives a replacement of a tensor's own
         self._held = [t.untyped_storage() for ts in (self.params, self.grads, self.masters or [], *self.states.values()) for t in ts]
-        # memory that a step writes belongs to one tensor alone
-        spans = [(t.data_ptr(), t.numel() * t.element_size(), k) for k, ts in
-                 (("params", self.params), ("grads", self.grads), ("masters", self.masters or []), *self.states.items())
-                 for t in ts if t.numel()]
-        end, end_written = 0, 0
-        for at, size, k in sorted(spans):
-            if at < (end_written if k == "grads" else end):
-                raise ValueError(f"{k} overlap another tensor of the optimiser")
-            end, end_written = max(end, at + size), end_written if k == "grads" else max(end_written, at + size)
+        _own_memory([("params", self.params), ("grads", self.grads), ("masters", self.masters or []), *self.states.items()])
 
     def step(self, lr: Optional[float] = None, step: Optional[int] = None, grad_scale: float = 1.0,
              seed: Optional[int] = None, control: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -774,6 +810,91 @@ class MoeAdamW:
         f = f.view(torch.int32)
         s = (step if seed is None else seed) & 0xFFFFFFFF
         control.copy_(torch.cat([f, torch.tensor([s - (1 << 32) if s >> 31 else s], dtype=torch.int32)]))
+
+
+class MoeMuon:
+    """The optimiser step with an orthogonalised update (momentum, then rounds
+    of a quintic; see include/moelora.h) over a list of tensors of matrices,
+    [..., m, n] with min(m, n) <= 256: the factors of one or more layers, an
+    expert-local factor [E, I, r] being a matrix per expert.  params, grads and
+    masters as in MoeAdamW (they stay where they are and the optimiser keeps
+    their memory).  states: {"momentum": [...]} fp32 to go on from, else zeros.
+    rms: the update's root mean square, as far as its singular values are one.
+    Keeps the workspace that its steps use: steps of one optimiser at the same
+    time (two streams, two captured graphs) are not allowed."""
+
+    def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
+                 masters: Optional[Sequence[torch.Tensor]] = None, lr: float = 0.02, momentum: float = 0.95,
+                 nesterov: bool = True, weight_decay: float = 0.0, rms: float = 0.2, eps: float = 1e-7, rounds: int = 5,
+                 coefficients: Tuple[float, float, float] = (3.4445, -4.7750, 2.0315),
+                 states: Optional[Dict[str, Sequence[torch.Tensor]]] = None):
+        if not params or len(grads) != len(params) or (masters is not None and len(masters) != len(params)):
+            raise ValueError("params, grads and masters are lists of one length, not empty")
+        if any(p.dim() < 2 for p in params):
+            raise ValueError("params are matrices, or stacks of them: [..., m, n]")
+        self.params, self.grads = list(params), list(grads)
+        self.masters = None if masters is None else list(masters)
+        self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
+        self.rms, self.eps, self.rounds, self.coefficients = rms, eps, rounds, coefficients
+        self._dev = _device_of(params[0], "params")
+        f32, ptype, gtype = torch.float32, params[0].dtype, grads[0].dtype
+        if masters is not None and ptype != torch.bfloat16:
+            raise ValueError("masters stand beside bf16 params")
+        if states is None:
+            states = {"momentum": [torch.zeros(p.shape, dtype=f32, device=p.device) for p in self.params]}
+        if set(states) != {"momentum"} or len(states["momentum"]) != len(params):
+            raise ValueError("states must hold 'momentum', one tensor each per param")
+        self.states = {"momentum": list(states["momentum"])}
+        lists = [("params", self.params, ptype), ("grads", self.grads, gtype), ("masters", self.masters or [], f32),
+                 ("momentum", self.states["momentum"], f32)]
+        self._table = (MoeMuonTensor * len(params))()
+        for i, p in enumerate(self.params):
+            ptr = {k: _on(self._dev, ts[i], ty, p.shape, k) if ts else None for k, ts, ty in lists}
+            self._table[i] = MoeMuonTensor(ptr["params"], ptr["masters"], ptr["grads"], ptr["momentum"],
+                                           p.numel() // max(1, p.shape[-2] * p.shape[-1]), *p.shape[-2:])
+        _own_memory([(k, ts) for k, ts, _ in lists])
+        # the memory outlives a replacement of a tensor's own
+        self._held = [t.untyped_storage() for _, ts, _ in lists for t in ts]
+        self._desc = MoeMuonDesc(_float_type(ptype, "params"), _float_type(gtype, "grads"))
+        self._dp = ctypes.byref(self._desc)
+        self._same = None
+        self._fill()
+        v = ctypes.c_size_t()
+        with torch.cuda.device(self._dev):
+            _check(library().moe_muon_workspace_size(self._dp, self._table, len(params), ctypes.byref(v)),
+                   "moe_muon_workspace_size")
+        self.workspace = torch.empty(v.value, dtype=torch.uint8, device=params[0].device)
+        self._ws = (self.workspace.data_ptr(), v.value)
+        self._held.append(self.workspace.untyped_storage())
+
+    def _fill(self) -> None:
+        d = self._desc
+        same = (self.momentum, self.weight_decay, self.rms, self.eps, *self.coefficients, self.nesterov, self.rounds)
+        if same != self._same:  # fields that seldom change
+            d.momentum, d.weight_decay, d.rms, d.eps, d.a, d.b, d.c = same[:7]
+            d.nesterov, d.rounds = int(self.nesterov), self.rounds
+            self._same = same
+
+    def step(self, lr: Optional[float] = None, grad_scale: float = 1.0, control: Optional[torch.Tensor] = None,
+             stream=None) -> None:
+        """One step.  lr: this step's rate (default: the optimiser's);
+        grad_scale multiplies the gradients.  control: both in device memory
+        (write_control), for a captured step."""
+        d = self._desc
+        self._fill()
+        d.lr = self.lr if lr is None else lr
+        d.grad_scale = grad_scale
+        d.control = _on(self._dev, control, torch.float32, (2,), "control")
+        _launch("moe_muon_step", library().moe_muon_step, self._dev, stream, self._dp, self._table, len(self._table), *self._ws)
+
+    def write_control(self, control: torch.Tensor, lr: float, grad_scale: float = 1.0) -> None:
+        """Fill a control buffer (fp32 [2] on the device) with one step's
+        values: before each replay of a graph that captured a step with it."""
+        _on(self._dev, control, torch.float32, (2,), "control")
+        f = torch.tensor([lr, grad_scale], dtype=torch.float64).to(torch.float32)
+        if not (lr >= 0 and bool(torch.isfinite(f).all())):
+            raise ValueError("write_control: lr >= 0 and grad_scale, finite in fp32")
+        control.copy_(f)
 
 
 # --------------------------------------------------------------------------
@@ -826,6 +947,12 @@ def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) 
     return tuple(out)
 
 
+def _pool_of(pool: Dict[str, torch.Tensor], E: int, dev: int, block_m: int) -> MoePool:
+    i32, r2r = torch.int32, pool["row_to_route"]
+    return MoePool(_on(dev, pool["counts"], i32, (E,), "counts"), _on(dev, pool["offsets"], i32, (E + 1,), "offsets"), None,
+                   _on(dev, r2r, i32, None, "row_to_route"), r2r.numel(), block_m)
+
+
 def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.Tensor, w: torch.Tensor,
                 w_scales: torch.Tensor, topk: int = 0, out: Optional[torch.Tensor] = None, block_m: int = 16,
                 stream=None) -> torch.Tensor:
@@ -844,13 +971,151 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
     dev = _device_of(a, "a")
     if out is None:
         out = _made(stream, torch.zeros, cap, N, dtype=torch.bfloat16, device=a.device)
-    i32, f32 = torch.int32, torch.float32
-    ps = MoePool(_on(dev, pool["counts"], i32, (E,), "counts"), _on(dev, pool["offsets"], i32, (E + 1,), "offsets"), None,
-                 _on(dev, pool["row_to_route"], i32, None, "row_to_route"), cap, block_m)
+    f32 = torch.float32
+    ps = _pool_of(pool, E, dev, block_m)
     d = MoeFp8Desc(E, N, K, topk, rows)
     _launch("moe_fp8_product", library().moe_fp8_product, dev, stream, ctypes.byref(d), ctypes.byref(ps),
             _on(dev, a, _E4M3, None, "a"), _on(dev, a_scales, f32, (rows, K // 128), "a_scales"),
             _on(dev, w, _E4M3, (E, N, K), "w"), _on(dev, w_scales, f32, (E, N // 128, K // 128), "w_scales"),
+            _on(dev, out, torch.bfloat16, (cap, N), "out"))
+    return out
+
+
+# --------------------------------------------------------------------------
+# expert products in bf16, and the weight's gradient
+# --------------------------------------------------------------------------
+def expert_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, w: torch.Tensor, topk: int = 0,
+                   transposed: bool = False, out: Optional[torch.Tensor] = None, block_m: int = 16,
+                   stream=None) -> torch.Tensor:
+    """Every pool row times its expert's weight: out bf16 [capacity, N].
+    pool as in MoeLoraLayer.pool; a bf16 [rows, K]: the tokens (topk > 0: pool
+    row r reads token row_to_route[r] / topk), or the pool rows themselves
+    (topk = 0); w bf16 [E, N, K], or [E, K, N] with transposed: the data
+    gradient of a product is this product of its output's gradient with the
+    same weight, transposed.  Rows of no route are left as they are (an `out`
+    made here holds zeros there).  block_m: the pool's (the library's own
+    choice is 16)."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K] and w [E, N, K], or [E, K, N] with transposed")
+    rows, K = a.shape
+    E, N = w.shape[0], w.shape[2 if transposed else 1]
+    cap = pool["row_to_route"].numel()
+    dev = _device_of(a, "a")
+    bf = torch.bfloat16
+    if out is None:
+        out = _made(stream, torch.zeros, cap, N, dtype=bf, device=a.device)
+    ps = _pool_of(pool, E, dev, block_m)
+    d = MoeExpertDesc(E, N, K, topk, rows, int(transposed), 0, 0)
+    _launch("moe_expert_product", library().moe_expert_product, dev, stream, ctypes.byref(d), ctypes.byref(ps),
+            _on(dev, a, bf, None, "a"), _on(dev, w, bf, (E, K, N) if transposed else (E, N, K), "w"),
+            _on(dev, out, bf, (cap, N), "out"))
+    return out
+
+
+def expert_weight_grad(pool: Dict[str, torch.Tensor], grad: torch.Tensor, a: torch.Tensor, topk: int = 0,
+                       out: Optional[torch.Tensor] = None, accumulate: bool = False, dtype=torch.bfloat16,
+                       block_m: int = 16, stream=None) -> torch.Tensor:
+    """The gradient [E, N, K] of expert_product's weight [E, N, K] from its
+    output's gradient, grad bf16 [capacity, N] (rows of no route are not
+    used), and its a (gathered by token with topk > 0, as there).  out: bf16 or
+    fp32, overwritten or, with accumulate, added to; made here of dtype if
+    None."""
+    if a.dim() != 2 or grad.dim() != 2:
+        raise ValueError("grad must be [capacity, N] and a [rows, K]")
+    rows, K = a.shape
+    E, N = pool["counts"].numel(), grad.shape[1]
+    cap = pool["row_to_route"].numel()
+    dev = _device_of(a, "a")
+    bf = torch.bfloat16
+    if out is None:
+        if accumulate:
+            raise ValueError("accumulate adds to an out that is given")
+        out = _made(stream, torch.empty, E, N, K, dtype=dtype, device=a.device)
+    ps = _pool_of(pool, E, dev, block_m)
+    d = MoeExpertDesc(E, N, K, topk, rows, 0, _float_type(out.dtype, "out"), int(accumulate))
+    _launch("moe_expert_weight_grad", library().moe_expert_weight_grad, dev, stream, ctypes.byref(d), ctypes.byref(ps),
+            _on(dev, grad, bf, (cap, N), "grad"), _on(dev, a, bf, None, "a"), _on(dev, out, out.dtype, (E, N, K), "out"))
+    return out
+
+
+# --------------------------------------------------------------------------
+# 4-bit rows, weights and expert products
+# --------------------------------------------------------------------------
+def mxfp4_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optional[torch.Tensor] = None,
+                        exponents: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """src bf16 [rows, K] (act None) or [rows, 2K] = gate | up (act "swiglu",
+    "geglu") to MXFP4: codes uint8 [rows, K/2] and exponents uint8 [rows,
+    K/32] (see include/moelora.h; the layout of an MXFP4 base)."""
+    if src.dim() != 2 or act not in _ACTS or (act is not None and src.shape[1] % 2):
+        raise ValueError("src must be [rows, K], or [rows, 2K] with act 'swiglu' or 'geglu'")
+    rows, K = src.shape
+    if act is not None:
+        K //= 2
+    dev, u8 = _device_of(src, "src"), torch.uint8
+    if codes is None:
+        codes = _made(stream, torch.empty, rows, K // 2, dtype=u8, device=src.device)
+    if exponents is None:
+        exponents = _made(stream, torch.empty, rows, K // 32, dtype=u8, device=src.device)
+    _launch("moe_mxfp4_quantize_rows", library().moe_mxfp4_quantize_rows, dev, stream,
+            _on(dev, src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], _on(dev, codes, u8, (rows, K // 2), "codes"),
+            _on(dev, exponents, u8, (rows, K // 32), "exponents"))
+    return codes, exponents
+
+
+def mxfp4_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) -> Tuple[torch.Tensor, ...]:
+    """W bf16 [E, N, K] to (codes [E, N, K/2], exponents [E, N, K/32]), blocks
+    along K: an MXFP4 base's W13 or W2 and its scales; with transposed also of
+    the transposed weight, (codes_t [E, K, N/2], exponents_t [E, K, N/32]),
+    blocks along N: the data gradient's operand."""
+    if W.dim() != 3:
+        raise ValueError("W must be [E, N, K]")
+    E, N, K = W.shape
+    dev = _device_of(W, "W")
+
+    def pair(n, k):
+        return [_made(stream, torch.empty, E, n, k // b, dtype=torch.uint8, device=W.device) for b in (2, 32)]
+    out = pair(N, K) + (pair(K, N) if transposed else [])
+    _launch("moe_mxfp4_quantize_weight", library().moe_mxfp4_quantize_weight, dev, stream,
+            _on(dev, W, torch.bfloat16, None, "W"), E, N, K, *[t.data_ptr() for t in out], *([] if transposed else [None, None]))
+    return tuple(out)
+
+
+def mxfp4_dequantize(codes: torch.Tensor, exponents: torch.Tensor, out: Optional[torch.Tensor] = None,
+                     stream=None) -> torch.Tensor:
+    """The values of codes uint8 [..., K/2] and exponents [..., K/32], exactly, as bf16 [..., K]."""
+    if codes.dim() < 1 or not codes.is_contiguous():
+        raise ValueError("codes must be [..., K/2], contiguous")
+    shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+    K, dev, u8 = shape[-1], _device_of(codes, "codes"), torch.uint8
+    if K % 128:
+        raise ValueError("K must be a multiple of 128")
+    rows = codes.numel() * 2 // K if K else 0
+    if out is None:
+        out = _made(stream, torch.empty, *shape, dtype=torch.bfloat16, device=codes.device)
+    _launch("moe_mxfp4_dequantize", library().moe_mxfp4_dequantize, dev, stream, _on(dev, codes, u8, None, "codes"),
+            _on(dev, exponents, u8, (*shape[:-1], K // 32), "exponents"), rows, K, _on(dev, out, torch.bfloat16, shape, "out"))
+    return out
+
+
+def mxfp4_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_exponents: torch.Tensor, w: torch.Tensor,
+                  w_exponents: torch.Tensor, topk: int = 0, out: Optional[torch.Tensor] = None, block_m: int = 16,
+                  stream=None) -> torch.Tensor:
+    """expert_product on MXFP4 operands: a uint8 [rows, K/2] with a_exponents
+    [rows, K/32], w uint8 [E, N, K/2] with w_exponents [E, N, K/32]; out bf16
+    [capacity, N]."""
+    if a.dim() != 2 or w.dim() != 3:
+        raise ValueError("a must be [rows, K/2] and w [E, N, K/2]")
+    rows, K = a.shape[0], 2 * a.shape[1]
+    E, N = w.shape[:2]
+    cap = pool["row_to_route"].numel()
+    dev, u8 = _device_of(a, "a"), torch.uint8
+    if out is None:
+        out = _made(stream, torch.zeros, cap, N, dtype=torch.bfloat16, device=a.device)
+    ps = _pool_of(pool, E, dev, block_m)
+    d = MoeMxfp4Desc(E, N, K, topk, rows)
+    _launch("moe_mxfp4_product", library().moe_mxfp4_product, dev, stream, ctypes.byref(d), ctypes.byref(ps),
+            _on(dev, a, u8, None, "a"), _on(dev, a_exponents, u8, (rows, K // 32), "a_exponents"),
+            _on(dev, w, u8, (E, N, K // 2), "w"), _on(dev, w_exponents, u8, (E, N, K // 32), "w_exponents"),
             _on(dev, out, torch.bfloat16, (cap, N), "out"))
     return out
 

@@ -20,7 +20,7 @@ CSRC = os.path.join(PKG, "csrc")
 OUT = os.path.join(PKG, "libmoelora.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 SOURCES = ["pool.hip", "forward.hip", "backward.hip", "pack.hip", "api.hip", "trace.hip", "branch.hip",
-           "router.hip", "adamw.hip", "fp8.hip"]
+           "router.hip", "adamw.hip", "fp8.hip", "product.hip", "mxfp4.hip", "muon.hip"]
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

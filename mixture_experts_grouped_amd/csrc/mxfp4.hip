@@ -1,0 +1,299 @@
+// mxfp4.hip -- rows and weights in microscaled 4-bit floating point (e2m1 codes,
+// one e8m0 exponent per 32), and the expert products on them
+// (include/moelora.h states the formulas).
+#include "../../include/moelora.h"
+#include "checks.hpp"
+#include "engine2.hpp"
+#include "lanes.hpp"
+#include "pool_tiles.hpp"
+#include "trace.hpp"
+
+namespace moelora {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+constexpr int MAX_DIM = 65536;
+
+// ---------------------------------------------------------------------------
+// quantisers
+// ---------------------------------------------------------------------------
+// The block's held exponent (plus 127) from its largest magnitude's bits, and
+// the multiplier that brings the block to the codes' range.
+__device__ __forceinline__ uint32_t block_exponent(uint32_t mag_max, float& mul) {
+  const int field = (int)(mag_max >> 23);
+  if (field == 255) {  // NaN or infinity
+    mul = 0.0f;
+    return 255;
+  }
+  const int e = field > 2 ? field - 2 : 0;  // max|x| < 2^-125: the smallest exponent
+  mul = __uint_as_float((uint32_t)(e == 0 ? 254 : 254 - e) << 23);  // 2^(127 - e); 254 - e >= 1
+  return (uint32_t)e;
+}
+// |x mul| to a code of e2m1: to nearest, ties to the even code, at most 7; the
+// sign stays with codes that are not zero.
+__device__ __forceinline__ uint32_t code4(float x, float mul) {
+  const float y = fminf(fabsf(x) * mul, 6.0f);
+  // spacing 1/2 below 2, 1 below 4, 2 above: codes 2y, y + 2, y / 2 + 4
+  const float n = y < 2.0f ? __builtin_rintf(2.0f * y) : y < 4.0f ? __builtin_rintf(y) + 2.0f : __builtin_rintf(0.5f * y) + 4.0f;
+  const uint32_t c = (uint32_t)n;
+  return c | (c != 0 && x < 0.0f ? 8u : 0u);
+}
+// The largest of four neighbouring lanes, in all of them.
+__device__ __forceinline__ uint32_t quad_max(uint32_t v) {
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0xB1, 0xF, 0xF, true));  // lanes 1 0 3 2
+  return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x4E, 0xF, 0xF, true));  // lanes 2 3 0 1
+}
+
+// Eight columns a thread, a block of 32 in four lanes.
+template <int ACT>
+__global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__ src, long n8, int K8,
+                                                    uint32_t* __restrict__ codes, uint8_t* __restrict__ exps) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;  // whole blocks: K % 128 == 0
+  float v[8];
+  if constexpr (ACT < 0) {
+    widen8(((const u32x4*)src)[i], v);
+  } else {
+    const long row = i / K8, c = i - row * K8;
+    const u32x4* p = (const u32x4*)src + row * 2 * K8 + c;
+    float u[8];
+    widen8(p[0], v);
+    widen8(p[K8], u);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = (ACT == MOE_ACT_SWIGLU ? v[q] * sigmoidf_(v[q]) : v[q] * norm_cdf_rel(v[q])) * u[q];
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) m = max(m, mag(v[q]));
+  float mul;
+  const uint32_t e = block_exponent(quad_max(m), mul);
+  uint32_t w = 0;
+#pragma unroll
+  for (int q = 0; q < 8; ++q) w |= code4(v[q], mul) << (4 * q);
+  codes[i] = w;
+  if ((threadIdx.x & 3) == 0) exps[i >> 2] = (uint8_t)e;
+}
+
+// The transposed weight's codes: a workgroup takes 128 rows n x 32 columns k of
+// one expert through LDS; thread t quantises block t / 32 (32 rows n) of column t % 32.
+__global__ __launch_bounds__(128) void k_mxfp4_weight_t(const uint16_t* __restrict__ W, int N, int K,
+                                                        uint8_t* __restrict__ codes, uint8_t* __restrict__ exps) {
+  __shared__ uint16_t tile[128][33];
+  const long e = blockIdx.z, n0 = (long)blockIdx.y * 128, k0 = (long)blockIdx.x * 32;
+  for (int i = threadIdx.x; i < 128 * 32; i += 128) tile[i >> 5][i & 31] = W[(e * N + n0 + (i >> 5)) * K + k0 + (i & 31)];
+  __syncthreads();
+  const int k = threadIdx.x & 31, b = threadIdx.x >> 5;
+  float v[32];
+  uint32_t m = 0;
+#pragma unroll
+  for (int q = 0; q < 32; ++q) {
+    v[q] = bf2f(tile[32 * b + q][k]);
+    m = max(m, mag(v[q]));
+  }
+  float mul;
+  const uint32_t x = block_exponent(m, mul);
+  u32x4 w;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    w[c] = 0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) w[c] |= code4(v[8 * c + q], mul) << (4 * q);
+  }
+  const long row = e * K + k0 + k;
+  *(u32x4*)(codes + row * (N / 2) + (n0 + 32 * b) / 2) = w;
+  exps[row * (N / 32) + n0 / 32 + b] = (uint8_t)x;
+}
+
+// Eight values a thread.
+__global__ __launch_bounds__(256) void k_mxfp4_values(const uint32_t* __restrict__ codes, const uint8_t* __restrict__ exps,
+                                                      long n8, u32x4* __restrict__ out) {
+  const long i = (long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;
+  const uint32_t w = codes[i], e = exps[i >> 2];
+  u32x4 o;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t n = (w >> (8 * c + 4 * q)) & 15u, m = n & 7u;
+      const float a = m < 2 ? 0.5f * (float)m : (1.0f + 0.5f * (float)(m & 1u)) * (float)(1u << (m >> 1)) * 0.5f;
+      const float s = e == 255 ? __uint_as_float(0x7FC00000u) : v2::e8m0_value(e);
+      v[q] = (n & 8u ? -a : a) * s;
+    }
+    o[c] = pack2(v[0], v[1]);
+  }
+  out[i] = o;
+}
+
+// ---------------------------------------------------------------------------
+// product
+// ---------------------------------------------------------------------------
+struct MxArgs : PoolArgs {
+  int N, K;
+  const uint8_t* a;
+  const uint8_t* ea;
+  const uint8_t* w;
+  const uint8_t* ew;
+  uint16_t* out;
+};
+
+__device__ __forceinline__ f32x4 mma4(u32x4 w, u32x4 x, f32x4 c, int ew, int ex) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0},
+                                                          i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0}, c,
+                                                          4, 4, 0, ew, 0, ex);
+}
+
+// One wave a tile of 16 activation rows x 16 weight rows, operands straight
+// into registers: lane l holds row l % 16 and block l / 16 of each 128.
+constexpr int FEW_ROWS = 16;
+__global__ __launch_bounds__(64) void k_mxfp4_few(MxArgs p) {
+  const int lane = threadIdx.x;
+  const int fr = lane & 15, fc = lane >> 4;
+  const int KB = p.K / 128, RB = p.K / 2, RE = p.K / 32;
+  int e, m, nt;
+  for (int b = blockIdx.x; pool_tile(p, FEW_ROWS, b, p.N / 16, TILE_GM, e, m, nt); b += gridDim.x) {
+    const int n0 = nt * 16;
+    const long row0 = (long)p.offsets[e] + (long)m * FEW_ROWS;
+    const int nrows = min(rows_of(p, e) - m * FEW_ROWS, FEW_ROWS);
+    long ar = -1;
+    if (fr < nrows) {
+      if (p.topk > 0)
+        ar = token_of(p, p.row2r[row0 + fr]);
+      else if (row0 + fr < p.a_rows)
+        ar = row0 + fr;
+    }
+    const uint8_t* w = p.w + ((long)e * p.N + n0 + fr) * RB + 16 * fc;
+    const uint8_t* ew = p.ew + ((long)e * p.N + n0 + fr) * RE + fc;
+    const uint8_t* x = p.a + ar * RB + 16 * fc;
+    const uint8_t* ex = p.ea + ar * RE + fc;
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int c = 0; c < KB; ++c) {
+      const u32x4 wv = *(const u32x4*)(w + 64 * c);
+      const int we = ew[4 * c];
+      u32x4 xv = {0, 0, 0, 0};
+      int xe = 0;
+      if (ar >= 0) {
+        xv = *(const u32x4*)(x + 64 * c);
+        xe = ex[4 * c];
+      }
+      acc = mma4(wv, xv, acc, we, xe);
+    }
+    if (fr < nrows)
+      *(u32x2*)(p.out + (row0 + fr) * p.N + n0 + 4 * fc) = u32x2{pack2(acc[0], acc[1]), pack2(acc[2], acc[3])};
+  }
+}
+
+moe_status check_weight(int32_t E, int32_t N, int32_t K, int32_t nstep) {
+  if (E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID;
+  if (E > MAX_E || N % nstep != 0 || K % 128 != 0 || N > MAX_DIM || K > MAX_DIM || (int64_t)N * K >= (int64_t)1 << 31)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+template <int ACT>
+hipError_t launch_rows(const void* src, long n8, int K8, void* codes, void* exps, hipStream_t st) {
+  MOE_LAUNCH_AS("k_mxfp4_rows", k_mxfp4_rows<ACT>, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, st,
+                (const uint16_t*)src, n8, K8, (uint32_t*)codes, (uint8_t*)exps);
+  return hipGetLastError();
+}
+// a launch holds fewer than 2^32 threads, eight columns each, in whole workgroups of 256
+constexpr int64_t MOST_VALUES = ((int64_t)1 << 35) - 2048;
+bool any_overlap(const Range* r, int n) {
+  for (int i = 0; i < n; ++i)
+    for (int j = 0; j < i; ++j)
+      if (overlap(r[i], r[j])) return true;
+  return false;
+}
+
+}  // namespace
+}  // namespace moelora
+
+using namespace moelora;
+
+extern "C" {
+
+moe_status moe_mxfp4_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes,
+                                   void* exponents, void* stream) {
+  if (rows < 0 || K < 1) return MOE_ERR_INVALID;
+  if (K % 128 != 0 || K > MAX_DIM || rows >= (int64_t)1 << 31 || rows * K > MOST_VALUES) return MOE_ERR_UNSUPPORTED;
+  if (act != MOE_FP8_PLAIN && act != MOE_ACT_SWIGLU && act != MOE_ACT_GEGLU) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(src) || !aligned16(codes) || !aligned(exponents, 4)) return MOE_ERR_INVALID;
+  const size_t n = (size_t)rows * K;
+  const Range r[] = {rng(src, n * (act == MOE_FP8_PLAIN ? 2 : 4)), rng(codes, n / 2), rng(exponents, n / 32)};
+  if (any_overlap(r, 3)) return MOE_ERR_INVALID;
+  const hipStream_t st = (hipStream_t)stream;
+  const hipError_t e = act == MOE_FP8_PLAIN    ? launch_rows<MOE_FP8_PLAIN>(src, (long)(n / 8), K / 8, codes, exponents, st)
+                       : act == MOE_ACT_SWIGLU ? launch_rows<MOE_ACT_SWIGLU>(src, (long)(n / 8), K / 8, codes, exponents, st)
+                                               : launch_rows<MOE_ACT_GEGLU>(src, (long)(n / 8), K / 8, codes, exponents, st);
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_mxfp4_quantize_weight(const void* W, int32_t E, int32_t N, int32_t K, void* codes, void* exponents,
+                                     void* codes_t, void* exponents_t, void* stream) {
+  const moe_status s = check_weight(E, N, K, 128);
+  if (s != MOE_OK) return s;
+  const size_t n = (size_t)E * N * K;
+  if (n > (size_t)MOST_VALUES) return MOE_ERR_UNSUPPORTED;
+  if (!aligned16(W) || !aligned16(codes) || !aligned(exponents, 4)) return MOE_ERR_INVALID;
+  if ((codes_t != nullptr) != (exponents_t != nullptr)) return MOE_ERR_INVALID;
+  if (codes_t != nullptr && (!aligned16(codes_t) || !aligned(exponents_t, 4))) return MOE_ERR_INVALID;
+  const Range r[] = {rng(W, 2 * n), rng(codes, n / 2), rng(exponents, n / 32), rng(codes_t, n / 2), rng(exponents_t, n / 32)};
+  if (any_overlap(r, 5)) return MOE_ERR_INVALID;
+  const hipStream_t st = (hipStream_t)stream;
+  hipError_t e = launch_rows<MOE_FP8_PLAIN>(W, (long)(n / 8), K / 8, codes, exponents, st);
+  if (e == hipSuccess && codes_t != nullptr) {
+    MOE_LAUNCH(k_mxfp4_weight_t, dim3(K / 32, N / 128, E), dim3(128), 0, st, (const uint16_t*)W, N, K, (uint8_t*)codes_t,
+               (uint8_t*)exponents_t);
+    e = hipGetLastError();
+  }
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_mxfp4_dequantize(const void* codes, const void* exponents, int64_t rows, int32_t K, void* out,
+                                void* stream) {
+  if (rows < 0 || K < 1) return MOE_ERR_INVALID;
+  if (K % 128 != 0 || K > MAX_DIM || rows >= (int64_t)1 << 31 || rows * K > MOST_VALUES) return MOE_ERR_UNSUPPORTED;
+  if (rows == 0) return MOE_OK;
+  if (!aligned16(codes) || !aligned(exponents, 4) || !aligned16(out)) return MOE_ERR_INVALID;
+  const size_t n = (size_t)rows * K;
+  const Range o = rng(out, 2 * n);
+  if (overlap(o, rng(codes, n / 2)) || overlap(o, rng(exponents, n / 32))) return MOE_ERR_INVALID;
+  const long n8 = (long)(n / 8);
+  MOE_LAUNCH(k_mxfp4_values, dim3((unsigned)((n8 + 255) / 256)), dim3(256), 0, (hipStream_t)stream, (const uint32_t*)codes,
+             (const uint8_t*)exponents, n8, (u32x4*)out);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+moe_status moe_mxfp4_product(const moe_mxfp4_desc* d, const moe_pool* pool, const void* a, const void* a_exponents,
+                             const void* w, const void* w_exponents, void* out, void* stream) {
+  if (d == nullptr || pool == nullptr) return MOE_ERR_INVALID;
+  const moe_status s = check_weight(d->E, d->N, d->K, 32);
+  if (s != MOE_OK) return s;
+  if (d->topk < 0 || d->a_rows < 1 || pool->capacity < 1 || pool->block_m < 1) return MOE_ERR_INVALID;
+  if (pool->capacity >= (int64_t)1 << 31 || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  // tile indices of the smallest tiles are 32 bits
+  if ((pool->capacity / FEW_ROWS + d->E) * (d->N / 16) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  if (d->topk > 0 && d->a_rows * d->K >= (int64_t)1 << 32) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor
+  if (!aligned(pool->counts, 4) || !aligned(pool->offsets, 4) || !aligned(pool->row_to_route, 4))
+    return MOE_ERR_INVALID;
+  if (!aligned16(a) || !aligned(a_exponents, 4) || !aligned16(w) || !aligned(w_exponents, 4) || !aligned16(out))
+    return MOE_ERR_INVALID;
+  const size_t na = (size_t)d->a_rows * d->K, nw = (size_t)d->E * d->N * d->K;
+  const Range ro = rng(out, (size_t)pool->capacity * d->N * 2);
+  const Range ins[] = {rng(a, na / 2), rng(a_exponents, na / 32), rng(w, nw / 2), rng(w_exponents, nw / 32),
+                       rng(pool->counts, (size_t)d->E * 4), rng(pool->offsets, (size_t)d->E * 4 + 4),
+                       rng(pool->row_to_route, (size_t)pool->capacity * 4)};
+  for (const Range& r : ins)
+    if (overlap(ro, r)) return MOE_ERR_INVALID;
+  const MxArgs p{pool_args(d->E, d->topk, d->a_rows, pool), d->N, d->K, (const uint8_t*)a, (const uint8_t*)a_exponents,
+                 (const uint8_t*)w, (const uint8_t*)w_exponents, (uint16_t*)out};
+  const int64_t routes = pool_routes(pool, d->E), live = routes < d->E ? routes : d->E;
+  int cus = 0;
+  if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
+  const unsigned grid = grid_of((routes / FEW_ROWS + live) * (d->N / 16), 8 * cus);
+  MOE_LAUNCH(k_mxfp4_few, dim3(grid), dim3(64), 0, (hipStream_t)stream, p);
+  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+}
+
+}  // extern "C"

@@ -14,9 +14,11 @@ on tiny inputs) live in ``tests/test_oracle_*.py``.
 Modules:
   pool     -- expert-contiguous pool padded per expert (integer metadata)
   moe_lora -- forward and backward of the layer, per route
-  mxfp4    -- exact dequantisation of e2m1 values with e8m0 block scales
+  mxfp4    -- e2m1 values with e8m0 block scales: exact dequantisation, quantisation
   multi_adapter -- several adapters in one pass, one root of tokens each
   router   -- top-k routing, expert loads, balance loss and their gradient
   float8   -- E4M3 / E5M2, block-scaled rows and products, the AdamW step
+  products -- expert products on the pool's rows and the weight's gradient
+  muon     -- the optimiser step with an orthogonalised update
 """
-from . import pool, moe_lora, mxfp4, multi_adapter, router, float8  # noqa: F401
+from . import pool, moe_lora, mxfp4, multi_adapter, router, float8, products, muon  # noqa: F401

@@ -32,6 +32,25 @@ def dequantize(packed: np.ndarray, scales: np.ndarray) -> np.ndarray:
     return (val.reshape(*val.shape[:-1], K // 32, 32) * sc[..., None]).reshape(val.shape)
 
 
+def quantize(x: np.ndarray):
+    """x [..., K] (K % 32 == 0) to (codes uint8 [..., K/2], exponents uint8 [..., K/32]) as include/moelora.h states:
+    exponent floor(log2 max|x|) - 2 held plus 127, the nearest code by distance, ties to the even one."""
+    x = np.asarray(x, dtype=np.float64)
+    blk = x.reshape(*x.shape[:-1], x.shape[-1] // 32, 32)
+    amax = np.abs(blk).max(axis=-1)
+    bad = ~np.isfinite(amax)
+    ok = np.where(bad | (amax == 0), 1.0, amax)
+    e = np.where(amax == 0, -127, np.clip(np.floor(np.log2(ok)) - 2, -127, 127)).astype(np.int64)
+    y = np.abs(np.where(bad[..., None], 0.0, blk)) * np.ldexp(1.0, -e)[..., None]
+    d = np.abs(y[..., None] - E2M1_VALUES)
+    code = np.argmin(d, axis=-1)  # the first of two at one distance: the lower
+    up = np.minimum(code + 1, 7)
+    tie = (np.take_along_axis(d, up[..., None], -1)[..., 0] == np.take_along_axis(d, code[..., None], -1)[..., 0]) & (code % 2 == 1)
+    code = np.where(tie, up, code)
+    nib = (code | np.where((code > 0) & (blk < 0), 8, 0)).astype(np.uint8).reshape(x.shape)
+    return (nib[..., 0::2] | (nib[..., 1::2] << 4)).astype(np.uint8), np.where(bad, 255, e + 127).astype(np.uint8)
+
+
 # --------------------------------------------------------------------------
 # Two-term FP6 (E2M3) split of activations, the operand form of a scaled
 # fp6 x fp4 matrix product whose activations must keep about bf16 precision.
