@@ -5,13 +5,11 @@
 #include "checks.hpp"
 #include "engine2.hpp"
 #include "lanes.hpp"
-#include "pool_tiles.hpp"
-#include "trace.hpp"
+#include "rows_tile.hpp"
 
 namespace moelora {
 namespace {
 
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int MAX_DIM = 65536;
 
 // ---------------------------------------------------------------------------
@@ -126,64 +124,6 @@ __global__ __launch_bounds__(256) void k_mxfp4_values(const uint32_t* __restrict
   out[i] = o;
 }
 
-// ---------------------------------------------------------------------------
-// product
-// ---------------------------------------------------------------------------
-struct MxArgs : PoolArgs {
-  int N, K;
-  const uint8_t* a;
-  const uint8_t* ea;
-  const uint8_t* w;
-  const uint8_t* ew;
-  uint16_t* out;
-};
-
-__device__ __forceinline__ f32x4 mma4(u32x4 w, u32x4 x, f32x4 c, int ew, int ex) {
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(i32x8{(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0},
-                                                          i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3], 0, 0, 0, 0}, c,
-                                                          4, 4, 0, ew, 0, ex);
-}
-
-// One wave a tile of 16 activation rows x 16 weight rows, operands straight
-// into registers: lane l holds row l % 16 and block l / 16 of each 128.
-constexpr int FEW_ROWS = 16;
-__global__ __launch_bounds__(64) void k_mxfp4_few(MxArgs p) {
-  const int lane = threadIdx.x;
-  const int fr = lane & 15, fc = lane >> 4;
-  const int KB = p.K / 128, RB = p.K / 2, RE = p.K / 32;
-  int e, m, nt;
-  for (int b = blockIdx.x; pool_tile(p, FEW_ROWS, b, p.N / 16, TILE_GM, e, m, nt); b += gridDim.x) {
-    const int n0 = nt * 16;
-    const long row0 = (long)p.offsets[e] + (long)m * FEW_ROWS;
-    const int nrows = min(rows_of(p, e) - m * FEW_ROWS, FEW_ROWS);
-    long ar = -1;
-    if (fr < nrows) {
-      if (p.topk > 0)
-        ar = token_of(p, p.row2r[row0 + fr]);
-      else if (row0 + fr < p.a_rows)
-        ar = row0 + fr;
-    }
-    const uint8_t* w = p.w + ((long)e * p.N + n0 + fr) * RB + 16 * fc;
-    const uint8_t* ew = p.ew + ((long)e * p.N + n0 + fr) * RE + fc;
-    const uint8_t* x = p.a + ar * RB + 16 * fc;
-    const uint8_t* ex = p.ea + ar * RE + fc;
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = 0; c < KB; ++c) {
-      const u32x4 wv = *(const u32x4*)(w + 64 * c);
-      const int we = ew[4 * c];
-      u32x4 xv = {0, 0, 0, 0};
-      int xe = 0;
-      if (ar >= 0) {
-        xv = *(const u32x4*)(x + 64 * c);
-        xe = ex[4 * c];
-      }
-      acc = mma4(wv, xv, acc, we, xe);
-    }
-    if (fr < nrows)
-      *(u32x2*)(p.out + (row0 + fr) * p.N + n0 + 4 * fc) = u32x2{pack2(acc[0], acc[1]), pack2(acc[2], acc[3])};
-  }
-}
-
 moe_status check_weight(int32_t E, int32_t N, int32_t K, int32_t nstep) {
   if (E < 1 || N < 1 || K < 1) return MOE_ERR_INVALID;
   if (E > MAX_E || N % nstep != 0 || K % 128 != 0 || N > MAX_DIM || K > MAX_DIM || (int64_t)N * K >= (int64_t)1 << 31)
@@ -286,14 +226,21 @@ moe_status moe_mxfp4_product(const moe_mxfp4_desc* d, const moe_pool* pool, cons
                        rng(pool->row_to_route, (size_t)pool->capacity * 4)};
   for (const Range& r : ins)
     if (overlap(ro, r)) return MOE_ERR_INVALID;
-  const MxArgs p{pool_args(d->E, d->topk, d->a_rows, pool), d->N, d->K, (const uint8_t*)a, (const uint8_t*)a_exponents,
-                 (const uint8_t*)w, (const uint8_t*)w_exponents, (uint16_t*)out};
+  const RowsArgs p{pool_args(d->E, d->topk, d->a_rows, pool), d->N, d->K, (const uint8_t*)a, (const uint8_t*)w,
+                   (const uint8_t*)a_exponents, (const uint8_t*)w_exponents, (uint16_t*)out};
   const int64_t routes = pool_routes(pool, d->E), live = routes < d->E ? routes : d->E;
+  auto tiles = [&](int tm) { return routes / tm + live; };
   int cus = 0;
-  if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
-  const unsigned grid = grid_of((routes / FEW_ROWS + live) * (d->N / 16), 8 * cus);
-  MOE_LAUNCH(k_mxfp4_few, dim3(grid), dim3(64), 0, (hipStream_t)stream, p);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  hipError_t e = device_cus(cus);
+  if (e != hipSuccess) return MOE_ERR_HIP;
+  const hipStream_t st = (hipStream_t)stream;
+  constexpr Kind KIND = Kind::mxfp4;
+  switch (pick(p, Costs{20000.0, 0.84, 0.5, 2.1, 1.35}, routes, cus, true)) {
+    case Pick::few: e = launch_rows_few<KIND>("k_mxfp4_few", p, tiles(FEW_ROWS), 8 * cus, st); break;
+    case Pick::mid: e = launch_rows_tile<KIND, GeoM>("k_mxfp4_tile64", p, tiles(GeoM::TM), 2 * cus, st); break;
+    case Pick::large: e = launch_rows_tile<KIND, GeoL>("k_mxfp4_tile256", p, tiles(GeoL::TM), cus, st); break;
+  }
+  return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
 }  // extern "C"

@@ -4,20 +4,13 @@
 #include "checks.hpp"
 #include "engine2.hpp"
 #include "lanes.hpp"
-#include "pool_tiles.hpp"
-#include "trace.hpp"
+#include "rows_tile.hpp"
 
 namespace moelora {
 namespace {
 
 constexpr int MAX_DIM = 65536;  // N and K: a tile's row offsets stay in 32 bits
 
-struct ProductArgs : PoolArgs {
-  int N, K;
-  const uint16_t* a;
-  const uint16_t* w;
-  uint16_t* out;
-};
 struct WgradArgs : PoolArgs {
   int N, K, accumulate;
   const uint16_t* g;
@@ -31,76 +24,6 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[G::NB][G::MB]) {
   for (int i = 0; i < G::NB; ++i)
 #pragma unroll
     for (int j = 0; j < G::MB; ++j) acc[i][j] = f32x16{};
-}
-
-template <class G, bool TR>
-struct ProductLoad {
-  using LA = v2::KLoad<G::TM, G::KT, G::NW>;
-  using LW = typename std::conditional<TR, v2::TLoad<G::TN, v2::TStrided, G::KT, G::NW>, v2::KLoad<G::TN, G::KT, G::NW>>::type;
-  static constexpr int INSTS = LA::NJ + LW::NJ;
-  LA m;
-  LW n;
-  __device__ void issue(int s, char* sM, char* sN) {
-    m.issue(s * G::KT, 0, false, sM);
-    if constexpr (TR)
-      n.issue(s * G::KT, sN);
-    else
-      n.issue(s * G::KT, 0, false, sN);
-  }
-};
-
-// 256 x 256 tiles, eight waves.
-template <bool TR>
-__global__ __launch_bounds__(512) void k_product_tile(ProductArgs p) {
-  extern __shared__ __align__(16) char smem[];
-  using G = v2::Geo2<4, 2, 2, 4, false, TR, 64>;
-  using L = ProductLoad<G, TR>;
-  const int nn = (p.N + G::TN - 1) / G::TN;
-  int e, m, nt;
-  for (int b = blockIdx.x; pool_tile(p, G::TM, b, nn, TILE_GM, e, m, nt); b += gridDim.x) {
-    const long row0 = (long)p.offsets[e] + (long)m * G::TM;
-    const int nrows = min(rows_of(p, e) - m * G::TM, G::TM), n0 = nt * G::TN;
-    L ld;
-    if (p.topk > 0) {
-      int tk[L::LA::NJ];
-#pragma unroll
-      for (int j = 0; j < L::LA::NJ; ++j) {
-        const int r = L::LA::row_of(j);
-        tk[j] = r < nrows ? token_of(p, p.row2r[row0 + r]) : -1;
-      }
-      ld.m.from_tokens(p.a, p.a_rows, p.K, tk);
-    } else {
-      const long have = p.a_rows - row0;
-      ld.m.contig(p.a, row0, have < nrows ? (have > 0 ? have : 0) : nrows, p.K);
-    }
-    ld.m.window(p.K);
-    const uint16_t* w = p.w + (long)e * p.N * p.K;
-    if constexpr (TR) {
-      ld.n.kp = v2::TStrided{make_rsrc(w, (uint64_t)p.K * p.N * 2), (uint32_t)p.N * 2u, 0, p.K, 0};
-      ld.n.cols(n0, p.N - n0);
-    } else {
-      ld.n.contig(w, n0, min(p.N - n0, G::TN), p.K);
-      ld.n.window(p.K);
-    }
-    f32x16 acc[G::NB][G::MB];
-    clear<G>(acc);
-    v2::run_stages2<G, 0>(ld, (p.K + G::KT - 1) / G::KT, acc, smem);
-    Epi<G> ep;
-#pragma unroll
-    for (int mb = 0; mb < G::MB; ++mb) {
-      if (ep.row(mb) >= nrows) continue;
-      uint16_t* o = p.out + (row0 + ep.row(mb)) * p.N;
-#pragma unroll
-      for (int nb = 0; nb < G::NB; ++nb)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = n0 + ep.col(nb, g);
-          if (c < p.N)
-            *(u32x2*)(o + c) = u32x2{pack2(acc[nb][mb][4 * g], acc[nb][mb][4 * g + 1]),
-                                     pack2(acc[nb][mb][4 * g + 2], acc[nb][mb][4 * g + 3])};
-        }
-    }
-  }
 }
 
 // T tile of the rows of an expert, columns c0 .. of a tensor with ldb bytes a
@@ -262,14 +185,24 @@ moe_status moe_expert_product(const moe_expert_desc* d, const moe_pool* pool, co
   int cus = 0;
   hipError_t e = device_cus(cus);
   if (e != hipSuccess) return MOE_ERR_HIP;
-  const ProductArgs p{pool_args(d->E, d->topk, d->a_rows, pool), d->N, d->K, (const uint16_t*)a, (const uint16_t*)w,
-                      (uint16_t*)out};
+  const RowsArgs p{pool_args(d->E, d->topk, d->a_rows, pool), d->N, d->K, (const uint8_t*)a, (const uint8_t*)w,
+                   nullptr, nullptr, (uint16_t*)out};
   const int64_t routes = pool_routes(pool, d->E), live = routes < d->E ? routes : d->E;
-  const int64_t tiles = (routes / 256 + live) * ((d->N + 255) / 256);
+  auto tiles = [&](int tm) { return routes / tm + live; };
   const hipStream_t st = (hipStream_t)stream;
-  static PerDeviceOnce plain, tr;
-  e = d->transposed ? launch("k_product_tile_t", k_product_tile<true>, tr, tiles, cus, p, st)
-                    : launch("k_product_tile", k_product_tile<false>, plain, tiles, cus, p, st);
+  constexpr Costs costs{20000.0, 0.84, 0.5, 2.1, 1.35};
+  if (d->transposed) {
+    if (pick(p, costs, routes, cus, false) == Pick::mid)
+      e = launch_rows_tile<Kind::bf16_t, GeoM>("k_product_t_tile64", p, tiles(GeoM::TM), 2 * cus, st);
+    else
+      e = launch_rows_tile<Kind::bf16_t, GeoL>("k_product_t_tile256", p, tiles(GeoL::TM), cus, st);
+  } else {
+    switch (pick(p, costs, routes, cus, true)) {
+      case Pick::few: e = launch_rows_few<Kind::bf16>("k_product_few", p, tiles(FEW_ROWS), 8 * cus, st); break;
+      case Pick::mid: e = launch_rows_tile<Kind::bf16, GeoM>("k_product_tile64", p, tiles(GeoM::TM), 2 * cus, st); break;
+      case Pick::large: e = launch_rows_tile<Kind::bf16, GeoL>("k_product_tile256", p, tiles(GeoL::TM), cus, st); break;
+    }
+  }
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
