@@ -18,129 +18,217 @@ struct WgradArgs : PoolArgs {
   void* out;
 };
 
-template <class G>
-__device__ __forceinline__ void clear(f32x16 (&acc)[G::NB][G::MB]) {
-#pragma unroll
-  for (int i = 0; i < G::NB; ++i)
-#pragma unroll
-    for (int j = 0; j < G::MB; ++j) acc[i][j] = f32x16{};
-}
+// dw_e = sum over e's rows of grad^T a on the stage stream: 256 columns n of grad
+// (x) by 256 columns k of a (w), both K-outer, a stage 64 of the expert's rows.
+// Gathered rows of a: a stage's token ids travel two stages ahead of its loads
+// into a ring of LDS; each wave keeps its own copy, so that its own wait covers
+// them.  The ids of a tile's first two stages have a place of their own, filled
+// when the tile is found.
+struct WgradTile {
+  int e, m0, n0, n;  // expert, first column of grad and of a, rows
+  long row0;
+};
+template <bool GATHER, class OUT>
+struct Wgrad {
+  using G = stream::Geo<256, 256, 4, 2, 2>;
+  using Tile = WgradTile;
+  static constexpr int NI = GATHER ? 1 : 0;
+  static constexpr int INSTS = NI + 8, FIRST = NI + 6;
+  static constexpr int RING = 4, IDS = G::END;                 // [RING][waves][64]
+  static constexpr int HEAD = IDS + RING * G::NW * 256;        // [2][waves][64]
+  static constexpr int LDS = HEAD + 2 * G::NW * 256;
+  static_assert(LDS <= 160 * 1024, "LDS");
 
-// T tile of the rows of an expert, columns c0 .. of a tensor with ldb bytes a
-// row: pool rows (consecutive, the descriptor based at each stage's first row),
-// or the tokens of the routes.  Rows past the expert's and columns past the
-// tensor's read zero.
-template <int R, bool GATHER>
-struct RowTile {
-  static constexpr int CPR = R / 8, RPI = 64 / CPR, NW = 8, NJ = 64 / (NW * RPI);
-  const char* base;
-  uint32_t ldb;
-  int c0, ncols;
-  __device__ __forceinline__ void issue(const PoolArgs& p, long row0, int n, int k0, char* tile) const {
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), L = threadIdx.x & 63;
-    const int left = n - k0;
-    const rsrc_t rs = GATHER ? make_rsrc(base, (uint64_t)p.a_rows * ldb)
-                             : make_rsrc(base + (row0 + k0) * (long)ldb, (uint64_t)(left > 0 ? left : 0) * ldb);
-#pragma unroll
-    for (int j = 0; j < NJ; ++j) {
-      const int kr = RPI * (w + NW * j) + L / CPR;
-      const int c = 8 * ((L % CPR) ^ v2::tswz(kr));
-      bool ok = c < ncols && kr < left;
-      uint32_t r = (uint32_t)kr;
+  const WgradArgs& p;
+  char* smem;
+  int b, nm, nn, lane, wv, wm, wn;
+  int sx;  // LDS offset of the wave's half of x
+  stream::ColFrags<64> fx, fw;
+  // the tile aimed at
+  const char *gx, *gw;
+  stream::desc_t da, di;
+  int n;
+  uint32_t vx[2], vw[2], tok[2];
+
+  __device__ __forceinline__ Wgrad(const WgradArgs& args, char* sm) : p(args), smem(sm) {
+    lane = threadIdx.x & 63;
+    wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wm = wv / G::WN;
+    wn = wv % G::WN;
+    b = blockIdx.x - gridDim.x;
+    nm = (p.N + G::TM - 1) / G::TM;
+    nn = (p.K + G::TN - 1) / G::TN;
+    fx.init(lane, (wm & 1) * 64);
+    fw.init(lane, wn * 64);
+    sx = (wm >> 1) * 16384;
+  }
+  // The following tile.  Tiles of one expert are consecutive, in chunks of
+  // TILE_GM of n, all k of a chunk, n fastest; each XCD walks a contiguous range.
+  __device__ __forceinline__ bool next(Tile& t) {
+    const int per = nm * nn, total = p.E * per;
+    while (true) {
+      b += gridDim.x;
+      if (b >= total) return false;
+      const int L = xcd_remap(b, total), e = L / per, r = L % per;
+      const int cs = r / (TILE_GM * nn) * TILE_GM, sz = min(nm - cs, TILE_GM), q = r - cs * nn;
+      int rows = __builtin_amdgcn_readfirstlane(rows_of(p, e));
+      const long row0 = rows > 0 ? __builtin_amdgcn_readfirstlane(p.offsets[e]) : 0;
+      if (rows == 0 && p.accumulate) continue;
+      if (!GATHER && p.a_rows - row0 < rows) rows = p.a_rows > row0 ? (int)(p.a_rows - row0) : 0;
+      t = Tile{e, (cs + q % sz) * G::TM, q / sz * G::TN, rows, row0};
       if constexpr (GATHER) {
-        const int t = ok ? token_of(p, p.row2r[row0 + k0 + kr]) : -1;
-        ok = t >= 0;
-        r = (uint32_t)t;
+        const stream::desc_t d = stream::make_desc(p.row2r + row0, (uint64_t)rows * 4);
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+          stream::load4(d, smem + HEAD + (s * G::NW + wv) * 256, 4u * (uint32_t)(64 * s + lane), 0);
       }
-      v2::lds_load16(rs, tile + 1024 * (w + NW * j), ok ? r * ldb + 2u * (uint32_t)(c0 + c) : OFF_NONE);
+      return true;
+    }
+  }
+  __device__ __forceinline__ bool first(Tile& t) {
+    if (!next(t)) return false;
+    v2::wait_vm<0>();
+    return true;
+  }
+  __device__ __forceinline__ int stages(const Tile& t) const { return cmax((t.n + 63) / 64, G::NBUF); }
+
+  __device__ __forceinline__ void aim(const Tile& t, bool any) {
+    int l = threadIdx.x & 63;
+    asm volatile("" : "+v"(l));
+    gx = stream::uniform(p.g + t.row0 * p.N);
+    gw = GATHER ? (const char*)p.a : stream::uniform(p.a + t.row0 * p.K);
+    n = (int)stream::uniform(any ? (uint32_t)t.n : 0u);
+    if constexpr (GATHER) {
+      da = stream::make_desc(p.a, any ? (uint64_t)p.a_rows * p.K * 2 : 0);
+      di = stream::make_desc(p.row2r + t.row0, (uint64_t)n * 4);
+    }
+    const int kr = 4 * wv + (l >> 4), c = 8 * ((l & 15) ^ ((l >> 4) << 2));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int cx = t.m0 + c + 128 * h, cw = t.n0 + c + (c >= 64 ? 64 : 0) + 64 * h;
+      vx[h] = cx < p.N ? (uint32_t)kr * (uint32_t)p.N * 2u + 2u * (uint32_t)cx : OFF_NONE;
+      vw[h] = cw < p.K ? (GATHER ? 0u : (uint32_t)kr * (uint32_t)p.K * 2u) + 2u * (uint32_t)cw : OFF_NONE;
+    }
+  }
+  __device__ __forceinline__ void fill(int) {}
+  __device__ __forceinline__ void begin() {}
+  __device__ __forceinline__ void turn() {}
+
+  // rows 64 s .. of an operand, as far as there are any
+  __device__ __forceinline__ stream::desc_t rows(const char* base, int s, int ld) const {
+    const int left = min(max(n - 64 * s, 0), 64);
+    return stream::make_desc(base + (long)(64 * s) * ld * 2, (uint64_t)left * ld * 2);
+  }
+  __device__ __forceinline__ void issue(int s, int g, int i) {
+    char* st = smem + g * G::STAGE;
+    if (i < NI) {
+      // the ids of stage s + 2, and the tokens of this one
+      const int l = threadIdx.x & 63;
+      stream::load4(di, smem + IDS + ((s & (RING - 1)) * G::NW + wv) * 256, 4u * (uint32_t)(64 * (s + 2) + l), 0);
+      const char* from = smem + (s < 2 ? HEAD + (s * G::NW + wv) * 256 : IDS + (((s - 2) & (RING - 1)) * G::NW + wv) * 256);
+      const int left = n - 64 * s;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int kr = 4 * wv + (l >> 4) + 32 * q;
+        const int t = token_of(p, *(const int*)(from + 4 * kr));
+        tok[q] = kr < left && t >= 0 ? (uint32_t)t * (uint32_t)p.K * 2u : OFF_NONE;
+      }
+      return;
+    }
+    const int q = (i - NI) & 3, h = q >> 1, r = 32 * (q & 1);
+    if (i - NI < 4) {
+      stream::load16(rows(gx, s, p.N), st + 16384 * h + 1024 * (wv + 8 * (q & 1)), vx[h], (uint32_t)r * (uint32_t)p.N * 2u);
+    } else {
+      char* to = st + G::X_BYTES + 16384 * h + 1024 * (wv + 8 * (q & 1));
+      if constexpr (GATHER) {
+        const uint32_t t = tok[q & 1];
+        stream::load16(da, to, (t | vw[h]) & OFF_NONE ? OFF_NONE : t + vw[h], 0);
+      } else {
+        stream::load16(rows(gw, s, p.K), to, vw[h], (uint32_t)r * (uint32_t)p.K * 2u);
+      }
+    }
+  }
+  __device__ __forceinline__ stream::Frag x(const char* buf, int j) const { return fx.get(buf + sx, j); }
+  __device__ __forceinline__ stream::Frag w(const char* buf, int i) const { return fw.get(buf + G::X_BYTES, i); }
+  template <int H>
+  __device__ __forceinline__ void mma(const stream::Frag& w, const stream::Frag& x, f32x4& acc) const {
+    acc = mma_bf16(H ? w.hi : w.lo, H ? x.hi : x.lo, acc);
+  }
+
+  // A lane holds four neighbouring k of a row n for each block; bf16: of two
+  // blocks, rows of 16 lanes trade so that it holds eight of one.
+  __device__ __forceinline__ void store(const Tile& t, const f32x4 (&acc)[G::FN][G::FM]) const {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    const int fr = l & 15, fc = l >> 4;
+    const int live = min(p.N - t.m0, G::TM);
+    OUT* base = (OUT*)p.out + ((long)t.e * p.N + t.m0) * p.K + t.n0;
+    // less what the columns before n0 take: the last row ends there
+    const rsrc_t ro = make_rsrc(base, ((uint64_t)live * p.K - t.n0) * sizeof(OUT));
+#pragma unroll
+    for (int j = 0; j < G::FM; ++j) {
+      const int r = (wm * G::FM + j) * 16 + fr;
+#pragma unroll
+      for (int i = 0; i < G::FN; i += 2) {
+        if constexpr (sizeof(OUT) == 4) {
+#pragma unroll
+          for (int q = 0; q < 2; ++q) {
+            const int c = (wn * G::FN + i + q) * 16 + 4 * fc;
+            const uint32_t off = r < live && t.n0 + c < p.K ? ((uint32_t)r * (uint32_t)p.K + (uint32_t)c) * 4u : OFF_NONE;
+            f32x4 v = acc[i + q][j];
+            if (p.accumulate) v += __builtin_bit_cast(f32x4, bload(ro, off));
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ro, (int)off, 0, 0);
+          }
+        } else {
+          const int c = (wn * G::FN + i + (fc & 1)) * 16 + 8 * (fc >> 1);
+          const uint32_t off = r < live && t.n0 + c < p.K ? ((uint32_t)r * (uint32_t)p.K + (uint32_t)c) * 2u : OFF_NONE;
+          if (p.accumulate) {
+            // in fp32 before the one rounding
+            f32x4 lo, hi;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][q]), __float_as_uint(acc[i + 1][j][q]), false, false);
+              lo[q] = __uint_as_float(s[0]);
+              hi[q] = __uint_as_float(s[1]);
+            }
+            float old[8];
+            widen8(bload(ro, off), old);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack2(lo[0] + old[0], lo[1] + old[1]), pack2(lo[2] + old[2], lo[3] + old[3]),
+                                                         pack2(hi[0] + old[4], hi[1] + old[5]), pack2(hi[2] + old[6], hi[3] + old[7])},
+                                                   ro, (int)off, 0, 0);
+          } else {
+            const auto lo = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][0], acc[i][j][1]),
+                                                             pack2(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
+            const auto hi = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][2], acc[i][j][3]),
+                                                             pack2(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
+            __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, (int)off, 0, 0);
+          }
+        }
+      }
     }
   }
 };
 
-template <class G, bool GATHER>
-struct WgradLoad {
-  using LM = RowTile<G::TM, false>;
-  using LN = RowTile<G::TN, GATHER>;
-  static constexpr int INSTS = LM::NJ + LN::NJ;
-  const PoolArgs* p;
-  long row0;
-  int n;
-  LM m;
-  LN a;
-  __device__ void issue(int s, char* sM, char* sN) {
-    m.issue(*p, row0, n, s * G::KT, sM);
-    a.issue(*p, row0, n, s * G::KT, sN);
-  }
-};
-
-// dw_e: 256 x 256 tiles, both operands K-outer.
 template <bool GATHER, class OUT>
 __global__ __launch_bounds__(512) void k_weight_grad(WgradArgs p) {
   extern __shared__ __align__(16) char smem[];
-  using G = v2::Geo2<4, 2, 2, 4, true, true, 64>;
-  const int nn = (p.K + G::TN - 1) / G::TN, per = (p.N + G::TM - 1) / G::TM * nn;
-  for (int b = blockIdx.x; b < p.E * per; b += gridDim.x) {
-    const int t = xcd_remap(b, p.E * per);
-    const int e = t / per, m0 = (t % per) / nn * G::TM, n0 = (t % per) % nn * G::TN;
-    const int n = rows_of(p, e);
-    if (n == 0 && p.accumulate) continue;
-    const long row0 = n > 0 ? p.offsets[e] : 0;
-    WgradLoad<G, GATHER> ld;
-    ld.p = &p;
-    ld.row0 = row0;
-    // pool rows past the tensor's: none are read
-    const long have = p.a_rows - row0;
-    ld.n = GATHER || have >= n ? n : (have > 0 ? (int)have : 0);
-    ld.m.base = (const char*)p.g;
-    ld.m.ldb = (uint32_t)p.N * 2u;
-    ld.m.c0 = m0;
-    ld.m.ncols = p.N - m0;
-    ld.a.base = (const char*)p.a;
-    ld.a.ldb = (uint32_t)p.K * 2u;
-    ld.a.c0 = n0;
-    ld.a.ncols = p.K - n0;
-    f32x16 acc[G::NB][G::MB];
-    clear<G>(acc);
-    v2::run_stages2<G, 0>(ld, (ld.n + G::KT - 1) / G::KT, acc, smem);
-    Epi<G> ep;
-#pragma unroll
-    for (int mb = 0; mb < G::MB; ++mb) {
-      const int r = m0 + ep.row(mb);
-      if (r >= p.N) continue;
-      OUT* o = (OUT*)p.out + ((long)e * p.N + r) * p.K;
-#pragma unroll
-      for (int nb = 0; nb < G::NB; ++nb)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int c = n0 + ep.col(nb, g);
-          if (c >= p.K) continue;
-          f32x4 v = {acc[nb][mb][4 * g], acc[nb][mb][4 * g + 1], acc[nb][mb][4 * g + 2], acc[nb][mb][4 * g + 3]};
-          if constexpr (sizeof(OUT) == 4) {
-            if (p.accumulate) v += *(const f32x4*)(o + c);
-            *(f32x4*)(o + c) = v;
-          } else {
-            if (p.accumulate) {
-              const u32x2 w = *(const u32x2*)(o + c);
-              v += f32x4{bf2f(w[0] & 0xffffu), bf2f(w[0] >> 16), bf2f(w[1] & 0xffffu), bf2f(w[1] >> 16)};
-            }
-            *(u32x2*)(o + c) = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-          }
-        }
-    }
-  }
+  Wgrad<GATHER, OUT> t(p, smem);
+  WgradTile cur{};
+  if (!t.first(cur)) return;
+  stream::run(t, cur, smem);
 }
 
-constexpr int TILE_LDS = 2 * (256 + 256) * 128;
-
-template <class Kern, class Args>
-hipError_t launch(const char* name, Kern kern, PerDeviceOnce& once, int64_t tiles, int cus, const Args& p, hipStream_t st) {
-  const hipError_t e = once.run([&] {
+template <bool GATHER, class OUT>
+hipError_t launch_wgrad(const WgradArgs& p, int64_t tiles, int cus, hipStream_t st) {
+  static PerDeviceOnce once;
+  using W = Wgrad<GATHER, OUT>;
+  const hipError_t e = once.run([] {
     AttrInit ai;
-    ai.lds((const void*)kern, TILE_LDS);
+    ai.lds((const void*)k_weight_grad<GATHER, OUT>, W::LDS);
     return ai.err;
   });
   if (e != hipSuccess) return e;
-  MOE_LAUNCH_AS(name, kern, dim3(grid_of(tiles, cus)), dim3(512), TILE_LDS, st, p);
+  MOE_LAUNCH_AS("k_weight_grad", (k_weight_grad<GATHER, OUT>), dim3(grid_of(tiles, cus)), dim3(512), W::LDS, st, p);
   return hipGetLastError();
 }
 
@@ -225,14 +313,11 @@ moe_status moe_expert_weight_grad(const moe_expert_desc* d, const moe_pool* pool
                     (const uint16_t*)a, dw};
   const int64_t tiles = (int64_t)d->E * ((d->N + 255) / 256) * ((d->K + 255) / 256);
   const hipStream_t st = (hipStream_t)stream;
-  static PerDeviceOnce once[4];
   const bool f32 = d->out_type == MOE_TYPE_F32;
   if (d->topk > 0)
-    e = f32 ? launch("k_weight_grad", k_weight_grad<true, float>, once[0], tiles, cus, p, st)
-            : launch("k_weight_grad", k_weight_grad<true, uint16_t>, once[1], tiles, cus, p, st);
+    e = f32 ? launch_wgrad<true, float>(p, tiles, cus, st) : launch_wgrad<true, uint16_t>(p, tiles, cus, st);
   else
-    e = f32 ? launch("k_weight_grad", k_weight_grad<false, float>, once[2], tiles, cus, p, st)
-            : launch("k_weight_grad", k_weight_grad<false, uint16_t>, once[3], tiles, cus, p, st);
+    e = f32 ? launch_wgrad<false, float>(p, tiles, cus, st) : launch_wgrad<false, uint16_t>(p, tiles, cus, st);
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 

@@ -49,22 +49,31 @@ struct Geo {
 // those the compiler waits for every direct load that it knows of, the stages
 // ahead included, so here the load is one that it does not see.  It has no
 // register results; the caller waits for it by count.  The descriptor is the
-// four words of a raw buffer (make_rsrc).
+// four words of a raw buffer (make_rsrc).  A vector instruction may have written
+// the scalar operands just before (v_readfirstlane), after which a buffer
+// instruction needs five wait states, and M0 needs one: the compiler counts
+// neither for inline assembly.
 typedef u32x4 desc_t;
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ const char* uniform(const void* p) {
+  const uint64_t b = (uint64_t)p;
+  return (const char*)((uint64_t)uniform((uint32_t)(b >> 32)) << 32 | uniform((uint32_t)b));
+}
 __device__ __forceinline__ desc_t make_desc(const void* base, uint64_t bytes) {
   const uint64_t b = (uint64_t)base;
-  return desc_t{(uint32_t)b, (uint32_t)(b >> 32) & 0xffffu, (uint32_t)(bytes < RSRC_MAX ? bytes : RSRC_MAX), 0x00020000u};
+  const uint32_t n = (uint32_t)(bytes < RSRC_MAX ? bytes : RSRC_MAX);
+  return desc_t{uniform((uint32_t)b), uniform((uint32_t)(b >> 32) & 0xffffu), uniform(n), 0x00020000u};
 }
 __device__ __forceinline__ uint32_t lds_address(const char* p) {
-  return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(v2::lds_void*)p);
+  return uniform((uint32_t)(uintptr_t)(v2::lds_void*)p);
 }
 __device__ __forceinline__ void load16(desc_t d, char* lds_wave_base, uint32_t off, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
-               :: "s"(lds_address(lds_wave_base)), "v"(off), "s"(d), "s"(soff) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
+               :: "s"(lds_address(lds_wave_base)), "v"(off), "s"(d), "s"(uniform(soff)) : "memory", "m0");
 }
 __device__ __forceinline__ void load4(desc_t d, char* lds_wave_base, uint32_t off, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, %3 offen lds"
-               :: "s"(lds_address(lds_wave_base)), "v"(off), "s"(d), "s"(soff) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dword %1, %2, %3 offen lds"
+               :: "s"(lds_address(lds_wave_base)), "v"(off), "s"(d), "s"(uniform(soff)) : "memory", "m0");
 }
 // The same through the compiler.
 __device__ __forceinline__ void load16(rsrc_t d, char* lds_wave_base, uint32_t off, uint32_t soff) {
