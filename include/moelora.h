@@ -638,7 +638,7 @@ moe_status moe_mxfp4_product(const moe_mxfp4_desc* desc, const moe_pool* pool, c
  * becomes NaN and leaves the others alone.  All sums run in a fixed order:
  * results are bitwise repeatable.
  *
- * min(m, n) <= 256, m * n < 2^31, batch <= 2^20, batch * m * n < 2^40 (more:
+ * min(m, n) <= 256, m * n < 2^31, batch <= 2^18, batch * m * n < 2^40 (more:
  * MOE_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------ */
 typedef struct moe_muon_tensor {

@@ -30,7 +30,8 @@ namespace {
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 constexpr int MAX_SHORT = 256;
 constexpr int TENSORS = 40;   // a launch: their table travels in the kernel's arguments
-constexpr int CHUNK = 64;     // entries of the long side in LDS at a time
+// entries of the long side in LDS at a time (registers: a thread holds its share of the next ones)
+__device__ __host__ constexpr int chunk_of(int RB) { return RB <= 128 ? 64 : 32; }
 constexpr int NT = 512, NW = 8;
 
 struct MuonTensor {
@@ -40,12 +41,12 @@ struct MuonTensor {
   float* momentum;
   long first;        // this tensor's first workgroup in a launch over splits
   long matrix0;      // index of its first matrix
-  double* part;      // [matrices][slots][R][R]: partial sums of S0, then the rounds' matrices
+  double* part;      // a matrix: partial sums of S0 [splits][lower tiles], then (long short sides) the rounds' matrices
   float* q;          // [matrices][R][R]
   int r, L, tall;    // tall: stored [L, r]
   int R;             // r in whole tiles of 16
   int splits, span;  // workgroups along L, entries each
-  int slots;         // at least four
+  int vec;           // groups of four neighbours in memory are whole and aligned
 };
 struct MuonArgs {
   MuonTensor t[TENSORS];
@@ -58,59 +59,85 @@ struct MuonArgs {
 };
 static_assert(sizeof(MuonArgs) <= 4096, "kernel arguments");
 
-template <class T>
-__device__ __forceinline__ float value(const T* p, long i) {
-  if constexpr (sizeof(T) == 2)
-    return bf2f(p[i]);
-  else
-    return p[i];
-}
-
 // A workgroup's tensor, matrix and part of the long side.
-__device__ __forceinline__ bool find(const MuonArgs& p, long b, int& t, long& mat, int& s) {
+__device__ __forceinline__ void find(const MuonArgs& p, long b, int& t, long& mat, int& s) {
   t = 0;
   while (t + 1 < p.count && b >= p.t[t + 1].first) ++t;
   const long i = b - p.t[t].first;
   mat = i / p.t[t].splits;
   s = (int)(i - mat * p.t[t].splits);
-  return b < p.groups;
 }
 
-// LDS pitch of U held by long entries, [CHUNK][R]: 18 of 64 banks on, so that
-// neither four entries side by side nor four rows of 16 meet in a bank.
-__device__ __host__ constexpr int pitch_long(int R) { return (R + 63 - 18) / 64 * 64 + 18; }
+// U (a chunk of the long side) lies in LDS as in memory: [l][c] of a tall
+// tensor, [c][l] of a wide one, at a pitch of 20 of 64 banks: 16 rows of four
+// neighbours meet in no bank.
+__device__ __host__ constexpr int pitch_of(int n) { return (n + 43) / 64 * 64 + 20; }
 
-// U of entries l0 .. l0 + CHUNK - 1 into LDS as S[l][c]; zeros past L and r.
-// WRITE: forms the new momentum and stores it, else reads it.
-template <class GT, bool WRITE>
-__device__ __forceinline__ void load_u(const MuonArgs& p, const MuonTensor& t, long mat, int l0, int lend, float gs, float* S) {
-  const int pitch = pitch_long(t.R);
-  const long at = mat * (long)t.r * t.L;
-  const GT* g = (const GT*)t.grad + at;
-  float* mo = t.momentum + at;
-  for (int i = threadIdx.x; i < CHUNK * t.R; i += NT) {
-    int l, c;
-    if (t.tall) {
-      l = i / t.R;
-      c = i - l * t.R;
-    } else {
-      c = i / CHUNK;
-      l = i - c * CHUNK;
+template <class T>
+__device__ __forceinline__ f32x4 load4(const T* p, bool vec, int live) {  // the first `live` of four
+  if (vec) {
+    if (live <= 0) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (sizeof(T) == 4) return *(const f32x4*)p;
+    else {
+      const u32x2 w = *(const u32x2*)p;
+      return f32x4{bf2f(w[0] & 0xffffu), bf2f(w[0] >> 16), bf2f(w[1] & 0xffffu), bf2f(w[1] >> 16)};
     }
-    float u = 0.0f;
-    if (l0 + l < lend && c < t.r) {
-      const long k = t.tall ? (long)(l0 + l) * t.r + c : (long)c * t.L + l0 + l;
-      const float x = value(g, k) * gs;
-      float m = mo[k];
-      if (WRITE) {
-        m = fmaf(p.momentum, m, x);
-        mo[k] = m;
-      }
-      u = p.nesterov ? fmaf(p.momentum, m, x) : m;
-    }
-    S[l * pitch + c] = u;
   }
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < live) {
+      if constexpr (sizeof(T) == 4) v[e] = p[e];
+      else v[e] = bf2f(p[e]);
+    }
+  return v;
 }
+template <class T>
+__device__ __forceinline__ void store4(T* p, bool vec, int live, f32x4 v) {
+  if (vec) {
+    if (live <= 0) return;
+    if constexpr (sizeof(T) == 4) *(f32x4*)p = v;
+    else *(u32x2*)p = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (e < live) {
+      if constexpr (sizeof(T) == 4) p[e] = v[e];
+      else p[e] = (T)f2bf(v[e]);
+    }
+}
+
+// What a thread moves of each chunk: groups of four neighbours in memory.
+template <int RB, bool TALL>
+struct Share {
+  static constexpr int CHUNK = chunk_of(RB), N = RB * CHUNK / (4 * NT);
+  static constexpr int PITCH = pitch_of(TALL ? RB : CHUNK);
+  // LDS steps along the short and the long side
+  static constexpr int KS = TALL ? 1 : PITCH, LS = TALL ? PITCH : 1;
+  int at[N], lds[N];  // element in the chunk; LDS place, -1: none
+  int live[N];        // tall: entries of the short side from here on, and 2^16 times the long side's; wide: of the chunk from here on
+  int step;           // elements from one chunk to the next
+  __device__ __forceinline__ void init(const MuonTensor& t) {
+    const int B = TALL ? t.R : CHUNK, A = TALL ? CHUNK : t.R;
+    step = TALL ? CHUNK * t.r : CHUNK;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int g = threadIdx.x + i * NT, a = g / (B / 4), b = 4 * (g - a * (B / 4));
+      lds[i] = a < A ? a * PITCH + b : -1;
+      at[i] = a * (TALL ? t.r : t.L) + b;
+      if (TALL)
+        live[i] = a < A && b < t.r ? (t.r - b) + (a << 16) : 0;
+      else
+        live[i] = a < A && a < t.r ? CHUNK - b : 0;
+    }
+  }
+  // of group i, the elements there are in the chunk with `left` entries
+  __device__ __forceinline__ int have(int i, int left) const {
+    if (TALL) return (live[i] >> 16) < left ? live[i] & 0xffff : 0;
+    return live[i] > 0 ? left - (CHUNK - live[i]) : 0;
+  }
+};
 
 // Tile t of the lower triangle of tiles.
 __device__ __forceinline__ void tri(int t, int& i, int& j) {
@@ -119,185 +146,443 @@ __device__ __forceinline__ void tri(int t, int& i, int& j) {
   while (i * (i + 1) / 2 > t) --i;
   j = t - i * (i + 1) / 2;
 }
+__device__ __host__ constexpr int tri_tiles(int n) { return n * (n + 1) / 2; }
 
-// Partial S0 of a part of the long side.
+// Where a matrix's part of the workspace begins.
+constexpr int SHORT_R = 128;   // up to here the rounds run in LDS
+constexpr int LONG_SLOTS = 6;  // beyond, they have matrices behind the partial sums
+__device__ __host__ constexpr long part_size(int R, int splits) {
+  return (long)splits * tri_tiles(R / 16) * 256 + (R > SHORT_R ? (long)LONG_SLOTS * R * R : 0);
+}
+__device__ __forceinline__ long part_at(const MuonTensor& t, long mat) { return mat * part_size(t.R, t.splits); }
+
+// The new momentum, and S0 of a part of the long side as lower tiles of 16 x 16.
+// The next chunk's loads are in flight while this one is multiplied.
+template <class GT, int RB, bool TALL>
+__device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
+  using Sh = Share<RB, TALL>;
+  constexpr int MT = (tri_tiles(RB / 16) + NW - 1) / NW;  // tiles a wave
+  const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int tiles = tri_tiles(t.R / 16);
+  Sh sh;
+  sh.init(t);
+  const int l_begin = s * t.span;
+  int left = min(t.L - l_begin, t.span);
+  const bool vec = t.vec != 0;
+  const long at = mat * (long)t.r * t.L + (TALL ? (long)l_begin * t.r : l_begin);
+  const GT* g = (const GT*)t.grad + at;
+  float* mo = t.momentum + at;
+  f32x4 gv[Sh::N], mv[Sh::N];
+  auto fetch = [&](int have) {
+#pragma unroll
+    for (int i = 0; i < Sh::N; ++i) {
+      gv[i] = load4(g + sh.at[i], vec, sh.have(i, have));
+      mv[i] = load4(mo + sh.at[i], vec, sh.have(i, have));
+    }
+  };
+  f64x4 acc[MT];
+  int xi[MT], yj[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    int i = 0, j = 0;
+    if (w + NW * q < tiles) tri(w + NW * q, i, j);
+    const int lo = (lane >> 4) * Sh::LS + (lane & 15) * Sh::KS;
+    xi[q] = lo + 16 * i * Sh::KS;
+    yj[q] = lo + 16 * j * Sh::KS;
+    acc[q] = f64x4{0.0, 0.0, 0.0, 0.0};
+  }
+  fetch(left);
+  for (; left > 0; left -= Sh::CHUNK) {
+#pragma unroll
+    for (int i = 0; i < Sh::N; ++i) {
+      f32x4 u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = gv[i][e] * gs;
+        mv[i][e] = fmaf(p.momentum, mv[i][e], x);
+        u[e] = p.nesterov ? fmaf(p.momentum, mv[i][e], x) : mv[i][e];
+      }
+      store4(mo + sh.at[i], vec, sh.have(i, left), mv[i]);
+      if (sh.lds[i] >= 0) *(f32x4*)(S + sh.lds[i]) = u;  // zeros where there is nothing
+    }
+    __syncthreads();
+    g += sh.step;
+    mo += sh.step;
+    if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
+#pragma unroll 4
+    for (int k4 = 0; k4 < Sh::CHUNK; k4 += 4)
+#pragma unroll
+      for (int q = 0; q < MT; ++q)
+        if (w + NW * q < tiles)
+          acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)S[xi[q] + k4 * Sh::LS], (double)S[yj[q] + k4 * Sh::LS], acc[q], 0, 0, 0);
+    __syncthreads();
+  }
+  double* out = t.part + part_at(t, mat) + s * (long)(tiles * 256);
+#pragma unroll
+  for (int q = 0; q < MT; ++q)
+    if (w + NW * q < tiles)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) out[(w + NW * q) * 256 + v * 64 + lane] = acc[q][v];  // row 4 v + lane / 16 of the tile
+}
+
 template <class GT, int RB>
 __global__ __launch_bounds__(NT) void k_muon_gram(MuonArgs p) {
   extern __shared__ __align__(16) char smem[];
-  float* S = (float*)smem;
-  constexpr int MT = ((RB / 16) * (RB / 16 + 1) / 2 + NW - 1) / NW;  // tiles a wave
   int ti, s;
   long mat;
-  if (!find(p, blockIdx.x, ti, mat, s)) return;
+  find(p, blockIdx.x, ti, mat, s);
   const MuonTensor& t = p.t[ti];
-  const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int nt = t.R / 16, pitch = pitch_long(t.R);
-  const int tiles = nt * (nt + 1) / 2;
-  f64x4 acc[MT];
+  if (t.tall)
+    gram<GT, RB, true>(p, t, mat, s, (float*)smem);
+  else
+    gram<GT, RB, false>(p, t, mat, s, (float*)smem);
+}
+
+// The rounds of a matrix of at most RB rows in LDS: two matrices as lower tiles,
+// element (r, c) of a tile at 16 r + (c ^ r), which gives a column and a row of
+// 16 distinct banks each.
+template <int RB>
+struct Rounds {
+  static constexpr int MT = (tri_tiles(RB / 16) + NW - 1) / NW;
+  static constexpr int SLOT = tri_tiles(RB / 16) * 256 * 8;
+  int nt, tiles, w, lane;
+  int ti[MT], tj[MT];
+  uint32_t oc[4], orow[4];  // lane offsets of a column block and of a row block at k-step s
+
+  __device__ __forceinline__ void init(int R) {
+    nt = R / 16;
+    tiles = tri_tiles(nt);
+    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    lane = threadIdx.x & 63;
+    const int a = lane & 15, g = lane >> 4;
 #pragma unroll
-  for (int q = 0; q < MT; ++q) acc[q] = f64x4{0.0, 0.0, 0.0, 0.0};
-  const int l_end = min(t.L, (s + 1) * t.span);
-  for (int l0 = s * t.span; l0 < l_end; l0 += CHUNK) {
-    load_u<GT, true>(p, t, mat, l0, l_end, gs, S);
-    __syncthreads();
+    for (int s = 0; s < 4; ++s) {
+      const int b = 4 * s + g;
+      oc[s] = 8u * (uint32_t)(a * 16 + (b ^ a));
+      orow[s] = 8u * (uint32_t)(b * 16 + (a ^ b));
+    }
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
-      const int k = w + NW * q;
-      if (k >= tiles) continue;
-      int i, j;
-      tri(k, i, j);
-      const float* x = S + (lane >> 4) * pitch + 16 * i + (lane & 15);
-      const float* y = S + (lane >> 4) * pitch + 16 * j + (lane & 15);
-#pragma unroll
-      for (int k4 = 0; k4 < CHUNK; k4 += 4)
-        acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)x[k4 * pitch], (double)y[k4 * pitch], acc[q], 0, 0, 0);
-    }
-    __syncthreads();
-  }
-  double* out = t.part + (mat * t.slots + s) * (long)t.R * t.R;
-#pragma unroll
-  for (int q = 0; q < MT; ++q) {
-    const int k = w + NW * q;
-    if (k >= tiles) continue;
-    int i, j;
-    tri(k, i, j);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = 16 * i + 4 * v + (lane >> 4), col = 16 * j + (lane & 15);
-      out[(long)row * t.R + col] = acc[q][v];
-      out[(long)col * t.R + row] = acc[q][v];
+      int i = 0, j = 0;
+      if (live(q)) tri(w + NW * q, i, j);
+      ti[q] = __builtin_amdgcn_readfirstlane(i);
+      tj[q] = __builtin_amdgcn_readfirstlane(j);
     }
   }
-}
+  __device__ __forceinline__ bool live(int q) const { return w + NW * q < tiles; }
+  // 16 rows of block i at k 16 kt + 4 s + lane / 16
+  __device__ __forceinline__ double get(const char* X, int i, int kt, int s) const {
+    return i >= kt ? *(const double*)(X + (tri_tiles(i) + kt) * 2048 + oc[s]) : *(const double*)(X + (tri_tiles(kt) + i) * 2048 + orow[s]);
+  }
+  __device__ __forceinline__ void mul(const char* X, const char* Y, f64x4 (&z)[MT]) const {
+#pragma unroll
+    for (int q = 0; q < MT; ++q) z[q] = f64x4{0.0, 0.0, 0.0, 0.0};
+    for (int kt = 0; kt < nt; ++kt)
+#pragma unroll
+      for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int q = 0; q < MT; ++q)
+          if (live(q)) z[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(get(X, ti[q], kt, s), get(Y, tj[q], kt, s), z[q], 0, 0, 0);
+  }
+  __device__ __forceinline__ void put(char* X, const f64x4 (&z)[MT]) const {
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+      if (live(q))
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const int r = 4 * v + (lane >> 4), c = lane & 15;
+          *(double*)(X + (w + NW * q) * 2048 + 8 * (r * 16 + (c ^ r))) = z[q][v];
+        }
+  }
+  __device__ __forceinline__ bool diagonal(int q, int v) const { return ti[q] == tj[q] && 4 * v + (lane >> 4) == (lane & 15); }
+};
 
-// The rounds on one matrix of R x R in memory: z = x y, lower tiles and their
-// mirror images; f(row, col, xy) is what is stored.
-template <class F>
-__device__ __forceinline__ void product(const double* x, const double* y, double* z, int R, F&& f) {
-  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int nt = R / 16, tiles = nt * (nt + 1) / 2;
-  for (int k = w; k < tiles; k += NW) {
-    int i, j;
-    tri(k, i, j);
-    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
-    const double* a = x + (long)(lane >> 4) * R + 16 * i + (lane & 15);  // symmetric: rows read as columns
-    const double* b = y + (long)(lane >> 4) * R + 16 * j + (lane & 15);
-    for (int k4 = 0; k4 < R; k4 += 4)
-      acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[(long)k4 * R], b[(long)k4 * R], acc, 0, 0, 0);
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int row = 16 * i + 4 * v + (lane >> 4), col = 16 * j + (lane & 15);
-      const double d = f(row, col, acc[v]);
-      z[(long)row * R + col] = d;
-      z[(long)col * R + row] = d;
-    }
-  }
-}
-
-// The rounds' matrices S, P, T and Q lie where the partial sums were: the sum at
-// an element goes to T's, by the thread that has read all parts there.
+template <int RB>
 __global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
+  extern __shared__ __align__(16) char smem[];
   __shared__ double red[NW];
   int ti = 0;
   while (ti + 1 < p.count && (long)blockIdx.x >= p.t[ti + 1].matrix0) ++ti;
   const MuonTensor& t = p.t[ti];
   const long mat = blockIdx.x - t.matrix0;
-  const int R = t.R;
-  const long RR = (long)R * R;
-  double* S = t.part + mat * t.slots * RR;  // the sum of the parts, in place of the first
-  double* P = S + RR;
-  double* T = P + RR;
-  double* Q = T + RR;
+  Rounds<RB> k;
+  constexpr int MT = Rounds<RB>::MT;
+  k.init(t.R);
+  const int size = k.tiles * 256;
+  char *A = smem, *B = smem + k.tiles * 2048;
+  f64x4 S[MT], Q[MT], z[MT];
+  // the parts in order, and the trace: the sum of U's squares
+  const double* part = t.part + part_at(t, mat);
   double tr = 0.0;
-  for (long i = threadIdx.x; i < RR; i += NT) {
-    double v = S[i];
-    for (int s = 1; s < t.splits; ++s) v += S[s * RR + i];
-    T[i] = v;
-    if (i / R == i % R) tr += v;
-  }
-  // fixed order: lanes, then waves
+#pragma unroll
+  for (int q = 0; q < MT; ++q)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      double x = 0.0;
+      if (k.live(q)) {
+        const double* at = part + (k.w + NW * q) * 256 + v * 64 + k.lane;
+        x = at[0];
+        for (int s = 1; s < t.splits; ++s) x += at[s * (long)size];
+        if (k.diagonal(q, v)) tr += x;
+      }
+      S[q][v] = x;
+    }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = tr;
+  if (k.lane == 0) red[k.w] = tr;
   __syncthreads();
   tr = 0.0;
 #pragma unroll
   for (int i = 0; i < NW; ++i) tr += red[i];
   const double inv = 1.0 / (sqrt(tr) + p.eps), inv2 = inv * inv;
-  for (long i = threadIdx.x; i < RR; i += NT) S[i] = T[i] * inv2;
+#pragma unroll
+  for (int q = 0; q < MT; ++q) S[q] *= inv2;
+  k.put(A, S);
   __syncthreads();
-  for (int k = 0; k < p.rounds; ++k) {
-    const bool last = k + 1 == p.rounds;
-    product(S, S, P, R, [&](int row, int col, double v) {
-      return fma(p.c, v, fma(p.b, S[(long)row * R + col], row == col ? p.a : 0.0));
-    });
-    __syncthreads();
-    if (k == 0) {
-      for (long i = threadIdx.x; i < RR; i += NT) Q[i] = P[i];
-    } else {
-      product(P, Q, T, R, [](int, int, double v) { return v; });
-      __syncthreads();
-      for (long i = threadIdx.x; i < RR; i += NT) Q[i] = T[i];
+  for (int n = 0; n < p.rounds; ++n) {
+    const bool last = n + 1 == p.rounds;
+    k.mul(A, A, z);  // A = S
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) z[q][v] = fma(p.c, z[q][v], fma(p.b, S[q][v], k.diagonal(q, v) ? p.a : 0.0));
+    k.put(B, z);  // P
+    if (n == 0) {
+#pragma unroll
+      for (int q = 0; q < MT; ++q) Q[q] = z[q];
     }
     __syncthreads();
-    if (last) break;
-    product(S, P, T, R, [](int, int, double v) { return v; });
-    __syncthreads();
-    product(T, P, S, R, [](int, int, double v) { return v; });
-    __syncthreads();
+    if (!last) {
+      k.mul(A, B, z);
+      __syncthreads();
+      k.put(A, z);  // S P
+      __syncthreads();
+      k.mul(A, B, S);  // S P P: the next S
+      __syncthreads();
+    }
+    if (n > 0) {
+      if (last) __syncthreads();
+      k.put(A, Q);
+      __syncthreads();
+      k.mul(B, A, Q);
+      __syncthreads();
+    }
+    if (!last) {
+      k.put(A, S);
+      __syncthreads();
+    }
   }
-  float* q = t.q + mat * RR;
-  for (long i = threadIdx.x; i < RR; i += NT) q[i] = (float)(Q[i] * inv);
+  float* out = t.q + mat * (long)t.R * t.R;
+#pragma unroll
+  for (int q = 0; q < MT; ++q)
+    if (k.live(q))
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int r = 16 * k.ti[q] + 4 * v + (k.lane >> 4), c = 16 * k.tj[q] + (k.lane & 15);
+        const float x = (float)(Q[q][v] * inv);
+        out[(long)r * t.R + c] = x;
+        out[(long)c * t.R + r] = x;
+      }
 }
 
-// Q U for a part of the long side, and the parameters.
-template <class PT, class GT>
-__global__ __launch_bounds__(NT) void k_muon_apply(MuonArgs p) {
-  extern __shared__ __align__(16) char smem[];
-  float* S = (float*)smem;
-  int ti, s;
+// Longer short sides: the rounds' matrices in memory, whole, a launch a product,
+// a wave a tile of 16 x 16.
+__device__ __forceinline__ const MuonTensor& long_matrix(const MuonArgs& p, long& mat, int& tile, int per) {
+  const long m = blockIdx.x / per;
+  tile = (int)(blockIdx.x - m * per) * NW + (threadIdx.x >> 6);
+  int ti = 0;
+  while (ti + 1 < p.count && m >= p.t[ti + 1].matrix0) ++ti;
+  mat = m - p.t[ti].matrix0;
+  return p.t[ti];
+}
+__device__ __forceinline__ double* long_slot(const MuonTensor& t, long mat, int slot) {
+  return t.part + part_at(t, mat) + t.splits * (long)(tri_tiles(t.R / 16) * 256) + slot * (long)t.R * t.R;
+}
+__device__ __forceinline__ double long_inv(const MuonArgs& p, const MuonTensor& t, long mat) {  // 1 / (|U| + eps), by every wave
+  const long tiles = (long)tri_tiles(t.R / 16) * 256;
+  const double* part = long_slot(t, mat, 0) - t.splits * tiles;
+  double tr = 0.0;
+  for (int c = threadIdx.x & 63; c < t.R; c += 64)
+    for (int s = 0; s < t.splits; ++s) {
+      const int i = c >> 4;
+      tr += part[s * tiles + (tri_tiles(i) + i) * 256 + (c & 15) * 17];
+    }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
+  return 1.0 / (sqrt(tr) + p.eps);
+}
+__global__ __launch_bounds__(NT) void k_muon_long_sum(MuonArgs p, int per) {
   long mat;
-  if (!find(p, blockIdx.x, ti, mat, s)) return;
-  const MuonTensor& t = p.t[ti];
+  int tile, i, j;
+  const MuonTensor& t = long_matrix(p, mat, tile, per);
+  if (tile >= tri_tiles(t.R / 16)) return;
+  tri(tile, i, j);
+  const double inv = long_inv(p, t, mat), inv2 = inv * inv;
+  const long tiles = (long)tri_tiles(t.R / 16) * 256;
+  double* S = long_slot(t, mat, 0);
+  const double* part = S - t.splits * tiles + tile * 256;
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    double x = 0.0;
+    for (int s = 0; s < t.splits; ++s) x += part[s * tiles + v * 64 + lane];
+    const int r = 16 * i + 4 * v + (lane >> 4), c = 16 * j + (lane & 15);
+    S[(long)r * t.R + c] = x * inv2;
+    S[(long)c * t.R + r] = x * inv2;
+  }
+}
+// z = fc x y + fb x + fa I (all symmetric); out: to q, over the norm, in fp32
+__global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x, int y, int z, double fc, double fb, double fa, int out) {
+  long mat;
+  int tile, i, j;
+  const MuonTensor& t = long_matrix(p, mat, tile, per);
+  if (tile >= tri_tiles(t.R / 16)) return;
+  tri(tile, i, j);
+  const int lane = threadIdx.x & 63;
+  const double *X = long_slot(t, mat, x), *Y = long_slot(t, mat, y);
+  // symmetric: a row block is read as a column block, 16 neighbours
+  const double* a = X + (long)(lane >> 4) * t.R + 16 * i + (lane & 15);
+  const double* b = Y + (long)(lane >> 4) * t.R + 16 * j + (lane & 15);
+  f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+  for (int k4 = 0; k4 < t.R; k4 += 4)
+    acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[(long)k4 * t.R], b[(long)k4 * t.R], acc, 0, 0, 0);
+  double* Z = long_slot(t, mat, z);
+  const double inv = out ? long_inv(p, t, mat) : 0.0;
+  float* q = t.q + mat * (long)t.R * t.R;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int r = 16 * i + 4 * v + (lane >> 4), c = 16 * j + (lane & 15);
+    const double d = fma(fc, acc[v], fb != 0.0 ? fma(fb, X[(long)r * t.R + c], r == c ? fa : 0.0) : 0.0);
+    if (out) {
+      q[(long)r * t.R + c] = (float)(d * inv);
+      q[(long)c * t.R + r] = (float)(d * inv);
+    } else {
+      Z[(long)r * t.R + c] = d;
+      Z[(long)c * t.R + r] = d;
+    }
+  }
+}
+
+// Q U for a part of the long side, and the parameters.  A wave keeps its columns
+// of Q in registers; the results go back to where U was in LDS, so that the
+// parameters are read and written in the order of memory.
+template <class PT, class GT, int RB, bool TALL>
+__device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
+  using Sh = Share<RB, TALL>;
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
   const float lr = p.control != nullptr ? p.control->lr : p.lr;
   const float step = lr * (p.rms * sqrtf((float)t.L)), decay = lr * p.weight_decay;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int nt = t.R / 16, pitch = pitch_long(t.R);
-  const float* q = t.q + mat * (long)t.R * t.R;
-  const long at = mat * (long)t.r * t.L;
-  const int l_end = min(t.L, (s + 1) * t.span);
-  for (int l0 = s * t.span; l0 < l_end; l0 += CHUNK) {
-    load_u<GT, false>(p, t, mat, l0, l_end, gs, S);
-    __syncthreads();
-    for (int k = w; k < nt * (CHUNK / 16); k += NW) {
-      const int i = k % nt, j = k / nt;  // 16 of the short side, 16 of the long
-      const float* x = q + (long)(lane >> 4) * t.R + 16 * i + (lane & 15);
-      const float* y = S + (16 * j + (lane & 15)) * pitch + (lane >> 4);
-      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-      // a lane's four results are neighbours in memory: along the short side where the tensor is tall
-      if (t.tall)
-        for (int k4 = 0; k4 < t.R; k4 += 4) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[(long)k4 * t.R], y[k4], acc, 0, 0, 0);
-      else
-        for (int k4 = 0; k4 < t.R; k4 += 4) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(y[k4], x[(long)k4 * t.R], acc, 0, 0, 0);
+  constexpr int KT = RB / 16;                        // blocks of Q's rows
+  constexpr int WI = RB <= 64 ? RB / 16 : NW;        // waves along the short side
+  constexpr int IW = RB / 16 / WI;                   // blocks of it a wave
+  constexpr int JW = (Sh::CHUNK / 16) * WI / NW;     // blocks of the chunk a wave
+  const int nt = t.R / 16, wi = w % WI, wj = w / WI * JW;
+  Sh sh;
+  sh.init(t);
+  const int l_begin = s * t.span;
+  int left = min(t.L - l_begin, t.span);
+  const bool vec = t.vec != 0;
+  const long at = mat * (long)t.r * t.L + (TALL ? (long)l_begin * t.r : l_begin);
+  const GT* g = (const GT*)t.grad + at;
+  const float* mo = t.momentum + at;
+  float* ma = t.master != nullptr ? t.master + at : nullptr;
+  PT* pa = (PT*)t.param + at;
+  f32x4 gv[Sh::N], mv[Sh::N], pv[Sh::N];
+  auto fetch = [&](int have) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int c = 16 * i + (t.tall ? 4 * (lane >> 4) + v : lane & 15);
-        const int l = l0 + 16 * j + (t.tall ? lane & 15 : 4 * (lane >> 4) + v);
-        if (c >= t.r || l >= l_end) continue;
-        const long n = at + (t.tall ? (long)l * t.r + c : (long)c * t.L + l);
-        float x0 = t.master != nullptr ? t.master[n] : value((const PT*)t.param, n);
-        x0 -= fmaf(step, acc[v], decay * x0);
-        if (t.master != nullptr) t.master[n] = x0;
-        if constexpr (sizeof(PT) == 2)
-          ((PT*)t.param)[n] = (PT)f2bf(x0);
-        else
-          ((PT*)t.param)[n] = x0;
+    for (int i = 0; i < Sh::N; ++i) {
+      gv[i] = load4(g + sh.at[i], vec, sh.have(i, have));
+      mv[i] = load4(mo + sh.at[i], vec, sh.have(i, have));
+    }
+  };
+  fetch(left);
+  float q[IW][KT][4];
+#pragma unroll
+  for (int i = 0; i < IW; ++i)
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int row = 16 * kt + 4 * e + (lane >> 4), col = 16 * (wi + WI * i) + (lane & 15);
+        q[i][kt][e] = kt < nt && wi + WI * i < nt ? t.q[mat * (long)t.R * t.R + (long)row * t.R + col] : 0.0f;
       }
+  const float* Sf = S + (lane >> 4) * Sh::KS + (lane & 15) * Sh::LS + 16 * wj * Sh::LS;
+  for (; left > 0; left -= Sh::CHUNK) {
+#pragma unroll
+    for (int i = 0; i < Sh::N; ++i) {
+      f32x4 u;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = p.nesterov ? fmaf(p.momentum, mv[i][e], gv[i][e] * gs) : mv[i][e];
+      if (sh.lds[i] >= 0) *(f32x4*)(S + sh.lds[i]) = u;
+      const int have = sh.have(i, left);
+      pv[i] = ma != nullptr ? load4(ma + sh.at[i], vec, have) : load4(pa + sh.at[i], vec, have);
     }
     __syncthreads();
+    g += sh.step;
+    mo += sh.step;
+    if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
+    f32x4 acc[IW][JW];
+#pragma unroll
+    for (int i = 0; i < IW; ++i)
+#pragma unroll
+      for (int j = 0; j < JW; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int kt = 0; kt < KT; ++kt)
+      if (kt < nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y[JW];
+#pragma unroll
+          for (int j = 0; j < JW; ++j) y[j] = Sf[(16 * kt + 4 * e) * Sh::KS + 16 * j * Sh::LS];
+          // a lane's four results are neighbours in memory: along the short side where the tensor is tall
+#pragma unroll
+          for (int i = 0; i < IW; ++i)
+#pragma unroll
+            for (int j = 0; j < JW; ++j)
+              acc[i][j] = TALL ? __builtin_amdgcn_mfma_f32_16x16x4f32(q[i][kt][e], y[j], acc[i][j], 0, 0, 0)
+                               : __builtin_amdgcn_mfma_f32_16x16x4f32(y[j], q[i][kt][e], acc[i][j], 0, 0, 0);
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < IW; ++i)
+#pragma unroll
+      for (int j = 0; j < JW; ++j)
+        if (wi + WI * i < nt) {
+          const int c = 16 * (wi + WI * i), l = 16 * (wj + j);
+          const int a = TALL ? l : c, b = TALL ? c : l;
+          *(f32x4*)(S + (a + (lane & 15)) * Sh::PITCH + b + 4 * (lane >> 4)) = acc[i][j];
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < Sh::N; ++i) {
+      if (sh.lds[i] < 0) continue;
+      const int have = sh.have(i, left);
+      const f32x4 o = *(const f32x4*)(S + sh.lds[i]);
+      f32x4 x = pv[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] -= fmaf(step, o[e], decay * x[e]);
+      if (ma != nullptr) store4(ma + sh.at[i], vec, have, x);
+      store4(pa + sh.at[i], vec, have, x);
+    }
+    __syncthreads();
+    pa += sh.step;
+    if (ma != nullptr) ma += sh.step;
   }
+}
+
+template <class PT, class GT, int RB>
+__global__ __launch_bounds__(NT) void k_muon_apply(MuonArgs p) {
+  extern __shared__ __align__(16) char smem[];
+  int ti, s;
+  long mat;
+  find(p, blockIdx.x, ti, mat, s);
+  const MuonTensor& t = p.t[ti];
+  if (t.tall)
+    apply<PT, GT, RB, true>(p, t, mat, s, (float*)smem);
+  else
+    apply<PT, GT, RB, false>(p, t, mat, s, (float*)smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -311,7 +596,7 @@ void split(int64_t matrices, int L, int cus, int& splits, int& span) {
   int64_t want = (4 * (int64_t)cus + matrices - 1) / matrices;
   const int64_t most = (L + 255) / 256;
   if (want > most) want = most;
-  span = (int)(((L + want - 1) / want + CHUNK - 1) / CHUNK * CHUNK);
+  span = (int)(((L + want - 1) / want + 63) / 64 * 64);
   splits = (L + span - 1) / span;
 }
 
@@ -333,7 +618,7 @@ moe_status check_desc(const moe_muon_desc* d, const moe_muon_tensor* t, int32_t 
     if (t[i].batch == 0) continue;
     if (t[i].m < 1 || t[i].n < 1) return MOE_ERR_INVALID;
     const int64_t mn = (int64_t)t[i].m * t[i].n;
-    if ((t[i].m < t[i].n ? t[i].m : t[i].n) > MAX_SHORT || mn >= (int64_t)1 << 31 || t[i].batch > (int64_t)1 << 20 ||
+    if ((t[i].m < t[i].n ? t[i].m : t[i].n) > MAX_SHORT || mn >= (int64_t)1 << 31 || t[i].batch > (int64_t)1 << 18 ||
         t[i].batch * mn >= (int64_t)1 << 40)
       return MOE_ERR_UNSUPPORTED;
   }
@@ -341,7 +626,7 @@ moe_status check_desc(const moe_muon_desc* d, const moe_muon_tensor* t, int32_t 
 }
 
 struct Plan {
-  int r, L, R, splits, span, slots;
+  int r, L, R, splits, span;
   size_t part, q;  // bytes
 };
 Plan plan_of(const moe_muon_tensor& t, int cus) {
@@ -350,59 +635,86 @@ Plan plan_of(const moe_muon_tensor& t, int cus) {
   p.L = t.m < t.n ? t.n : t.m;
   p.R = round16(p.r);
   split(t.batch, p.L, cus, p.splits, p.span);
-  const size_t RR = (size_t)p.R * p.R;
-  p.slots = p.splits > 4 ? p.splits : 4;
-  p.part = (size_t)t.batch * p.slots * RR * 8;
-  p.q = ((size_t)t.batch * RR * 4 + 15) / 16 * 16;
+  p.part = (size_t)t.batch * part_size(p.R, p.splits) * 8;
+  p.q = ((size_t)t.batch * p.R * p.R * 4 + 15) / 16 * 16;
   return p;
 }
 
-constexpr int lds_of(int RB) { return pitch_long(RB) * CHUNK * 4; }
+// LDS of a chunk of U for short sides up to RB, either way round
+constexpr int lds_of(int RB) { return cmax(pitch_of(RB) * chunk_of(RB), pitch_of(chunk_of(RB)) * RB) * 4; }
 
-template <class GT>
-hipError_t launch_gram(const MuonArgs& p, int R, hipStream_t st) {
-  const dim3 g((unsigned)p.groups), b(NT);
-  if (R <= 64)
-    MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, 64>), g, b, lds_of(64), st, p);
-  else if (R <= 128)
-    MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, 128>), g, b, lds_of(128), st, p);
-  else
-    MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, 256>), g, b, lds_of(256), st, p);
+template <class GT, int RB>
+hipError_t launch_gram(const MuonArgs& p, hipStream_t st) {
+  MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB), st, p);
   return hipGetLastError();
 }
-template <class PT, class GT>
-hipError_t launch_apply(const MuonArgs& p, int R, hipStream_t st) {
-  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT>), dim3((unsigned)p.groups), dim3(NT),
-                lds_of(R <= 64 ? 64 : R <= 128 ? 128 : 256), st, p);
+template <class PT, class GT, int RB>
+hipError_t launch_apply(const MuonArgs& p, hipStream_t st) {
+  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB), st, p);
+  return hipGetLastError();
+}
+hipError_t launch_long_rounds(const MuonArgs& p, int R, hipStream_t st) {
+  const int per = (tri_tiles(R / 16) + NW - 1) / NW;
+  const dim3 g((unsigned)(p.matrices * per)), b(NT);
+  MOE_LAUNCH(k_muon_long_sum, g, b, 0, st, p, per);
+  auto mul = [&](int x, int y, int z, double c, double fb, double a, int out) {
+    MOE_LAUNCH(k_muon_long_mul, g, b, 0, st, p, per, x, y, z, c, fb, a, out);
+  };
+  int S = 0, T = 1, Q = 2, spare[3] = {3, 4, 5};
+  for (int n = 0; n < p.rounds; ++n) {
+    const bool last = n + 1 == p.rounds;
+    const int P = spare[0], next = spare[1];
+    if (n == 0) {
+      mul(S, S, Q, p.c, p.b, p.a, last);  // P is Q
+      if (!last) {
+        mul(S, Q, T, 1.0, 0.0, 0.0, 0);
+        mul(T, Q, S, 1.0, 0.0, 0.0, 0);
+      }
+      continue;
+    }
+    mul(S, S, P, p.c, p.b, p.a, 0);
+    mul(P, Q, next, 1.0, 0.0, 0.0, last);
+    spare[1] = Q;
+    Q = next;
+    if (!last) {
+      mul(S, P, T, 1.0, 0.0, 0.0, 0);
+      mul(T, P, S, 1.0, 0.0, 0.0, 0);
+    }
+  }
   return hipGetLastError();
 }
 
+template <int RB>
 hipError_t prepare_kernels() {
   static PerDeviceOnce once;
   return once.run([] {
     AttrInit ai;
-    ai.lds((const void*)k_muon_gram<uint16_t, 64>, lds_of(64));
-    ai.lds((const void*)k_muon_gram<uint16_t, 128>, lds_of(128));
-    ai.lds((const void*)k_muon_gram<uint16_t, 256>, lds_of(256));
-    ai.lds((const void*)k_muon_gram<float, 64>, lds_of(64));
-    ai.lds((const void*)k_muon_gram<float, 128>, lds_of(128));
-    ai.lds((const void*)k_muon_gram<float, 256>, lds_of(256));
-    ai.lds((const void*)k_muon_apply<uint16_t, uint16_t>, lds_of(256));
-    ai.lds((const void*)k_muon_apply<uint16_t, float>, lds_of(256));
-    ai.lds((const void*)k_muon_apply<float, uint16_t>, lds_of(256));
-    ai.lds((const void*)k_muon_apply<float, float>, lds_of(256));
+    ai.lds((const void*)k_muon_gram<uint16_t, RB>, lds_of(RB));
+    ai.lds((const void*)k_muon_gram<float, RB>, lds_of(RB));
+    if constexpr (RB <= SHORT_R) ai.lds((const void*)k_muon_rounds<RB>, 2 * Rounds<RB>::SLOT);
+    ai.lds((const void*)k_muon_apply<uint16_t, uint16_t, RB>, lds_of(RB));
+    ai.lds((const void*)k_muon_apply<uint16_t, float, RB>, lds_of(RB));
+    ai.lds((const void*)k_muon_apply<float, uint16_t, RB>, lds_of(RB));
+    ai.lds((const void*)k_muon_apply<float, float, RB>, lds_of(RB));
     return ai.err;
   });
 }
 
+// R: the longest short side of the tensors
+template <int RB>
 hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t st) {
-  hipError_t e = gbf ? launch_gram<uint16_t>(p, R, st) : launch_gram<float>(p, R, st);
+  hipError_t e = prepare_kernels<RB>();
+  if (e == hipSuccess) e = gbf ? launch_gram<uint16_t, RB>(p, st) : launch_gram<float, RB>(p, st);
   if (e != hipSuccess) return e;
-  MOE_LAUNCH(k_muon_rounds, dim3((unsigned)p.matrices), dim3(NT), 0, st, p);
-  e = hipGetLastError();
+  if constexpr (RB <= SHORT_R) {
+    MOE_LAUNCH_AS("k_muon_rounds", k_muon_rounds<RB>, dim3((unsigned)p.matrices), dim3(NT), 2 * tri_tiles(R / 16) * 2048, st, p);
+    e = hipGetLastError();
+  } else {
+    e = launch_long_rounds(p, R, st);
+  }
   if (e != hipSuccess) return e;
-  if (pbf) return gbf ? launch_apply<uint16_t, uint16_t>(p, R, st) : launch_apply<uint16_t, float>(p, R, st);
-  return gbf ? launch_apply<float, uint16_t>(p, R, st) : launch_apply<float, float>(p, R, st);
+  if (pbf) return gbf ? launch_apply<uint16_t, uint16_t, RB>(p, st) : launch_apply<uint16_t, float, RB>(p, st);
+  return gbf ? launch_apply<float, uint16_t, RB>(p, st) : launch_apply<float, float, RB>(p, st);
 }
 
 }  // namespace
@@ -455,7 +767,7 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
   if (!aligned16(workspace)) return MOE_ERR_INVALID;
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   int cus = 0;
-  if (device_cus(cus) != hipSuccess || prepare_kernels() != hipSuccess) return MOE_ERR_HIP;
+  if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
   MuonArgs p{};
   p.nesterov = d->nesterov;
   p.rounds = d->rounds;
@@ -469,32 +781,43 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
   p.c = d->c;
   p.eps = d->eps;
   p.control = d->control;
+  // short sides up to SHORT_R, then longer ones: the launches of a group take one
+  // kernel each
   char* at = (char*)workspace;
   int R = 0;
+  const bool pbf = d->param_type == MOE_TYPE_BF16, gbf = d->grad_type == MOE_TYPE_BF16;
+  const hipStream_t st = (hipStream_t)stream;
   auto flush = [&]() {
     if (p.count == 0) return hipSuccess;
-    const hipError_t e =
-        launch_step(p, R, d->param_type == MOE_TYPE_BF16, d->grad_type == MOE_TYPE_BF16, (hipStream_t)stream);
+    const hipError_t e = R <= 64        ? launch_step<64>(p, R, pbf, gbf, st)
+                         : R <= SHORT_R ? launch_step<SHORT_R>(p, R, pbf, gbf, st)
+                                        : launch_step<MAX_SHORT>(p, R, pbf, gbf, st);
     p.count = R = 0;
     p.groups = p.matrices = 0;
     return e;
   };
-  for (int32_t i = 0; i < count; ++i) {
-    const moe_muon_tensor& x = t[i];
-    if (x.batch == 0) continue;
-    const Plan pl = plan_of(x, cus);
-    // a launch holds fewer than 2^32 threads
-    if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23)
-      if (flush() != hipSuccess) return MOE_ERR_HIP;
-    MuonTensor& m = p.t[p.count++];
-    m = MuonTensor{x.param, x.master, x.grad, x.momentum, p.groups, p.matrices, (double*)at, (float*)(at + pl.part),
-                   pl.r, pl.L, x.m > x.n, pl.R, pl.splits, pl.span, pl.slots};
-    at += pl.part + pl.q;
-    p.groups += x.batch * pl.splits;
-    p.matrices += x.batch;
-    if (pl.R > R) R = pl.R;
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int32_t i = 0; i < count; ++i) {
+      const moe_muon_tensor& x = t[i];
+      if (x.batch == 0) continue;
+      const Plan pl = plan_of(x, cus);
+      if ((pl.R > SHORT_R) != (pass == 1)) continue;
+      // a launch holds fewer than 2^32 threads; long rounds take 17 workgroups a matrix
+      if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23 ||
+          (pass == 1 && p.matrices + x.batch >= (int64_t)1 << 18))
+        if (flush() != hipSuccess) return MOE_ERR_HIP;
+      MuonTensor& m = p.t[p.count++];
+      const bool tall = x.m > x.n;
+      m = MuonTensor{x.param, x.master, x.grad, x.momentum, p.groups, p.matrices, (double*)at, (float*)(at + pl.part),
+                     pl.r, pl.L, tall, pl.R, pl.splits, pl.span, (tall ? pl.r : pl.L) % 4 == 0};
+      at += pl.part + pl.q;
+      p.groups += x.batch * pl.splits;
+      p.matrices += x.batch;
+      if (pl.R > R) R = pl.R;
+    }
+    if (flush() != hipSuccess) return MOE_ERR_HIP;
   }
-  return flush() == hipSuccess ? MOE_OK : MOE_ERR_HIP;
+  return MOE_OK;
 }
 
 }  // extern "C"

@@ -179,7 +179,7 @@ def test_muon_desc(kw, status):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(batch=-1), INV), (dict(m=0), INV), (dict(n=-5), INV), (dict(m=257, n=257), UNS), (dict(m=256, n=1 << 23), UNS),
-    (dict(batch=(1 << 20) + 1), UNS), (dict(batch=1 << 20, m=256, n=1 << 13), UNS)])
+    (dict(batch=(1 << 18) + 1), UNS), (dict(batch=1 << 18, m=256, n=1 << 14), UNS)])
 def test_muon_sizes(kw, status):
     assert muon_size(muon_desc(), muon_tensor(**kw)) == status
     assert muon_size(None, muon_tensor()) == INV and muon_size(muon_desc(), count=-1) == INV
