@@ -30,8 +30,10 @@ namespace {
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 constexpr int MAX_SHORT = 256;
 constexpr int TENSORS = 40;   // a launch: their table travels in the kernel's arguments
-// entries of the long side in LDS at a time (registers: a thread holds its share of the next ones)
-__device__ __host__ constexpr int chunk_of(int RB) { return RB <= 128 ? 64 : 32; }
+// Entries of the long side in LDS at a time: a thread holds its share of the next
+// ones in registers, of which two workgroups on a CU leave it 128.
+__device__ __host__ constexpr int gram_chunk(int RB) { return RB <= 128 ? 64 : 32; }
+__device__ __host__ constexpr int apply_chunk(int RB) { return RB <= 64 ? 64 : 32; }
 constexpr int NT = 512, NW = 8;
 
 struct MuonTensor {
@@ -109,9 +111,9 @@ __device__ __forceinline__ void store4(T* p, bool vec, int live, f32x4 v) {
 }
 
 // What a thread moves of each chunk: groups of four neighbours in memory.
-template <int RB, bool TALL>
+template <int RB, bool TALL, int CHUNK_>
 struct Share {
-  static constexpr int CHUNK = chunk_of(RB), N = RB * CHUNK / (4 * NT);
+  static constexpr int CHUNK = CHUNK_, N = RB * CHUNK / (4 * NT);
   static constexpr int PITCH = pitch_of(TALL ? RB : CHUNK);
   // LDS steps along the short and the long side
   static constexpr int KS = TALL ? 1 : PITCH, LS = TALL ? PITCH : 1;
@@ -158,10 +160,9 @@ __device__ __forceinline__ long part_at(const MuonTensor& t, long mat) { return 
 
 // The new momentum, and S0 of a part of the long side as lower tiles of 16 x 16.
 // The next chunk's loads are in flight while this one is multiplied.
-template <class GT, int RB, bool TALL>
+template <class GT, int RB, bool TALL, int N>
 __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
-  using Sh = Share<RB, TALL>;
-  constexpr int MT = (tri_tiles(RB / 16) + NW - 1) / NW;  // tiles a wave
+  using Sh = Share<RB, TALL, gram_chunk(RB)>;
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int tiles = tri_tiles(t.R / 16);
@@ -181,10 +182,10 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
       mv[i] = load4(mo + sh.at[i], vec, sh.have(i, have));
     }
   };
-  f64x4 acc[MT];
-  int xi[MT], yj[MT];
+  f64x4 acc[cmax(N, 1)];
+  int xi[cmax(N, 1)], yj[cmax(N, 1)];
 #pragma unroll
-  for (int q = 0; q < MT; ++q) {
+  for (int q = 0; q < N; ++q) {
     int i = 0, j = 0;
     if (w + NW * q < tiles) tri(w + NW * q, i, j);
     const int lo = (lane >> 4) * Sh::LS + (lane & 15) * Sh::KS;
@@ -210,58 +211,86 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
     g += sh.step;
     mo += sh.step;
     if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
-#pragma unroll 4
-    for (int k4 = 0; k4 < Sh::CHUNK; k4 += 4)
+    if constexpr (N > 0) {
+      // operands of the next step are read while this one is multiplied
+      float x[2][N], y[2][N];
+      auto load = [&](int to, int k4) {
 #pragma unroll
-      for (int q = 0; q < MT; ++q)
-        if (w + NW * q < tiles)
-          acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)S[xi[q] + k4 * Sh::LS], (double)S[yj[q] + k4 * Sh::LS], acc[q], 0, 0, 0);
+        for (int q = 0; q < N; ++q) {
+          x[to][q] = S[xi[q] + k4 * Sh::LS];
+          y[to][q] = S[yj[q] + k4 * Sh::LS];
+        }
+      };
+      load(0, 0);
+#pragma unroll
+      for (int k4 = 0; k4 < Sh::CHUNK; k4 += 4) {
+        const int b = (k4 >> 2) & 1;
+        if (k4 + 4 < Sh::CHUNK) load(b ^ 1, k4 + 4);
+#pragma unroll
+        for (int q = 0; q < N; ++q) acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)x[b][q], (double)y[b][q], acc[q], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
     __syncthreads();
   }
   double* out = t.part + part_at(t, mat) + s * (long)(tiles * 256);
 #pragma unroll
-  for (int q = 0; q < MT; ++q)
+  for (int q = 0; q < N; ++q)
     if (w + NW * q < tiles)
 #pragma unroll
       for (int v = 0; v < 4; ++v) out[(w + NW * q) * 256 + v * 64 + lane] = acc[q][v];  // row 4 v + lane / 16 of the tile
 }
+// Waves of at most N tiles; what a wave has less is multiplied and not stored.
+template <class GT, int RB, bool TALL>
+__device__ __forceinline__ void gram_of(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = (tri_tiles(t.R / 16) - w + NW - 1) / NW;
+  if constexpr (RB <= 64) {
+    if (n >= 2) gram<GT, RB, TALL, 2>(p, t, mat, s, S);
+    else if (n == 1) gram<GT, RB, TALL, 1>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, 0>(p, t, mat, s, S);
+  } else if constexpr (RB <= 128) {
+    if (n >= 5) gram<GT, RB, TALL, 5>(p, t, mat, s, S);
+    else if (n == 4) gram<GT, RB, TALL, 4>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, 3>(p, t, mat, s, S);
+  } else {
+    if (n > 12) gram<GT, RB, TALL, 17>(p, t, mat, s, S);
+    else if (n > 7) gram<GT, RB, TALL, 12>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, 7>(p, t, mat, s, S);
+  }
+}
 
 template <class GT, int RB>
-__global__ __launch_bounds__(NT) void k_muon_gram(MuonArgs p) {
+__global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_gram(MuonArgs p) {
   extern __shared__ __align__(16) char smem[];
   int ti, s;
   long mat;
   find(p, blockIdx.x, ti, mat, s);
   const MuonTensor& t = p.t[ti];
   if (t.tall)
-    gram<GT, RB, true>(p, t, mat, s, (float*)smem);
+    gram_of<GT, RB, true>(p, t, mat, s, (float*)smem);
   else
-    gram<GT, RB, false>(p, t, mat, s, (float*)smem);
+    gram_of<GT, RB, false>(p, t, mat, s, (float*)smem);
 }
 
-// The rounds of a matrix of at most RB rows in LDS: two matrices as lower tiles,
-// element (r, c) of a tile at 16 r + (c ^ r), which gives a column and a row of
-// 16 distinct banks each.
+// The rounds of a matrix of at most RB rows in LDS: two matrices as lower tiles
+// of 16 x 16 at a pitch of 17, at which a column and a row of 16 lie in 16
+// different pairs of banks.
 template <int RB>
 struct Rounds {
   static constexpr int MT = (tri_tiles(RB / 16) + NW - 1) / NW;
-  static constexpr int SLOT = tri_tiles(RB / 16) * 256 * 8;
-  int nt, tiles, w, lane;
+  static constexpr int PITCH = 17 * 8, TILE = 16 * PITCH;
+  int nt, tiles, w, lane, mine;  // mine: tiles of the wave
   int ti[MT], tj[MT];
-  uint32_t oc[4], orow[4];  // lane offsets of a column block and of a row block at k-step s
+  int oc, orow;  // lane offsets of a column block and of a row block
 
   __device__ __forceinline__ void init(int R) {
     nt = R / 16;
     tiles = tri_tiles(nt);
     w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     lane = threadIdx.x & 63;
-    const int a = lane & 15, g = lane >> 4;
-#pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      const int b = 4 * s + g;
-      oc[s] = 8u * (uint32_t)(a * 16 + (b ^ a));
-      orow[s] = 8u * (uint32_t)(b * 16 + (a ^ b));
-    }
+    mine = max(0, (tiles - w + NW - 1) / NW);
+    oc = (lane & 15) * PITCH + (lane >> 4) * 8;
+    orow = (lane >> 4) * PITCH + (lane & 15) * 8;
 #pragma unroll
     for (int q = 0; q < MT; ++q) {
       int i = 0, j = 0;
@@ -271,29 +300,60 @@ struct Rounds {
     }
   }
   __device__ __forceinline__ bool live(int q) const { return w + NW * q < tiles; }
-  // 16 rows of block i at k 16 kt + 4 s + lane / 16
-  __device__ __forceinline__ double get(const char* X, int i, int kt, int s) const {
-    return i >= kt ? *(const double*)(X + (tri_tiles(i) + kt) * 2048 + oc[s]) : *(const double*)(X + (tri_tiles(kt) + i) * 2048 + orow[s]);
-  }
-  __device__ __forceinline__ void mul(const char* X, const char* Y, f64x4 (&z)[MT]) const {
+  // z = X Y for the wave's first N tiles.  Operands of a k-step (k = 16 kt + 4 s +
+  // lane / 16) are read while the one before is multiplied: 16 rows of block i come
+  // from a column of tile (i, kt), or above the diagonal from a row of (kt, i).
+  template <int N>
+  __device__ __forceinline__ void mul_n(const char* X, const char* Y, f64x4 (&z)[MT]) const {
+    double v[2][2 * N];
+    const char* at[2 * N];
+    int step[2 * N];
+    auto aim = [&](int kt) {
 #pragma unroll
-    for (int q = 0; q < MT; ++q) z[q] = f64x4{0.0, 0.0, 0.0, 0.0};
+      for (int o = 0; o < 2 * N; ++o) {
+        const int i = o < N ? ti[o] : tj[o - N];
+        const bool low = i >= kt;
+        const int base = (low ? tri_tiles(i) + kt : tri_tiles(kt) + i) * TILE;
+        at[o] = (o < N ? X : Y) + base + (low ? oc : orow);
+        step[o] = low ? 32 : 4 * PITCH;
+      }
+    };
+    auto load = [&](int to) {
+#pragma unroll
+      for (int o = 0; o < 2 * N; ++o) {
+        v[to][o] = *(const double*)at[o];
+        at[o] += step[o];
+      }
+    };
+#pragma unroll
+    for (int q = 0; q < N; ++q) z[q] = f64x4{0.0, 0.0, 0.0, 0.0};
+    aim(0);
+    load(0);
     for (int kt = 0; kt < nt; ++kt)
 #pragma unroll
-      for (int s = 0; s < 4; ++s)
+      for (int s = 0; s < 4; ++s) {
+        if (s == 3) aim(min(kt + 1, nt - 1));  // after the last step: read again, not used
+        load((s + 1) & 1);
 #pragma unroll
-        for (int q = 0; q < MT; ++q)
-          if (live(q)) z[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(get(X, ti[q], kt, s), get(Y, tj[q], kt, s), z[q], 0, 0, 0);
+        for (int q = 0; q < N; ++q) z[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(v[s & 1][q], v[s & 1][N + q], z[q], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+  }
+  template <int N = MT>
+  __device__ __forceinline__ void mul(const char* X, const char* Y, f64x4 (&z)[MT]) const {
+    if constexpr (N > 0) {
+      if (mine == N)
+        mul_n<N>(X, Y, z);
+      else
+        mul<N - 1>(X, Y, z);
+    }
   }
   __device__ __forceinline__ void put(char* X, const f64x4 (&z)[MT]) const {
 #pragma unroll
     for (int q = 0; q < MT; ++q)
       if (live(q))
 #pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          const int r = 4 * v + (lane >> 4), c = lane & 15;
-          *(double*)(X + (w + NW * q) * 2048 + 8 * (r * 16 + (c ^ r))) = z[q][v];
-        }
+        for (int v = 0; v < 4; ++v) *(double*)(X + (w + NW * q) * TILE + orow + 4 * v * PITCH) = z[q][v];
   }
   __device__ __forceinline__ bool diagonal(int q, int v) const { return ti[q] == tj[q] && 4 * v + (lane >> 4) == (lane & 15); }
 };
@@ -310,7 +370,7 @@ __global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
   constexpr int MT = Rounds<RB>::MT;
   k.init(t.R);
   const int size = k.tiles * 256;
-  char *A = smem, *B = smem + k.tiles * 2048;
+  char *A = smem, *B = smem + k.tiles * Rounds<RB>::TILE;
   f64x4 S[MT], Q[MT], z[MT];
   // the parts in order, and the trace: the sum of U's squares
   const double* part = t.part + part_at(t, mat);
@@ -322,8 +382,8 @@ __global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
       double x = 0.0;
       if (k.live(q)) {
         const double* at = part + (k.w + NW * q) * 256 + v * 64 + k.lane;
-        x = at[0];
-        for (int s = 1; s < t.splits; ++s) x += at[s * (long)size];
+#pragma unroll 4
+        for (int s = 0; s < t.splits; ++s) x += at[s * (long)size];
         if (k.diagonal(q, v)) tr += x;
       }
       S[q][v] = x;
@@ -469,7 +529,7 @@ __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x
 // parameters are read and written in the order of memory.
 template <class PT, class GT, int RB, bool TALL>
 __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
-  using Sh = Share<RB, TALL>;
+  using Sh = Share<RB, TALL, apply_chunk(RB)>;
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
   const float lr = p.control != nullptr ? p.control->lr : p.lr;
   const float step = lr * (p.rms * sqrtf((float)t.L)), decay = lr * p.weight_decay;
@@ -573,7 +633,7 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
 }
 
 template <class PT, class GT, int RB>
-__global__ __launch_bounds__(NT) void k_muon_apply(MuonArgs p) {
+__global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p) {
   extern __shared__ __align__(16) char smem[];
   int ti, s;
   long mat;
@@ -590,14 +650,14 @@ __global__ __launch_bounds__(NT) void k_muon_apply(MuonArgs p) {
 // ---------------------------------------------------------------------------
 int round16(int r) { return (r + 15) / 16 * 16; }
 
-// The split of the long side: enough workgroups for the chip, none with less
-// than 256 entries.
-void split(int64_t matrices, int L, int cus, int& splits, int& span) {
-  int64_t want = (4 * (int64_t)cus + matrices - 1) / matrices;
-  const int64_t most = (L + 255) / 256;
-  if (want > most) want = most;
-  span = (int)(((L + want - 1) / want + 63) / 64 * 64);
-  splits = (L + span - 1) / span;
+// Entries of the long side that a workgroup takes: enough workgroups for the
+// chip over all tensors of the call, in whole chunks.
+int span_of(const moe_muon_tensor* t, int32_t count, int cus) {
+  double total = 0;
+  for (int32_t i = 0; i < count; ++i)
+    if (t[i].batch > 0) total += (double)t[i].batch * (t[i].m > t[i].n ? t[i].m : t[i].n);
+  const double span = total / (4.0 * cus);
+  return span < 64 ? 64 : span > 0x1p30 ? 1 << 30 : (int)((span + 63) / 64) * 64;
 }
 
 moe_status check_desc(const moe_muon_desc* d, const moe_muon_tensor* t, int32_t count) {
@@ -629,28 +689,29 @@ struct Plan {
   int r, L, R, splits, span;
   size_t part, q;  // bytes
 };
-Plan plan_of(const moe_muon_tensor& t, int cus) {
+Plan plan_of(const moe_muon_tensor& t, int span) {
   Plan p;
   p.r = t.m < t.n ? t.m : t.n;
   p.L = t.m < t.n ? t.n : t.m;
   p.R = round16(p.r);
-  split(t.batch, p.L, cus, p.splits, p.span);
+  p.span = span;
+  p.splits = (p.L + span - 1) / span;
   p.part = (size_t)t.batch * part_size(p.R, p.splits) * 8;
   p.q = ((size_t)t.batch * p.R * p.R * 4 + 15) / 16 * 16;
   return p;
 }
 
 // LDS of a chunk of U for short sides up to RB, either way round
-constexpr int lds_of(int RB) { return cmax(pitch_of(RB) * chunk_of(RB), pitch_of(chunk_of(RB)) * RB) * 4; }
+constexpr int lds_of(int RB, int chunk) { return cmax(pitch_of(RB) * chunk, pitch_of(chunk) * RB) * 4; }
 
 template <class GT, int RB>
 hipError_t launch_gram(const MuonArgs& p, hipStream_t st) {
-  MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB), st, p);
+  MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB, gram_chunk(RB)), st, p);
   return hipGetLastError();
 }
 template <class PT, class GT, int RB>
 hipError_t launch_apply(const MuonArgs& p, hipStream_t st) {
-  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB), st, p);
+  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB, apply_chunk(RB)), st, p);
   return hipGetLastError();
 }
 hipError_t launch_long_rounds(const MuonArgs& p, int R, hipStream_t st) {
@@ -689,13 +750,13 @@ hipError_t prepare_kernels() {
   static PerDeviceOnce once;
   return once.run([] {
     AttrInit ai;
-    ai.lds((const void*)k_muon_gram<uint16_t, RB>, lds_of(RB));
-    ai.lds((const void*)k_muon_gram<float, RB>, lds_of(RB));
-    if constexpr (RB <= SHORT_R) ai.lds((const void*)k_muon_rounds<RB>, 2 * Rounds<RB>::SLOT);
-    ai.lds((const void*)k_muon_apply<uint16_t, uint16_t, RB>, lds_of(RB));
-    ai.lds((const void*)k_muon_apply<uint16_t, float, RB>, lds_of(RB));
-    ai.lds((const void*)k_muon_apply<float, uint16_t, RB>, lds_of(RB));
-    ai.lds((const void*)k_muon_apply<float, float, RB>, lds_of(RB));
+    ai.lds((const void*)k_muon_gram<uint16_t, RB>, lds_of(RB, gram_chunk(RB)));
+    ai.lds((const void*)k_muon_gram<float, RB>, lds_of(RB, gram_chunk(RB)));
+    if constexpr (RB <= SHORT_R) ai.lds((const void*)k_muon_rounds<RB>, 2 * tri_tiles(RB / 16) * Rounds<RB>::TILE);
+    ai.lds((const void*)k_muon_apply<uint16_t, uint16_t, RB>, lds_of(RB, apply_chunk(RB)));
+    ai.lds((const void*)k_muon_apply<uint16_t, float, RB>, lds_of(RB, apply_chunk(RB)));
+    ai.lds((const void*)k_muon_apply<float, uint16_t, RB>, lds_of(RB, apply_chunk(RB)));
+    ai.lds((const void*)k_muon_apply<float, float, RB>, lds_of(RB, apply_chunk(RB)));
     return ai.err;
   });
 }
@@ -707,7 +768,7 @@ hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t
   if (e == hipSuccess) e = gbf ? launch_gram<uint16_t, RB>(p, st) : launch_gram<float, RB>(p, st);
   if (e != hipSuccess) return e;
   if constexpr (RB <= SHORT_R) {
-    MOE_LAUNCH_AS("k_muon_rounds", k_muon_rounds<RB>, dim3((unsigned)p.matrices), dim3(NT), 2 * tri_tiles(R / 16) * 2048, st, p);
+    MOE_LAUNCH_AS("k_muon_rounds", k_muon_rounds<RB>, dim3((unsigned)p.matrices), dim3(NT), 2 * tri_tiles(R / 16) * Rounds<RB>::TILE, st, p);
     e = hipGetLastError();
   } else {
     e = launch_long_rounds(p, R, st);
@@ -730,10 +791,11 @@ moe_status moe_muon_workspace_size(const moe_muon_desc* d, const moe_muon_tensor
   if (s != MOE_OK) return s;
   int cus = 0;
   if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
+  const int span = span_of(t, count, cus);
   size_t n = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].batch == 0) continue;
-    const Plan p = plan_of(t[i], cus);
+    const Plan p = plan_of(t[i], span);
     n += p.part + p.q;
   }
   *bytes = n;
@@ -768,6 +830,7 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   int cus = 0;
   if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
+  const int span = span_of(t, count, cus);
   MuonArgs p{};
   p.nesterov = d->nesterov;
   p.rounds = d->rounds;
@@ -800,7 +863,7 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
     for (int32_t i = 0; i < count; ++i) {
       const moe_muon_tensor& x = t[i];
       if (x.batch == 0) continue;
-      const Plan pl = plan_of(x, cus);
+      const Plan pl = plan_of(x, span);
       if ((pl.R > SHORT_R) != (pass == 1)) continue;
       // a launch holds fewer than 2^32 threads; long rounds take 17 workgroups a matrix
       if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23 ||
