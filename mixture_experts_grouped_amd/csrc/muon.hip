@@ -17,6 +17,7 @@
 // sums added in a fixed order), the rounds (a workgroup a matrix), Q U and the
 // parameters.
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/moelora.h"
 #include "checks.hpp"
@@ -30,10 +31,6 @@ namespace {
 typedef double f64x4 __attribute__((ext_vector_type(4)));
 constexpr int MAX_SHORT = 256;
 constexpr int TENSORS = 40;   // a launch: their table travels in the kernel's arguments
-// Entries of the long side in LDS at a time: a thread holds its share of the next
-// ones in registers, of which two workgroups on a CU leave it 128.
-__device__ __host__ constexpr int gram_chunk(int RB) { return RB <= 128 ? 64 : 32; }
-__device__ __host__ constexpr int apply_chunk(int RB) { return RB <= 64 ? 64 : 32; }
 constexpr int NT = 512, NW = 8;
 
 struct MuonTensor {
@@ -48,7 +45,6 @@ struct MuonTensor {
   int r, L, tall;    // tall: stored [L, r]
   int R;             // r in whole tiles of 16
   int splits, span;  // workgroups along L, entries each
-  int vec;           // groups of four neighbours in memory are whole and aligned
 };
 struct MuonArgs {
   MuonTensor t[TENSORS];
@@ -70,76 +66,102 @@ __device__ __forceinline__ void find(const MuonArgs& p, long b, int& t, long& ma
   s = (int)(i - mat * p.t[t].splits);
 }
 
-// U (a chunk of the long side) lies in LDS as in memory: [l][c] of a tall
-// tensor, [c][l] of a wide one, at a pitch of 20 of 64 banks: 16 rows of four
-// neighbours meet in no bank.
-__device__ __host__ constexpr int pitch_of(int n) { return (n + 43) / 64 * 64 + 20; }
-
+// Four neighbours in memory as they are loaded (converted where they are used, so
+// that nothing waits for a load before that).
 template <class T>
-__device__ __forceinline__ f32x4 load4(const T* p, bool vec, int live) {  // the first `live` of four
-  if (vec) {
-    if (live <= 0) return f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if constexpr (sizeof(T) == 4) return *(const f32x4*)p;
-    else {
-      const u32x2 w = *(const u32x2*)p;
-      return f32x4{bf2f(w[0] & 0xffffu), bf2f(w[0] >> 16), bf2f(w[1] & 0xffffu), bf2f(w[1] >> 16)};
-    }
+struct Four {
+  typename std::conditional<sizeof(T) == 4, f32x4, u32x2>::type v;
+  __device__ __forceinline__ f32x4 get() const {
+    if constexpr (sizeof(T) == 4)
+      return v;
+    else
+      return f32x4{bf2f(v[0] & 0xffffu), bf2f(v[0] >> 16), bf2f(v[1] & 0xffffu), bf2f(v[1] >> 16)};
   }
-  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  __device__ __forceinline__ void set(f32x4 x) {
+    if constexpr (sizeof(T) == 4)
+      v = x;
+    else
+      v = u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
+  }
+};
+// VEC: groups of four are whole and aligned.  What is not there is read from
+// `safe`, without a branch, and masked by the caller.
+template <bool VEC, class T>
+__device__ __forceinline__ void load4(Four<T>& f, const T* base, int at, int have, const T* safe) {
+  if constexpr (VEC) {
+    f.v = *(const decltype(f.v)*)(have > 0 ? base + at : safe);
+  } else if constexpr (sizeof(T) == 4) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < live) {
-      if constexpr (sizeof(T) == 4) v[e] = p[e];
-      else v[e] = bf2f(p[e]);
-    }
-  return v;
+    for (int e = 0; e < 4; ++e) f.v[e] = *(e < have ? base + at + e : safe);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      f.v[e] = (uint32_t)*(2 * e < have ? base + at + 2 * e : safe) | (uint32_t)*(2 * e + 1 < have ? base + at + 2 * e + 1 : safe) << 16;
+  }
 }
-template <class T>
-__device__ __forceinline__ void store4(T* p, bool vec, int live, f32x4 v) {
-  if (vec) {
-    if (live <= 0) return;
-    if constexpr (sizeof(T) == 4) *(f32x4*)p = v;
-    else *(u32x2*)p = u32x2{pack2(v[0], v[1]), pack2(v[2], v[3])};
-    return;
-  }
+template <bool VEC, class T>
+__device__ __forceinline__ void store4(T* base, int at, int have, f32x4 x) {
+  Four<T> f;
+  f.set(x);
+  if constexpr (VEC) {
+    if (have > 0) *(decltype(f.v)*)(base + at) = f.v;
+  } else {
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    if (e < live) {
-      if constexpr (sizeof(T) == 4) p[e] = v[e];
-      else p[e] = (T)f2bf(v[e]);
-    }
+    for (int e = 0; e < 4; ++e)
+      if (e < have) {
+        if constexpr (sizeof(T) == 4)
+          base[at + e] = f.v[e];
+        else
+          base[at + e] = (T)(f.v[e >> 1] >> (16 * (e & 1)));
+      }
+  }
 }
 
-// What a thread moves of each chunk: groups of four neighbours in memory.
-template <int RB, bool TALL, int CHUNK_>
+// What a thread moves of each chunk (CHUNK entries of the long side): groups of
+// four neighbours in memory.  A chunk lies in LDS as in memory: [l][c] of a tall
+// tensor, [c][l] of a wide one.
+template <int RB, bool TALL, int CHUNK_, int PITCH_>
 struct Share {
-  static constexpr int CHUNK = CHUNK_, N = RB * CHUNK / (4 * NT);
-  static constexpr int PITCH = pitch_of(TALL ? RB : CHUNK);
+  static constexpr int CHUNK = CHUNK_, PITCH = PITCH_, N = cmax(RB * CHUNK / (4 * NT), 1);
   // LDS steps along the short and the long side
   static constexpr int KS = TALL ? 1 : PITCH, LS = TALL ? PITCH : 1;
-  int at[N], lds[N];  // element in the chunk; LDS place, -1: none
-  int live[N];        // tall: entries of the short side from here on, and 2^16 times the long side's; wide: of the chunk from here on
-  int step;           // elements from one chunk to the next
+  int lds[N];   // LDS place, -1: none
+  int live[N];  // tall: entries of the short side from here on, and 2^16 times the long side's; wide: of the chunk from here on
+  int at[N];    // element in the chunk (a matrix has fewer than 2^31)
   __device__ __forceinline__ void init(const MuonTensor& t) {
     const int B = TALL ? t.R : CHUNK, A = TALL ? CHUNK : t.R;
-    step = TALL ? CHUNK * t.r : CHUNK;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int g = threadIdx.x + i * NT, a = g / (B / 4), b = 4 * (g - a * (B / 4));
+      const bool have0 = a < A && (TALL ? b < t.r : a < t.r);
       lds[i] = a < A ? a * PITCH + b : -1;
-      at[i] = a * (TALL ? t.r : t.L) + b;
+      at[i] = have0 ? a * (TALL ? t.r : t.L) + b : 0;
       if (TALL)
-        live[i] = a < A && b < t.r ? (t.r - b) + (a << 16) : 0;
+        live[i] = have0 ? (t.r - b) + (a << 16) : 0;
       else
-        live[i] = a < A && a < t.r ? CHUNK - b : 0;
+        live[i] = have0 ? CHUNK - b : 0;
     }
   }
-  // of group i, the elements there are in the chunk with `left` entries
+  // elements from one chunk to the next
+  __device__ __forceinline__ static long step(const MuonTensor& t) { return TALL ? (long)CHUNK * t.r : CHUNK; }
+  // of group i, the elements there are in a chunk with `left` entries
   __device__ __forceinline__ int have(int i, int left) const {
     if (TALL) return (live[i] >> 16) < left ? live[i] & 0xffff : 0;
     return live[i] > 0 ? left - (CHUNK - live[i]) : 0;
   }
+  __device__ __forceinline__ static f32x4 only(f32x4 x, int have) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = e < have ? x[e] : 0.0f;
+    return x;
+  }
 };
+// Entries of the long side in LDS at a time, and pitches that keep the operands'
+// reads free of bank conflicts: S0 reads doubles, 16 of the short side by 4 of the
+// long side; Q U reads floats, 16 of the long side by 4 of the short side.
+__device__ __host__ constexpr int gram_chunk(int RB) { return RB <= 128 ? 64 : 32; }
+__device__ __host__ constexpr int gram_pitch(int RB, bool tall) { return tall ? (RB + 15) / 32 * 32 + 16 : gram_chunk(RB) + 2; }
+__device__ __host__ constexpr int apply_chunk(int RB) { return RB <= 64 ? 64 : 32; }
+__device__ __host__ constexpr int apply_pitch(int RB, bool tall) { return tall ? (RB + 43) / 64 * 64 + 20 : apply_chunk(RB) + 16; }
 
 // Tile t of the lower triangle of tiles.
 __device__ __forceinline__ void tri(int t, int& i, int& j) {
@@ -159,10 +181,14 @@ __device__ __host__ constexpr long part_size(int R, int splits) {
 __device__ __forceinline__ long part_at(const MuonTensor& t, long mat) { return mat * part_size(t.R, t.splits); }
 
 // The new momentum, and S0 of a part of the long side as lower tiles of 16 x 16.
-// The next chunk's loads are in flight while this one is multiplied.
-template <class GT, int RB, bool TALL, int N>
-__device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
-  using Sh = Share<RB, TALL, gram_chunk(RB)>;
+// The next chunk's loads are in flight while this one is multiplied.  U goes to
+// LDS as doubles, so that no instruction stands between the reads and the matrix
+// instructions: on the fp64 matrix path vector instructions take their time from
+// it (each about 4 clocks of the 72 that a product takes).
+// N: tiles of the waves, at most; what a wave has less is multiplied and not stored.
+template <class GT, int RB, bool TALL, bool VEC, int N>
+__device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, long mat, int s, double* S) {
+  using Sh = Share<RB, TALL, gram_chunk(RB), gram_pitch(RB, TALL)>;
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int tiles = tri_tiles(t.R / 16);
@@ -170,16 +196,16 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
   sh.init(t);
   const int l_begin = s * t.span;
   int left = min(t.L - l_begin, t.span);
-  const bool vec = t.vec != 0;
   const long at = mat * (long)t.r * t.L + (TALL ? (long)l_begin * t.r : l_begin);
   const GT* g = (const GT*)t.grad + at;
   float* mo = t.momentum + at;
-  f32x4 gv[Sh::N], mv[Sh::N];
+  Four<GT> gv[Sh::N];
+  Four<float> mv[Sh::N];
   auto fetch = [&](int have) {
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      gv[i] = load4(g + sh.at[i], vec, sh.have(i, have));
-      mv[i] = load4(mo + sh.at[i], vec, sh.have(i, have));
+      load4<VEC>(gv[i], g, sh.at[i], sh.have(i, have), (const GT*)t.grad);
+      load4<VEC>(mv[i], mo, sh.at[i], sh.have(i, have), t.momentum);
     }
   };
   f64x4 acc[cmax(N, 1)];
@@ -197,38 +223,46 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
   for (; left > 0; left -= Sh::CHUNK) {
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      f32x4 u;
+      const f32x4 x = gv[i].get();
+      f32x4 m = mv[i].get(), u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float x = gv[i][e] * gs;
-        mv[i][e] = fmaf(p.momentum, mv[i][e], x);
-        u[e] = p.nesterov ? fmaf(p.momentum, mv[i][e], x) : mv[i][e];
+        const float y = x[e] * gs;
+        m[e] = fmaf(p.momentum, m[e], y);
+        u[e] = p.nesterov ? fmaf(p.momentum, m[e], y) : m[e];
       }
-      store4(mo + sh.at[i], vec, sh.have(i, left), mv[i]);
-      if (sh.lds[i] >= 0) *(f32x4*)(S + sh.lds[i]) = u;  // zeros where there is nothing
+      store4<VEC>(mo, sh.at[i], sh.have(i, left), m);
+      u = Sh::only(u, sh.have(i, left));
+      if (sh.lds[i] >= 0) {
+        typedef double f64x2 __attribute__((ext_vector_type(2)));
+        *(f64x2*)(S + sh.lds[i]) = f64x2{u[0], u[1]};
+        *(f64x2*)(S + sh.lds[i] + 2) = f64x2{u[2], u[3]};
+      }
     }
     __syncthreads();
-    g += sh.step;
-    mo += sh.step;
+    g += Sh::step(t);
+    mo += Sh::step(t);
     if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
     if constexpr (N > 0) {
-      // operands of the next step are read while this one is multiplied
-      float x[2][N], y[2][N];
-      auto load = [&](int to, int k4) {
+      // a pair's operands of the next step are read behind its product
+      double x[2][N], y[2][N];
 #pragma unroll
-        for (int q = 0; q < N; ++q) {
-          x[to][q] = S[xi[q] + k4 * Sh::LS];
-          y[to][q] = S[yj[q] + k4 * Sh::LS];
-        }
-      };
-      load(0, 0);
+      for (int q = 0; q < N; ++q) {
+        x[0][q] = S[xi[q]];
+        y[0][q] = S[yj[q]];
+      }
 #pragma unroll
       for (int k4 = 0; k4 < Sh::CHUNK; k4 += 4) {
         const int b = (k4 >> 2) & 1;
-        if (k4 + 4 < Sh::CHUNK) load(b ^ 1, k4 + 4);
 #pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64((double)x[b][q], (double)y[b][q], acc[q], 0, 0, 0);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int q = 0; q < N; ++q) {
+          acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[b][q], y[b][q], acc[q], 0, 0, 0);
+          if (k4 + 4 < Sh::CHUNK) {
+            x[b ^ 1][q] = S[xi[q] + (k4 + 4) * Sh::LS];
+            y[b ^ 1][q] = S[yj[q] + (k4 + 4) * Sh::LS];
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     __syncthreads();
@@ -240,26 +274,28 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
 #pragma unroll
       for (int v = 0; v < 4; ++v) out[(w + NW * q) * 256 + v * 64 + lane] = acc[q][v];  // row 4 v + lane / 16 of the tile
 }
-// Waves of at most N tiles; what a wave has less is multiplied and not stored.
-template <class GT, int RB, bool TALL>
-__device__ __forceinline__ void gram_of(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
+template <class GT, int RB, bool TALL, bool VEC>
+__device__ __forceinline__ void gram_of(const MuonArgs& p, const MuonTensor& t, long mat, int s, double* S) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = (tri_tiles(t.R / 16) - w + NW - 1) / NW;
-  if constexpr (RB <= 64) {
-    if (n >= 2) gram<GT, RB, TALL, 2>(p, t, mat, s, S);
-    else if (n == 1) gram<GT, RB, TALL, 1>(p, t, mat, s, S);
-    else gram<GT, RB, TALL, 0>(p, t, mat, s, S);
+  if constexpr (RB <= 16) {
+    if (n >= 1) gram<GT, RB, TALL, VEC, 1>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, VEC, 0>(p, t, mat, s, S);
+  } else if constexpr (RB <= 64) {
+    if (n >= 2) gram<GT, RB, TALL, VEC, 2>(p, t, mat, s, S);
+    else if (n == 1) gram<GT, RB, TALL, VEC, 1>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, VEC, 0>(p, t, mat, s, S);
   } else if constexpr (RB <= 128) {
-    if (n >= 5) gram<GT, RB, TALL, 5>(p, t, mat, s, S);
-    else if (n == 4) gram<GT, RB, TALL, 4>(p, t, mat, s, S);
-    else gram<GT, RB, TALL, 3>(p, t, mat, s, S);
+    if (n >= 5) gram<GT, RB, TALL, VEC, 5>(p, t, mat, s, S);
+    else if (n == 4) gram<GT, RB, TALL, VEC, 4>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, VEC, 3>(p, t, mat, s, S);
   } else {
-    if (n > 12) gram<GT, RB, TALL, 17>(p, t, mat, s, S);
-    else if (n > 7) gram<GT, RB, TALL, 12>(p, t, mat, s, S);
-    else gram<GT, RB, TALL, 7>(p, t, mat, s, S);
+    if (n > 12) gram<GT, RB, TALL, VEC, 17>(p, t, mat, s, S);
+    else if (n > 7) gram<GT, RB, TALL, VEC, 12>(p, t, mat, s, S);
+    else gram<GT, RB, TALL, VEC, 7>(p, t, mat, s, S);
   }
 }
 
-template <class GT, int RB>
+template <class GT, int RB, bool VEC>
 __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_gram(MuonArgs p) {
   extern __shared__ __align__(16) char smem[];
   int ti, s;
@@ -267,182 +303,277 @@ __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_gram(MuonArgs p)
   find(p, blockIdx.x, ti, mat, s);
   const MuonTensor& t = p.t[ti];
   if (t.tall)
-    gram_of<GT, RB, true>(p, t, mat, s, (float*)smem);
+    gram_of<GT, RB, true, VEC>(p, t, mat, s, (double*)smem);
   else
-    gram_of<GT, RB, false>(p, t, mat, s, (float*)smem);
+    gram_of<GT, RB, false, VEC>(p, t, mat, s, (double*)smem);
 }
 
-// The rounds of a matrix of at most RB rows in LDS: two matrices as lower tiles
-// of 16 x 16 at a pitch of 17, at which a column and a row of 16 lie in 16
-// different pairs of banks.
-template <int RB>
-struct Rounds {
-  static constexpr int MT = (tri_tiles(RB / 16) + NW - 1) / NW;
-  static constexpr int PITCH = 17 * 8, TILE = 16 * PITCH;
-  int nt, tiles, w, lane, mine;  // mine: tiles of the wave
-  int ti[MT], tj[MT];
-  int oc, orow;  // lane offsets of a column block and of a row block
+// ---------------------------------------------------------------------------
+// rounds
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ const MuonTensor& find_matrix(const MuonArgs& p, long m, long& mat) {
+  int ti = 0;
+  while (ti + 1 < p.count && m >= p.t[ti + 1].matrix0) ++ti;
+  mat = m - p.t[ti].matrix0;
+  return p.t[ti];
+}
 
-  __device__ __forceinline__ void init(int R) {
-    nt = R / 16;
-    tiles = tri_tiles(nt);
-    w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    lane = threadIdx.x & 63;
-    mine = max(0, (tiles - w + NW - 1) / NW);
-    oc = (lane & 15) * PITCH + (lane >> 4) * 8;
-    orow = (lane >> 4) * PITCH + (lane & 15) * 8;
+// Up to 16 rows: one wave, all in registers.  Element v of a lane's result is row
+// 4 v + lane / 16, column lane % 16, which is the operand of k-step v on either
+// side, the matrices being symmetric.
+__device__ __forceinline__ f64x4 mul16(f64x4 x, f64x4 y) {
+  f64x4 z = {0.0, 0.0, 0.0, 0.0};
 #pragma unroll
-    for (int q = 0; q < MT; ++q) {
-      int i = 0, j = 0;
-      if (live(q)) tri(w + NW * q, i, j);
-      ti[q] = __builtin_amdgcn_readfirstlane(i);
-      tj[q] = __builtin_amdgcn_readfirstlane(j);
+  for (int s = 0; s < 4; ++s) z = __builtin_amdgcn_mfma_f64_16x16x4f64(x[s], y[s], z, 0, 0, 0);
+  return z;
+}
+__global__ __launch_bounds__(64) void k_muon_rounds16(MuonArgs p) {
+  long mat;
+  const MuonTensor& t = find_matrix(p, blockIdx.x, mat);
+  const int lane = threadIdx.x;
+  const double* part = t.part + part_at(t, mat) + lane;
+  f64x4 S = {0.0, 0.0, 0.0, 0.0}, Q = S, one = S;
+#pragma unroll 4
+  for (int s = 0; s < t.splits; ++s)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) S[v] += part[s * 256 + v * 64];
+  double tr = 0.0;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    one[v] = 4 * v + (lane >> 4) == (lane & 15) ? 1.0 : 0.0;
+    tr += one[v] != 0.0 ? S[v] : 0.0;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
+  const double inv = 1.0 / (sqrt(tr) + p.eps);
+  S *= inv * inv;
+  for (int n = 0; n < p.rounds; ++n) {
+    f64x4 P = mul16(S, S);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) P[v] = fma(p.c, P[v], fma(p.b, S[v], p.a * one[v]));
+    Q = n == 0 ? P : mul16(P, Q);
+    if (n + 1 < p.rounds) S = mul16(mul16(S, P), P);
+  }
+  float* out = t.q + mat * 256;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) out[v * 64 + lane] = (float)(Q[v] * inv);
+}
+
+// 16 B rows, B from 2 to 8: two matrices as lower tiles of 16 x 16 in LDS, at a
+// pitch of 17, at which a column and a row of 16 lie in 16 different pairs of
+// banks.  A wave's tiles are w, w + 8, ... of the lower triangle, known when this
+// is compiled for each wave, so that every operand is one LDS read at a fixed
+// offset: on the fp64 matrix path each vector instruction takes its time from the
+// products (addresses formed for each read: 250 us for 195 matrices of 128 rows).
+template <int B>
+struct Rounds {
+  static constexpr int TILES = tri_tiles(B), MT = (TILES + NW - 1) / NW;
+  static constexpr int PITCH = 17 * 8, TILE = 16 * PITCH, HIGH = 18;  // offsets from tile HIGH on have a base of their own
+  static constexpr int LDS = 2 * TILES * TILE;
+  struct Bases {
+    const char *c[2], *r[2];  // of columns and of rows of a tile
+  };
+  __device__ static constexpr int row_of(int t) {
+    int i = 0;
+    while (tri_tiles(i + 1) <= t) ++i;
+    return i;
+  }
+  // 16 rows of block I at k = 16 KT + 4 s + lane / 16: from a column of tile (I, KT),
+  // or above the diagonal from a row of (KT, I)
+  template <int I, int KT, int SS>
+  __device__ static __forceinline__ double get(const Bases& m) {
+    constexpr int t = I >= KT ? tri_tiles(I) + KT : tri_tiles(KT) + I, h = t >= HIGH ? 1 : 0;
+    return *(const double*)((I >= KT ? m.c[h] : m.r[h]) + (t - h * HIGH) * TILE + SS * (I >= KT ? 32 : 4 * PITCH));
+  }
+  template <int W, int STEP, int Q>
+  __device__ static __forceinline__ void read(const Bases& X, const Bases& Y, double (&v)[2 * MT]) {
+    constexpr int t = W + NW * Q;
+    if constexpr (Q < MT) {
+      if constexpr (t < TILES && STEP < 4 * B) {
+        constexpr int i = row_of(t), j = t - tri_tiles(i);
+        v[Q] = get<i, STEP / 4, STEP % 4>(X);
+        v[MT + Q] = get<j, STEP / 4, STEP % 4>(Y);
+      }
     }
   }
-  __device__ __forceinline__ bool live(int q) const { return w + NW * q < tiles; }
-  // z = X Y for the wave's first N tiles.  Operands of a k-step (k = 16 kt + 4 s +
-  // lane / 16) are read while the one before is multiplied: 16 rows of block i come
-  // from a column of tile (i, kt), or above the diagonal from a row of (kt, i).
-  template <int N>
-  __device__ __forceinline__ void mul_n(const char* X, const char* Y, f64x4 (&z)[MT]) const {
-    double v[2][2 * N];
-    const char* at[2 * N];
-    int step[2 * N];
-    auto aim = [&](int kt) {
-#pragma unroll
-      for (int o = 0; o < 2 * N; ++o) {
-        const int i = o < N ? ti[o] : tj[o - N];
-        const bool low = i >= kt;
-        const int base = (low ? tri_tiles(i) + kt : tri_tiles(kt) + i) * TILE;
-        at[o] = (o < N ? X : Y) + base + (low ? oc : orow);
-        step[o] = low ? 32 : 4 * PITCH;
-      }
-    };
-    auto load = [&](int to) {
-#pragma unroll
-      for (int o = 0; o < 2 * N; ++o) {
-        v[to][o] = *(const double*)at[o];
-        at[o] += step[o];
-      }
-    };
-#pragma unroll
-    for (int q = 0; q < N; ++q) z[q] = f64x4{0.0, 0.0, 0.0, 0.0};
-    aim(0);
-    load(0);
-    for (int kt = 0; kt < nt; ++kt)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        if (s == 3) aim(min(kt + 1, nt - 1));  // after the last step: read again, not used
-        load((s + 1) & 1);
-#pragma unroll
-        for (int q = 0; q < N; ++q) z[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(v[s & 1][q], v[s & 1][N + q], z[q], 0, 0, 0);
+  template <int W, int Q>
+  __device__ static __forceinline__ void first(const Bases& X, const Bases& Y, double (&v)[2 * MT]) {
+    if constexpr (Q < MT) {
+      read<W, 0, Q>(X, Y, v);
+      first<W, Q + 1>(X, Y, v);
+    }
+  }
+  // a pair's operands of the next step are read behind its product
+  template <int W, int STEP, int Q>
+  __device__ static __forceinline__ void steps(const Bases& X, const Bases& Y, double (&cur)[2 * MT], double (&nxt)[2 * MT], f64x4 (&z)[MT]) {
+    if constexpr (STEP < 4 * B) {
+      if constexpr (Q < MT && W + NW * Q < TILES) {
+        z[Q] = __builtin_amdgcn_mfma_f64_16x16x4f64(cur[Q], cur[MT + Q], z[Q], 0, 0, 0);
+        read<W, STEP + 1, Q>(X, Y, nxt);
         __builtin_amdgcn_sched_barrier(0);
+        steps<W, STEP, Q + 1>(X, Y, cur, nxt, z);
+      } else {
+        steps<W, STEP + 1, 0>(X, Y, nxt, cur, z);
       }
-  }
-  template <int N = MT>
-  __device__ __forceinline__ void mul(const char* X, const char* Y, f64x4 (&z)[MT]) const {
-    if constexpr (N > 0) {
-      if (mine == N)
-        mul_n<N>(X, Y, z);
-      else
-        mul<N - 1>(X, Y, z);
     }
   }
-  __device__ __forceinline__ void put(char* X, const f64x4 (&z)[MT]) const {
+  template <int W>
+  __device__ static __forceinline__ void mul_of(int w, const Bases& X, const Bases& Y, f64x4 (&z)[MT]) {
+    if constexpr (W < NW && W < TILES) {
+      if (w == W) {
+        double a[2 * MT], b[2 * MT];
+        first<W, 0>(X, Y, a);
+        steps<W, 0, 0>(X, Y, a, b, z);
+      } else {
+        mul_of<W + 1>(w, X, Y, z);
+      }
+    }
+  }
+  __device__ static __forceinline__ Bases bases(const char* m, int lane) {
+    const char* c = m + (lane & 15) * PITCH + (lane >> 4) * 8;
+    const char* r = m + (lane >> 4) * PITCH + (lane & 15) * 8;
+    return Bases{{c, c + HIGH * TILE}, {r, r + HIGH * TILE}};
+  }
+};
+
+template <int B>
+__global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
+  extern __shared__ __align__(16) char smem[];
+  __shared__ double red[NW];
+  using K = Rounds<B>;
+  constexpr int MT = K::MT, R = 16 * B;
+  long mat;
+  const MuonTensor& t = find_matrix(p, blockIdx.x, mat);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  char *const A = smem, *const Bm = smem + K::TILES * K::TILE;
+  auto live = [&](int q) { return w + NW * q < K::TILES; };
+  int ti[MT], tj[MT];
+#pragma unroll
+  for (int q = 0; q < MT; ++q) {
+    int i = 0, j = 0;
+    if (live(q)) tri(w + NW * q, i, j);
+    ti[q] = __builtin_amdgcn_readfirstlane(i);
+    tj[q] = __builtin_amdgcn_readfirstlane(j);
+  }
+  auto diagonal = [&](int q, int v) { return ti[q] == tj[q] && 4 * v + (lane >> 4) == (lane & 15); };
+  // element v of the wave's tile q: row 4 v + lane / 16, column lane % 16
+  auto place = [&](char* m, int q, int v) { return (double*)(m + (w + NW * q) * K::TILE + (lane >> 4) * K::PITCH + (lane & 15) * 8 + 4 * v * K::PITCH); };
+  auto put = [&](char* m, const f64x4 (&z)[MT]) {
 #pragma unroll
     for (int q = 0; q < MT; ++q)
       if (live(q))
 #pragma unroll
-        for (int v = 0; v < 4; ++v) *(double*)(X + (w + NW * q) * TILE + orow + 4 * v * PITCH) = z[q][v];
-  }
-  __device__ __forceinline__ bool diagonal(int q, int v) const { return ti[q] == tj[q] && 4 * v + (lane >> 4) == (lane & 15); }
-};
-
-template <int RB>
-__global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
-  extern __shared__ __align__(16) char smem[];
-  __shared__ double red[NW];
-  int ti = 0;
-  while (ti + 1 < p.count && (long)blockIdx.x >= p.t[ti + 1].matrix0) ++ti;
-  const MuonTensor& t = p.t[ti];
-  const long mat = blockIdx.x - t.matrix0;
-  Rounds<RB> k;
-  constexpr int MT = Rounds<RB>::MT;
-  k.init(t.R);
-  const int size = k.tiles * 256;
-  char *A = smem, *B = smem + k.tiles * Rounds<RB>::TILE;
-  f64x4 S[MT], Q[MT], z[MT];
-  // the parts in order, and the trace: the sum of U's squares
-  const double* part = t.part + part_at(t, mat);
+        for (int v = 0; v < 4; ++v) *place(m, q, v) = z[q][v];
+  };
+  // Q waits in memory between its products, where the first part was: each thread
+  // its own elements
+  double* const Qm = t.part + part_at(t, mat) + w * 256 + lane;
+  auto save_q = [&](const f64x4 (&z)[MT]) {
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+      if (live(q))
+#pragma unroll
+        for (int v = 0; v < 4; ++v) Qm[NW * q * 256 + v * 64] = z[q][v];
+  };
+  auto put_q = [&](char* m) {
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+      if (live(q))
+#pragma unroll
+        for (int v = 0; v < 4; ++v) *place(m, q, v) = Qm[NW * q * 256 + v * 64];
+  };
+  f64x4 next[MT], z[MT];
+  // the parts in order, all of one part's loads together, and the trace: the sum
+  // of U's squares
+  const double* part = t.part + part_at(t, mat) + w * 256 + lane;
+#pragma unroll
+  for (int q = 0; q < MT; ++q) z[q] = f64x4{0.0, 0.0, 0.0, 0.0};
+  for (int s = 0; s < t.splits; ++s, part += K::TILES * 256)
+#pragma unroll
+    for (int q = 0; q < MT; ++q)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) z[q][v] += live(q) ? part[NW * q * 256 + v * 64] : 0.0;
   double tr = 0.0;
 #pragma unroll
   for (int q = 0; q < MT; ++q)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      double x = 0.0;
-      if (k.live(q)) {
-        const double* at = part + (k.w + NW * q) * 256 + v * 64 + k.lane;
-#pragma unroll 4
-        for (int s = 0; s < t.splits; ++s) x += at[s * (long)size];
-        if (k.diagonal(q, v)) tr += x;
-      }
-      S[q][v] = x;
-    }
+    for (int v = 0; v < 4; ++v) tr += live(q) && diagonal(q, v) ? z[q][v] : 0.0;
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
-  if (k.lane == 0) red[k.w] = tr;
+  if (lane == 0) red[w] = tr;
   __syncthreads();
   tr = 0.0;
 #pragma unroll
   for (int i = 0; i < NW; ++i) tr += red[i];
   const double inv = 1.0 / (sqrt(tr) + p.eps), inv2 = inv * inv;
 #pragma unroll
-  for (int q = 0; q < MT; ++q) S[q] *= inv2;
-  k.put(A, S);
+  for (int q = 0; q < MT; ++q) z[q] *= inv2;
+  put(A, z);
   __syncthreads();
-  for (int n = 0; n < p.rounds; ++n) {
+  // The products of round n in turn: S S (to P), S P, (S P) P (the next S), P Q.
+  // A holds S, then S P, then Q; Bm holds P.
+  enum { SS, SP, SPP, PQ } what = SS;
+  const char *X = A, *Y = A;
+  for (int n = 0;;) {
     const bool last = n + 1 == p.rounds;
-    k.mul(A, A, z);  // A = S
 #pragma unroll
-    for (int q = 0; q < MT; ++q)
+    for (int q = 0; q < MT; ++q) z[q] = f64x4{0.0, 0.0, 0.0, 0.0};
+    K::template mul_of<0>(w, K::bases(X, lane), K::bases(Y, lane), z);
+    if (what == SS) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) z[q][v] = fma(p.c, z[q][v], fma(p.b, S[q][v], k.diagonal(q, v) ? p.a : 0.0));
-    k.put(B, z);  // P
-    if (n == 0) {
+      for (int q = 0; q < MT; ++q)
+        if (live(q))
 #pragma unroll
-      for (int q = 0; q < MT; ++q) Q[q] = z[q];
-    }
-    __syncthreads();
-    if (!last) {
-      k.mul(A, B, z);
+          for (int v = 0; v < 4; ++v) z[q][v] = fma(p.c, z[q][v], fma(p.b, *place(A, q, v), diagonal(q, v) ? p.a : 0.0));
+      put(Bm, z);
+      if (n == 0) {
+        if (last) break;  // z is Q
+        save_q(z);
+      }
       __syncthreads();
-      k.put(A, z);  // S P
+      if (last) {
+        put_q(A);
+        __syncthreads();
+        what = PQ, X = Bm, Y = A;
+      } else {
+        what = SP, X = A, Y = Bm;
+      }
+    } else if (what == SP) {
       __syncthreads();
-      k.mul(A, B, S);  // S P P: the next S
+      put(A, z);
       __syncthreads();
-    }
-    if (n > 0) {
-      if (last) __syncthreads();
-      k.put(A, Q);
+      what = SPP;
+    } else if (what == SPP) {
       __syncthreads();
-      k.mul(B, A, Q);
+      if (n == 0) {
+        put(A, z);
+        what = SS, X = A, Y = A, ++n;
+      } else {
+#pragma unroll
+        for (int q = 0; q < MT; ++q) next[q] = z[q];
+        put_q(A);
+        what = PQ, X = Bm, Y = A;
+      }
       __syncthreads();
-    }
-    if (!last) {
-      k.put(A, S);
+    } else {
+      if (last) break;  // z is Q
+      save_q(z);
       __syncthreads();
+      put(A, next);
+      __syncthreads();
+      what = SS, X = A, Y = A, ++n;
     }
   }
-  float* out = t.q + mat * (long)t.R * t.R;
+  float* out = t.q + mat * (long)R * R;
 #pragma unroll
   for (int q = 0; q < MT; ++q)
-    if (k.live(q))
+    if (live(q))
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
-        const int r = 16 * k.ti[q] + 4 * v + (k.lane >> 4), c = 16 * k.tj[q] + (k.lane & 15);
-        const float x = (float)(Q[q][v] * inv);
-        out[(long)r * t.R + c] = x;
-        out[(long)c * t.R + r] = x;
+        const int r = 16 * ti[q] + 4 * v + (lane >> 4), c = 16 * tj[q] + (lane & 15);
+        const float x = (float)(z[q][v] * inv);
+        out[(long)r * R + c] = x;
+        out[(long)c * R + r] = x;
       }
 }
 
@@ -451,10 +582,7 @@ __global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
 __device__ __forceinline__ const MuonTensor& long_matrix(const MuonArgs& p, long& mat, int& tile, int per) {
   const long m = blockIdx.x / per;
   tile = (int)(blockIdx.x - m * per) * NW + (threadIdx.x >> 6);
-  int ti = 0;
-  while (ti + 1 < p.count && m >= p.t[ti + 1].matrix0) ++ti;
-  mat = m - p.t[ti].matrix0;
-  return p.t[ti];
+  return find_matrix(p, m, mat);
 }
 __device__ __forceinline__ double* long_slot(const MuonTensor& t, long mat, int slot) {
   return t.part + part_at(t, mat) + t.splits * (long)(tri_tiles(t.R / 16) * 256) + slot * (long)t.R * t.R;
@@ -527,34 +655,36 @@ __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x
 // Q U for a part of the long side, and the parameters.  A wave keeps its columns
 // of Q in registers; the results go back to where U was in LDS, so that the
 // parameters are read and written in the order of memory.
-template <class PT, class GT, int RB, bool TALL>
+template <class PT, class GT, int RB, bool TALL, bool VEC>
 __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
-  using Sh = Share<RB, TALL, apply_chunk(RB)>;
+  using Sh = Share<RB, TALL, apply_chunk(RB), apply_pitch(RB, TALL)>;
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
   const float lr = p.control != nullptr ? p.control->lr : p.lr;
   const float step = lr * (p.rms * sqrtf((float)t.L)), decay = lr * p.weight_decay;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   constexpr int KT = RB / 16;                        // blocks of Q's rows
-  constexpr int WI = RB <= 64 ? RB / 16 : NW;        // waves along the short side
-  constexpr int IW = RB / 16 / WI;                   // blocks of it a wave
-  constexpr int JW = (Sh::CHUNK / 16) * WI / NW;     // blocks of the chunk a wave
+  constexpr int JT = Sh::CHUNK / 16;                 // blocks of the chunk
+  constexpr int WI = cmax(KT <= 4 ? KT : NW, NW / JT);  // waves along the short side
+  constexpr int IW = cmax(KT / WI, 1);               // blocks of it a wave
+  constexpr int JW = cmax(JT * WI / NW, 1);          // blocks of the chunk a wave
   const int nt = t.R / 16, wi = w % WI, wj = w / WI * JW;
   Sh sh;
   sh.init(t);
   const int l_begin = s * t.span;
   int left = min(t.L - l_begin, t.span);
-  const bool vec = t.vec != 0;
+  const bool masters = t.master != nullptr;
   const long at = mat * (long)t.r * t.L + (TALL ? (long)l_begin * t.r : l_begin);
   const GT* g = (const GT*)t.grad + at;
   const float* mo = t.momentum + at;
-  float* ma = t.master != nullptr ? t.master + at : nullptr;
+  float* ma = t.master + at;  // used where there are masters
   PT* pa = (PT*)t.param + at;
-  f32x4 gv[Sh::N], mv[Sh::N], pv[Sh::N];
+  Four<GT> gv[Sh::N];
+  Four<float> mv[Sh::N];
   auto fetch = [&](int have) {
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      gv[i] = load4(g + sh.at[i], vec, sh.have(i, have));
-      mv[i] = load4(mo + sh.at[i], vec, sh.have(i, have));
+      load4<VEC>(gv[i], g, sh.at[i], sh.have(i, have), (const GT*)t.grad);
+      load4<VEC>(mv[i], mo, sh.at[i], sh.have(i, have), (const float*)t.momentum);
     }
   };
   fetch(left);
@@ -570,18 +700,24 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
       }
   const float* Sf = S + (lane >> 4) * Sh::KS + (lane & 15) * Sh::LS + 16 * wj * Sh::LS;
   for (; left > 0; left -= Sh::CHUNK) {
+    Four<float> mav[Sh::N];
+    Four<PT> pav[Sh::N];
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
+      const int have = sh.have(i, left);
+      const f32x4 x = gv[i].get(), m = mv[i].get();
       f32x4 u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = p.nesterov ? fmaf(p.momentum, mv[i][e], gv[i][e] * gs) : mv[i][e];
-      if (sh.lds[i] >= 0) *(f32x4*)(S + sh.lds[i]) = u;
-      const int have = sh.have(i, left);
-      pv[i] = ma != nullptr ? load4(ma + sh.at[i], vec, have) : load4(pa + sh.at[i], vec, have);
+      for (int e = 0; e < 4; ++e) u[e] = p.nesterov ? fmaf(p.momentum, m[e], x[e] * gs) : m[e];
+      if (sh.lds[i] >= 0) *(f32x4*)(S + sh.lds[i]) = Sh::only(u, have);
+      if (masters)
+        load4<VEC>(mav[i], (const float*)ma, sh.at[i], have, (const float*)t.master);
+      else
+        load4<VEC>(pav[i], (const PT*)pa, sh.at[i], have, (const PT*)t.param);
     }
     __syncthreads();
-    g += sh.step;
-    mo += sh.step;
+    g += Sh::step(t);
+    mo += Sh::step(t);
     if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
     f32x4 acc[IW][JW];
 #pragma unroll
@@ -620,19 +756,19 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
       if (sh.lds[i] < 0) continue;
       const int have = sh.have(i, left);
       const f32x4 o = *(const f32x4*)(S + sh.lds[i]);
-      f32x4 x = pv[i];
+      f32x4 x = masters ? mav[i].get() : pav[i].get();
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] -= fmaf(step, o[e], decay * x[e]);
-      if (ma != nullptr) store4(ma + sh.at[i], vec, have, x);
-      store4(pa + sh.at[i], vec, have, x);
+      if (masters) store4<VEC>(ma, sh.at[i], have, x);
+      store4<VEC>(pa, sh.at[i], have, x);
     }
     __syncthreads();
-    pa += sh.step;
-    if (ma != nullptr) ma += sh.step;
+    pa += Sh::step(t);
+    ma += Sh::step(t);
   }
 }
 
-template <class PT, class GT, int RB>
+template <class PT, class GT, int RB, bool VEC>
 __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p) {
   extern __shared__ __align__(16) char smem[];
   int ti, s;
@@ -640,9 +776,9 @@ __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p
   find(p, blockIdx.x, ti, mat, s);
   const MuonTensor& t = p.t[ti];
   if (t.tall)
-    apply<PT, GT, RB, true>(p, t, mat, s, (float*)smem);
+    apply<PT, GT, RB, true, VEC>(p, t, mat, s, (float*)smem);
   else
-    apply<PT, GT, RB, false>(p, t, mat, s, (float*)smem);
+    apply<PT, GT, RB, false, VEC>(p, t, mat, s, (float*)smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -702,18 +838,52 @@ Plan plan_of(const moe_muon_tensor& t, int span) {
 }
 
 // LDS of a chunk of U for short sides up to RB, either way round
-constexpr int lds_of(int RB, int chunk) { return cmax(pitch_of(RB) * chunk, pitch_of(chunk) * RB) * 4; }
+constexpr int gram_lds(int RB) { return cmax(gram_pitch(RB, true) * gram_chunk(RB), gram_pitch(RB, false) * RB) * 8; }
+constexpr int apply_lds(int RB) { return cmax(apply_pitch(RB, true) * apply_chunk(RB), apply_pitch(RB, false) * RB) * 4; }
 
-template <class GT, int RB>
+template <class GT, int RB, bool VEC>
 hipError_t launch_gram(const MuonArgs& p, hipStream_t st) {
-  MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB, gram_chunk(RB)), st, p);
+  static PerDeviceOnce once;
+  const hipError_t e = once.run([] {
+    AttrInit ai;
+    ai.lds((const void*)k_muon_gram<GT, RB, VEC>, gram_lds(RB));
+    return ai.err;
+  });
+  if (e != hipSuccess) return e;
+  MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, RB, VEC>), dim3((unsigned)p.groups), dim3(NT), gram_lds(RB), st, p);
   return hipGetLastError();
 }
-template <class PT, class GT, int RB>
+template <class PT, class GT, int RB, bool VEC>
 hipError_t launch_apply(const MuonArgs& p, hipStream_t st) {
-  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT, RB>), dim3((unsigned)p.groups), dim3(NT), lds_of(RB, apply_chunk(RB)), st, p);
+  static PerDeviceOnce once;
+  const hipError_t e = once.run([] {
+    AttrInit ai;
+    ai.lds((const void*)k_muon_apply<PT, GT, RB, VEC>, apply_lds(RB));
+    return ai.err;
+  });
+  if (e != hipSuccess) return e;
+  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT, RB, VEC>), dim3((unsigned)p.groups), dim3(NT), apply_lds(RB), st, p);
   return hipGetLastError();
 }
+template <int B>
+hipError_t launch_rounds(const MuonArgs& p, int R, hipStream_t st) {
+  if (R < 16 * B) return launch_rounds<B - 1>(p, R, st);
+  if constexpr (B == 1) {
+    MOE_LAUNCH_AS("k_muon_rounds", k_muon_rounds16, dim3((unsigned)p.matrices), dim3(64), 0, st, p);
+  } else {
+    static PerDeviceOnce once;
+    const hipError_t e = once.run([] {
+      AttrInit ai;
+      ai.lds((const void*)k_muon_rounds<B>, Rounds<B>::LDS);
+      return ai.err;
+    });
+    if (e != hipSuccess) return e;
+    MOE_LAUNCH_AS("k_muon_rounds", k_muon_rounds<B>, dim3((unsigned)p.matrices), dim3(NT), Rounds<B>::LDS, st, p);
+  }
+  return hipGetLastError();
+}
+template <>
+hipError_t launch_rounds<0>(const MuonArgs&, int, hipStream_t) { return hipErrorInvalidValue; }
 hipError_t launch_long_rounds(const MuonArgs& p, int R, hipStream_t st) {
   const int per = (tri_tiles(R / 16) + NW - 1) / NW;
   const dim3 g((unsigned)(p.matrices * per)), b(NT);
@@ -745,37 +915,22 @@ hipError_t launch_long_rounds(const MuonArgs& p, int R, hipStream_t st) {
   return hipGetLastError();
 }
 
-template <int RB>
-hipError_t prepare_kernels() {
-  static PerDeviceOnce once;
-  return once.run([] {
-    AttrInit ai;
-    ai.lds((const void*)k_muon_gram<uint16_t, RB>, lds_of(RB, gram_chunk(RB)));
-    ai.lds((const void*)k_muon_gram<float, RB>, lds_of(RB, gram_chunk(RB)));
-    if constexpr (RB <= SHORT_R) ai.lds((const void*)k_muon_rounds<RB>, 2 * tri_tiles(RB / 16) * Rounds<RB>::TILE);
-    ai.lds((const void*)k_muon_apply<uint16_t, uint16_t, RB>, lds_of(RB, apply_chunk(RB)));
-    ai.lds((const void*)k_muon_apply<uint16_t, float, RB>, lds_of(RB, apply_chunk(RB)));
-    ai.lds((const void*)k_muon_apply<float, uint16_t, RB>, lds_of(RB, apply_chunk(RB)));
-    ai.lds((const void*)k_muon_apply<float, float, RB>, lds_of(RB, apply_chunk(RB)));
-    return ai.err;
-  });
-}
-
-// R: the longest short side of the tensors
-template <int RB>
+// All tensors of p have short sides of R (in whole tiles) and are VEC or not.
+template <int RB, bool VEC>
 hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t st) {
-  hipError_t e = prepare_kernels<RB>();
-  if (e == hipSuccess) e = gbf ? launch_gram<uint16_t, RB>(p, st) : launch_gram<float, RB>(p, st);
+  hipError_t e = gbf ? launch_gram<uint16_t, RB, VEC>(p, st) : launch_gram<float, RB, VEC>(p, st);
   if (e != hipSuccess) return e;
-  if constexpr (RB <= SHORT_R) {
-    MOE_LAUNCH_AS("k_muon_rounds", k_muon_rounds<RB>, dim3((unsigned)p.matrices), dim3(NT), 2 * tri_tiles(R / 16) * Rounds<RB>::TILE, st, p);
-    e = hipGetLastError();
-  } else {
-    e = launch_long_rounds(p, R, st);
-  }
+  e = R <= SHORT_R ? launch_rounds<SHORT_R / 16>(p, R, st) : launch_long_rounds(p, R, st);
   if (e != hipSuccess) return e;
-  if (pbf) return gbf ? launch_apply<uint16_t, uint16_t, RB>(p, st) : launch_apply<uint16_t, float, RB>(p, st);
-  return gbf ? launch_apply<float, uint16_t, RB>(p, st) : launch_apply<float, float, RB>(p, st);
+  if (pbf) return gbf ? launch_apply<uint16_t, uint16_t, RB, VEC>(p, st) : launch_apply<uint16_t, float, RB, VEC>(p, st);
+  return gbf ? launch_apply<float, uint16_t, RB, VEC>(p, st) : launch_apply<float, float, RB, VEC>(p, st);
+}
+template <bool VEC>
+hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t st) {
+  if (R <= 16) return launch_step<16, VEC>(p, R, pbf, gbf, st);
+  if (R <= 64) return launch_step<64, VEC>(p, R, pbf, gbf, st);
+  if (R <= SHORT_R) return launch_step<SHORT_R, VEC>(p, R, pbf, gbf, st);
+  return launch_step<MAX_SHORT, VEC>(p, R, pbf, gbf, st);
 }
 
 }  // namespace
@@ -844,42 +999,38 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
   p.c = d->c;
   p.eps = d->eps;
   p.control = d->control;
-  // short sides up to SHORT_R, then longer ones: the launches of a group take one
-  // kernel each
+  // One launch of each kernel for the tensors that take the same ones: equal short
+  // sides in whole tiles, and groups of four in memory whole or not.
   char* at = (char*)workspace;
-  int R = 0;
   const bool pbf = d->param_type == MOE_TYPE_BF16, gbf = d->grad_type == MOE_TYPE_BF16;
   const hipStream_t st = (hipStream_t)stream;
-  auto flush = [&]() {
-    if (p.count == 0) return hipSuccess;
-    const hipError_t e = R <= 64        ? launch_step<64>(p, R, pbf, gbf, st)
-                         : R <= SHORT_R ? launch_step<SHORT_R>(p, R, pbf, gbf, st)
-                                        : launch_step<MAX_SHORT>(p, R, pbf, gbf, st);
-    p.count = R = 0;
-    p.groups = p.matrices = 0;
-    return e;
-  };
-  for (int pass = 0; pass < 2; ++pass) {
-    for (int32_t i = 0; i < count; ++i) {
-      const moe_muon_tensor& x = t[i];
-      if (x.batch == 0) continue;
-      const Plan pl = plan_of(x, span);
-      if ((pl.R > SHORT_R) != (pass == 1)) continue;
-      // a launch holds fewer than 2^32 threads; long rounds take 17 workgroups a matrix
-      if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23 ||
-          (pass == 1 && p.matrices + x.batch >= (int64_t)1 << 18))
-        if (flush() != hipSuccess) return MOE_ERR_HIP;
-      MuonTensor& m = p.t[p.count++];
-      const bool tall = x.m > x.n;
-      m = MuonTensor{x.param, x.master, x.grad, x.momentum, p.groups, p.matrices, (double*)at, (float*)(at + pl.part),
-                     pl.r, pl.L, tall, pl.R, pl.splits, pl.span, (tall ? pl.r : pl.L) % 4 == 0};
-      at += pl.part + pl.q;
-      p.groups += x.batch * pl.splits;
-      p.matrices += x.batch;
-      if (pl.R > R) R = pl.R;
+  for (int R = 16; R <= MAX_SHORT; R += 16)
+    for (int vec = 0; vec < 2; ++vec) {
+      auto flush = [&]() {
+        if (p.count == 0) return hipSuccess;
+        const hipError_t e = vec ? launch_step<true>(p, R, pbf, gbf, st) : launch_step<false>(p, R, pbf, gbf, st);
+        p.count = 0;
+        p.groups = p.matrices = 0;
+        return e;
+      };
+      for (int32_t i = 0; i < count; ++i) {
+        const moe_muon_tensor& x = t[i];
+        if (x.batch == 0) continue;
+        const bool tall = x.m > x.n;
+        if (round16(tall ? x.n : x.m) != R || (x.n % 4 == 0) != (vec != 0)) continue;
+        const Plan pl = plan_of(x, span);
+        // a launch holds fewer than 2^32 threads; long rounds take 17 workgroups a matrix
+        if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23 ||
+            (R > SHORT_R && p.matrices + x.batch >= (int64_t)1 << 18))
+          if (flush() != hipSuccess) return MOE_ERR_HIP;
+        p.t[p.count++] = MuonTensor{x.param, x.master, x.grad, x.momentum, p.groups, p.matrices, (double*)at,
+                                    (float*)(at + pl.part), pl.r, pl.L, tall, pl.R, pl.splits, pl.span};
+        at += pl.part + pl.q;
+        p.groups += x.batch * pl.splits;
+        p.matrices += x.batch;
+      }
+      if (flush() != hipSuccess) return MOE_ERR_HIP;
     }
-    if (flush() != hipSuccess) return MOE_ERR_HIP;
-  }
   return MOE_OK;
 }
 
