@@ -1053,12 +1053,17 @@ def mxfp4_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Opt
         K //= 2
     dev, u8 = _device_of(src, "src"), torch.uint8
     if codes is None:
-        codes = _made(stream, torch.empty, rows, K // 2, dtype=u8, device=src.device)
+        codes = _made(stream, torch.empty, (rows, K // 2), dtype=u8, device=src.device)
+        to = codes.data_ptr()
+    else:
+        to = _on(dev, codes, u8, (rows, K // 2), "codes")
     if exponents is None:
-        exponents = _made(stream, torch.empty, rows, K // 32, dtype=u8, device=src.device)
+        exponents = _made(stream, torch.empty, (rows, K // 32), dtype=u8, device=src.device)
+        eto = exponents.data_ptr()
+    else:
+        eto = _on(dev, exponents, u8, (rows, K // 32), "exponents")
     _launch("moe_mxfp4_quantize_rows", library().moe_mxfp4_quantize_rows, dev, stream,
-            _on(dev, src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], _on(dev, codes, u8, (rows, K // 2), "codes"),
-            _on(dev, exponents, u8, (rows, K // 32), "exponents"))
+            _on(dev, src, torch.bfloat16, None, "src"), rows, K, _ACTS[act], to, eto)
     return codes, exponents
 
 
@@ -1091,9 +1096,12 @@ def mxfp4_dequantize(codes: torch.Tensor, exponents: torch.Tensor, out: Optional
         raise ValueError("K must be a multiple of 128")
     rows = codes.numel() * 2 // K if K else 0
     if out is None:
-        out = _made(stream, torch.empty, *shape, dtype=torch.bfloat16, device=codes.device)
+        out = _made(stream, torch.empty, shape, dtype=torch.bfloat16, device=codes.device)
+        to = out.data_ptr()
+    else:
+        to = _on(dev, out, torch.bfloat16, shape, "out")
     _launch("moe_mxfp4_dequantize", library().moe_mxfp4_dequantize, dev, stream, _on(dev, codes, u8, None, "codes"),
-            _on(dev, exponents, u8, (*shape[:-1], K // 32), "exponents"), rows, K, _on(dev, out, torch.bfloat16, shape, "out"))
+            _on(dev, exponents, u8, (*shape[:-1], K // 32), "exponents"), rows, K, to)
     return out
 
 

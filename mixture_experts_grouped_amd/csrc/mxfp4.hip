@@ -15,26 +15,37 @@ constexpr int MAX_DIM = 65536;
 // ---------------------------------------------------------------------------
 // quantisers
 // ---------------------------------------------------------------------------
-// The block's held exponent (plus 127) from its largest magnitude's bits, and
-// the multiplier that brings the block to the codes' range.
-__device__ __forceinline__ uint32_t block_exponent(uint32_t mag_max, float& mul) {
+// The block's held exponent (plus 127) from its largest magnitude's bits, 255 with
+// a NaN or an infinity, and the scale that it stands for (2^(e - 127)).
+__device__ __forceinline__ uint32_t block_exponent(uint32_t mag_max, float& scale) {
   const int field = (int)(mag_max >> 23);
-  if (field == 255) {  // NaN or infinity
-    mul = 0.0f;
-    return 255;
-  }
-  const int e = field > 2 ? field - 2 : 0;  // max|x| < 2^-125: the smallest exponent
-  mul = __uint_as_float((uint32_t)(e == 0 ? 254 : 254 - e) << 23);  // 2^(127 - e); 254 - e >= 1
-  return (uint32_t)e;
+  const uint32_t e = field == 255 ? 255u : field > 2 ? (uint32_t)(field - 2) : 0u;  // max|x| < 2^-125: the smallest exponent
+  scale = e == 255 ? 1.0f : v2::e8m0_value(e);
+  return e;
 }
-// |x mul| to a code of e2m1: to nearest, ties to the even code, at most 7; the
-// sign stays with codes that are not zero.
-__device__ __forceinline__ uint32_t code4(float x, float mul) {
-  const float y = fminf(fabsf(x) * mul, 6.0f);
-  // spacing 1/2 below 2, 1 below 4, 2 above: codes 2y, y + 2, y / 2 + 4
-  const float n = y < 2.0f ? __builtin_rintf(2.0f * y) : y < 4.0f ? __builtin_rintf(y) + 2.0f : __builtin_rintf(0.5f * y) + 4.0f;
-  const uint32_t c = (uint32_t)n;
-  return c | (c != 0 && x < 0.0f ? 8u : 0u);
+// Eight values over the scale to codes of e2m1 (v_cvt_scalef32_pk_fp4: to nearest,
+// ties to even, what is beyond 6 to 6; over a million values of all binades and
+// scales, ties among them, every code was the formula's but for -0, which becomes
+// +0 here: a nibble's magnitude plus 7 carries into bit 3 where it is not zero).
+__device__ __forceinline__ uint32_t no_minus_zero(uint32_t w) {
+  return w & (0x77777777u | ((w & 0x77777777u) + 0x77777777u));
+}
+__device__ __forceinline__ uint32_t codes8(const float (&v)[8], float scale) {
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[0], v[1], scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[2], v[3], scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[4], v[5], scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, v[6], v[7], scale, 3);
+  return no_minus_zero(w);
+}
+__device__ __forceinline__ uint32_t codes8(u32x4 v, float scale) {  // bf16 pairs
+  auto pair = [](uint32_t x) { return __builtin_bit_cast(bf16x2_t, x); };
+  uint32_t w = 0;
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(v[0]), scale, 0);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(v[1]), scale, 1);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(v[2]), scale, 2);
+  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(w, pair(v[3]), scale, 3);
+  return no_minus_zero(w);
 }
 // The largest of four neighbouring lanes, in all of them.
 __device__ __forceinline__ uint32_t quad_max(uint32_t v) {
@@ -48,28 +59,30 @@ __global__ __launch_bounds__(256) void k_mxfp4_rows(const uint16_t* __restrict__
                                                     uint32_t* __restrict__ codes, uint8_t* __restrict__ exps) {
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= n8) return;  // whole blocks: K % 128 == 0
-  float v[8];
+  uint32_t m = 0;
+  float scale;
   if constexpr (ACT < 0) {
-    widen8(((const u32x4*)src)[i], v);
+    const u32x4 x = ((const u32x4*)src)[i];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) m = max(m, max((x[q] << 16) & 0x7FFFFFFFu, x[q] & 0x7FFF0000u));
+    const uint32_t e = block_exponent(quad_max(m), scale);
+    codes[i] = codes8(x, scale);
+    if ((threadIdx.x & 3) == 0) exps[i >> 2] = (uint8_t)e;
   } else {
     const long row = i / K8, c = i - row * K8;
     const u32x4* p = (const u32x4*)src + row * 2 * K8 + c;
-    float u[8];
+    float v[8], u[8];
     widen8(p[0], v);
     widen8(p[K8], u);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = (ACT == MOE_ACT_SWIGLU ? v[q] * sigmoidf_(v[q]) : v[q] * norm_cdf_rel(v[q])) * u[q];
+    for (int q = 0; q < 8; ++q) {
+      v[q] = (ACT == MOE_ACT_SWIGLU ? v[q] * sigmoidf_(v[q]) : v[q] * norm_cdf_rel(v[q])) * u[q];
+      m = max(m, mag(v[q]));
+    }
+    const uint32_t e = block_exponent(quad_max(m), scale);
+    codes[i] = codes8(v, scale);
+    if ((threadIdx.x & 3) == 0) exps[i >> 2] = (uint8_t)e;
   }
-  uint32_t m = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) m = max(m, mag(v[q]));
-  float mul;
-  const uint32_t e = block_exponent(quad_max(m), mul);
-  uint32_t w = 0;
-#pragma unroll
-  for (int q = 0; q < 8; ++q) w |= code4(v[q], mul) << (4 * q);
-  codes[i] = w;
-  if ((threadIdx.x & 3) == 0) exps[i >> 2] = (uint8_t)e;
 }
 
 // The transposed weight's codes: a workgroup takes 128 rows n x 32 columns k of
@@ -88,14 +101,13 @@ __global__ __launch_bounds__(128) void k_mxfp4_weight_t(const uint16_t* __restri
     v[q] = bf2f(tile[32 * b + q][k]);
     m = max(m, mag(v[q]));
   }
-  float mul;
-  const uint32_t x = block_exponent(m, mul);
+  float scale;
+  const uint32_t x = block_exponent(m, scale);
   u32x4 w;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    w[c] = 0;
-#pragma unroll
-    for (int q = 0; q < 8; ++q) w[c] |= code4(v[8 * c + q], mul) << (4 * q);
+    const float(&v8)[8] = *(const float(*)[8])(v + 8 * c);
+    w[c] = codes8(v8, scale);
   }
   const long row = e * K + k0 + k;
   *(u32x4*)(codes + row * (N / 2) + (n0 + 32 * b) / 2) = w;
@@ -108,19 +120,8 @@ __global__ __launch_bounds__(256) void k_mxfp4_values(const uint32_t* __restrict
   const long i = (long)blockIdx.x * 256 + threadIdx.x;
   if (i >= n8) return;
   const uint32_t w = codes[i], e = exps[i >> 2];
-  u32x4 o;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float v[2];
-#pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const uint32_t n = (w >> (8 * c + 4 * q)) & 15u, m = n & 7u;
-      const float a = m < 2 ? 0.5f * (float)m : (1.0f + 0.5f * (float)(m & 1u)) * (float)(1u << (m >> 1)) * 0.5f;
-      const float s = e == 255 ? __uint_as_float(0x7FC00000u) : v2::e8m0_value(e);
-      v[q] = (n & 8u ? -a : a) * s;
-    }
-    o[c] = pack2(v[0], v[1]);
-  }
+  u32x4 o = v2::fp4x8_bf16(w, v2::e8m0_value(e));
+  if (e == 255) o = u32x4{0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u};
   out[i] = o;
 }
 
@@ -235,7 +236,7 @@ moe_status moe_mxfp4_product(const moe_mxfp4_desc* d, const moe_pool* pool, cons
   if (e != hipSuccess) return MOE_ERR_HIP;
   const hipStream_t st = (hipStream_t)stream;
   constexpr Kind KIND = Kind::mxfp4;
-  switch (pick(p, Costs{20000.0, 0.84, 0.5, 2.1, 1.35}, routes, cus, true)) {
+  switch (pick(p, Costs{21000.0, 4.0, 0.45, 1.15, 8.0, 1.2, 2.2}, routes, cus, d->K / 2)) {
     case Pick::few: e = launch_rows_few<KIND>("k_mxfp4_few", p, tiles(FEW_ROWS), 8 * cus, st); break;
     case Pick::mid: e = launch_rows_tile<KIND, GeoM>("k_mxfp4_tile64", p, tiles(GeoM::TM), 2 * cus, st); break;
     case Pick::large: e = launch_rows_tile<KIND, GeoL>("k_mxfp4_tile256", p, tiles(GeoL::TM), cus, st); break;

@@ -102,7 +102,7 @@ struct Wgrad {
       da = stream::make_desc(p.a, any ? (uint64_t)p.a_rows * p.K * 2 : 0);
       di = stream::make_desc(p.row2r + t.row0, (uint64_t)n * 4);
     }
-    const int kr = 4 * wv + (l >> 4), c = 8 * ((l & 15) ^ ((l >> 4) << 2));
+    const int kr = 4 * wv + (l >> 4), c = 8 * ((l & 15) ^ stream::t_swz(kr));
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int cx = t.m0 + c + 128 * h, cw = t.n0 + c + (c >= 64 ? 64 : 0) + 64 * h;
@@ -278,14 +278,13 @@ moe_status moe_expert_product(const moe_expert_desc* d, const moe_pool* pool, co
   const int64_t routes = pool_routes(pool, d->E), live = routes < d->E ? routes : d->E;
   auto tiles = [&](int tm) { return routes / tm + live; };
   const hipStream_t st = (hipStream_t)stream;
-  constexpr Costs costs{20000.0, 0.84, 0.5, 2.1, 1.35};
   if (d->transposed) {
-    if (pick(p, costs, routes, cus, false) == Pick::mid)
+    if (pick(p, Costs{0.0, 4.0, 0.4, 0.9, 9.0, 1.2, 1.65}, routes, cus, 2 * d->K) == Pick::mid)
       e = launch_rows_tile<Kind::bf16_t, GeoM>("k_product_t_tile64", p, tiles(GeoM::TM), 2 * cus, st);
     else
       e = launch_rows_tile<Kind::bf16_t, GeoL>("k_product_t_tile256", p, tiles(GeoL::TM), cus, st);
   } else {
-    switch (pick(p, costs, routes, cus, true)) {
+    switch (pick(p, Costs{27000.0, 4.0, 0.31, 0.84, 9.0, 1.0, 1.65}, routes, cus, 2 * d->K)) {
       case Pick::few: e = launch_rows_few<Kind::bf16>("k_product_few", p, tiles(FEW_ROWS), 8 * cus, st); break;
       case Pick::mid: e = launch_rows_tile<Kind::bf16, GeoM>("k_product_tile64", p, tiles(GeoM::TM), 2 * cus, st); break;
       case Pick::large: e = launch_rows_tile<Kind::bf16, GeoL>("k_product_tile256", p, tiles(GeoL::TM), cus, st); break;

@@ -139,9 +139,11 @@ struct RowsTile {
     }
     if constexpr (TR) {
       rw = desc(p.w + (long)t.e * p.N * RB, any ? (uint64_t)p.K * p.N * 2 : 0);
-      const int kr = 4 * wv + (l >> 4), c = 8 * ((l & 15) ^ ((l >> 4) << 2));
+      const int kr = 4 * wv + (l >> 4);
+      // vw[h]: half h of the columns, or (one tile of 128) even and odd instructions, 16 rows apart
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
+        const int c = 8 * ((l & 15) ^ stream::t_swz(kr + (G::SPLIT ? 0 : 16 * h)));
         const int col = n0 + (G::SPLIT ? c + (c >= 64 ? 64 : 0) + 64 * h : c);
         vw[h] = col < p.N ? (uint32_t)kr * (uint32_t)p.N * 2u + 2u * (uint32_t)col : OFF_NONE;
       }
@@ -180,7 +182,7 @@ struct RowsTile {
         // instruction q: half q / 2 (one half: all four), K-rows 4 (wave + ..)
         const int h = G::SPLIT ? q >> 1 : 0, r = G::SPLIT ? 32 * (q & 1) : 16 * q;
         char* to = st + G::X_BYTES + 16384 * h + 1024 * (wv + (G::SPLIT ? 8 * (q & 1) : 4 * q));
-        stream::load16(rw, to, vw[h], (uint32_t)(64 * s + r) * (uint32_t)p.N * 2u);
+        stream::load16(rw, to, vw[G::SPLIT ? h : q & 1], (uint32_t)(64 * s + r) * (uint32_t)p.N * 2u);
       } else {
         const int j = !G::SPLIT ? q : q < 2 ? 2 * q : 2 * q - 3;  // the first halves of the waves' rows first
         stream::load16(rw, st + G::X_BYTES + 1024 * (wv + G::NW * j), in_row(j) ? vw[j & 1] : OFF_NONE,
@@ -252,7 +254,10 @@ __global__ __launch_bounds__(G::NT) void k_rows_tile(RowsArgs p) {
 // time, so they go from memory straight into the registers that the matrix
 // instruction takes.  A workgroup is one wave: 16 activation rows x 16 weight
 // rows, the next FEW_CH stages of 128 bytes in flight while FEW_CH are
-// multiplied.
+// multiplied.  bf16: an instruction takes 64 bytes of each row in one piece (the
+// order of k inside a stage is free; 16 bytes at a distance of 32: 2 % slower; eight
+// stages in flight: 25 %); 4 bits: 32 bytes a lane, whose two blocks' exponents lie
+// side by side.
 constexpr int FEW_ROWS = 16, FEW_CH = 4;
 template <Kind KIND>
 __global__ __launch_bounds__(64) void k_rows_few(RowsArgs p) {
@@ -265,7 +270,8 @@ __global__ __launch_bounds__(64) void k_rows_few(RowsArgs p) {
     const long row0 = (long)p.offsets[e] + (long)m * FEW_ROWS;
     const int nrows = min(rows_of(p, e) - m * FEW_ROWS, FEW_ROWS);
     const rsrc_t rw = make_rsrc(p.w + ((long)e * p.N + n0) * RB, (uint64_t)ncols * RB);
-    const uint32_t wo = (uint32_t)fr * (uint32_t)RB + 32u * (uint32_t)fc;
+    constexpr uint32_t CB = MX ? 32u : 16u, HB = MX ? 16u : 64u;
+    const uint32_t wo = (uint32_t)fr * (uint32_t)RB + CB * (uint32_t)fc;
     // this lane's activation row
     rsrc_t ra, rea, rew;
     long ar = -1;
@@ -281,7 +287,7 @@ __global__ __launch_bounds__(64) void k_rows_few(RowsArgs p) {
       if (fr < live) ar = fr;
     }
     if constexpr (MX) rew = make_rsrc(p.ew + ((long)e * p.N + n0) * RE, (uint64_t)ncols * RE);
-    const uint32_t ao = (uint32_t)ar * (uint32_t)RB + 32u * (uint32_t)fc;
+    const uint32_t ao = (uint32_t)ar * (uint32_t)RB + CB * (uint32_t)fc;
     const uint32_t eo = (uint32_t)ar * (uint32_t)RE + 2u * (uint32_t)fc, eow = (uint32_t)fr * (uint32_t)RE + 2u * (uint32_t)fc;
     struct Set {
       stream::Frag w[FEW_CH], x[FEW_CH];
@@ -290,12 +296,12 @@ __global__ __launch_bounds__(64) void k_rows_few(RowsArgs p) {
 #pragma unroll
       for (int i = 0; i < FEW_CH; ++i) {
         const uint32_t k = 128u * (uint32_t)(c0 + i);
-        const int left = RB - (int)k - 32 * fc;  // bytes of the row from this lane's on
-        const bool lo = left > 0, hi = left > 16, has = ar >= 0;
+        const int left = RB - (int)k - (int)CB * fc;  // bytes of the row from this lane's on
+        const bool lo = left > 0, hi = left > (int)HB, has = ar >= 0;
         q.w[i].lo = bload(rw, lo ? wo + k : OFF_NONE);
-        q.w[i].hi = bload(rw, hi ? wo + k + 16u : OFF_NONE);
+        q.w[i].hi = bload(rw, hi ? wo + k + HB : OFF_NONE);
         q.x[i].lo = bload(ra, lo && has ? ao + k : OFF_NONE);
-        q.x[i].hi = bload(ra, hi && has ? ao + k + 16u : OFF_NONE);
+        q.x[i].hi = bload(ra, hi && has ? ao + k + HB : OFF_NONE);
         if constexpr (MX) {  // K % 128 == 0: both halves or none
           const uint32_t x = 8u * (uint32_t)(c0 + i);
           q.w[i].scale = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rew, (int)(lo ? eow + x : OFF_NONE), 0, 0);
@@ -354,20 +360,26 @@ hipError_t launch_rows_tile(const char* name, const RowsArgs& p, int64_t mtiles,
 
 // Which kernel: the routes are known, how they fall on the experts is not, so
 // an expert with rows is taken to have the mean, and an M tile more in half the
-// cases.
+// cases.  Costs in us, fitted to a sweep of 1 to 64 experts of 512 x 512 to 4096 x
+// 4096 with 1 to 512 rows each: a start, and for each stage of 128 bytes of K
+// what the rounds of tiles over the CUs take, or the least that one tile does.
 enum class Pick { few, mid, large };
 struct Costs {
-  double few;              // tiles of 16 rows, by the rows that they read, that single waves may take
-  double mid, mid_least;   // us a stage: two 64-row tiles on a CU; the least
-  double large, large_least;
+  double few;  // weight and activation rows read by all tiles of 16 rows, up to which single waves are faster
+  double mid_start, mid_least, mid;  // two 64-row tiles on a CU
+  double large_start, large_least, large;
 };
-inline Pick pick(const RowsArgs& p, const Costs& c, int64_t routes, int cus, bool few) {
+inline Pick pick(const RowsArgs& p, const Costs& c, int64_t routes, int cus, int row_bytes) {
   const double live = (double)(routes < p.E ? routes : p.E), avg = (double)routes / live, fill = cus / 256.0;
+  const double stages = (row_bytes + 127) / 128;
   auto mtiles = [&](int tm) { return live * (avg / tm + 0.5 > 1.0 ? avg / tm + 0.5 : 1.0); };
-  if (few && mtiles(FEW_ROWS) * ((p.N + 15) / 16) * (16.0 + (avg < 16.0 ? avg : 16.0)) <= c.few * fill) return Pick::few;
+  if (mtiles(FEW_ROWS) * ((p.N + 15) / 16) * (16.0 + (avg < 16.0 ? avg : 16.0)) <= c.few * fill) return Pick::few;
   const double mid = c.mid * mtiles(GeoM::TM) * ((p.N + GeoM::TN - 1) / GeoM::TN) / (2 * cus);
   const double large = c.large * mtiles(GeoL::TM) * ((p.N + GeoL::TN - 1) / GeoL::TN) / cus;
-  return (mid > c.mid_least ? mid : c.mid_least) <= (large > c.large_least ? large : c.large_least) ? Pick::mid : Pick::large;
+  return c.mid_start + stages * (mid > c.mid_least ? mid : c.mid_least) <=
+                 c.large_start + stages * (large > c.large_least ? large : c.large_least)
+             ? Pick::mid
+             : Pick::large;
 }
 
 }  // namespace moelora

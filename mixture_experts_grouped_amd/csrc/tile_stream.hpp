@@ -108,25 +108,31 @@ struct RowFrags {
   }
 };
 
-// Lane offsets of the 16-column blocks of a T tile (K-outer): [64 k][128 columns]
-// of bf16, pitch 256 bytes, chunk j of row k in slot j ^ 4 (k & 3); a tile of 256
-// columns is two of them, the first holding columns 0 .. 63 and 128 .. 191.  A
-// lane takes k 16 (l / 16) .. + 15 of a column by four transposing reads.  PER:
-// columns of a wave in one such tile.
+// T tiles (K-outer): [64 k][128 columns] of bf16, pitch 256 bytes, 16-byte chunk j
+// of row k in slot j ^ swz(k); a tile of 256 columns is two of them, the first
+// holding columns 0 .. 63 and 128 .. 191.  A transposing read touches, for each 16
+// lanes, two chunks of four rows k0 .. k0 + 3, and two such groups of lanes, 16 rows
+// apart, are served together: with the last two bits of k in the slot's upper bits
+// and bit 4 in bit 1 the two cover all banks once (without the latter half of the
+// LDS cycles of the weight gradient were conflicts).
+__device__ __forceinline__ int t_swz(int k) { return ((k & 3) << 2) ^ (((k >> 4) & 1) << 1); }
+
+// Lane offsets of its 16-column blocks.  A lane takes k 16 (l / 16) .. + 15 of a
+// column by four reads.  PER: columns of a wave in one tile.
 template <int PER>
 struct ColFrags {
-  uint32_t o[2];
+  uint32_t o[4];
   __device__ __forceinline__ void init(int lane, int first) {  // first: the wave's first column in the tile
-    const int g = lane >> 4, i = lane & 15;
+    const int g = lane >> 4, i = lane & 15, k = 16 * g + (i >> 2);
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      const int chunk = (first >> 3) + 4 * v + ((i & 3) >> 1);
-      o[v] = (uint32_t)((16 * g + (i >> 2)) * 256 + ((chunk ^ ((i >> 2) << 2)) << 4) + (i & 1) * 8);
+    for (int v = 0; v < 4; ++v) {
+      const int chunk = (first >> 3) + 2 * v + ((i & 3) >> 1);
+      o[v] = (uint32_t)(k * 256 + ((chunk ^ t_swz(k)) << 4) + (i & 1) * 8);
     }
   }
   __device__ __forceinline__ Frag get(const char* tile, int i) const {
     constexpr int N = PER / 16;  // blocks of the wave in a tile
-    const char* p = tile + (i / N) * 16384 + o[(i % N) >> 1] + (i & 1) * 32;
+    const char* p = tile + (i / N) * 16384 + o[i % N];
     auto rd = [&](int t) {
       return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v2::s16x4*)(p + 1024 * t)));
     };
