@@ -239,7 +239,10 @@ moe_status moe_mxfp4_product(const moe_mxfp4_desc* d, const moe_pool* pool, cons
   switch (pick(p, Costs{21000.0, 4.0, 0.45, 1.15, 8.0, 1.2, 2.2}, routes, cus, d->K / 2)) {
     case Pick::few: e = launch_rows_few<KIND>("k_mxfp4_few", p, tiles(FEW_ROWS), 8 * cus, st); break;
     case Pick::mid: e = launch_rows_tile<KIND, GeoM>("k_mxfp4_tile64", p, tiles(GeoM::TM), 2 * cus, st); break;
-    case Pick::large: e = launch_rows_tile<KIND, GeoL>("k_mxfp4_tile256", p, tiles(GeoL::TM), cus, st); break;
+    case Pick::large:
+      e = d->K % 512 == 0 ? launch_rows_tile<Kind::mxfp4_pairs, GeoL>("k_mxfp4_tile256", p, tiles(GeoL::TM), cus, st)
+                          : launch_rows_tile<KIND, GeoL>("k_mxfp4_tile256", p, tiles(GeoL::TM), cus, st);
+      break;
   }
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }

@@ -17,7 +17,7 @@ struct RowsArgs : PoolArgs {
   uint16_t* out;
 };
 
-enum class Kind { bf16, bf16_t, mxfp4 };
+enum class Kind { bf16, bf16_t, mxfp4, mxfp4_pairs };
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ f32x4 mma_bf16(u32x4 w, u32x4 x, f32x4 c) {
@@ -35,15 +35,22 @@ template <Kind KIND, class G_>
 struct RowsTile {
   using G = G_;
   using Tile = PoolTile;
-  static constexpr bool MX = KIND == Kind::mxfp4, TR = KIND == Kind::bf16_t;
+  static constexpr bool PAIRS = KIND == Kind::mxfp4_pairs, MX = KIND == Kind::mxfp4 || PAIRS, TR = KIND == Kind::bf16_t;
   static constexpr int NX = G::X_BYTES / (1024 * G::NW), NWT = G::W_BYTES / (1024 * G::NW);
-  static constexpr int NS = MX ? 2 : 0;
+  // Exponents: 8 bytes of each row a stage, by one load a wave and operand; or
+  // (PAIRS, whole pairs of stages) 16 bytes for two stages, by one load a wave at
+  // even stages and none at odd ones, which halves the lines of memory touched: a
+  // stage's 512 pieces of 8 bytes cost as many as its codes (98,304 rows of 4096 x
+  // 4096: 110 of 930 us).
+  static constexpr int NS = PAIRS ? 1 : MX ? 2 : 0;
   static constexpr int INSTS = NX + NWT + NS, FIRST = NX + NS + NWT / 2;
-  static constexpr int SLOT = 2 * G::NW * 256;  // bytes of a stage's exponents: x, then w
+  static constexpr int SLOT = PAIRS ? (G::TM + G::TN) * 16 : 2 * G::NW * 256;  // bytes of a stage's (a pair's) exponents: x, then w
+  static constexpr int SLOTS = PAIRS ? 2 : 3, COUNT = PAIRS ? 4 : 3;  // sl and fl count stages modulo COUNT
   static constexpr int SCALES = G::END;
-  static constexpr int TABLE = SCALES + (MX ? 3 * SLOT : 0);
+  static constexpr int TABLE = SCALES + (MX ? SLOTS * SLOT : 0) + (PAIRS ? 1024 : 0);  // and where the loads of odd stages go
   static constexpr int lds(int E) { return TABLE + 12 * E + 4 * G::TM; }
-  static_assert(!MX || (G::TM * 8 <= G::NW * 256 && G::TN * 8 == G::NW * 256), "one load of exponents a wave and operand");
+  static_assert(!MX || PAIRS || (G::TM * 8 <= G::NW * 256 && G::TN * 8 == G::NW * 256), "one load of exponents a wave and operand");
+  static_assert(!PAIRS || (G::SPLIT && G::TM == 64 * 4 && G::TN == 64 * 4), "waves 0-3 load x's exponents, 4-7 w's");
   static_assert(lds(MAX_E) <= 160 * 1024, "LDS");
   using Desc = typename std::conditional<TR, stream::desc_t, rsrc_t>::type;
   __device__ static __forceinline__ Desc desc(const void* base, uint64_t bytes) {
@@ -79,7 +86,7 @@ struct RowsTile {
       ft.init(lane, wn * (G::SPLIT ? 64 : 32));
     else
       fw.init(lane, wn * G::FN);
-    sl = 2;
+    sl = COUNT - 1;
   }
   __device__ __forceinline__ bool first(Tile& t) {
     fill_table<G::TM>(p, tab, smem + TABLE);
@@ -109,21 +116,24 @@ struct RowsTile {
     const int n0 = t.nt * G::TN, ncols = min(p.N - n0, G::TN);
     auto row_of = [&](int j) { return 8 * (wv + G::NW * j) + (l >> 3); };
     auto chunk = [&](int j) { return 16u * (uint32_t)((l & 7) ^ v2::kswz<64>(row_of(j))); };
+    // the row whose exponents this lane loads, of either operand, and its bytes in them
+    const int erow = PAIRS ? 64 * (wv & 3) + l : 32 * wv + (l >> 1);
+    const uint32_t ebyte = PAIRS ? 0u : 4u * (l & 1);
     if (p.topk > 0) {
       int tk[NX + 1];
       const int* routes = (const int*)(smem + TABLE + 12 * p.E);
 #pragma unroll
       for (int j = 0; j <= NX; ++j) {
-        const int r = j < NX ? row_of(j) : min(32 * wv + (l >> 1), G::TM - 1);
-        tk[j] = j < NX || MX ? routes[r] : -1;
-        tk[j] = token_of(p, (j < NX ? r : 32 * wv + (l >> 1)) < t.nrows ? tk[j] : -1);
+        const int r = j < NX ? row_of(j) : erow;
+        tk[j] = j < NX || MX ? routes[min(r, G::TM - 1)] : -1;
+        tk[j] = token_of(p, r < t.nrows ? tk[j] : -1);
       }
       rx = desc(p.a, any ? (uint64_t)p.a_rows * RB : 0);
 #pragma unroll
       for (int j = 0; j < NX; ++j) vx[j] = tk[j] >= 0 ? (uint32_t)tk[j] * (uint32_t)RB + chunk(j) : OFF_NONE;
       if constexpr (MX) {
         rsx = desc(p.ea, any ? (uint64_t)p.a_rows * RE : 0);
-        vsx = tk[NX] >= 0 ? (uint32_t)tk[NX] * (uint32_t)RE + 4u * (l & 1) : OFF_NONE;
+        vsx = tk[NX] >= 0 ? (uint32_t)tk[NX] * (uint32_t)RE + ebyte : OFF_NONE;
       }
     } else {
       const long have = p.a_rows - t.row0;
@@ -133,8 +143,7 @@ struct RowsTile {
       for (int j = 0; j < NX; ++j) vx[j] = row_of(j) < live ? (uint32_t)row_of(j) * (uint32_t)RB + chunk(j) : OFF_NONE;
       if constexpr (MX) {
         rsx = desc(p.ea + t.row0 * RE, (uint64_t)live * RE);
-        const int r = 32 * wv + (l >> 1);
-        vsx = r < live ? (uint32_t)r * (uint32_t)RE + 4u * (l & 1) : OFF_NONE;
+        vsx = erow < live ? (uint32_t)erow * (uint32_t)RE + ebyte : OFF_NONE;
       }
     }
     if constexpr (TR) {
@@ -153,14 +162,19 @@ struct RowsTile {
       for (int j = 0; j < 2; ++j) vw[j] = (uint32_t)(8 * wv + (l >> 3)) * (uint32_t)RB + chunk(j);
       if constexpr (MX) {
         rsw = desc(p.ew + ((long)t.e * p.N + n0) * RE, any ? (uint64_t)ncols * RE : 0);
-        vsw = (uint32_t)(32 * wv + (l >> 1)) * (uint32_t)RE + 4u * (l & 1);
+        vsw = (uint32_t)erow * (uint32_t)RE + ebyte;
+        if (PAIRS && wv >= 4) vsx = vsw;
       }
     }
   }
 
   __device__ __forceinline__ void fill(int s) { fl = s; }
-  __device__ __forceinline__ void begin() { fl = !G::SPLIT ? sl : sl == 0 ? 2 : sl - 1; }
-  __device__ __forceinline__ void turn() { sl = sl == 2 ? 0 : sl + 1; }
+  __device__ __forceinline__ void begin() { fl = !G::SPLIT ? sl : PAIRS ? (sl + 2) & 3 : sl == 0 ? 2 : sl - 1; }
+  __device__ __forceinline__ void turn() { sl = sl == COUNT - 1 ? 0 : sl + 1; }
+  // exponents of the stage that x() and w() read: where row r's begin
+  __device__ __forceinline__ const char* scales(int r) const {
+    return PAIRS ? smem + SCALES + (sl >> 1) * SLOT + 16 * r + 8 * (sl & 1) : smem + SCALES + sl * SLOT + 8 * r;
+  }
 
   // Load i of stage s into buffer g.  What lies past the row's end reads zero.
   __device__ __forceinline__ void issue(int s, int g, int i) const {
@@ -173,6 +187,13 @@ struct RowsTile {
     if (i < NX) {
       stream::load16(rx, st + 1024 * (wv + G::NW * i), in_row(i) ? vx[i] : OFF_NONE, 128u * (uint32_t)s);
     } else if (i < NX + NS) {
+      if constexpr (PAIRS) {
+        // waves 0-3: 64 rows of x each, 4-7 of w
+        const bool even = (s & 1) == 0;
+        char* to = even ? smem + SCALES + (fl >> 1) * SLOT + 1024 * wv : smem + SCALES + 2 * SLOT;
+        stream::load16(wv < 4 ? rsx : rsw, to, even && 8 * s < RE ? vsx : OFF_NONE, 8u * (uint32_t)s);
+        return;
+      }
       const bool in = 8 * s + 4 * (l & 1) < RE;
       char* to = smem + SCALES + fl * SLOT + (i > NX ? G::NW * 256 : 0) + 256 * wv;
       stream::load4(i > NX ? rsw : rsx, to, in ? (i > NX ? vsw : vsx) : OFF_NONE, 8u * (uint32_t)s);
@@ -194,7 +215,7 @@ struct RowsTile {
   __device__ __forceinline__ stream::Frag x(const char* buf, int j) const {
     stream::Frag f = fx.get(buf + wm * G::FM * 2048, j);
     if constexpr (MX)
-      f.scale = *(const uint16_t*)(smem + SCALES + sl * SLOT + ((wm * G::FM + j) * 16 + (lane & 15)) * 8 + 2 * (lane >> 4));
+      f.scale = *(const uint16_t*)(scales((wm * G::FM + j) * 16 + (lane & 15)) + 2 * (lane >> 4));
     return f;
   }
   __device__ __forceinline__ stream::Frag w(const char* buf, int i) const {
@@ -203,8 +224,7 @@ struct RowsTile {
     } else {
       stream::Frag f = fw.get(buf + G::X_BYTES + wn * G::FN * 2048, i);
       if constexpr (MX)
-        f.scale = *(const uint16_t*)(smem + SCALES + sl * SLOT + G::NW * 256 + ((wn * G::FN + i) * 16 + (lane & 15)) * 8 +
-                                     2 * (lane >> 4));
+        f.scale = *(const uint16_t*)(scales((PAIRS ? G::TM : G::NW * 32) + (wn * G::FN + i) * 16 + (lane & 15)) + 2 * (lane >> 4));
       return f;
     }
   }

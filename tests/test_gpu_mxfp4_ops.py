@@ -9,7 +9,7 @@ from mixture_experts_grouped_amd import binding as B
 from oracle import mxfp4 as OMX
 from oracle import products as OP
 from tests import harness as Hn
-from tests.test_gpu_product import build, extents, f64, half_step, routing
+from tests.test_gpu_product import Kernels, build, extents, f64, half_step, routing
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
@@ -149,6 +149,38 @@ SHAPES = [
 @pytest.mark.parametrize("T,E,k,N,K,drop,only", SHAPES)
 def test_product(T, E, k, N, K, drop, only, gather):
     check(routing(T, E, k, T + N, drop, only), E, N, K, gather, seed=K)
+
+
+@pytest.mark.parametrize("name,T,E,k,N,K,gather", [
+    ("k_mxfp4_few", 9, 3, 1, 64, 1152, True), ("k_mxfp4_few", 100, 4, 1, 256, 128, False),
+    ("k_mxfp4_tile64", 600, 3, 2, 544, 384, True), ("k_mxfp4_tile64", 900, 5, 1, 288, 512, False),
+    ("k_mxfp4_tile256", 8000, 3, 1, 4128, 512, True), ("k_mxfp4_tile256", 8000, 2, 1, 4096, 640, True),
+    ("k_mxfp4_tile256", 8000, 3, 1, 3872, 1024, False), ("k_mxfp4_tile256", 8000, 2, 1, 4096, 128, False)])
+def test_every_kernel(name, T, E, k, N, K, gather):
+    with Kernels() as ran:
+        check(routing(T, E, k, T, 0.1), E, N, K, gather, seed=N)
+    assert name in ran.names, ran.names
+
+
+def test_nan_exponents_in_a_large_tile():
+    """One token's and one weight row's last block, where pairs of stages and single ones are loaded."""
+    for K in (512, 640):
+        idx = torch.zeros(8192, 1, dtype=torch.int32)
+        idx[::2] = 1
+        pool = build(idx, 2)
+        a, ea, w, ew = operands(8192, 2, 4096, K, K)
+        ea[777, K // 32 - 1] = 255
+        ew[0, 4001, K // 32 - 1] = 255
+        with Kernels() as ran:
+            out = M.mxfp4_product(pool, a, ea, w, ew, topk=1)
+        assert "k_mxfp4_tile256" in ran.names
+        bad = torch.isnan(out).cpu()
+        for e, rows, routes in extents(pool):
+            want = torch.zeros(rows.size, 4096, dtype=torch.bool)
+            want[torch.from_numpy(routes == 777)] = True
+            if e == 0:
+                want[:, 4001] = True
+            assert torch.equal(bad[rows], want), (K, e)
 
 
 def test_nan_exponents_stay_in_their_rows_and_columns():

@@ -126,6 +126,32 @@ def test_weight_gradient(T, E, k, N, K, drop, only, gather, dtype, add):
     check_grad(routing(T, E, k, T + N, drop, only), E, N, K, gather, dtype, add, seed=K)
 
 
+class Kernels:
+    """The kernels that calls take, from the library's own trace."""
+
+    def __enter__(self):
+        B.moe_lora_trace_reset()
+        B.moe_lora_trace_enable(True)
+        return self
+
+    def __exit__(self, *a):
+        B.moe_lora_trace_enable(False)
+        self.names = set(B.moe_lora_trace_collect())
+        B.moe_lora_trace_reset()
+
+
+@pytest.mark.parametrize("name,T,E,k,N,K,gather,transposed", [
+    ("k_product_few", 9, 3, 1, 40, 1048, True, False), ("k_product_few", 100, 4, 1, 256, 72, False, False),
+    ("k_product_tile64", 600, 3, 2, 520, 200, True, False), ("k_product_tile64", 900, 5, 1, 264, 64, False, False),
+    ("k_product_tile256", 6000, 3, 1, 2056, 520, True, False), ("k_product_tile256", 5000, 2, 1, 2304, 1024, False, False),
+    ("k_product_t_tile64", 600, 3, 2, 520, 200, True, True), ("k_product_t_tile64", 40, 5, 1, 264, 72, False, True),
+    ("k_product_t_tile256", 6000, 3, 1, 2056, 520, True, True), ("k_product_t_tile256", 5000, 2, 1, 2304, 1024, False, True)])
+def test_every_kernel(name, T, E, k, N, K, gather, transposed):
+    with Kernels() as ran:
+        check_product(routing(T, E, k, T, 0.1), E, N, K, gather, transposed, seed=N)
+    assert name in ran.names, ran.names
+
+
 def test_infinities_stay_in_their_rows():
     """A NaN or an infinity in one token, one expert's weight, and past the widths' ends in memory."""
     idx = torch.tensor([[0, 1], [1, 2], [0, 2]], dtype=torch.int32)
