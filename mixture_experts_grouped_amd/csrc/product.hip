@@ -165,45 +165,49 @@ struct Wgrad {
     OUT* base = (OUT*)p.out + ((long)t.e * p.N + t.m0) * p.K + t.n0;
     // less what the columns before n0 take: the last row ends there
     const rsrc_t ro = make_rsrc(base, ((uint64_t)live * p.K - t.n0) * sizeof(OUT));
+    // what a row of blocks is added to is loaded together: one after another, each
+    // waited for before its store, the loads took most of a short tile's time
+    constexpr int ADDS = sizeof(OUT) == 4 ? G::FN : G::FN / 2;  // 16-byte pieces of a lane and row of blocks
 #pragma unroll
     for (int j = 0; j < G::FM; ++j) {
       const int r = (wm * G::FM + j) * 16 + fr;
+      auto place = [&](int q) {
+        const int c = sizeof(OUT) == 4 ? (wn * G::FN + q) * 16 + 4 * fc : (wn * G::FN + 2 * q + (fc & 1)) * 16 + 8 * (fc >> 1);
+        return r < live && t.n0 + c < p.K ? ((uint32_t)r * (uint32_t)p.K + (uint32_t)c) * (uint32_t)sizeof(OUT) : OFF_NONE;
+      };
+      u32x4 old[ADDS];
+      if (p.accumulate) {
 #pragma unroll
-      for (int i = 0; i < G::FN; i += 2) {
+        for (int q = 0; q < ADDS; ++q) old[q] = bload(ro, place(q));
+      }
+#pragma unroll
+      for (int q = 0; q < ADDS; ++q) {
+        u32x4 w;
         if constexpr (sizeof(OUT) == 4) {
+          f32x4 v = acc[q][j];
+          if (p.accumulate) v += __builtin_bit_cast(f32x4, old[q]);
+          w = __builtin_bit_cast(u32x4, v);
+        } else if (p.accumulate) {  // in fp32 before the one rounding
+          const int i = 2 * q;
+          float o[8];
+          widen8(old[q], o);
+          f32x4 lo, hi;
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int c = (wn * G::FN + i + q) * 16 + 4 * fc;
-            const uint32_t off = r < live && t.n0 + c < p.K ? ((uint32_t)r * (uint32_t)p.K + (uint32_t)c) * 4u : OFF_NONE;
-            f32x4 v = acc[i + q][j];
-            if (p.accumulate) v += __builtin_bit_cast(f32x4, bload(ro, off));
-            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), ro, (int)off, 0, 0);
+          for (int e = 0; e < 4; ++e) {
+            const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][e]), __float_as_uint(acc[i + 1][j][e]), false, false);
+            lo[e] = __uint_as_float(s[0]) + o[e];
+            hi[e] = __uint_as_float(s[1]) + o[4 + e];
           }
+          w = u32x4{pack2(lo[0], lo[1]), pack2(lo[2], lo[3]), pack2(hi[0], hi[1]), pack2(hi[2], hi[3])};
         } else {
-          const int c = (wn * G::FN + i + (fc & 1)) * 16 + 8 * (fc >> 1);
-          const uint32_t off = r < live && t.n0 + c < p.K ? ((uint32_t)r * (uint32_t)p.K + (uint32_t)c) * 2u : OFF_NONE;
-          if (p.accumulate) {
-            // in fp32 before the one rounding
-            f32x4 lo, hi;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[i][j][q]), __float_as_uint(acc[i + 1][j][q]), false, false);
-              lo[q] = __uint_as_float(s[0]);
-              hi[q] = __uint_as_float(s[1]);
-            }
-            float old[8];
-            widen8(bload(ro, off), old);
-            __builtin_amdgcn_raw_buffer_store_b128(u32x4{pack2(lo[0] + old[0], lo[1] + old[1]), pack2(lo[2] + old[2], lo[3] + old[3]),
-                                                         pack2(hi[0] + old[4], hi[1] + old[5]), pack2(hi[2] + old[6], hi[3] + old[7])},
-                                                   ro, (int)off, 0, 0);
-          } else {
-            const auto lo = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][0], acc[i][j][1]),
-                                                             pack2(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
-            const auto hi = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][2], acc[i][j][3]),
-                                                             pack2(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
-            __builtin_amdgcn_raw_buffer_store_b128(u32x4{lo[0], hi[0], lo[1], hi[1]}, ro, (int)off, 0, 0);
-          }
+          const int i = 2 * q;
+          const auto lo = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][0], acc[i][j][1]),
+                                                           pack2(acc[i + 1][j][0], acc[i + 1][j][1]), false, false);
+          const auto hi = __builtin_amdgcn_permlane16_swap(pack2(acc[i][j][2], acc[i][j][3]),
+                                                           pack2(acc[i + 1][j][2], acc[i + 1][j][3]), false, false);
+          w = u32x4{lo[0], hi[0], lo[1], hi[1]};
         }
+        __builtin_amdgcn_raw_buffer_store_b128(w, ro, (int)place(q), 0, 0);
       }
     }
   }
