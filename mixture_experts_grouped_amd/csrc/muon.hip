@@ -84,38 +84,69 @@ struct Four {
       v = u32x2{pack2(x[0], x[1]), pack2(x[2], x[3])};
   }
 };
-// VEC: groups of four are whole and aligned.  What is not there is read from
-// `safe`, without a branch, and masked by the caller.
+// A tensor's part of the long side, a chunk at a time.  VEC: groups of four are
+// whole and a matrix is within 2 GB (fewer than 2^29 elements): they go through a
+// buffer descriptor, which reads zeros for and does not write what is not there,
+// so that nothing branches and the loads in flight stay countable.  Else element
+// by element: what is not there is read from the tensor's start, without a branch,
+// and masked by the caller.
 template <bool VEC, class T>
-__device__ __forceinline__ void load4(Four<T>& f, const T* base, int at, int have, const T* safe) {
-  if constexpr (VEC) {
-    f.v = *(const decltype(f.v)*)(have > 0 ? base + at : safe);
-  } else if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f.v[e] = *(e < have ? base + at + e : safe);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      f.v[e] = (uint32_t)*(2 * e < have ? base + at + 2 * e : safe) | (uint32_t)*(2 * e + 1 < have ? base + at + 2 * e + 1 : safe) << 16;
+struct Part {
+  T* base;
+  const T* safe;
+  long left;  // elements from base to the matrix's end
+  rsrc_t r;
+  __device__ __forceinline__ void init(const T* tensor, long matrix, long size, long at) {
+    base = const_cast<T*>(tensor) + matrix + at;
+    safe = tensor;
+    left = size - at;
+    next(0);
   }
-}
-template <bool VEC, class T>
-__device__ __forceinline__ void store4(T* base, int at, int have, f32x4 x) {
-  Four<T> f;
-  f.set(x);
-  if constexpr (VEC) {
-    if (have > 0) *(decltype(f.v)*)(base + at) = f.v;
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < have) {
-        if constexpr (sizeof(T) == 4)
-          base[at + e] = f.v[e];
-        else
-          base[at + e] = (T)(f.v[e >> 1] >> (16 * (e & 1)));
-      }
+  __device__ __forceinline__ void next(long step) {
+    base += step;
+    left -= step;
+    if constexpr (VEC) r = make_rsrc(base, left > 0 ? (uint64_t)left * sizeof(T) : 0);
   }
-}
+  // (none: past the extent of either type, 2^30 bytes for two a piece)
+  __device__ __forceinline__ static int place(int at, int have) {
+    return have > 0 ? at * (int)sizeof(T) : (int)(OFF_NONE / (4 / sizeof(T)));
+  }
+  __device__ __forceinline__ void load(Four<T>& f, int at, int have) const {
+    if constexpr (VEC) {
+      if constexpr (sizeof(T) == 4)
+        f.v = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(r, place(at, have), 0, 0));
+      else
+        f.v = __builtin_amdgcn_raw_buffer_load_b64(r, place(at, have), 0, 0);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f.v[e] = *(e < have ? base + at + e : safe);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        f.v[e] = (uint32_t)*(2 * e < have ? base + at + 2 * e : safe) |
+                 (uint32_t)*(2 * e + 1 < have ? base + at + 2 * e + 1 : safe) << 16;
+    }
+  }
+  __device__ __forceinline__ void store(int at, int have, f32x4 x) const {
+    Four<T> f;
+    f.set(x);
+    if constexpr (VEC) {
+      if constexpr (sizeof(T) == 4)
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f.v), r, place(at, have), 0, 0);
+      else
+        __builtin_amdgcn_raw_buffer_store_b64(f.v, r, place(at, have), 0, 0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < have) {
+          if constexpr (sizeof(T) == 4)
+            base[at + e] = f.v[e];
+          else
+            base[at + e] = (T)(f.v[e >> 1] >> (16 * (e & 1)));
+        }
+    }
+  }
+};
 
 // What a thread moves of each chunk (CHUNK entries of the long side): groups of
 // four neighbours in memory.  A chunk lies in LDS as in memory: [l][c] of a tall
@@ -125,31 +156,32 @@ struct Share {
   static constexpr int CHUNK = CHUNK_, PITCH = PITCH_, N = cmax(RB * CHUNK / (4 * NT), 1);
   // LDS steps along the short and the long side
   static constexpr int KS = TALL ? 1 : PITCH, LS = TALL ? PITCH : 1;
-  int lds[N];   // LDS place, -1: none
-  int live[N];  // tall: entries of the short side from here on, and 2^16 times the long side's; wide: of the chunk from here on
-  int at[N];    // element in the chunk (a matrix has fewer than 2^31)
+  static constexpr int SIZE = (TALL ? CHUNK : RB) * PITCH;  // elements in LDS; four more behind them for what is nowhere
+  int lds[N];    // LDS place
+  int first[N];  // the group's first entry of the chunk's long side (2^30: it is not there)
+  int live[N];   // tall: entries of the short side from here on
+  int at[N];     // element in the chunk (a matrix has fewer than 2^31)
   __device__ __forceinline__ void init(const MuonTensor& t) {
     const int B = TALL ? t.R : CHUNK, A = TALL ? CHUNK : t.R;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int g = threadIdx.x + i * NT, a = g / (B / 4), b = 4 * (g - a * (B / 4));
-      const bool have0 = a < A && (TALL ? b < t.r : a < t.r);
-      lds[i] = a < A ? a * PITCH + b : -1;
-      at[i] = have0 ? a * (TALL ? t.r : t.L) + b : 0;
-      if (TALL)
-        live[i] = have0 ? (t.r - b) + (a << 16) : 0;
-      else
-        live[i] = have0 ? CHUNK - b : 0;
+      const bool there = a < A && (TALL ? b < t.r : a < t.r);
+      lds[i] = a < A ? a * PITCH + b : SIZE;
+      at[i] = there ? a * (TALL ? t.r : t.L) + b : 0;
+      first[i] = there ? (TALL ? a : b) : 1 << 30;
+      live[i] = t.r - b;
     }
   }
   // elements from one chunk to the next
   __device__ __forceinline__ static long step(const MuonTensor& t) { return TALL ? (long)CHUNK * t.r : CHUNK; }
   // of group i, the elements there are in a chunk with `left` entries
   __device__ __forceinline__ int have(int i, int left) const {
-    if (TALL) return (live[i] >> 16) < left ? live[i] & 0xffff : 0;
-    return live[i] > 0 ? left - (CHUNK - live[i]) : 0;
+    return TALL ? (first[i] < left ? live[i] : 0) : left - first[i];
   }
+  template <bool VEC>
   __device__ __forceinline__ static f32x4 only(f32x4 x, int have) {
+    if constexpr (VEC) return x;  // zeros were read
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] = e < have ? x[e] : 0.0f;
     return x;
@@ -196,16 +228,18 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
   sh.init(t);
   const int l_begin = s * t.span;
   int left = min(t.L - l_begin, t.span);
-  const long at = mat * (long)t.r * t.L + (TALL ? (long)l_begin * t.r : l_begin);
-  const GT* g = (const GT*)t.grad + at;
-  float* mo = t.momentum + at;
+  const long size = (long)t.r * t.L, at = TALL ? (long)l_begin * t.r : l_begin;
+  Part<VEC, GT> g;
+  Part<VEC, float> mo;
+  g.init((const GT*)t.grad, mat * size, size, at);
+  mo.init(t.momentum, mat * size, size, at);
   Four<GT> gv[Sh::N];
   Four<float> mv[Sh::N];
   auto fetch = [&](int have) {
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      load4<VEC>(gv[i], g, sh.at[i], sh.have(i, have), (const GT*)t.grad);
-      load4<VEC>(mv[i], mo, sh.at[i], sh.have(i, have), t.momentum);
+      g.load(gv[i], sh.at[i], sh.have(i, have));
+      mo.load(mv[i], sh.at[i], sh.have(i, have));
     }
   };
   f64x4 acc[cmax(N, 1)];
@@ -231,38 +265,30 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
         m[e] = fmaf(p.momentum, m[e], y);
         u[e] = p.nesterov ? fmaf(p.momentum, m[e], y) : m[e];
       }
-      store4<VEC>(mo, sh.at[i], sh.have(i, left), m);
-      u = Sh::only(u, sh.have(i, left));
-      if (sh.lds[i] >= 0) {
-        typedef double f64x2 __attribute__((ext_vector_type(2)));
-        *(f64x2*)(S + sh.lds[i]) = f64x2{u[0], u[1]};
-        *(f64x2*)(S + sh.lds[i] + 2) = f64x2{u[2], u[3]};
-      }
+      mo.store(sh.at[i], sh.have(i, left), m);
+      u = Sh::template only<VEC>(u, sh.have(i, left));
+      typedef double f64x2 __attribute__((ext_vector_type(2)));
+      *(f64x2*)(S + sh.lds[i]) = f64x2{u[0], u[1]};
+      *(f64x2*)(S + sh.lds[i] + 2) = f64x2{u[2], u[3]};
     }
     __syncthreads();
-    g += Sh::step(t);
-    mo += Sh::step(t);
-    if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
+    g.next(Sh::step(t));
+    mo.next(Sh::step(t));
+    fetch(left - Sh::CHUNK);
+    __builtin_amdgcn_sched_barrier(0);
     if constexpr (N > 0) {
-      // a pair's operands of the next step are read behind its product
-      double x[2][N], y[2][N];
+      // operands are read D products ahead
+      constexpr int D = N < 6 ? N : 6, STEPS = Sh::CHUNK / 4 * N;
+      double x[D], y[D];
 #pragma unroll
-      for (int q = 0; q < N; ++q) {
-        x[0][q] = S[xi[q]];
-        y[0][q] = S[yj[q]];
-      }
-#pragma unroll
-      for (int k4 = 0; k4 < Sh::CHUNK; k4 += 4) {
-        const int b = (k4 >> 2) & 1;
-#pragma unroll
-        for (int q = 0; q < N; ++q) {
-          acc[q] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[b][q], y[b][q], acc[q], 0, 0, 0);
-          if (k4 + 4 < Sh::CHUNK) {
-            x[b ^ 1][q] = S[xi[q] + (k4 + 4) * Sh::LS];
-            y[b ^ 1][q] = S[yj[q] + (k4 + 4) * Sh::LS];
-          }
-          __builtin_amdgcn_sched_barrier(0);
+      for (int n = -D; n < STEPS; ++n) {
+        const int b = (n + D) % D;
+        if (n >= 0) acc[n % N] = __builtin_amdgcn_mfma_f64_16x16x4f64(x[b], y[b], acc[n % N], 0, 0, 0);
+        if (n + D < STEPS) {
+          x[b] = S[xi[(n + D) % N] + (n + D) / N * 4 * Sh::LS];
+          y[b] = S[yj[(n + D) % N] + (n + D) / N * 4 * Sh::LS];
         }
+        if (n >= 0) __builtin_amdgcn_sched_barrier(0);
       }
     }
     __syncthreads();
@@ -653,9 +679,12 @@ __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x
 }
 
 // Q U for a part of the long side, and the parameters.  A wave keeps its columns
-// of Q in registers; the results go back to where U was in LDS, so that the
-// parameters are read and written in the order of memory.
-template <class PT, class GT, int RB, bool TALL, bool VEC>
+// of Q in registers; the results go through LDS, so that the parameters are read
+// and written in the order of memory.  The next chunk's gradient and momentum and
+// this one's parameters are in flight behind the products.
+// XT: what is updated, the master copy (then `param`, bf16, gets its rounding) or
+// the parameter itself.
+template <class XT, bool COPY, class GT, int RB, bool TALL, bool VEC>
 __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, long mat, int s, float* S) {
   using Sh = Share<RB, TALL, apply_chunk(RB), apply_pitch(RB, TALL)>;
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
@@ -672,19 +701,22 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
   sh.init(t);
   const int l_begin = s * t.span;
   int left = min(t.L - l_begin, t.span);
-  const bool masters = t.master != nullptr;
-  const long at = mat * (long)t.r * t.L + (TALL ? (long)l_begin * t.r : l_begin);
-  const GT* g = (const GT*)t.grad + at;
-  const float* mo = t.momentum + at;
-  float* ma = t.master + at;  // used where there are masters
-  PT* pa = (PT*)t.param + at;
+  const long size = (long)t.r * t.L, at = TALL ? (long)l_begin * t.r : l_begin;
+  Part<VEC, GT> g;
+  Part<VEC, float> mo;
+  Part<VEC, XT> xs;
+  Part<VEC, uint16_t> copy;
+  g.init((const GT*)t.grad, mat * size, size, at);
+  mo.init(t.momentum, mat * size, size, at);
+  xs.init(COPY ? (const XT*)t.master : (const XT*)t.param, mat * size, size, at);
+  if (COPY) copy.init((const uint16_t*)t.param, mat * size, size, at);
   Four<GT> gv[Sh::N];
   Four<float> mv[Sh::N];
   auto fetch = [&](int have) {
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      load4<VEC>(gv[i], g, sh.at[i], sh.have(i, have), (const GT*)t.grad);
-      load4<VEC>(mv[i], mo, sh.at[i], sh.have(i, have), (const float*)t.momentum);
+      g.load(gv[i], sh.at[i], sh.have(i, have));
+      mo.load(mv[i], sh.at[i], sh.have(i, have));
     }
   };
   fetch(left);
@@ -698,77 +730,83 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
         const int row = 16 * kt + 4 * e + (lane >> 4), col = 16 * (wi + WI * i) + (lane & 15);
         q[i][kt][e] = kt < nt && wi + WI * i < nt ? t.q[mat * (long)t.R * t.R + (long)row * t.R + col] : 0.0f;
       }
+  // rows past the short side are multiplied by zeros of Q and must be finite
+  float* O = S + Sh::SIZE + 4;
+  for (int i = threadIdx.x; i < Sh::SIZE; i += NT) S[i] = 0.0f;
+  __syncthreads();
   const float* Sf = S + (lane >> 4) * Sh::KS + (lane & 15) * Sh::LS + 16 * wj * Sh::LS;
   for (; left > 0; left -= Sh::CHUNK) {
-    Four<float> mav[Sh::N];
-    Four<PT> pav[Sh::N];
+    Four<XT> xv[Sh::N];
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      const int have = sh.have(i, left);
       const f32x4 x = gv[i].get(), m = mv[i].get();
       f32x4 u;
 #pragma unroll
       for (int e = 0; e < 4; ++e) u[e] = p.nesterov ? fmaf(p.momentum, m[e], x[e] * gs) : m[e];
-      if (sh.lds[i] >= 0) *(f32x4*)(S + sh.lds[i]) = Sh::only(u, have);
-      if (masters)
-        load4<VEC>(mav[i], (const float*)ma, sh.at[i], have, (const float*)t.master);
-      else
-        load4<VEC>(pav[i], (const PT*)pa, sh.at[i], have, (const PT*)t.param);
+      *(f32x4*)(S + sh.lds[i]) = Sh::template only<VEC>(u, sh.have(i, left));
     }
+#pragma unroll
+    for (int i = 0; i < Sh::N; ++i) xs.load(xv[i], sh.at[i], sh.have(i, left));
     __syncthreads();
-    g += Sh::step(t);
-    mo += Sh::step(t);
-    if (left > Sh::CHUNK) fetch(left - Sh::CHUNK);
+    g.next(Sh::step(t));
+    mo.next(Sh::step(t));
+    fetch(left - Sh::CHUNK);
+    __builtin_amdgcn_sched_barrier(0);
     f32x4 acc[IW][JW];
 #pragma unroll
     for (int i = 0; i < IW; ++i)
 #pragma unroll
       for (int j = 0; j < JW; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // a lane's four results are neighbours in memory: along the short side where the tensor is tall
+    // operands are read two steps ahead
+    auto blocks = [&](auto lo, auto hi) {
+      constexpr int FROM = 4 * lo.value, TO = 4 * hi.value;
+      float y[4][JW];
 #pragma unroll
-    for (int kt = 0; kt < KT; ++kt)
-      if (kt < nt)
+      for (int k = FROM - 2; k < TO; ++k) {
+        if (k + 2 < TO)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float y[JW];
+          for (int j = 0; j < JW; ++j) y[(k + 2) & 3][j] = Sf[4 * (k + 2) * Sh::KS + 16 * j * Sh::LS];
+        if (k < FROM) continue;
 #pragma unroll
-          for (int j = 0; j < JW; ++j) y[j] = Sf[(16 * kt + 4 * e) * Sh::KS + 16 * j * Sh::LS];
-          // a lane's four results are neighbours in memory: along the short side where the tensor is tall
+        for (int i = 0; i < IW; ++i)
 #pragma unroll
-          for (int i = 0; i < IW; ++i)
-#pragma unroll
-            for (int j = 0; j < JW; ++j)
-              acc[i][j] = TALL ? __builtin_amdgcn_mfma_f32_16x16x4f32(q[i][kt][e], y[j], acc[i][j], 0, 0, 0)
-                               : __builtin_amdgcn_mfma_f32_16x16x4f32(y[j], q[i][kt][e], acc[i][j], 0, 0, 0);
-        }
-    __syncthreads();
+          for (int j = 0; j < JW; ++j)
+            acc[i][j] = TALL ? __builtin_amdgcn_mfma_f32_16x16x4f32(q[i][k / 4][k % 4], y[k & 3][j], acc[i][j], 0, 0, 0)
+                             : __builtin_amdgcn_mfma_f32_16x16x4f32(y[k & 3][j], q[i][k / 4][k % 4], acc[i][j], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+    // short sides that come here have more than half of RB: few branches, for long runs between them
+    constexpr int K1 = KT / 2 + KT % 2 + (KT > 2 ? 1 : 0), K2 = cmax(K1, KT * 3 / 4);
+    blocks(std::integral_constant<int, 0>{}, std::integral_constant<int, K1>{});
+    if (K2 > K1 && nt > K1) blocks(std::integral_constant<int, K1>{}, std::integral_constant<int, K2>{});
+    if (KT > K2 && nt > K2) blocks(std::integral_constant<int, K2>{}, std::integral_constant<int, KT>{});
 #pragma unroll
     for (int i = 0; i < IW; ++i)
 #pragma unroll
-      for (int j = 0; j < JW; ++j)
-        if (wi + WI * i < nt) {
-          const int c = 16 * (wi + WI * i), l = 16 * (wj + j);
-          const int a = TALL ? l : c, b = TALL ? c : l;
-          *(f32x4*)(S + (a + (lane & 15)) * Sh::PITCH + b + 4 * (lane >> 4)) = acc[i][j];
-        }
+      for (int j = 0; j < JW; ++j) {
+        const int c = 16 * (wi + WI * i), l = 16 * (wj + j);
+        const int a = TALL ? l : c, b = TALL ? c : l;
+        if (KT >= WI || wi < KT) *(f32x4*)(O + (a + (lane & 15)) * Sh::PITCH + b + 4 * (lane >> 4)) = acc[i][j];
+      }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < Sh::N; ++i) {
-      if (sh.lds[i] < 0) continue;
       const int have = sh.have(i, left);
-      const f32x4 o = *(const f32x4*)(S + sh.lds[i]);
-      f32x4 x = masters ? mav[i].get() : pav[i].get();
+      const f32x4 o = *(const f32x4*)(O + sh.lds[i]);
+      f32x4 x = xv[i].get();
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] -= fmaf(step, o[e], decay * x[e]);
-      if (masters) store4<VEC>(ma, sh.at[i], have, x);
-      store4<VEC>(pa, sh.at[i], have, x);
+      xs.store(sh.at[i], have, x);
+      if (COPY) copy.store(sh.at[i], have, x);
     }
-    __syncthreads();
-    pa += Sh::step(t);
-    ma += Sh::step(t);
+    xs.next(Sh::step(t));
+    if (COPY) copy.next(Sh::step(t));
   }
 }
 
-template <class PT, class GT, int RB, bool VEC>
+template <class XT, bool COPY, class GT, int RB, bool VEC>
 __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p) {
   extern __shared__ __align__(16) char smem[];
   int ti, s;
@@ -776,9 +814,9 @@ __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p
   find(p, blockIdx.x, ti, mat, s);
   const MuonTensor& t = p.t[ti];
   if (t.tall)
-    apply<PT, GT, RB, true, VEC>(p, t, mat, s, (float*)smem);
+    apply<XT, COPY, GT, RB, true, VEC>(p, t, mat, s, (float*)smem);
   else
-    apply<PT, GT, RB, false, VEC>(p, t, mat, s, (float*)smem);
+    apply<XT, COPY, GT, RB, false, VEC>(p, t, mat, s, (float*)smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -837,9 +875,11 @@ Plan plan_of(const moe_muon_tensor& t, int span) {
   return p;
 }
 
-// LDS of a chunk of U for short sides up to RB, either way round
-constexpr int gram_lds(int RB) { return cmax(gram_pitch(RB, true) * gram_chunk(RB), gram_pitch(RB, false) * RB) * 8; }
-constexpr int apply_lds(int RB) { return cmax(apply_pitch(RB, true) * apply_chunk(RB), apply_pitch(RB, false) * RB) * 4; }
+// LDS for short sides up to RB, either way round: a chunk of U (and of Q U), with what is nowhere behind it
+constexpr int gram_lds(int RB) { return (cmax(gram_pitch(RB, true) * gram_chunk(RB), gram_pitch(RB, false) * RB) + 4) * 8; }
+constexpr int apply_lds(int RB) {
+  return (cmax(apply_pitch(RB, true) * apply_chunk(RB), apply_pitch(RB, false) * RB) + 4) * 2 * 4;
+}
 
 template <class GT, int RB, bool VEC>
 hipError_t launch_gram(const MuonArgs& p, hipStream_t st) {
@@ -853,16 +893,17 @@ hipError_t launch_gram(const MuonArgs& p, hipStream_t st) {
   MOE_LAUNCH_AS("k_muon_gram", (k_muon_gram<GT, RB, VEC>), dim3((unsigned)p.groups), dim3(NT), gram_lds(RB), st, p);
   return hipGetLastError();
 }
-template <class PT, class GT, int RB, bool VEC>
+template <class XT, bool COPY, class GT, int RB, bool VEC>
 hipError_t launch_apply(const MuonArgs& p, hipStream_t st) {
   static PerDeviceOnce once;
   const hipError_t e = once.run([] {
     AttrInit ai;
-    ai.lds((const void*)k_muon_apply<PT, GT, RB, VEC>, apply_lds(RB));
+    ai.lds((const void*)k_muon_apply<XT, COPY, GT, RB, VEC>, apply_lds(RB));
     return ai.err;
   });
   if (e != hipSuccess) return e;
-  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<PT, GT, RB, VEC>), dim3((unsigned)p.groups), dim3(NT), apply_lds(RB), st, p);
+  MOE_LAUNCH_AS("k_muon_apply", (k_muon_apply<XT, COPY, GT, RB, VEC>), dim3((unsigned)p.groups), dim3(NT), apply_lds(RB),
+                st, p);
   return hipGetLastError();
 }
 template <int B>
@@ -916,14 +957,19 @@ hipError_t launch_long_rounds(const MuonArgs& p, int R, hipStream_t st) {
 }
 
 // All tensors of p have short sides of R (in whole tiles) and are VEC or not.
-template <int RB, bool VEC>
-hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t st) {
-  hipError_t e = gbf ? launch_gram<uint16_t, RB, VEC>(p, st) : launch_gram<float, RB, VEC>(p, st);
+template <class GT, int RB, bool VEC>
+hipError_t launch_step(const MuonArgs& p, int R, bool pbf, hipStream_t st) {
+  hipError_t e = launch_gram<GT, RB, VEC>(p, st);
   if (e != hipSuccess) return e;
   e = R <= SHORT_R ? launch_rounds<SHORT_R / 16>(p, R, st) : launch_long_rounds(p, R, st);
   if (e != hipSuccess) return e;
-  if (pbf) return gbf ? launch_apply<uint16_t, uint16_t, RB, VEC>(p, st) : launch_apply<uint16_t, float, RB, VEC>(p, st);
-  return gbf ? launch_apply<float, uint16_t, RB, VEC>(p, st) : launch_apply<float, float, RB, VEC>(p, st);
+  if (!pbf) return launch_apply<float, false, GT, RB, VEC>(p, st);
+  return p.t[0].master != nullptr ? launch_apply<float, true, GT, RB, VEC>(p, st)
+                                  : launch_apply<uint16_t, false, GT, RB, VEC>(p, st);
+}
+template <int RB, bool VEC>
+hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t st) {
+  return gbf ? launch_step<uint16_t, RB, VEC>(p, R, pbf, st) : launch_step<float, RB, VEC>(p, R, pbf, st);
 }
 template <bool VEC>
 hipError_t launch_step(const MuonArgs& p, int R, bool pbf, bool gbf, hipStream_t st) {
@@ -1017,7 +1063,8 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
         const moe_muon_tensor& x = t[i];
         if (x.batch == 0) continue;
         const bool tall = x.m > x.n;
-        if (round16(tall ? x.n : x.m) != R || (x.n % 4 == 0) != (vec != 0)) continue;
+        const bool whole = x.n % 4 == 0 && (int64_t)x.m * x.n < (int64_t)1 << 29;  // see Part
+        if (round16(tall ? x.n : x.m) != R || whole != (vec != 0)) continue;
         const Plan pl = plan_of(x, span);
         // a launch holds fewer than 2^32 threads; long rounds take 17 workgroups a matrix
         if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23 ||
