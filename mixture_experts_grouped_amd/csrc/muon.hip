@@ -156,7 +156,7 @@ struct Share {
   static constexpr int CHUNK = CHUNK_, PITCH = PITCH_, N = cmax(RB * CHUNK / (4 * NT), 1);
   // LDS steps along the short and the long side
   static constexpr int KS = TALL ? 1 : PITCH, LS = TALL ? PITCH : 1;
-  static constexpr int SIZE = (TALL ? CHUNK : RB) * PITCH;  // elements in LDS; four more behind them for what is nowhere
+  static constexpr int SIZE = (TALL ? CHUNK : RB) * PITCH;  // elements in LDS; a lane's four more behind them for what is nowhere
   int lds[N];    // LDS place
   int first[N];  // the group's first entry of the chunk's long side (2^30: it is not there)
   int live[N];   // tall: entries of the short side from here on
@@ -167,7 +167,7 @@ struct Share {
     for (int i = 0; i < N; ++i) {
       const int g = threadIdx.x + i * NT, a = g / (B / 4), b = 4 * (g - a * (B / 4));
       const bool there = a < A && (TALL ? b < t.r : a < t.r);
-      lds[i] = a < A ? a * PITCH + b : SIZE;
+      lds[i] = a < A ? a * PITCH + b : SIZE + 4 * (threadIdx.x & 63);
       at[i] = there ? a * (TALL ? t.r : t.L) + b : 0;
       first[i] = there ? (TALL ? a : b) : 1 << 30;
       live[i] = t.r - b;
@@ -190,9 +190,9 @@ struct Share {
 // Entries of the long side in LDS at a time, and pitches that keep the operands'
 // reads free of bank conflicts: S0 reads doubles, 16 of the short side by 4 of the
 // long side; Q U reads floats, 16 of the long side by 4 of the short side.
-__device__ __host__ constexpr int gram_chunk(int RB) { return RB <= 128 ? 64 : 32; }
+__device__ __host__ constexpr int gram_chunk(int RB) { return RB <= 16 ? 128 : RB <= 128 ? 64 : 32; }
 __device__ __host__ constexpr int gram_pitch(int RB, bool tall) { return tall ? (RB + 15) / 32 * 32 + 16 : gram_chunk(RB) + 2; }
-__device__ __host__ constexpr int apply_chunk(int RB) { return RB <= 64 ? 64 : 32; }
+__device__ __host__ constexpr int apply_chunk(int RB) { return RB <= 16 ? 128 : RB <= 64 ? 64 : 32; }
 __device__ __host__ constexpr int apply_pitch(int RB, bool tall) { return tall ? (RB + 43) / 64 * 64 + 20 : apply_chunk(RB) + 16; }
 
 // Tile t of the lower triangle of tiles.
@@ -224,6 +224,8 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
   const float gs = p.control != nullptr ? p.control->grad_scale : p.grad_scale;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int tiles = tri_tiles(t.R / 16);
+  constexpr bool ALONG = RB <= 16;                         // one tile: the waves share its chunk
+  constexpr int PART = ALONG ? Sh::CHUNK / NW : Sh::CHUNK;  // entries of a chunk that a wave multiplies
   Sh sh;
   sh.init(t);
   const int l_begin = s * t.span;
@@ -247,8 +249,8 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
 #pragma unroll
   for (int q = 0; q < N; ++q) {
     int i = 0, j = 0;
-    if (w + NW * q < tiles) tri(w + NW * q, i, j);
-    const int lo = (lane >> 4) * Sh::LS + (lane & 15) * Sh::KS;
+    if (!ALONG && w + NW * q < tiles) tri(w + NW * q, i, j);
+    const int lo = (lane >> 4) * Sh::LS + (lane & 15) * Sh::KS + (ALONG ? w * PART * Sh::LS : 0);
     xi[q] = lo + 16 * i * Sh::KS;
     yj[q] = lo + 16 * j * Sh::KS;
     acc[q] = f64x4{0.0, 0.0, 0.0, 0.0};
@@ -278,7 +280,7 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
     __builtin_amdgcn_sched_barrier(0);
     if constexpr (N > 0) {
       // operands are read D products ahead
-      constexpr int D = N < 6 ? N : 6, STEPS = Sh::CHUNK / 4 * N;
+      constexpr int D = N < 4 ? 4 : N < 6 ? N : 6, STEPS = PART / 4 * N;
       double x[D], y[D];
 #pragma unroll
       for (int n = -D; n < STEPS; ++n) {
@@ -294,6 +296,18 @@ __device__ __forceinline__ void gram(const MuonArgs& p, const MuonTensor& t, lon
     __syncthreads();
   }
   double* out = t.part + part_at(t, mat) + s * (long)(tiles * 256);
+  if constexpr (ALONG) {
+#pragma unroll
+    for (int v = 0; v < 4; ++v) S[w * 256 + v * 64 + lane] = acc[0][v];
+    __syncthreads();
+    if (threadIdx.x < 256) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < NW; ++i) sum += S[i * 256 + threadIdx.x];
+      out[threadIdx.x] = sum;
+    }
+    return;
+  }
 #pragma unroll
   for (int q = 0; q < N; ++q)
     if (w + NW * q < tiles)
@@ -304,8 +318,7 @@ template <class GT, int RB, bool TALL, bool VEC>
 __device__ __forceinline__ void gram_of(const MuonArgs& p, const MuonTensor& t, long mat, int s, double* S) {
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = (tri_tiles(t.R / 16) - w + NW - 1) / NW;
   if constexpr (RB <= 16) {
-    if (n >= 1) gram<GT, RB, TALL, VEC, 1>(p, t, mat, s, S);
-    else gram<GT, RB, TALL, VEC, 0>(p, t, mat, s, S);
+    gram<GT, RB, TALL, VEC, 1>(p, t, mat, s, S);
   } else if constexpr (RB <= 64) {
     if (n >= 2) gram<GT, RB, TALL, VEC, 2>(p, t, mat, s, S);
     else if (n == 1) gram<GT, RB, TALL, VEC, 1>(p, t, mat, s, S);
@@ -731,7 +744,7 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
         q[i][kt][e] = kt < nt && wi + WI * i < nt ? t.q[mat * (long)t.R * t.R + (long)row * t.R + col] : 0.0f;
       }
   // rows past the short side are multiplied by zeros of Q and must be finite
-  float* O = S + Sh::SIZE + 4;
+  float* O = S + Sh::SIZE + 256;
   for (int i = threadIdx.x; i < Sh::SIZE; i += NT) S[i] = 0.0f;
   __syncthreads();
   const float* Sf = S + (lane >> 4) * Sh::KS + (lane & 15) * Sh::LS + 16 * wj * Sh::LS;
@@ -811,7 +824,8 @@ __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p
   extern __shared__ __align__(16) char smem[];
   int ti, s;
   long mat;
-  find(p, blockIdx.x, ti, mat, s);
+  // backwards: what the first pass read last may still be in the memory-side cache (wide: 208 -> 190 us)
+  find(p, p.groups - 1 - blockIdx.x, ti, mat, s);
   const MuonTensor& t = p.t[ti];
   if (t.tall)
     apply<XT, COPY, GT, RB, true, VEC>(p, t, mat, s, (float*)smem);
@@ -876,9 +890,9 @@ Plan plan_of(const moe_muon_tensor& t, int span) {
 }
 
 // LDS for short sides up to RB, either way round: a chunk of U (and of Q U), with what is nowhere behind it
-constexpr int gram_lds(int RB) { return (cmax(gram_pitch(RB, true) * gram_chunk(RB), gram_pitch(RB, false) * RB) + 4) * 8; }
+constexpr int gram_lds(int RB) { return (cmax(gram_pitch(RB, true) * gram_chunk(RB), gram_pitch(RB, false) * RB) + 256) * 8; }
 constexpr int apply_lds(int RB) {
-  return (cmax(apply_pitch(RB, true) * apply_chunk(RB), apply_pitch(RB, false) * RB) + 4) * 2 * 4;
+  return (cmax(apply_pitch(RB, true) * apply_chunk(RB), apply_pitch(RB, false) * RB) + 256) * 2 * 4;
 }
 
 template <class GT, int RB, bool VEC>
