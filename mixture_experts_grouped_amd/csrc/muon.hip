@@ -208,7 +208,7 @@ __device__ __host__ constexpr int tri_tiles(int n) { return n * (n + 1) / 2; }
 constexpr int SHORT_R = 128;   // up to here the rounds run in LDS
 constexpr int LONG_SLOTS = 6;  // beyond, they have matrices behind the partial sums
 __device__ __host__ constexpr long part_size(int R, int splits) {
-  return (long)splits * tri_tiles(R / 16) * 256 + (R > SHORT_R ? (long)LONG_SLOTS * R * R : 0);
+  return (long)splits * tri_tiles(R / 16) * 256 + (R > SHORT_R ? (long)LONG_SLOTS * R * R + 2 : 0);
 }
 __device__ __forceinline__ long part_at(const MuonTensor& t, long mat) { return mat * part_size(t.R, t.splits); }
 
@@ -626,37 +626,47 @@ __device__ __forceinline__ const MuonTensor& long_matrix(const MuonArgs& p, long
 __device__ __forceinline__ double* long_slot(const MuonTensor& t, long mat, int slot) {
   return t.part + part_at(t, mat) + t.splits * (long)(tri_tiles(t.R / 16) * 256) + slot * (long)t.R * t.R;
 }
-__device__ __forceinline__ double long_inv(const MuonArgs& p, const MuonTensor& t, long mat) {  // 1 / (|U| + eps), by every wave
-  const long tiles = (long)tri_tiles(t.R / 16) * 256;
-  const double* part = long_slot(t, mat, 0) - t.splits * tiles;
-  double tr = 0.0;
-  for (int c = threadIdx.x & 63; c < t.R; c += 64)
-    for (int s = 0; s < t.splits; ++s) {
-      const int i = c >> 4;
-      tr += part[s * tiles + (tri_tiles(i) + i) * 256 + (c & 15) * 17];
-    }
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
-  return 1.0 / (sqrt(tr) + p.eps);
-}
+// 1 / (|U| + eps), behind a matrix's slots
+__device__ __forceinline__ double* long_inv(const MuonTensor& t, long mat) { return long_slot(t, mat, LONG_SLOTS); }
+
 __global__ __launch_bounds__(NT) void k_muon_long_sum(MuonArgs p, int per) {
+  __shared__ double sums[NW];
   long mat;
   int tile, i, j;
   const MuonTensor& t = long_matrix(p, mat, tile, per);
-  if (tile >= tri_tiles(t.R / 16)) return;
-  tri(tile, i, j);
-  const double inv = long_inv(p, t, mat), inv2 = inv * inv;
+  const int lane = threadIdx.x & 63;
   const long tiles = (long)tri_tiles(t.R / 16) * 256;
   double* S = long_slot(t, mat, 0);
-  const double* part = S - t.splits * tiles + tile * 256;
-  const int lane = threadIdx.x & 63;
+  const double* part = S - t.splits * tiles;
+  // every workgroup adds up the diagonals by itself, in the same order: no launch before this one
+  double tr = 0.0;
+#pragma unroll 8
+  for (int n = threadIdx.x; n < t.splits * t.R; n += NT) {
+    const int s = n / t.R, c = n - s * t.R, d = c >> 4;
+    tr += part[s * tiles + (tri_tiles(d) + d) * 256 + (c & 15) * 17];
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
+  if (lane == 0) sums[threadIdx.x >> 6] = tr;
+  __syncthreads();
+  tr = 0.0;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) tr += sums[w];
+  const double inv = 1.0 / (sqrt(tr) + p.eps), inv2 = inv * inv;
+  if (tile >= tri_tiles(t.R / 16)) return;
+  if (tile == 0) *long_inv(t, mat) = inv;
+  tri(tile, i, j);
+  part += tile * 256;
+  double x[4] = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll 4
+  for (int s = 0; s < t.splits; ++s)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) x[v] += part[s * tiles + v * 64 + lane];
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
-    double x = 0.0;
-    for (int s = 0; s < t.splits; ++s) x += part[s * tiles + v * 64 + lane];
     const int r = 16 * i + 4 * v + (lane >> 4), c = 16 * j + (lane & 15);
-    S[(long)r * t.R + c] = x * inv2;
-    S[(long)c * t.R + r] = x * inv2;
+    S[(long)r * t.R + c] = x[v] * inv2;
+    S[(long)c * t.R + r] = x[v] * inv2;
   }
 }
 // z = fc x y + fb x + fa I (all symmetric); out: to q, over the norm, in fp32
@@ -672,10 +682,21 @@ __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x
   const double* a = X + (long)(lane >> 4) * t.R + 16 * i + (lane & 15);
   const double* b = Y + (long)(lane >> 4) * t.R + 16 * j + (lane & 15);
   f64x4 acc = {0.0, 0.0, 0.0, 0.0};
-  for (int k4 = 0; k4 < t.R; k4 += 4)
-    acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[(long)k4 * t.R], b[(long)k4 * t.R], acc, 0, 0, 0);
+  // the loads of 64 rows at a time in flight (one at a time, a product of 256 x 256 waited 64 times for memory)
+  for (int k0 = 0; k0 < t.R; k0 += 64) {
+    double av[16], bv[16];
+#pragma unroll
+    for (int s = 0; s < 16; ++s) {
+      const long k = k0 + 4 * s < t.R ? k0 + 4 * s : 0;
+      av[s] = a[k * t.R];
+      bv[s] = b[k * t.R];
+    }
+#pragma unroll
+    for (int s = 0; s < 16; ++s)
+      if (k0 + s / 4 * 16 < t.R) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(av[s], bv[s], acc, 0, 0, 0);
+  }
   double* Z = long_slot(t, mat, z);
-  const double inv = out ? long_inv(p, t, mat) : 0.0;
+  const double inv = out ? *long_inv(t, mat) : 0.0;
   float* q = t.q + mat * (long)t.R * t.R;
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
