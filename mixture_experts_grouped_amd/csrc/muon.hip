@@ -859,14 +859,12 @@ __global__ __launch_bounds__(NT, RB <= 128 ? 4 : 2) void k_muon_apply(MuonArgs p
 // ---------------------------------------------------------------------------
 int round16(int r) { return (r + 15) / 16 * 16; }
 
-// Entries of the long side that a workgroup takes: enough workgroups for the
-// chip over all tensors of the call, in whole chunks.
-int span_of(const moe_muon_tensor* t, int32_t count, int cus) {
+// The long sides of all matrices of the call, a CU.
+double share_of(const moe_muon_tensor* t, int32_t count, int cus) {
   double total = 0;
   for (int32_t i = 0; i < count; ++i)
     if (t[i].batch > 0) total += (double)t[i].batch * (t[i].m > t[i].n ? t[i].m : t[i].n);
-  const double span = total / (4.0 * cus);
-  return span < 64 ? 64 : span > 0x1p30 ? 1 << 30 : (int)((span + 63) / 64) * 64;
+  return total / cus;
 }
 
 moe_status check_desc(const moe_muon_desc* d, const moe_muon_tensor* t, int32_t count) {
@@ -898,13 +896,17 @@ struct Plan {
   int r, L, R, splits, span;
   size_t part, q;  // bytes
 };
-Plan plan_of(const moe_muon_tensor& t, int span) {
+Plan plan_of(const moe_muon_tensor& t, double share) {
   Plan p;
   p.r = t.m < t.n ? t.m : t.n;
   p.L = t.m < t.n ? t.n : t.m;
   p.R = round16(p.r);
-  p.span = span;
-  p.splits = (p.L + span - 1) / span;
+  // Entries of the long side that a workgroup takes, in whole chunks: two rounds of two workgroups a CU; beyond
+  // SHORT_R one workgroup a CU, since a part's tiles of S0 weigh more than its U (16 matrices of 256 x 4096: 64 parts
+  // of each 811 us, 16 of each 637)
+  const double span = p.R > SHORT_R ? share : share / 4;
+  p.span = span < 64 ? 64 : span > 0x1p30 ? 1 << 30 : (int)((span + 63) / 64) * 64;
+  p.splits = (p.L + p.span - 1) / p.span;
   p.part = (size_t)t.batch * part_size(p.R, p.splits) * 8;
   p.q = ((size_t)t.batch * p.R * p.R * 4 + 15) / 16 * 16;
   return p;
@@ -1027,11 +1029,11 @@ moe_status moe_muon_workspace_size(const moe_muon_desc* d, const moe_muon_tensor
   if (s != MOE_OK) return s;
   int cus = 0;
   if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
-  const int span = span_of(t, count, cus);
+  const double share = share_of(t, count, cus);
   size_t n = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].batch == 0) continue;
-    const Plan p = plan_of(t[i], span);
+    const Plan p = plan_of(t[i], share);
     n += p.part + p.q;
   }
   *bytes = n;
@@ -1066,7 +1068,7 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
   if (workspace_bytes < need) return MOE_ERR_WORKSPACE;
   int cus = 0;
   if (device_cus(cus) != hipSuccess) return MOE_ERR_HIP;
-  const int span = span_of(t, count, cus);
+  const double share = share_of(t, count, cus);
   MuonArgs p{};
   p.nesterov = d->nesterov;
   p.rounds = d->rounds;
@@ -1100,7 +1102,7 @@ moe_status moe_muon_step(const moe_muon_desc* d, const moe_muon_tensor* t, int32
         const bool tall = x.m > x.n;
         const bool whole = x.n % 4 == 0 && (int64_t)x.m * x.n < (int64_t)1 << 29;  // see Part
         if (round16(tall ? x.n : x.m) != R || whole != (vec != 0)) continue;
-        const Plan pl = plan_of(x, span);
+        const Plan pl = plan_of(x, share);
         // a launch holds fewer than 2^32 threads; long rounds take 17 workgroups a matrix
         if (p.count == TENSORS || p.groups + x.batch * pl.splits >= (int64_t)1 << 23 ||
             (R > SHORT_R && p.matrices + x.batch >= (int64_t)1 << 18))
