@@ -8,8 +8,8 @@ with their gradients (``expert_product``, ``expert_weight_grad``), in 8-bit
 floating point (``fp8_quantize_rows``, ``fp8_quantize_weight``,
 ``fp8_product``) and in microscaled 4-bit floating point
 (``mxfp4_quantize_rows``, ``mxfp4_quantize_weight``, ``mxfp4_dequantize``,
-``mxfp4_product``).  This package adds the ctypes binding (``binding``), the build script and the seeded
-synthetic inputs (``inputs``).
+``mxfp4_product``).  This package adds the ctypes binding (``binding``), the
+build script and the seeded synthetic inputs (``inputs``).
 """
 from .binding import (  # noqa: F401
     MoeAdamW, MoeLoraDesc, MoeLoraError, MoeLoraLayer, MoeMuon, MoeRouter, build_pool, expert_product,

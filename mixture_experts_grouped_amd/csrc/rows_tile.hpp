@@ -261,6 +261,19 @@ struct RowsTile {
   }
 };
 
+// 256 x 256 tiles, eight waves of 128 x 64, two buffers refilled in halves: many
+// rows an expert, where an operand's read must feed as many products as the
+// registers hold sums for.  bf16, 98,304 rows of 4096 x 4096: 2,550 us, 1,295
+// TFLOP/s, the rate that the library's 8192^3 product reaches (matrix cores busy 76 %
+// at the power cap's 1.73 GHz; without the results' stores 2,448 us).  Weight stored
+// K-outer (4096 x 2048): 1,390 us, 1,185 TFLOP/s, 65 % at 1.91 GHz: the transposing
+// reads carry half as much an instruction.  4 bits: 900 us, 3,660 TFLOP/s; a block
+// product takes 19 clocks of a SIMD, its operands' reads and refills together 83 % of
+// the same time in LDS; without the exponents' loads 819 us, without the stores 830,
+// without both 744.
+// 64 x 128 tiles, four waves, three buffers, two workgroups a CU: in between, bound
+// by reading the weights (689 tokens, a fifth of the routes dropped, 4096 x 2048: 208
+// us, 5.2 TB/s; 4-bit weights for one token: 12.4 us).
 template <Kind KIND, class G>
 __global__ __launch_bounds__(G::NT) void k_rows_tile(RowsArgs p) {
   extern __shared__ __align__(16) char smem[];
@@ -277,7 +290,8 @@ __global__ __launch_bounds__(G::NT) void k_rows_tile(RowsArgs p) {
 // multiplied.  bf16: an instruction takes 64 bytes of each row in one piece (the
 // order of k inside a stage is free; 16 bytes at a distance of 32: 2 % slower; eight
 // stages in flight: 25 %); 4 bits: 32 bytes a lane, whose two blocks' exponents lie
-// side by side.
+// side by side.  One token, six experts of 4096 x 4096 in bf16: 36.5 us, 5.5 TB/s
+// (non-temporal loads 39); 64-row tiles 41.
 constexpr int FEW_ROWS = 16, FEW_CH = 4;
 template <Kind KIND>
 __global__ __launch_bounds__(64) void k_rows_few(RowsArgs p) {
