@@ -674,7 +674,8 @@ __global__ __launch_bounds__(NT) void k_muon_long_sum(MuonArgs p, int per) {
     S[(long)c * t.R + r] = x[v] * inv2;
   }
 }
-// z = fc x y + fb x + fa I (all symmetric); out: to q, over the norm, in fp32
+// z = fc x y + fb x + fa I (all symmetric; a plain product has fb = fa = 0, a
+// polynomial may have either alone); out: to q, over the norm, in fp32
 __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x, int y, int z, double fc, double fb, double fa, int out) {
   long mat;
   int tile, i, j;
@@ -706,7 +707,8 @@ __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int r = 16 * i + 4 * v + (lane >> 4), c = 16 * j + (lane & 15);
-    const double d = fma(fc, acc[v], fb != 0.0 ? fma(fb, X[(long)r * t.R + c], r == c ? fa : 0.0) : 0.0);
+    const double one = r == c ? fa : 0.0;
+    const double d = fma(fc, acc[v], fb != 0.0 ? fma(fb, X[(long)r * t.R + c], one) : one);
     if (out) {
       q[(long)r * t.R + c] = (float)(d * inv);
       q[(long)c * t.R + r] = (float)(d * inv);
