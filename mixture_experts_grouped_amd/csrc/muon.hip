@@ -42,7 +42,7 @@ struct MuonTensor {
   long first;        // this tensor's first workgroup in a launch over splits
   long matrix0;      // index of its first matrix
   double* part;      // a matrix: partial sums of S0 [splits][lower tiles], then (long short sides) the rounds' matrices
-  float* q;          // [matrices][R][R]
+  float* q;          // a matrix: Q over U's norm [R][R], and what U is multiplied by (see Norm)
   int r, L, tall;    // tall: stored [L, r]
   int R;             // r in whole tiles of 16
   int splits, span;  // workgroups along L, entries each
@@ -204,6 +204,27 @@ __device__ __forceinline__ void tri(int t, int& i, int& j) {
   j = t - i * (i + 1) / 2;
 }
 __device__ __host__ constexpr int tri_tiles(int n) { return n * (n + 1) / 2; }
+
+// 1 / (|U| + eps) in two factors: a power of two for U, in fp32, and the rest for
+// Q before its rounding to fp32.  As one factor of Q it leaves fp32's range where
+// |U| is within a^rounds of either end (a matrix of zeros beside a small eps:
+// infinities times zero).  Powers of two change no result inside the range.
+struct Norm {
+  double all, of_q;  // of_q: 0 for a matrix of zeros, whatever the polynomial's value there
+  float of_u;
+  __device__ __forceinline__ Norm(double squares, double eps) {
+    const double n = sqrt(squares) + eps;
+    all = 1.0 / n;
+    const int e = min(max((int)(__builtin_bit_cast(uint64_t, n) >> 52) - 1023, -126), 126);  // NaN, infinity: 126
+    of_u = __uint_as_float((uint32_t)(127 - e) << 23);
+    const double up = __builtin_bit_cast(double, (uint64_t)(1023 + e) << 52);
+    // infinite squares: S is NaN, and Q has to stay so
+    of_q = squares == 0.0 ? 0.0 : (squares < __builtin_inf() ? all : 1.0) * up;
+  }
+};
+__device__ __forceinline__ float over_norm(double q, double of_q) { return of_q != 0.0 ? (float)(q * of_q) : 0.0f; }
+// A matrix's part of q, in floats.
+__device__ __host__ constexpr long q_size(int R) { return (long)R * R + 4; }
 
 // Where a matrix's part of the workspace begins.
 constexpr int SHORT_R = 128;   // up to here the rounds run in LDS
@@ -387,8 +408,8 @@ __global__ __launch_bounds__(64) void k_muon_rounds16(MuonArgs p) {
   }
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1) tr += __shfl_xor(tr, o, 64);
-  const double inv = 1.0 / (sqrt(tr) + p.eps);
-  S *= inv * inv;
+  const Norm norm(tr, p.eps);
+  S *= norm.all * norm.all;
   for (int n = 0; n < p.rounds; ++n) {
     f64x4 P = mul16(S, S);
 #pragma unroll
@@ -396,9 +417,10 @@ __global__ __launch_bounds__(64) void k_muon_rounds16(MuonArgs p) {
     Q = n == 0 ? P : mul16(P, Q);
     if (n + 1 < p.rounds) S = mul16(mul16(S, P), P);
   }
-  float* out = t.q + mat * 256;
+  float* out = t.q + mat * q_size(16);
 #pragma unroll
-  for (int v = 0; v < 4; ++v) out[v * 64 + lane] = (float)(Q[v] * inv);
+  for (int v = 0; v < 4; ++v) out[v * 64 + lane] = over_norm(Q[v], norm.of_q);
+  if (lane == 0) out[256] = norm.of_u;
 }
 
 // 16 B rows, B from 2 to 8: two matrices as lower tiles of 16 x 16 in LDS, at a
@@ -549,7 +571,8 @@ __global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
   tr = 0.0;
 #pragma unroll
   for (int i = 0; i < NW; ++i) tr += red[i];
-  const double inv = 1.0 / (sqrt(tr) + p.eps), inv2 = inv * inv;
+  const Norm norm(tr, p.eps);
+  const double inv2 = norm.all * norm.all;
 #pragma unroll
   for (int q = 0; q < MT; ++q) z[q] *= inv2;
   put(A, z);
@@ -608,14 +631,15 @@ __global__ __launch_bounds__(NT) void k_muon_rounds(MuonArgs p) {
       what = SS, X = A, Y = A, ++n;
     }
   }
-  float* out = t.q + mat * (long)R * R;
+  float* out = t.q + mat * q_size(R);
+  if (threadIdx.x == 0) out[R * R] = norm.of_u;
 #pragma unroll
   for (int q = 0; q < MT; ++q)
     if (live(q))
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int r = 16 * ti[q] + 4 * v + (lane >> 4), c = 16 * tj[q] + (lane & 15);
-        const float x = (float)(z[q][v] * inv);
+        const float x = over_norm(z[q][v], norm.of_q);
         out[(long)r * R + c] = x;
         out[(long)c * R + r] = x;
       }
@@ -631,8 +655,8 @@ __device__ __forceinline__ const MuonTensor& long_matrix(const MuonArgs& p, long
 __device__ __forceinline__ double* long_slot(const MuonTensor& t, long mat, int slot) {
   return t.part + part_at(t, mat) + t.splits * (long)(tri_tiles(t.R / 16) * 256) + slot * (long)t.R * t.R;
 }
-// 1 / (|U| + eps), behind a matrix's slots
-__device__ __forceinline__ double* long_inv(const MuonTensor& t, long mat) { return long_slot(t, mat, LONG_SLOTS); }
+// the norm's factor of Q, behind a matrix's slots
+__device__ __forceinline__ double* long_norm(const MuonTensor& t, long mat) { return long_slot(t, mat, LONG_SLOTS); }
 
 __global__ __launch_bounds__(NT) void k_muon_long_sum(MuonArgs p, int per) {
   __shared__ double sums[NW];
@@ -657,9 +681,13 @@ __global__ __launch_bounds__(NT) void k_muon_long_sum(MuonArgs p, int per) {
   tr = 0.0;
 #pragma unroll
   for (int w = 0; w < NW; ++w) tr += sums[w];
-  const double inv = 1.0 / (sqrt(tr) + p.eps), inv2 = inv * inv;
+  const Norm norm(tr, p.eps);
+  const double inv2 = norm.all * norm.all;
   if (tile >= tri_tiles(t.R / 16)) return;
-  if (tile == 0) *long_inv(t, mat) = inv;
+  if (tile == 0) {
+    *long_norm(t, mat) = norm.of_q;
+    t.q[mat * q_size(t.R) + (long)t.R * t.R] = norm.of_u;
+  }
   tri(tile, i, j);
   part += tile * 256;
   double x[4] = {0.0, 0.0, 0.0, 0.0};
@@ -702,16 +730,16 @@ __global__ __launch_bounds__(NT) void k_muon_long_mul(MuonArgs p, int per, int x
       if (k0 + s / 4 * 16 < t.R) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(av[s], bv[s], acc, 0, 0, 0);
   }
   double* Z = long_slot(t, mat, z);
-  const double inv = out ? *long_inv(t, mat) : 0.0;
-  float* q = t.q + mat * (long)t.R * t.R;
+  const double of_q = out ? *long_norm(t, mat) : 0.0;
+  float* q = t.q + mat * q_size(t.R);
 #pragma unroll
   for (int v = 0; v < 4; ++v) {
     const int r = 16 * i + 4 * v + (lane >> 4), c = 16 * j + (lane & 15);
     const double one = r == c ? fa : 0.0;
     const double d = fma(fc, acc[v], fb != 0.0 ? fma(fb, X[(long)r * t.R + c], one) : one);
     if (out) {
-      q[(long)r * t.R + c] = (float)(d * inv);
-      q[(long)c * t.R + r] = (float)(d * inv);
+      q[(long)r * t.R + c] = over_norm(d, of_q);
+      q[(long)c * t.R + r] = over_norm(d, of_q);
     } else {
       Z[(long)r * t.R + c] = d;
       Z[(long)c * t.R + r] = d;
@@ -763,6 +791,7 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
     }
   };
   fetch(left);
+  const float* Q = t.q + mat * q_size(t.R);
   float q[IW][KT][4];
 #pragma unroll
   for (int i = 0; i < IW; ++i)
@@ -771,8 +800,9 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int row = 16 * kt + 4 * e + (lane >> 4), col = 16 * (wi + WI * i) + (lane & 15);
-        q[i][kt][e] = kt < nt && wi + WI * i < nt ? t.q[mat * (long)t.R * t.R + (long)row * t.R + col] : 0.0f;
+        q[i][kt][e] = kt < nt && wi + WI * i < nt ? Q[(long)row * t.R + col] : 0.0f;
       }
+  const float of_u = Q[(long)t.R * t.R];
   // rows past the short side are multiplied by zeros of Q and must be finite
   float* O = S + Sh::SIZE + 256;
   for (int i = threadIdx.x; i < Sh::SIZE; i += NT) S[i] = 0.0f;
@@ -785,7 +815,7 @@ __device__ __forceinline__ void apply(const MuonArgs& p, const MuonTensor& t, lo
       const f32x4 x = gv[i].get(), m = mv[i].get();
       f32x4 u;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) u[e] = p.nesterov ? fmaf(p.momentum, m[e], x[e] * gs) : m[e];
+      for (int e = 0; e < 4; ++e) u[e] = (p.nesterov ? fmaf(p.momentum, m[e], x[e] * gs) : m[e]) * of_u;
       *(f32x4*)(S + sh.lds[i]) = Sh::template only<VEC>(u, sh.have(i, left));
     }
 #pragma unroll
@@ -917,7 +947,7 @@ Plan plan_of(const moe_muon_tensor& t, double share) {
   p.span = span < 64 ? 64 : span > 0x1p30 ? 1 << 30 : (int)((span + 63) / 64) * 64;
   p.splits = (p.L + p.span - 1) / p.span;
   p.part = (size_t)t.batch * part_size(p.R, p.splits) * 8;
-  p.q = ((size_t)t.batch * p.R * p.R * 4 + 15) / 16 * 16;
+  p.q = (size_t)t.batch * q_size(p.R) * 4;  // a multiple of 16
   return p;
 }
 
