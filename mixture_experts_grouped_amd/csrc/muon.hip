@@ -945,7 +945,7 @@ Plan plan_of(const moe_muon_tensor& t, double share) {
   // of each 811 us, 16 of each 637)
   const double span = p.R > SHORT_R ? share : share / 4;
   p.span = span < 64 ? 64 : span > 0x1p30 ? 1 << 30 : (int)((span + 63) / 64) * 64;
-  p.splits = (p.L + p.span - 1) / p.span;
+  p.splits = 1 + (p.L - 1) / p.span;  // a long side just below 2^31 leaves no room for another span
   p.part = (size_t)t.batch * part_size(p.R, p.splits) * 8;
   p.q = (size_t)t.batch * q_size(p.R) * 4;  // a multiple of 16
   return p;
