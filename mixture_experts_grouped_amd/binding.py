@@ -712,6 +712,33 @@ def _own_memory(tensors: Sequence[Tuple[str, Sequence[torch.Tensor]]], read: str
         end, end_written = max(end, at + size), end_written if k == read else max(end_written, at + size)
 
 
+class _Made:
+    """The memory that an optimiser made for itself, `tensors`, on device dev:
+    for steps on any stream.  It is filled, and what it was used for before has
+    ended, when this returns (in a capture: when the stream gets there)."""
+
+    def __init__(self, dev: int, tensors: Sequence[torch.Tensor]):
+        # aliases: an attribute that is given another tensor does not let the memory go
+        self._dev, self._tensors = dev, [t.detach() for t in tensors]
+        with torch.cuda.device(dev):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
+        self._streams = {_raw_stream(dev)}
+
+    def used_on(self, stream) -> Optional[int]:
+        """A call on `stream` (None: the device's current one) is about to use it: once the optimiser is dropped, the
+        memory is not handed out again before that call has ended.  A stream that is not torch's own may be destroyed
+        by then and cannot be waited for.  Returns the stream's handle."""
+        handle = _raw_stream(self._dev) if stream is None else _stream(stream)
+        if handle not in self._streams:
+            self._streams.add(handle)
+            s = torch.cuda.current_stream(self._dev) if stream is None else stream
+            if isinstance(s, torch.cuda.Stream) and not isinstance(s, torch.cuda.ExternalStream):
+                for t in self._tensors:
+                    t.record_stream(s)
+        return handle
+
+
 class MoeAdamW:
     """AdamW over a list of tensors (the factors of one or more layers) in one
     call per step.  params: bf16 or fp32, all of one type, updated in place;
@@ -821,7 +848,9 @@ class MoeMuon:
     their memory).  states: {"momentum": [...]} fp32 to go on from, else zeros.
     rms: the update's root mean square, as far as its singular values are one.
     Keeps the workspace that its steps use: steps of one optimiser at the same
-    time (two streams, two captured graphs) are not allowed."""
+    time (two streams, two captured graphs) are not allowed.  It is kept as long
+    as a graph that captured a step of it, and, where a step ran on a stream
+    given by its handle, until that step has ended."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  masters: Optional[Sequence[torch.Tensor]] = None, lr: float = 0.02, momentum: float = 0.95,
@@ -840,8 +869,10 @@ class MoeMuon:
         f32, ptype, gtype = torch.float32, params[0].dtype, grads[0].dtype
         if masters is not None and ptype != torch.bfloat16:
             raise ValueError("masters stand beside bf16 params")
+        made = []
         if states is None:
-            states = {"momentum": [torch.zeros(p.shape, dtype=f32, device=p.device) for p in self.params]}
+            made = [torch.zeros(p.shape, dtype=f32, device=p.device) for p in self.params]
+            states = {"momentum": made}
         if set(states) != {"momentum"} or len(states["momentum"]) != len(params):
             raise ValueError("states must hold 'momentum', one tensor each per param")
         self.states = {"momentum": list(states["momentum"])}
@@ -865,7 +896,7 @@ class MoeMuon:
                    "moe_muon_workspace_size")
         self.workspace = torch.empty(v.value, dtype=torch.uint8, device=params[0].device)
         self._ws = (self.workspace.data_ptr(), v.value)
-        self._held.append(self.workspace.untyped_storage())
+        self._made = _Made(self._dev, [*made, self.workspace])
 
     def _fill(self) -> None:
         d = self._desc
@@ -885,7 +916,8 @@ class MoeMuon:
         d.lr = self.lr if lr is None else lr
         d.grad_scale = grad_scale
         d.control = _on(self._dev, control, torch.float32, (2,), "control")
-        _launch("moe_muon_step", library().moe_muon_step, self._dev, stream, self._dp, self._table, len(self._table), *self._ws)
+        _launch("moe_muon_step", library().moe_muon_step, self._dev, self._made.used_on(stream), self._dp, self._table,
+                len(self._table), *self._ws)
 
     def write_control(self, control: torch.Tensor, lr: float, grad_scale: float = 1.0) -> None:
         """Fill a control buffer (fp32 [2] on the device) with one step's
