@@ -574,7 +574,7 @@ def _launch(what: str, fn, dev: int, stream, *args) -> None:
     is not); stream None: that device's current one."""
     if dev < 0:
         raise ValueError(f"{what}: tensors must be device tensors")
-    handle = _raw_stream(dev) if stream is None else _stream(stream)
+    handle = _raw_stream(dev) if stream is None else stream if type(stream) is int else _stream(stream)
     if torch.cuda.current_device() == dev:
         st = fn(*args, handle)
     else:
@@ -720,23 +720,21 @@ class _Made:
     def __init__(self, dev: int, tensors: Sequence[torch.Tensor]):
         # aliases: an attribute that is given another tensor does not let the memory go
         self._dev, self._tensors = dev, [t.detach() for t in tensors]
-        with torch.cuda.device(dev):
-            if not torch.cuda.is_current_stream_capturing():
-                torch.cuda.current_stream().synchronize()
-        self._streams = {_raw_stream(dev)}
+        if tensors:
+            with torch.cuda.device(dev):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
+        self.streams = {_raw_stream(dev)}  # handles of those that used_on knows of
 
-    def used_on(self, stream) -> Optional[int]:
-        """A call on `stream` (None: the device's current one) is about to use it: once the optimiser is dropped, the
-        memory is not handed out again before that call has ended.  A stream that is not torch's own may be destroyed
-        by then and cannot be waited for.  Returns the stream's handle."""
-        handle = _raw_stream(self._dev) if stream is None else _stream(stream)
-        if handle not in self._streams:
-            self._streams.add(handle)
-            s = torch.cuda.current_stream(self._dev) if stream is None else stream
-            if isinstance(s, torch.cuda.Stream) and not isinstance(s, torch.cuda.ExternalStream):
-                for t in self._tensors:
-                    t.record_stream(s)
-        return handle
+    def used_on(self, handle: Optional[int], stream) -> None:
+        """A call on `stream` (its handle; None: the device's current one) is about to use it: once the optimiser is
+        dropped, the memory is not handed out again before that call has ended.  A stream that is not torch's own may
+        be destroyed by then and cannot be waited for."""
+        self.streams.add(handle)
+        s = torch.cuda.current_stream(self._dev) if stream is None else stream
+        if isinstance(s, torch.cuda.Stream) and not isinstance(s, torch.cuda.ExternalStream):
+            for t in self._tensors:
+                t.record_stream(s)
 
 
 class MoeAdamW:
@@ -748,7 +746,8 @@ class MoeAdamW:
     other memory, by `p.data = ...`, say); masters: fp32 copies of bf16 params that are
     updated instead, the params getting their rounding.  state_bits 32 or 8
     (see include/moelora.h); states: {"m": [...], "v": [...], "m_scale":
-    [...], "v_scale": [...]} to go on from, else zeros."""
+    [...], "v_scale": [...]} to go on from, else zeros.  Where a step runs on a
+    stream given by its handle, the optimiser is kept until that step has ended."""
 
     def __init__(self, params: Sequence[torch.Tensor], grads: Sequence[torch.Tensor],
                  masters: Optional[Sequence[torch.Tensor]] = None, state_bits: int = 32, lr: float = 1e-3,
@@ -768,7 +767,8 @@ class MoeAdamW:
         eight = state_bits == 8
         kinds = {"m": torch.float8_e4m3fn, "v": torch.float8_e5m2} if eight else dict.fromkeys("mv", torch.float32)
         runs = [-(-p.numel() // 128) for p in self.params]
-        if states is None:
+        own = states is None
+        if own:
             states = {n: [torch.zeros(p.shape, dtype=torch.uint8 if eight else t, device=p.device).view(t)
                           for p in self.params] for n, t in kinds.items()}
             if eight:
@@ -801,6 +801,8 @@ class MoeAdamW:
         # the memory outlives a replacement of a tensor's own
         self._held = [t.untyped_storage() for ts in (self.params, self.grads, self.masters or [], *self.states.values()) for t in ts]
         _own_memory([("params", self.params), ("grads", self.grads), ("masters", self.masters or []), *self.states.items()])
+        self._made = _Made(self._dev, [t for ts in self.states.values() for t in ts] if own else [])
+        self._streams, self._call = self._made.streams, library().moe_adamw_step
 
     def step(self, lr: Optional[float] = None, step: Optional[int] = None, grad_scale: float = 1.0,
              seed: Optional[int] = None, control: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -820,7 +822,10 @@ class MoeAdamW:
         if self.state_bits == 8:
             d.seed = (number if seed is None else seed) & 0xFFFFFFFF
         d.control = _on(self._dev, control, torch.int32, (5,), "control")
-        _launch("moe_adamw_step", library().moe_adamw_step, self._dev, stream, self._dp, self._table, len(self._table))
+        handle = _raw_stream(self._dev) if stream is None else _stream(stream)
+        if handle not in self._streams:
+            self._made.used_on(handle, stream)
+        _launch("moe_adamw_step", self._call, self._dev, handle, self._dp, self._table, len(self._table))
         self.steps = number  # only a step that was taken
 
     def write_control(self, control: torch.Tensor, lr: float, step: int, grad_scale: float = 1.0,
@@ -897,6 +902,7 @@ class MoeMuon:
         self.workspace = torch.empty(v.value, dtype=torch.uint8, device=params[0].device)
         self._ws = (self.workspace.data_ptr(), v.value)
         self._made = _Made(self._dev, [*made, self.workspace])
+        self._streams, self._call = self._made.streams, library().moe_muon_step
 
     def _fill(self) -> None:
         d = self._desc
@@ -916,8 +922,10 @@ class MoeMuon:
         d.lr = self.lr if lr is None else lr
         d.grad_scale = grad_scale
         d.control = _on(self._dev, control, torch.float32, (2,), "control")
-        _launch("moe_muon_step", library().moe_muon_step, self._dev, self._made.used_on(stream), self._dp, self._table,
-                len(self._table), *self._ws)
+        handle = _raw_stream(self._dev) if stream is None else _stream(stream)
+        if handle not in self._streams:
+            self._made.used_on(handle, stream)
+        _launch("moe_muon_step", self._call, self._dev, handle, self._dp, self._table, len(self._table), *self._ws)
 
     def write_control(self, control: torch.Tensor, lr: float, grad_scale: float = 1.0) -> None:
         """Fill a control buffer (fp32 [2] on the device) with one step's

@@ -9,7 +9,8 @@ from tests import harness as Hn
 
 pytestmark = pytest.mark.gpu
 BF = torch.bfloat16
-MAKE = {"muon": lambda p, g: M.MoeMuon([p], [g], lr=0.05)}
+MAKE = {"muon": lambda p, g: M.MoeMuon([p], [g], lr=0.05), "adamw": lambda p, g: M.MoeAdamW([p], [g], lr=0.05),
+        "adamw8": lambda p, g: M.MoeAdamW([p], [g], lr=0.05, state_bits=8)}
 
 
 @pytest.fixture(scope="module", autouse=True)
