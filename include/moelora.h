@@ -531,7 +531,7 @@ typedef struct moe_fp8_desc {
 /* out [pool->capacity, N] bf16: the rows of routes are written, padding and
  * unused rows are left as they were.  pool: counts, offsets and row_to_route
  * as build_pool wrote them (route_to_row is not read and may be NULL), E
- * experts, capacity = its allocated rows, at least 1.  a [a_rows, K], a_scales [a_rows,
+ * experts, capacity = its allocated rows, 1 to 2^31 - 256.  a [a_rows, K], a_scales [a_rows,
  * K/128], w [E, N, K], w_scales [E, N/128, K/128].  A route whose activation
  * row is not below a_rows reads zeros; rows past the capacity are not
  * touched whatever the pool says.  Which kernel runs follows from the shapes;
@@ -565,8 +565,9 @@ typedef struct moe_expert_desc {
 /* out [pool->capacity, N] bf16: the rows of routes are written, padding and
  * unused rows are left as they were.  a [a_rows, K] bf16, w bf16.  pool:
  * counts, offsets and row_to_route as build_pool wrote them (route_to_row is
- * not read and may be NULL).  A route whose activation row is not below a_rows
- * reads zeros; rows past the capacity are not touched whatever the pool says. */
+ * not read and may be NULL), capacity 1 to 2^31 - 256.  A route whose
+ * activation row is not below a_rows reads zeros; rows past the capacity are
+ * not touched whatever the pool says. */
 moe_status moe_expert_product(const moe_expert_desc* desc, const moe_pool* pool, const void* a, const void* w,
                               void* out, void* stream);
 

@@ -683,7 +683,7 @@ moe_status moe_fp8_product(const moe_fp8_desc* d, const moe_pool* pool, const vo
   if (st != MOE_OK) return st;
   if (d->topk < 0 || d->a_rows < 1 || pool->capacity < 1 || pool->block_m < 1)
     return MOE_ERR_INVALID;
-  if (pool->capacity >= (int64_t)1 << 31 || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  if (pool->capacity > MOST_ROWS || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   // tile indices of the smallest tiles are 32 bits
   if ((pool->capacity / FEW_ROWS + d->E) * (d->N / 16) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (d->topk > 0 && d->a_rows * d->K >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor

@@ -250,7 +250,7 @@ moe_status check_common(const moe_expert_desc* d, const moe_pool* pool) {
       (int64_t)d->N * d->K >= (int64_t)1 << 30)
     return MOE_ERR_UNSUPPORTED;
   if (d->topk < 0 || d->a_rows < 1 || pool->capacity < 1 || pool->block_m < 1) return MOE_ERR_INVALID;
-  if (pool->capacity >= (int64_t)1 << 31 || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+  if (pool->capacity > MOST_ROWS || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   // tile indices of the smallest tiles are 32 bits
   if ((pool->capacity / 16 + d->E) * ((d->N + 15) / 16) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (d->topk > 0 && d->a_rows * d->K >= (int64_t)1 << 30) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor

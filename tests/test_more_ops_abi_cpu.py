@@ -214,3 +214,17 @@ def test_python_calls_refuse_shapes():
                  lambda: M.MoeMuon([], []), lambda: M.MoeMuon([cpu(4, 8)], []), lambda: M.MoeMuon([cpu(8)], [cpu(8)])):
         with pytest.raises(ValueError):
             call()
+
+
+def fp8(p, a=4 * MB):
+    d = B.MoeFp8Desc(4, 128, 128, 2, 100)
+    return B.library().moe_fp8_product(ref(d), ref(p), a, 5 * MB, 6 * MB, 7 * MB, 8 * MB, None)
+
+
+@pytest.mark.parametrize("call", [lambda p, a: product(expert_desc(), p, a=a), lambda p, a: grad(expert_desc(), p, a=a),
+                                  lambda p, a: mx(mx_desc(), p, a=a), fp8])
+def test_most_rows_of_a_pool(call):
+    """An expert's rows and a tile's less one: 32 bits.  (At the limit the call gets to the pointer that is missing.)"""
+    for capacity in ((1 << 31) - 1, (1 << 31) - 255):
+        assert call(pool(capacity=capacity), None) == UNS
+    assert call(pool(capacity=(1 << 31) - 256), None) == INV
