@@ -35,7 +35,10 @@ struct WgradTile {
   int e, m0, n0, n;  // expert, first column of grad and of a, rows
   long row0;
 };
-template <bool GATHER, class OUT>
+// FAR: an expert's ids may be more than the 2 GB that a descriptor spans, and each
+// stage's have one of their own; 0.9 % slower at 98,304 rows (3,017 for 2,992 us),
+// so it is a kernel by itself, for pools of 2^29 - 4 rows and more.
+template <bool GATHER, bool FAR, class OUT>
 struct Wgrad {
   using G = stream::Geo<256, 256, 4, 2, 2>;
   using Tile = WgradTile;
@@ -53,6 +56,7 @@ struct Wgrad {
   stream::ColFrags<64> fx, fw;
   // the tile aimed at
   const char *gx, *gw;
+  const char* gi;  // FAR: the ids that the next stage's loads fetch
   stream::desc_t da, di;
   int n;
   uint32_t vx[2], vw[2], tok[2];
@@ -107,7 +111,10 @@ struct Wgrad {
     n = (int)stream::uniform(any ? (uint32_t)t.n : 0u);
     if constexpr (GATHER) {
       da = stream::make_desc(p.a, any ? (uint64_t)p.a_rows * p.K * 2 : 0);
-      di = stream::make_desc(p.row2r + t.row0, (uint64_t)n * 4);
+      if constexpr (FAR)
+        gi = stream::uniform(p.row2r + t.row0 + 128);
+      else
+        di = stream::make_desc(p.row2r + t.row0, (uint64_t)n * 4);
     }
     const int kr = 4 * wv + (l >> 4), c = 8 * ((l & 15) ^ stream::t_swz(kr));
 #pragma unroll
@@ -131,7 +138,13 @@ struct Wgrad {
     if (i < NI) {
       // the ids of stage s + 2, and the tokens of this one
       const int l = threadIdx.x & 63;
-      stream::load4(di, smem + IDS + ((s & (RING - 1)) * G::NW + wv) * 256, 4u * (uint32_t)(64 * (s + 2) + l), 0);
+      char* to = smem + IDS + ((s & (RING - 1)) * G::NW + wv) * 256;
+      if constexpr (FAR) {
+        stream::load4(stream::make_desc(gi, 4u * (uint32_t)min(max(n - 64 * s - 128, 0), 64)), to, 4u * (uint32_t)l, 0);
+        gi += 256;
+      } else {
+        stream::load4(di, to, 4u * (uint32_t)(64 * (s + 2) + l), 0);
+      }
       const char* from = smem + (s < 2 ? HEAD + (s * G::NW + wv) * 256 : IDS + (((s - 2) & (RING - 1)) * G::NW + wv) * 256);
       const int left = n - 64 * s;
 #pragma unroll
@@ -220,27 +233,33 @@ struct Wgrad {
   }
 };
 
-template <bool GATHER, class OUT>
+template <bool GATHER, bool FAR, class OUT>
 __global__ __launch_bounds__(512) void k_weight_grad(WgradArgs p) {
   extern __shared__ __align__(16) char smem[];
-  Wgrad<GATHER, OUT> t(p, smem);
+  Wgrad<GATHER, FAR, OUT> t(p, smem);
   WgradTile cur{};
   if (!t.first(cur)) return;
   stream::run(t, cur, smem);
 }
 
-template <bool GATHER, class OUT>
+template <bool GATHER, bool FAR, class OUT>
 hipError_t launch_wgrad(const WgradArgs& p, int64_t tiles, int cus, hipStream_t st) {
   static PerDeviceOnce once;
-  using W = Wgrad<GATHER, OUT>;
+  using W = Wgrad<GATHER, FAR, OUT>;
   const hipError_t e = once.run([] {
     AttrInit ai;
-    ai.lds((const void*)k_weight_grad<GATHER, OUT>, W::LDS);
+    ai.lds((const void*)k_weight_grad<GATHER, FAR, OUT>, W::LDS);
     return ai.err;
   });
   if (e != hipSuccess) return e;
-  MOE_LAUNCH_AS("k_weight_grad", (k_weight_grad<GATHER, OUT>), dim3(grid_of(tiles, cus)), dim3(512), W::LDS, st, p);
+  MOE_LAUNCH_AS("k_weight_grad", (k_weight_grad<GATHER, FAR, OUT>), dim3(grid_of(tiles, cus)), dim3(512), W::LDS, st, p);
   return hipGetLastError();
+}
+template <class OUT>
+hipError_t launch_wgrad(const WgradArgs& p, int64_t tiles, int cus, hipStream_t st) {
+  if (p.topk == 0) return launch_wgrad<false, false, OUT>(p, tiles, cus, st);
+  return (uint64_t)p.cap * 4 < RSRC_MAX ? launch_wgrad<true, false, OUT>(p, tiles, cus, st)
+                                        : launch_wgrad<true, true, OUT>(p, tiles, cus, st);
 }
 
 moe_status check_common(const moe_expert_desc* d, const moe_pool* pool) {
@@ -323,11 +342,7 @@ moe_status moe_expert_weight_grad(const moe_expert_desc* d, const moe_pool* pool
                     (const uint16_t*)a, dw};
   const int64_t tiles = (int64_t)d->E * ((d->N + 255) / 256) * ((d->K + 255) / 256);
   const hipStream_t st = (hipStream_t)stream;
-  const bool f32 = d->out_type == MOE_TYPE_F32;
-  if (d->topk > 0)
-    e = f32 ? launch_wgrad<true, float>(p, tiles, cus, st) : launch_wgrad<true, uint16_t>(p, tiles, cus, st);
-  else
-    e = f32 ? launch_wgrad<false, float>(p, tiles, cus, st) : launch_wgrad<false, uint16_t>(p, tiles, cus, st);
+  e = d->out_type == MOE_TYPE_F32 ? launch_wgrad<float>(p, tiles, cus, st) : launch_wgrad<uint16_t>(p, tiles, cus, st);
   return e == hipSuccess ? MOE_OK : MOE_ERR_HIP;
 }
 
