@@ -270,8 +270,6 @@ moe_status check_common(const moe_expert_desc* d, const moe_pool* pool) {
     return MOE_ERR_UNSUPPORTED;
   if (d->topk < 0 || d->a_rows < 1 || pool->capacity < 1 || pool->block_m < 1) return MOE_ERR_INVALID;
   if (pool->capacity > MOST_ROWS || d->a_rows >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
-  // tile indices of the smallest tiles are 32 bits
-  if ((pool->capacity / 16 + d->E) * ((d->N + 15) / 16) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (d->topk > 0 && d->a_rows * d->K >= (int64_t)1 << 30) return MOE_ERR_UNSUPPORTED;  // one buffer descriptor
   if (!aligned(pool->counts, 4) || !aligned(pool->offsets, 4) || !aligned(pool->row_to_route, 4))
     return MOE_ERR_INVALID;
@@ -295,6 +293,8 @@ moe_status moe_expert_product(const moe_expert_desc* d, const moe_pool* pool, co
   const moe_status s = check_common(d, pool);
   if (s != MOE_OK) return s;
   if (d->transposed != 0 && d->transposed != 1) return MOE_ERR_INVALID;
+  // tile indices of the smallest tiles are 32 bits
+  if ((pool->capacity / FEW_ROWS + d->E) * ((d->N + 15) / 16) >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
   if (!aligned16(a) || !aligned16(w) || !aligned16(out)) return MOE_ERR_INVALID;
   const Range in[] = {rng(a, (size_t)d->a_rows * d->K * 2), rng(w, (size_t)d->E * d->N * d->K * 2),
                       rng(pool->counts, (size_t)d->E * 4), rng(pool->offsets, (size_t)d->E * 4 + 4),

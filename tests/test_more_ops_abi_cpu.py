@@ -228,3 +228,9 @@ def test_most_rows_of_a_pool(call):
     for capacity in ((1 << 31) - 1, (1 << 31) - 255):
         assert call(pool(capacity=capacity), None) == UNS
     assert call(pool(capacity=(1 << 31) - 256), None) == INV
+
+
+def test_a_products_tiles_are_no_limit_of_the_gradient():
+    p = pool(capacity=(1 << 31) - 256)
+    assert product(expert_desc(N=65528), p, a=None) == UNS
+    assert grad(expert_desc(N=65528), p, g=None) == INV  # gets to the pointer that is missing
