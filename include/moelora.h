@@ -567,12 +567,13 @@ typedef struct moe_expert_desc {
  * counts, offsets and row_to_route as build_pool wrote them (route_to_row is
  * not read and may be NULL), capacity 1 to 2^31 - 256.  A route whose
  * activation row is not below a_rows reads zeros; rows past the capacity are
- * not touched whatever the pool says. */
+ * not touched whatever the pool says.  (capacity / 16 + E) * ceil(N / 16) <
+ * 2^31. */
 moe_status moe_expert_product(const moe_expert_desc* desc, const moe_pool* pool, const void* a, const void* w,
                               void* out, void* stream);
 
 /* grad [pool->capacity, N] bf16 (rows of no route are not used), a [a_rows, K]
- * bf16, dw [E, N, K] of out_type. */
+ * bf16, dw [E, N, K] of out_type; pool as in moe_expert_product. */
 moe_status moe_expert_weight_grad(const moe_expert_desc* desc, const moe_pool* pool, const void* grad, const void* a,
                                   void* dw, void* stream);
 
@@ -589,7 +590,8 @@ moe_status moe_expert_weight_grad(const moe_expert_desc* desc, const moe_pool* p
  * ------------------------------------------------------------------------ */
 /* act as in moe_fp8_quantize_rows: src [rows, K] bf16 (MOE_FP8_PLAIN) or
  * [rows, 2K] = [gate | up].  codes [rows, K / 2] bytes, exponents [rows, K / 32]
- * bytes.  K % 128 == 0 and at most 65536, rows >= 0, rows * K at most 2^35. */
+ * bytes.  K % 128 == 0 and at most 65536, 0 <= rows < 2^31 (0: nothing is
+ * done), rows * K at most 2^35 - 2048. */
 moe_status moe_mxfp4_quantize_rows(const void* src, int64_t rows, int32_t K, int32_t act, void* codes,
                                    void* exponents, void* stream);
 
@@ -597,12 +599,13 @@ moe_status moe_mxfp4_quantize_rows(const void* src, int64_t rows, int32_t K, int
  * along K) and, if both are given, of the transposed weight: codes_t [E, K,
  * N / 2] and exponents_t [E, K, N / 32] (blocks along N: other roundings of the
  * same weight), the data gradient's operand.  N, K % 128 == 0 and at most
- * 65536, 1 <= E <= 512, N * K < 2^31. */
+ * 65536, 1 <= E <= 512, N * K < 2^31, E * N * K at most 2^35 - 2048. */
 moe_status moe_mxfp4_quantize_weight(const void* W, int32_t E, int32_t N, int32_t K, void* codes, void* exponents,
                                      void* codes_t, void* exponents_t, void* stream);
 
 /* What codes and exponents stand for, exactly, as bf16 [rows, K] (values below
- * bf16's smallest normal 2^-126 included; 255: NaN).  K % 128 == 0. */
+ * bf16's smallest normal 2^-126 included; beyond its largest: infinities; 255:
+ * NaN).  rows and K as in moe_mxfp4_quantize_rows. */
 moe_status moe_mxfp4_dequantize(const void* codes, const void* exponents, int64_t rows, int32_t K, void* out,
                                 void* stream);
 
@@ -617,7 +620,8 @@ typedef struct moe_mxfp4_desc {
  * K / 32] (an MXFP4 base's W13 or W2 as the layer takes it): the products of
  * what the codes stand for, added by the scaled matrix instructions in fp32,
  * 128 at a time.  A NaN exponent makes its row's results NaN (a weight's: its
- * column's). */
+ * column's).  pool as in moe_expert_product; (capacity / 16 + E) * (N / 16) <
+ * 2^31. */
 moe_status moe_mxfp4_product(const moe_mxfp4_desc* desc, const moe_pool* pool, const void* a, const void* a_exponents,
                              const void* w, const void* w_exponents, void* out, void* stream);
 

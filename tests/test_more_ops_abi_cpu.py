@@ -234,3 +234,21 @@ def test_a_products_tiles_are_no_limit_of_the_gradient():
     p = pool(capacity=(1 << 31) - 256)
     assert product(expert_desc(N=65528), p, a=None) == UNS
     assert grad(expert_desc(N=65528), p, g=None) == INV  # gets to the pointer that is missing
+
+
+def test_mxfp4_most_values():
+    """2^35 - 2048 values; one row or matrix more is refused (at the limit a call gets to the pointer that is missing)."""
+    lib = B.library()
+
+    def rows(n, K):
+        return lib.moe_mxfp4_quantize_rows(None, n, K, B.MOE_FP8_PLAIN, 2 * MB, 3 * MB, None)
+
+    def back(n, K):
+        return lib.moe_mxfp4_dequantize(None, 2 * MB, n, K, 3 * MB, None)
+
+    def weight(E, N, K):
+        return lib.moe_mxfp4_quantize_weight(None, E, N, K, 2 * MB, 3 * MB, None, None, None)
+    for f in (rows, back):
+        assert f(1 << 24, 2048) == UNS and f((1 << 24) - 1, 2048) == INV
+        assert f(1 << 28, 128) == UNS and f((1 << 28) - 16, 128) == INV and f((1 << 28) - 15, 128) == UNS
+    assert weight(64, 32768, 16384) == UNS and weight(63, 32768, 16384) == INV and weight(64, 32640, 16384) == INV
