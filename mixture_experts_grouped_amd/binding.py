@@ -537,6 +537,7 @@ def moe_lora_split_e2m3x2(src: torch.Tensor, stream=None) -> Tuple[torch.Tensor,
     if src.dim() != 2:
         raise ValueError("src must be [rows, K]")
     rows, K = src.shape
+    _in32(K)
     codes = torch.empty(rows, 2 * K, dtype=torch.uint8, device=src.device)
     scales = torch.empty(K // 64, rows, dtype=torch.int32, device=src.device)
     st = library().moe_lora_split_e2m3x2(_ptr(src, torch.bfloat16, None, "src"), rows, K,
@@ -560,6 +561,13 @@ def _on(dev: int, t: Optional[torch.Tensor], dtype, shape, name: str) -> Optiona
     if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}: one call runs on one device")
     return p
+
+
+def _in32(bits: int) -> None:
+    """bits: the sizes of a call, or-ed.  ctypes keeps the lower 32 bits of what does not fit: a width of 2^32 + 8
+    would run as one of 8."""
+    if bits >> 31:
+        raise ValueError("a size of 2^31 or more")
 
 
 def _device_of(t: torch.Tensor, name: str) -> int:
@@ -866,6 +874,8 @@ class MoeMuon:
             raise ValueError("params, grads and masters are lists of one length, not empty")
         if any(p.dim() < 2 for p in params):
             raise ValueError("params are matrices, or stacks of them: [..., m, n]")
+        for p in params:
+            _in32(p.shape[-2] | p.shape[-1])
         self.params, self.grads = list(params), list(grads)
         self.masters = None if masters is None else list(masters)
         self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
@@ -953,6 +963,7 @@ def fp8_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Optio
     rows, K = src.shape
     if act is not None:
         K //= 2
+    _in32(K)
     dev = _device_of(src, "src")
     if codes is None:
         codes = _made(stream, torch.empty, rows, K, dtype=_E4M3, device=src.device)
@@ -976,6 +987,7 @@ def fp8_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None) 
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     E, N, K = W.shape
+    _in32(E | N | K)
     dev = _device_of(W, "W")
 
     def pair(n, k):
@@ -1007,6 +1019,7 @@ def fp8_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_scales: torch.
         raise ValueError("a must be [rows, K] and w [E, N, K]")
     rows, K = a.shape
     E, N = w.shape[:2]
+    _in32(E | N | K | abs(topk) | abs(block_m))
     cap = pool["row_to_route"].numel()
     dev = _device_of(a, "a")
     if out is None:
@@ -1039,6 +1052,7 @@ def expert_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, w: torch.Tens
         raise ValueError("a must be [rows, K] and w [E, N, K], or [E, K, N] with transposed")
     rows, K = a.shape
     E, N = w.shape[0], w.shape[2 if transposed else 1]
+    _in32(E | N | K | abs(topk) | abs(block_m))
     cap = pool["row_to_route"].numel()
     dev = _device_of(a, "a")
     bf = torch.bfloat16
@@ -1064,6 +1078,7 @@ def expert_weight_grad(pool: Dict[str, torch.Tensor], grad: torch.Tensor, a: tor
         raise ValueError("grad must be [capacity, N] and a [rows, K]")
     rows, K = a.shape
     E, N = pool["counts"].numel(), grad.shape[1]
+    _in32(E | N | K | abs(topk) | abs(block_m))
     cap = pool["row_to_route"].numel()
     dev = _device_of(a, "a")
     bf = torch.bfloat16
@@ -1091,6 +1106,7 @@ def mxfp4_quantize_rows(src: torch.Tensor, act: Optional[str] = None, codes: Opt
     rows, K = src.shape
     if act is not None:
         K //= 2
+    _in32(K)
     dev, u8 = _device_of(src, "src"), torch.uint8
     if codes is None:
         codes = _made(stream, torch.empty, (rows, K // 2), dtype=u8, device=src.device)
@@ -1115,6 +1131,7 @@ def mxfp4_quantize_weight(W: torch.Tensor, transposed: bool = False, stream=None
     if W.dim() != 3:
         raise ValueError("W must be [E, N, K]")
     E, N, K = W.shape
+    _in32(E | N | K)
     dev = _device_of(W, "W")
 
     def pair(n, k):
@@ -1131,6 +1148,7 @@ def mxfp4_dequantize(codes: torch.Tensor, exponents: torch.Tensor, out: Optional
     if codes.dim() < 1 or not codes.is_contiguous():
         raise ValueError("codes must be [..., K/2], contiguous")
     shape = (*codes.shape[:-1], 2 * codes.shape[-1])
+    _in32(shape[-1])
     K, dev, u8 = shape[-1], _device_of(codes, "codes"), torch.uint8
     if K % 128:
         raise ValueError("K must be a multiple of 128")
@@ -1155,6 +1173,7 @@ def mxfp4_product(pool: Dict[str, torch.Tensor], a: torch.Tensor, a_exponents: t
         raise ValueError("a must be [rows, K/2] and w [E, N, K/2]")
     rows, K = a.shape[0], 2 * a.shape[1]
     E, N = w.shape[:2]
+    _in32(E | N | K | abs(topk) | abs(block_m))
     cap = pool["row_to_route"].numel()
     dev, u8 = _device_of(a, "a"), torch.uint8
     if out is None:

@@ -252,3 +252,26 @@ def test_mxfp4_most_values():
         assert f(1 << 24, 2048) == UNS and f((1 << 24) - 1, 2048) == INV
         assert f(1 << 28, 128) == UNS and f((1 << 28) - 16, 128) == INV and f((1 << 28) - 15, 128) == UNS
     assert weight(64, 32768, 16384) == UNS and weight(63, 32768, 16384) == INV and weight(64, 32640, 16384) == INV
+
+
+def test_python_calls_refuse_sizes_that_32_bits_do_not_hold():
+    """They would run as what the lower 32 bits say."""
+    def wide(*shape, dtype=torch.bfloat16):
+        return torch.empty(1, dtype=dtype).expand(*shape)
+    far, u8 = (1 << 32) + 128, torch.uint8
+    p = {n: cpu(4, dtype=torch.int32) for n in ("counts", "offsets", "row_to_route")}
+    e4 = torch.float8_e4m3fn
+    for call in (lambda: M.expert_product(p, wide(1, far), wide(1, 8, far)), lambda: M.expert_product(p, wide(1, 8), wide(1, far, 8)),
+                 lambda: M.expert_product(p, cpu(4, 8), cpu(4, 8, 8), topk=1 << 32),
+                 lambda: M.expert_product(p, cpu(4, 8), cpu(4, 8, 8), block_m=(1 << 32) + 16),
+                 lambda: M.expert_weight_grad(p, wide(4, far), cpu(4, 8)), lambda: M.expert_weight_grad(p, cpu(4, 8), wide(4, far)),
+                 lambda: M.mxfp4_quantize_rows(wide(1, far)), lambda: M.mxfp4_quantize_rows(wide(1, 2 * far), act="swiglu"),
+                 lambda: M.mxfp4_quantize_weight(wide(1, far, 128)), lambda: M.mxfp4_quantize_weight(wide(1, 128, far)),
+                 lambda: M.mxfp4_dequantize(torch.empty(1, 1 << 30, dtype=u8), cpu(1, 1 << 20, dtype=u8)),
+                 lambda: M.mxfp4_product(p, wide(1, far, dtype=u8), wide(1, 4, dtype=u8), wide(1, 32, far, dtype=u8), wide(1, dtype=u8)),
+                 lambda: M.MoeMuon([wide(1, far)], [wide(1, far)]), lambda: M.MoeMuon([wide(far, 1)], [wide(far, 1)]),
+                 lambda: M.fp8_quantize_rows(wide(1, far)), lambda: M.fp8_quantize_weight(wide(1, 128, far)),
+                 lambda: M.fp8_product(p, wide(1, far, dtype=e4), cpu(1, 1), wide(1, 128, far, dtype=e4), cpu(1, 1)),
+                 lambda: B.moe_lora_split_e2m3x2(wide(1, far))):
+        with pytest.raises(ValueError, match="2\\^31"):
+            call()
