@@ -24,13 +24,16 @@ struct WgradArgs : PoolArgs {
 // into a ring of LDS; each wave keeps its own copy, so that its own wait covers
 // them.  The ids of a tile's first two stages have a place of their own, filled
 // when the tile is found.
-// 256 x 256 tiles for every size: what a tile writes weighs more than its stages
-// where an expert has few rows.  98,304 rows, 64 x 4096 x 4096 in bf16: 3,000 us,
-// 1,100 TFLOP/s (matrix cores busy 54 % at 2.0 GHz: both operands come through
-// transposing reads; rows of a already in the pool's order 2,844 us; ids fetched a
-// stage earlier: no change).  One token: 500 us for 2.1 GB of zeros and six experts'
-// tiles, 4.2 TB/s (non-temporal stores 630).  40 x 520 x 1000 in fp32, added to: 37.5
-// us for 166 MB read and written.
+// 256 x 256 tiles for every size, each tile's rows one chain of stages.  98,304
+// rows, 64 x 4096 x 4096 in bf16: 2,984 to 3,137 us by card, 1,050 to 1,100 TFLOP/s
+// (matrix cores busy 53 % at 2.0 GHz: both operands come through transposing reads;
+// rows of a already in the pool's order 5 % less; ids fetched a stage earlier: no
+// change).  One token: 500 us for 2.1 GB of zeros and six experts' tiles, 4.2 TB/s
+// (non-temporal stores 630).  40 x 520 x 1000 in fp32, added to: 37.6 us for 166 MB
+// read and written, 480 tiles in two rounds over the CUs.  Where there are fewer
+// tiles than CUs the others stand idle: 24,576 rows on one expert of 256 x 256 take
+// 465 us on one CU (gathered 545), of 64 x 64 as long; 16 experts of 512 x 512 with
+// 2,048 rows each 54 us on 64.
 struct WgradTile {
   int e, m0, n0, n;  // expert, first column of grad and of a, rows
   long row0;

@@ -265,7 +265,8 @@ struct RowsTile {
 // rows an expert, where an operand's read must feed as many products as the
 // registers hold sums for.  bf16, 98,304 rows of 4096 x 4096: 2,550 us, 1,295
 // TFLOP/s, the rate that the library's 8192^3 product reaches (matrix cores busy 76 %
-// at the power cap's 1.73 GHz; without the results' stores 2,448 us).  Weight stored
+// at the power cap's 1.73 GHz; without the results' stores 2,448 us; on other cards
+// up to 2,680, and the next two by as much).  Weight stored
 // K-outer (4096 x 2048): 1,390 us, 1,185 TFLOP/s, 65 % at 1.91 GHz: the transposing
 // reads carry half as much an instruction.  4 bits: 900 us, 3,660 TFLOP/s; a block
 // product takes 19 clocks of a SIMD, its operands' reads and refills together 83 % of
