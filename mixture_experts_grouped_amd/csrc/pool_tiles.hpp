@@ -39,8 +39,8 @@ __device__ __forceinline__ int token_of(const PoolArgs& p, int route) {
 // group_tile: each XCD a contiguous range of (expert's M chunk, N tile, M
 // tile), so that workgroups of one XCD share a weight panel in its L2.
 constexpr int MAX_E = 512;
-// Rows of a pool, at most: an expert's with those of a tile (256 or fewer) less
-// one are rounded down to tiles in 32 bits.
+// Rows of a pool, at most: an expert's are rounded up to whole tiles (of 256 rows or
+// fewer) in 32 bits.
 constexpr int64_t MOST_ROWS = ((int64_t)1 << 31) - 256;
 // More tiles than a pool can have: the sums stop there, so that no counts make
 // them wrap.

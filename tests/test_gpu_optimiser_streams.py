@@ -113,3 +113,12 @@ def test_made_in_a_capture(kind):
         torch.cuda.synchronize()
         assert torch.equal(p, q)
     del opt
+
+
+@pytest.mark.parametrize("kind", MAKE)
+def test_nothing_to_update_on_another_stream(kind):
+    p, g = torch.zeros(0, 4, 6, device="cuda"), torch.zeros(0, 4, 6, device="cuda")
+    opt, s = MAKE[kind](p, g), torch.cuda.Stream()
+    opt.step(stream=s)
+    opt.step()
+    torch.cuda.synchronize()
